@@ -10,4 +10,9 @@ from ._lib import (  # noqa: F401
     fbob_bob_workspace_bytes, fbob_debug_stall_producer, fbob_device_status, fbob_profile_enable,
     fbob_profile_report, fbob_set_wait_limit_ns, load, problem_for,
 )
+from ._model import (  # noqa: F401
+    Norm, Rotary, fbob_layer_norm_bob, fbob_layer_norm_bwd, fbob_layer_norm_fwd, fbob_layer_norm_workspace_bytes,
+    fbob_rotary_apply, fbob_rotary_frequencies, norm_for,
+)
 from .autograd import attention, hvp  # noqa: F401
+from .model import layer_norm, rotary  # noqa: F401

@@ -25,6 +25,8 @@ FUNCTIONS = (
     "fbob_device_status", "fbob_set_wait_limit_ns", "fbob_status_string", "fbob_last_error",
     "fbob_abi_version", "fbob_attn_bob_noalloc", "fbob_profile_enable", "fbob_profile_report",
     "fbob_debug_stall_producer", "fbob_attn_bob_four_pass",
+    "fbob_rotary_frequencies", "fbob_rotary_apply",
+    "fbob_layer_norm_workspace_bytes", "fbob_layer_norm_fwd", "fbob_layer_norm_bwd", "fbob_layer_norm_bob",
 )
 
 
@@ -32,6 +34,38 @@ class Problem(ctypes.Structure):
     """fbob_problem: B x H heads of N x d matrices, score scale tau."""
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int), ("d", ctypes.c_int),
                 ("tau", ctypes.c_float), ("dtype", ctypes.c_int), ("causal", ctypes.c_int)]
+
+
+ROTARY_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+class Rotary(ctypes.Structure):
+    """fbob_rotary: the rotation of the leading ``rot`` columns of a head by
+    position.  ``interleaved``: pairs (2i, 2i+1), else (i, i + rot/2).
+    ``scaling``: "none", "linear", "base" or "parts" (include/fbob.h has the
+    formulas); ``magnitude`` multiplies the rotated columns."""
+    _fields_ = [("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("original", ctypes.c_double),
+                ("slow", ctypes.c_double), ("fast", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+    def __init__(self, rot, base=10000.0, interleaved=False, scaling="none", factor=1.0, original=0.0, slow=1.0,
+                 fast=4.0, magnitude=1.0):
+        if scaling not in ROTARY_SCALING:
+            raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALING)}, got {scaling!r}")
+        super().__init__(rot, int(bool(interleaved)), ROTARY_SCALING[scaling], base, factor, original, slow, fast,
+                         magnitude)
+
+
+class RotaryHeads(ctypes.Structure):
+    """fbob_rotary_heads."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int),
+                ("x_stride", ctypes.c_longlong * 3), ("y_stride", ctypes.c_longlong * 3)]
+
+
+class Norm(ctypes.Structure):
+    """fbob_norm: rows of D elements."""
+    _fields_ = [("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 class FbobError(RuntimeError):
@@ -64,6 +98,21 @@ def load():
     lib.fbob_attn_bob_four_pass.restype = st
     lib.fbob_attn_bob_noalloc.argtypes = [cp] + [vp] * 15
     lib.fbob_attn_bob_noalloc.restype = st
+    ll, sz = ctypes.c_longlong, ctypes.c_size_t
+    lib.fbob_rotary_frequencies.argtypes = [ctypes.POINTER(Rotary), ctypes.POINTER(ctypes.c_double)]
+    lib.fbob_rotary_frequencies.restype = st
+    lib.fbob_rotary_apply.argtypes = [ctypes.POINTER(Rotary), st, st, st, st, ctypes.POINTER(RotaryHeads), st, vp, st,
+                                      ll, ll, st, vp]
+    lib.fbob_rotary_apply.restype = st
+    np = ctypes.POINTER(Norm)
+    lib.fbob_layer_norm_workspace_bytes.argtypes = [np]
+    lib.fbob_layer_norm_workspace_bytes.restype = sz
+    lib.fbob_layer_norm_fwd.argtypes = [np] + [vp] * 7
+    lib.fbob_layer_norm_fwd.restype = st
+    lib.fbob_layer_norm_bwd.argtypes = [np] + [vp] * 9 + [sz, vp]
+    lib.fbob_layer_norm_bwd.restype = st
+    lib.fbob_layer_norm_bob.argtypes = [np] + [vp] * 12 + [sz, vp]
+    lib.fbob_layer_norm_bob.restype = st
     lib.fbob_device_status.argtypes = [vp]
     lib.fbob_device_status.restype = st
     lib.fbob_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]

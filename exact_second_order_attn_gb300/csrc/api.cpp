@@ -10,14 +10,12 @@
 
 #include <atomic>
 
+#include "api_check.h"
 #include "internal.h"
 
-namespace {
+namespace fbob {
 
 thread_local char g_last_error[512] = "";
-std::atomic<unsigned long long> g_wait_ns{2000000000ull};
-std::atomic<int> g_stall{0};
-constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 
 fbob_status fail(fbob_status s, const char* fmt, ...) {
   va_list ap;
@@ -31,7 +29,17 @@ fbob_status cuda_fail(cudaError_t e, const char* where) {
   return fail(FBOB_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace fbob
+
+namespace {
+
+using fbob::aligned16;
+using fbob::cuda_fail;
+using fbob::fail;
+
+std::atomic<unsigned long long> g_wait_ns{2000000000ull};
+std::atomic<int> g_stall{0};
+constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 
 // Shared checks of the problem descriptor.  Returns FBOB_OK and sets *empty
 // when there is nothing to compute.
@@ -67,15 +75,21 @@ fbob_status check_ptrs(const Ptr* ps, int n) {
   return FBOB_OK;
 }
 
-fbob_status make_ctx(fbob::DevCtx* c) {
-  cudaError_t e = fbob::dev_status_word(&c->err);
+}  // namespace
+
+namespace fbob {
+
+fbob_status make_ctx(DevCtx* c) {
+  cudaError_t e = dev_status_word(&c->err);
   if (e != cudaSuccess) return cuda_fail(e, "device status word");
   c->wait_ns = g_wait_ns.load();
   c->stall = g_stall.load();
   return FBOB_OK;
 }
 
-}  // namespace
+}  // namespace fbob
+
+using fbob::make_ctx;
 
 extern "C" {
 
@@ -93,7 +107,7 @@ const char* fbob_status_string(fbob_status s) {
   return "FBOB_UNKNOWN_STATUS";
 }
 
-const char* fbob_last_error(void) { return g_last_error; }
+const char* fbob_last_error(void) { return fbob::g_last_error; }
 
 unsigned long long fbob_set_wait_limit_ns(unsigned long long ns) {
   return g_wait_ns.exchange(ns == 0 ? kDefaultWaitNs : ns);

@@ -1,0 +1,277 @@
+// C ABI of libfbob.so: the operators around the attention (rotary positions,
+// layer norm).  Argument validation and dispatch, as in api.cpp.
+#include <cuda_runtime_api.h>
+#include <math.h>
+#include <string.h>
+
+#include "api_check.h"
+#include "fbob.h"
+#include "internal.h"
+
+namespace {
+
+using fbob::aligned16;
+using fbob::cuda_fail;
+using fbob::fail;
+
+fbob_status check_dtype(int dtype) {
+  if (dtype != FBOB_BF16 && dtype != FBOB_FP32) return fail(FBOB_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  return FBOB_OK;
+}
+
+bool element_aligned(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == FBOB_BF16 ? 1u : 3u)) == 0;
+}
+
+fbob_status check_rotary(const fbob_rotary* r) {
+  if (!r) return fail(FBOB_ERR_INVALID_ARG, "rotary descriptor is null");
+  if (r->rot < 2 || r->rot % 2 != 0)
+    return fail(FBOB_ERR_INVALID_ARG, "rot=%d must be an even number of columns, at least 2", r->rot);
+  if (r->rot / 2 > fbob::kRotaryMaxPairs)
+    return fail(FBOB_ERR_UNSUPPORTED, "rot=%d exceeds %d columns", r->rot, 2 * fbob::kRotaryMaxPairs);
+  if (!isfinite(r->base) || r->base <= 1.0) return fail(FBOB_ERR_INVALID_ARG, "base must be above 1 (got %g)", r->base);
+  if (!isfinite(r->magnitude) || r->magnitude == 0.0)
+    return fail(FBOB_ERR_INVALID_ARG, "magnitude must be finite and nonzero (got %g)", r->magnitude);
+  if (r->scaling < FBOB_ROTARY_NONE || r->scaling > FBOB_ROTARY_PARTS)
+    return fail(FBOB_ERR_INVALID_ARG, "unknown scaling %d", r->scaling);
+  if (r->scaling == FBOB_ROTARY_NONE) return FBOB_OK;
+  if (!isfinite(r->factor) || r->factor < 1.0)
+    return fail(FBOB_ERR_INVALID_ARG, "factor must be at least 1 (got %g)", r->factor);
+  if (r->scaling == FBOB_ROTARY_BASE && r->rot == 2)
+    return fail(FBOB_ERR_INVALID_ARG, "scaling the base needs rot above 2");
+  if (r->scaling == FBOB_ROTARY_PARTS) {
+    if (!isfinite(r->original) || r->original <= 0.0)
+      return fail(FBOB_ERR_INVALID_ARG, "original length must be positive (got %g)", r->original);
+    if (!isfinite(r->slow) || !isfinite(r->fast) || r->slow < 0.0 || r->fast <= r->slow)
+      return fail(FBOB_ERR_INVALID_ARG, "0 <= slow < fast is needed (got %g, %g)", r->slow, r->fast);
+  }
+  return FBOB_OK;
+}
+
+// theta_i of a checked descriptor.
+double theta(const fbob_rotary* r, int i) {
+  double base = r->base;
+  if (r->scaling == FBOB_ROTARY_BASE) base *= pow(r->factor, (double)r->rot / (r->rot - 2));
+  double t = pow(base, -2.0 * i / r->rot);
+  if (r->scaling == FBOB_ROTARY_LINEAR) t /= r->factor;
+  if (r->scaling == FBOB_ROTARY_PARTS) {
+    const double n = r->original * t / (2.0 * M_PI);
+    const double w = fmin(fmax((n - r->slow) / (r->fast - r->slow), 0.0), 1.0);
+    t *= w + (1.0 - w) / r->factor;
+  }
+  return t;
+}
+
+// Whether no two elements of [B, H, N, d] with these strides (last one 1)
+// share an address: each stride, from the smallest, steps over all that the
+// smaller ones reach.
+bool distinct(const long long* st, int B, int H, int N, int d) {
+  const long long size[3] = {B, H, N};
+  bool used[3] = {false, false, false};
+  long long reach = d;  // elements spanned so far
+  for (int k = 0; k < 3; ++k) {
+    int best = -1;
+    for (int i = 0; i < 3; ++i) {
+      if (!used[i] && (best < 0 || (size[i] > 1 ? st[i] : -1) < (size[best] > 1 ? st[best] : -1))) best = i;
+    }
+    used[best] = true;
+    if (size[best] <= 1) continue;
+    if (st[best] < reach) return false;
+    reach += (size[best] - 1) * st[best];
+  }
+  return true;
+}
+
+fbob_status check_norm(const fbob_norm* p) {
+  if (!p) return fail(FBOB_ERR_INVALID_ARG, "norm descriptor is null");
+  fbob_status st = check_dtype(p->dtype);
+  if (st != FBOB_OK || (st = check_dtype(p->weight_dtype)) != FBOB_OK) return st;
+  if (p->rows < 0 || p->D <= 0) return fail(FBOB_ERR_INVALID_ARG, "bad sizes rows=%lld D=%d", p->rows, p->D);
+  if (p->D > 16384) return fail(FBOB_ERR_UNSUPPORTED, "D=%d exceeds 16384 columns", p->D);
+  if (p->rows > (1ll << 40) / p->D) return fail(FBOB_ERR_UNSUPPORTED, "%lld rows of %d are too large", p->rows, p->D);
+  if (!isfinite(p->eps) || p->eps < 0.f) return fail(FBOB_ERR_INVALID_ARG, "eps must be >= 0 (got %g)", (double)p->eps);
+  if (p->dtype == FBOB_FP32 && p->weight_dtype == FBOB_BF16)
+    return fail(FBOB_ERR_UNSUPPORTED, "fp32 rows with bf16 weights");
+  return FBOB_OK;
+}
+
+struct Arg {
+  const void* p;
+  const char* name;
+  int dtype;
+  bool required;
+};
+
+fbob_status check_args(const Arg* a, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (!a[i].p && a[i].required) return fail(FBOB_ERR_INVALID_ARG, "pointer %s is null", a[i].name);
+    if (!element_aligned(a[i].p, a[i].dtype))
+      return fail(FBOB_ERR_INVALID_ARG, "pointer %s is not aligned to its elements", a[i].name);
+  }
+  return FBOB_OK;
+}
+
+fbob_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return FBOB_OK;
+  if (!ws) return fail(FBOB_ERR_WORKSPACE, "workspace pointer is null");
+  if (!aligned16(ws)) return fail(FBOB_ERR_WORKSPACE, "workspace is not 16-byte aligned");
+  if (have < need) return fail(FBOB_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", have, need);
+  return FBOB_OK;
+}
+
+fbob::NormArgs norm_args(const fbob_norm* p) {
+  fbob::NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.rows = p->rows, a.D = p->D, a.eps = p->eps;
+  a.bf16 = p->dtype == FBOB_BF16, a.wbf16 = p->weight_dtype == FBOB_BF16;
+  return a;
+}
+
+// Column sums over no rows are zero.
+fbob_status zero_columns(const fbob_norm* p, void* const* outs, int n, cudaStream_t stream) {
+  const size_t bytes = (size_t)p->D * (p->weight_dtype == FBOB_BF16 ? 2 : 4);
+  for (int i = 0; i < n; ++i) {
+    if (!outs[i]) continue;
+    const cudaError_t e = cudaMemsetAsync(outs[i], 0, bytes, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "layer_norm memset");
+  }
+  return FBOB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fbob_status fbob_rotary_frequencies(const fbob_rotary* r, double* out) {
+  const fbob_status st = check_rotary(r);
+  if (st != FBOB_OK) return st;
+  if (!out) return fail(FBOB_ERR_INVALID_ARG, "pointer theta is null");
+  for (int i = 0; i < r->rot / 2; ++i) out[i] = theta(r, i);
+  return FBOB_OK;
+}
+
+fbob_status fbob_rotary_apply(const fbob_rotary* r, int B, int N, int d, int dtype, const fbob_rotary_heads* t,
+                              int count, const void* positions, int position_bytes, long long position_stride,
+                              long long offset, int transpose, cudaStream_t stream) {
+  fbob_status st = check_rotary(r);
+  if (st != FBOB_OK || (st = check_dtype(dtype)) != FBOB_OK) return st;
+  if (B < 0 || N < 0 || d <= 0) return fail(FBOB_ERR_INVALID_ARG, "bad sizes B=%d N=%d d=%d", B, N, d);
+  if (d > 2 * fbob::kRotaryMaxPairs) return fail(FBOB_ERR_UNSUPPORTED, "head size d=%d exceeds %d", d, 2 * fbob::kRotaryMaxPairs);
+  if (r->rot > d) return fail(FBOB_ERR_INVALID_ARG, "rot=%d exceeds the head size d=%d", r->rot, d);
+  if ((long long)B * N > 0x7fffffffll) return fail(FBOB_ERR_UNSUPPORTED, "B*N=%lld exceeds 2^31 - 1", (long long)B * N);
+  if (!t || count < 1 || count > 2) return fail(FBOB_ERR_INVALID_ARG, "one or two tensors are needed (got %d)", count);
+  if (positions && position_bytes != 4 && position_bytes != 8)
+    return fail(FBOB_ERR_INVALID_ARG, "positions of %d bytes (4 or 8)", position_bytes);
+  if (positions && (reinterpret_cast<uintptr_t>(positions) % position_bytes) != 0)
+    return fail(FBOB_ERR_INVALID_ARG, "pointer positions is not aligned to its elements");
+  if (positions && position_stride < 0) return fail(FBOB_ERR_INVALID_ARG, "position_stride is negative");
+  long long heads = 0;
+  for (int k = 0; k < count; ++k) {
+    if (t[k].H < 0) return fail(FBOB_ERR_INVALID_ARG, "bad size H=%d", t[k].H);
+    heads += t[k].H;
+    for (int i = 0; i < 3; ++i) {
+      if (t[k].x_stride[i] < 0 || t[k].y_stride[i] < 0) return fail(FBOB_ERR_INVALID_ARG, "a stride is negative");
+    }
+  }
+  if (heads > 65535) return fail(FBOB_ERR_UNSUPPORTED, "%lld heads exceed 65535", heads);
+  if (heads == 0 || B == 0 || N == 0) return FBOB_OK;
+  fbob::RotaryArgs a;
+  memset(&a, 0, sizeof(a));
+  for (int k = 0, m = 0; k < count; ++k) {
+    if (t[k].H == 0) continue;
+    const Arg ps[] = {{t[k].x, "x", dtype, true}, {t[k].y, "y", dtype, true}};
+    if ((st = check_args(ps, 2)) != FBOB_OK) return st;
+    if (!distinct(t[k].y_stride, B, t[k].H, N, d))
+      return fail(FBOB_ERR_INVALID_ARG, "elements of output %d share addresses", k);
+    fbob::RotarySide& o = a.side[m++];
+    o.x = t[k].x, o.y = t[k].y, o.H = t[k].H;
+    const int size[3] = {B, t[k].H, N};
+    for (int i = 0; i < 3; ++i) {  // the stride of a dimension of one is never stepped
+      o.xs[i] = size[i] > 1 ? t[k].x_stride[i] : 0;
+      o.ys[i] = size[i] > 1 ? t[k].y_stride[i] : 0;
+    }
+  }
+  for (int i = 0; i < r->rot / 2; ++i) {
+    const double turns = theta(r, i) / (2.0 * M_PI);  // below 2^-2, since theta <= 1
+    a.freq[i] = (unsigned long long)ldexp(turns, 64);
+  }
+  a.positions = positions, a.pos_bytes = position_bytes, a.pos_stride = position_stride, a.offset = offset;
+  a.B = B, a.N = N, a.d = d, a.rot = r->rot;
+  a.interleaved = r->interleaved != 0, a.transpose = transpose != 0, a.bf16 = dtype == FBOB_BF16;
+  a.magnitude = (float)r->magnitude;
+  const cudaError_t e = fbob::rotary(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
+  return FBOB_OK;
+}
+
+size_t fbob_layer_norm_workspace_bytes(const fbob_norm* p) {
+  if (!p || p->rows <= 0 || p->D <= 0) return 0;
+  return sizeof(float) * fbob::layer_norm_workspace_floats(p->rows, p->D);
+}
+
+fbob_status fbob_layer_norm_fwd(const fbob_norm* p, const void* x, const void* w, const void* b, void* y, float* mean,
+                                float* rstd, cudaStream_t stream) {
+  fbob_status st = check_norm(p);
+  if (st != FBOB_OK) return st;
+  if (p->rows == 0) return FBOB_OK;
+  const Arg ps[] = {{x, "x", p->dtype, true},         {w, "w", p->weight_dtype, false},
+                    {b, "b", p->weight_dtype, false}, {y, "y", p->dtype, true},
+                    {mean, "mean", FBOB_FP32, true},  {rstd, "rstd", FBOB_FP32, true}};
+  if ((st = check_args(ps, 6)) != FBOB_OK) return st;
+  fbob::NormArgs a = norm_args(p);
+  a.x = x, a.w = w, a.b = b, a.y = y, a.mean = mean, a.rstd = rstd;
+  const cudaError_t e = fbob::layer_norm_fwd(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "layer_norm_fwd launch");
+  return FBOB_OK;
+}
+
+fbob_status fbob_layer_norm_bwd(const fbob_norm* p, const void* x, const void* w, const float* mean, const float* rstd,
+                                const void* dy, void* dx, void* dw, void* db, float* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+  fbob_status st = check_norm(p);
+  if (st != FBOB_OK) return st;
+  const Arg ps[] = {{x, "x", p->dtype, p->rows > 0},         {w, "w", p->weight_dtype, false},
+                    {mean, "mean", FBOB_FP32, p->rows > 0},  {rstd, "rstd", FBOB_FP32, p->rows > 0},
+                    {dy, "dy", p->dtype, p->rows > 0},       {dx, "dx", p->dtype, false},
+                    {dw, "dw", p->weight_dtype, false},      {db, "db", p->weight_dtype, false}};
+  if ((st = check_args(ps, 8)) != FBOB_OK) return st;
+  if (p->rows == 0) {
+    void* const outs[] = {dw, db};
+    return zero_columns(p, outs, 2, stream);
+  }
+  if (!dx && !dw && !db) return FBOB_OK;
+  const size_t need = (dw || db) ? fbob_layer_norm_workspace_bytes(p) / ((dw && db) ? 1 : 2) : 0;
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != FBOB_OK) return st;
+  fbob::NormArgs a = norm_args(p);
+  a.x = x, a.w = w, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd), a.dy = dy;
+  a.dx = dx, a.dw = dw, a.db = db, a.ws = workspace;
+  const cudaError_t e = fbob::layer_norm_bwd(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "layer_norm_bwd launch");
+  return FBOB_OK;
+}
+
+fbob_status fbob_layer_norm_bob(const fbob_norm* p, const void* x, const void* w, const float* mean, const float* rstd,
+                                const void* dy, const void* ux, const void* uw, const void* ub, void* gx, void* gw,
+                                void* gdy, float* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  fbob_status st = check_norm(p);
+  if (st != FBOB_OK) return st;
+  const Arg ps[] = {{x, "x", p->dtype, p->rows > 0},        {w, "w", p->weight_dtype, false},
+                    {mean, "mean", FBOB_FP32, p->rows > 0}, {rstd, "rstd", FBOB_FP32, p->rows > 0},
+                    {dy, "dy", p->dtype, p->rows > 0},      {ux, "ux", p->dtype, p->rows > 0},
+                    {uw, "uw", p->weight_dtype, false},     {ub, "ub", p->weight_dtype, false},
+                    {gx, "gx", p->dtype, false},            {gw, "gw", p->weight_dtype, false},
+                    {gdy, "gdy", p->dtype, false}};
+  if ((st = check_args(ps, 11)) != FBOB_OK) return st;
+  if (p->rows == 0) return zero_columns(p, &gw, 1, stream);
+  if (!gx && !gw && !gdy) return FBOB_OK;
+  const size_t need = gw ? fbob_layer_norm_workspace_bytes(p) / 2 : 0;
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != FBOB_OK) return st;
+  fbob::NormArgs a = norm_args(p);
+  a.x = x, a.w = w, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd), a.dy = dy;
+  a.ux = ux, a.uw = uw, a.ub = ub, a.gx = gx, a.gw = gw, a.gdy = gdy, a.ws = workspace;
+  const cudaError_t e = fbob::layer_norm_bob(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "layer_norm_bob launch");
+  return FBOB_OK;
+}
+
+}  // extern "C"

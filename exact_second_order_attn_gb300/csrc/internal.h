@@ -43,6 +43,38 @@ struct BobArgs {
   int causal;
 };
 
+// Rotary positions on up to two tensors of heads (H = 0: absent); strides in
+// elements of batch, head and position.
+struct RotarySide {
+  const void* x;
+  void* y;
+  int H;
+  long long xs[3], ys[3];
+};
+
+constexpr int kRotaryMaxPairs = 128;
+
+struct RotaryArgs {
+  unsigned long long freq[kRotaryMaxPairs];  // turns per position, 64-bit fraction
+  RotarySide side[2];
+  const void* positions;  // null: position = offset + n
+  int pos_bytes;
+  long long pos_stride, offset;
+  int B, N, d, rot, interleaved, transpose, bf16;
+  float magnitude;
+};
+
+// Layer norm of `rows` rows of D elements; w, b and their gradients may be null.
+struct NormArgs {
+  const void *x, *w, *b, *dy, *ux, *uw, *ub;
+  void *y, *dx, *dw, *db, *gx, *gw, *gdy;
+  float *mean, *rstd;  // outputs of the forward, inputs of the others
+  float* ws;
+  long long rows;
+  int D, bf16, wbf16;
+  float eps;
+};
+
 // Status word bits.
 constexpr unsigned int kErrTimeout = 1u;
 
@@ -61,6 +93,13 @@ cudaError_t tc_bob(const BobArgs& a, const DevCtx& c, cudaStream_t s);
 cudaError_t tc_bob_four_pass(const BobArgs& a, const DevCtx& c, cudaStream_t s);  // ablation schedule
 // tc_bob_cols.cu: BoB pass 2 (gK, gV) for heads of 65 to 128 columns.
 cudaError_t tc_bob_cols_wide(const BobArgs& a, const DevCtx& c, cudaStream_t s);
+
+// rotary.cu, layer_norm_*.cu
+cudaError_t rotary(const RotaryArgs& a, cudaStream_t s);
+cudaError_t layer_norm_fwd(const NormArgs& a, cudaStream_t s);
+cudaError_t layer_norm_bwd(const NormArgs& a, cudaStream_t s);
+cudaError_t layer_norm_bob(const NormArgs& a, cudaStream_t s);
+size_t layer_norm_workspace_floats(long long rows, int D);  // of bwd (bob needs half)
 
 // bob_static.cu: the fixed (alpha, E) workspace of fbob_attn_bob_noalloc.
 size_t static_workspace_rows();           // capacity in query rows (B*H*N)

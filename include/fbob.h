@@ -207,6 +207,118 @@ fbob_status fbob_attn_bob_noalloc(const fbob_problem* p,
                                   float* gQ, float* gK, float* gV, float* gdO,
                                   cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The operators of a model around the attention.  Each has its forward, its
+ * first backward and the vector-Jacobian product of that backward, so that a
+ * Hessian-vector product passes through a whole model.  The pages have no
+ * counterpart: the formulas stand at each call.
+ *
+ * Differences from the conventions above: tensors and gradients have the
+ * descriptor's element types (row statistics, losses and workspaces are
+ * fp32); a pointer needs the alignment of its elements only, unless a call
+ * says otherwise (workspaces: 16 bytes), and rows that all start on 16 bytes
+ * are read faster; an output that is marked optional is not computed when its
+ * pointer is null.
+ * ------------------------------------------------------------------------ */
+
+/* Scaling of the rotary frequencies theta_i = base^(-2 i / rot). */
+typedef enum {
+  FBOB_ROTARY_NONE = 0,
+  FBOB_ROTARY_LINEAR = 1,  /* theta / factor                                  */
+  FBOB_ROTARY_BASE = 2,    /* base * factor^(rot / (rot - 2)) as the base     */
+  FBOB_ROTARY_PARTS = 3    /* theta (w + (1 - w) / factor) with the turns     */
+                           /* n = original theta / 2 pi and                   */
+                           /* w = (n - slow) / (fast - slow) clamped to [0,1] */
+} fbob_rotary_scaling;
+
+typedef struct {
+  int rot;          /* leading columns of a head that are rotated: even, 2..d */
+  int interleaved;  /* 0: pairs (i, i + rot/2); else pairs (2i, 2i + 1)       */
+  int scaling;      /* fbob_rotary_scaling                                    */
+  double base;      /* > 1                                                    */
+  double factor;    /* >= 1 (all scalings but NONE)                           */
+  double original, slow, fast;  /* PARTS only: > 0 and 0 <= slow < fast       */
+  double magnitude; /* multiplies the rotated columns; finite, nonzero        */
+} fbob_rotary;
+
+/* Heads of one tensor: x and y are [B, H, N, d] with element strides of
+ * batch, head and position (not negative) and contiguous rows of d. */
+typedef struct {
+  const void* x;
+  void* y;
+  int H;
+  long long x_stride[3], y_stride[3];
+} fbob_rotary_heads;
+
+/* theta_i, i < rot/2, into host memory. */
+fbob_status fbob_rotary_frequencies(const fbob_rotary* r, double* theta);
+
+/*
+ * Rotary positions on one or two tensors (Q, K) in one launch:
+ *   (y_a, y_b) = magnitude * (x_a cos - x_b sin, x_a sin + x_b cos) for each
+ *   pair (a, b) = pair i and angle position * theta_i; columns from rot on
+ *   are copied.  transpose != 0 turns the other way: the map's transpose, so
+ *   the gradient of x from that of y (its own second order is the map again).
+ *   positions: null (position of token n is offset + n) or integers of
+ *   position_bytes (4 or 8), read at [b * position_stride + n] and added to
+ *   offset (position_stride 0: shared by the batches); any sign.
+ *   d <= 256; angles are reduced exactly, whatever the position.
+ *   An output whose elements share addresses is refused.
+ */
+fbob_status fbob_rotary_apply(const fbob_rotary* r, int B, int N, int d, int dtype,
+                              const fbob_rotary_heads* tensors, int count,
+                              const void* positions, int position_bytes,
+                              long long position_stride, long long offset,
+                              int transpose, cudaStream_t stream);
+
+/* Rows of D elements (1 <= D <= 16384), contiguous. */
+typedef struct {
+  long long rows;
+  int D;
+  int dtype;         /* x, y, dy, dx, ux, gx, gdy                             */
+  int weight_dtype;  /* w, b, dw, db, uw, ub, gw: fp32, or bf16 with bf16 rows */
+  float eps;         /* >= 0; the forward's only                              */
+} fbob_norm;
+
+/* Bytes of fp32 workspace of fbob_layer_norm_bwd with dw and db; half of it
+ * serves one of them, or fbob_layer_norm_bob. */
+size_t fbob_layer_norm_workspace_bytes(const fbob_norm* p);
+
+/*
+ * Layer norm: y = w xh + b, xh = (x - mean) rstd,
+ * rstd = (mean((x - mean)^2) + eps)^(-1/2) over each row of D.
+ * w and b are optional (null: ones, zeros).
+ *   out: y [rows, D]; mean, rstd [rows] fp32
+ */
+fbob_status fbob_layer_norm_fwd(const fbob_norm* p, const void* x, const void* w, const void* b,
+                                void* y, float* mean, float* rstd, cudaStream_t stream);
+
+/*
+ * Its backward: with a = w dy and m() the mean over a row,
+ *   dx = rstd (a - m(a) - xh m(a xh)), dw = sum over rows of dy xh,
+ *   db = sum over rows of dy; each optional.  dw and db are zero for no rows.
+ * The sums over rows are taken in an order fixed by the sizes.
+ */
+fbob_status fbob_layer_norm_bwd(const fbob_norm* p, const void* x, const void* w,
+                                const float* mean, const float* rstd, const void* dy,
+                                void* dx, void* dw, void* db,
+                                float* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The vector-Jacobian product of (x, w, dy) -> (dx, dw, db) along
+ * (ux, uw, ub): gradients of <ux, dx> + <uw, dw> + <ub, db>.  uw and ub are
+ * optional (null: zeros).  With pu = ux - m(ux) - xh m(ux xh):
+ *   gdy = rstd w pu + uw xh + ub;  gw = sum over rows of rstd pu dy;
+ *   gx  = rstd (h - m(h) - xh m(h xh)) - rstd^2 xh m(pu a),
+ *   h   = uw dy - rstd (a m(ux xh) + ux m(a xh));
+ * each optional.
+ */
+fbob_status fbob_layer_norm_bob(const fbob_norm* p, const void* x, const void* w,
+                                const float* mean, const float* rstd, const void* dy,
+                                const void* ux, const void* uw, const void* ub,
+                                void* gx, void* gw, void* gdy,
+                                float* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /*
  * Device status: waits for `stream` to finish (this call DOES synchronise),
  * then returns FBOB_ERR_TIMEOUT if any kernel of this library on the current
