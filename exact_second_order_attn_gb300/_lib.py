@@ -27,6 +27,7 @@ FUNCTIONS = (
     "fbob_debug_stall_producer", "fbob_attn_bob_four_pass",
     "fbob_rotary_frequencies", "fbob_rotary_apply",
     "fbob_layer_norm_workspace_bytes", "fbob_layer_norm_fwd", "fbob_layer_norm_bwd", "fbob_layer_norm_bob",
+    "fbob_linear_ce_workspace_bytes", "fbob_linear_ce_fwd", "fbob_linear_ce_bwd", "fbob_linear_ce_bob",
 )
 
 
@@ -66,6 +67,12 @@ class Norm(ctypes.Structure):
     """fbob_norm: rows of D elements."""
     _fields_ = [("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class LinearCe(ctypes.Structure):
+    """fbob_linear_ce: T tokens of D columns, V classes."""
+    _fields_ = [("T", ctypes.c_int), ("D", ctypes.c_int), ("V", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("ignore_index", ctypes.c_longlong), ("piece", ctypes.c_int)]
 
 
 class FbobError(RuntimeError):
@@ -113,6 +120,15 @@ def load():
     lib.fbob_layer_norm_bwd.restype = st
     lib.fbob_layer_norm_bob.argtypes = [np] + [vp] * 12 + [sz, vp]
     lib.fbob_layer_norm_bob.restype = st
+    ce = ctypes.POINTER(LinearCe)
+    lib.fbob_linear_ce_workspace_bytes.argtypes = [ce, st]
+    lib.fbob_linear_ce_workspace_bytes.restype = sz
+    lib.fbob_linear_ce_fwd.argtypes = [ce] + [vp] * 6 + [sz, vp]
+    lib.fbob_linear_ce_fwd.restype = st
+    lib.fbob_linear_ce_bwd.argtypes = [ce] + [vp] * 8 + [sz, vp]
+    lib.fbob_linear_ce_bwd.restype = st
+    lib.fbob_linear_ce_bob.argtypes = [ce] + [vp] * 11 + [sz, vp]
+    lib.fbob_linear_ce_bob.restype = st
     lib.fbob_device_status.argtypes = [vp]
     lib.fbob_device_status.restype = st
     lib.fbob_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]

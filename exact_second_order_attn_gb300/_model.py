@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import Norm, Rotary, RotaryHeads, _check, _ptr, load
+from ._lib import LinearCe, Norm, Rotary, RotaryHeads, _check, _ptr, load
 
 DTYPES = {torch.bfloat16: _lib.BF16, torch.float32: _lib.FP32}
 
@@ -226,3 +226,84 @@ def fbob_layer_norm_bob(x, weight, mean, rstd, dy, ux, uw=None, ub=None, gx=None
          _ptr(ux), _ptr(uw), _ptr(ub), _ptr(gx), _ptr(gw), _ptr(gdy), _ptr(workspace),
          ctypes.c_size_t(workspace.numel() * 4))
     return gx, gw, gdy
+
+
+# --- cross entropy of a linear head -----------------------------------------------------------------
+
+def linear_ce_for(H: torch.Tensor, W: torch.Tensor, ignore_index: int = -100, piece: int = 0) -> LinearCe:
+    if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1]:
+        raise ValueError(f"H [T, D] and W [V, D] are needed, got {tuple(H.shape)} and {tuple(W.shape)}")
+    if max(H.shape[0], W.shape[0], W.shape[1]) > 2 ** 31 - 1:
+        raise ValueError("sizes must fit 32 bits")
+    return LinearCe(H.shape[0], H.shape[1], W.shape[0], _dtype(H), int(ignore_index), int(piece))
+
+
+def fbob_linear_ce_workspace_bytes(p: LinearCe, which: int) -> int:
+    """Bytes of workspace of the forward (0), backward (1) or its product (2)."""
+    return int(load().fbob_linear_ce_workspace_bytes(ctypes.byref(p), which))
+
+
+def _ce_common(H, W, target, lse=None, g=None):
+    _tensor(H, "H", H, H.dtype)
+    _tensor(W, "W", H, H.dtype)
+    _tensor(target, "target", H, torch.int64, H.shape[:1])
+    _tensor(lse, "lse", H, torch.float32, H.shape[:1])
+    _tensor(g, "g", H, torch.float32, H.shape[:1])
+
+
+def _ce_workspace(p, which, H, workspace, stream):
+    if workspace is None:
+        workspace = _new(H, (fbob_linear_ce_workspace_bytes(p, which),), torch.uint8, stream)
+    _tensor(workspace, "workspace", H, torch.uint8)
+    return workspace, ctypes.c_size_t(workspace.numel())
+
+
+def fbob_linear_ce_fwd(H, W, target, ignore_index=-100, loss=None, lse=None, workspace=None, stream=None):
+    """(loss, lse) [T] fp32 of the tokens H [T, D] under logits H W^T, W [V, D];
+    target [T] int64.  ``workspace``: uint8."""
+    p = linear_ce_for(H, W, ignore_index)
+    _ce_common(H, W, target)
+    loss = _new(H, H.shape[:1], torch.float32, stream) if loss is None else loss
+    lse = _new(H, H.shape[:1], torch.float32, stream) if lse is None else lse
+    _tensor(loss, "loss", H, torch.float32, H.shape[:1])
+    _tensor(lse, "lse", H, torch.float32, H.shape[:1])
+    workspace, size = _ce_workspace(p, 0, H, workspace, stream)
+    _run("fbob_linear_ce_fwd", H, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(target), _ptr(loss), _ptr(lse),
+         _ptr(workspace), size)
+    return loss, lse
+
+
+def fbob_linear_ce_bwd(H, W, target, lse, g, ignore_index=-100, piece=0, dH=None, dW=None, want=(True, True),
+                       workspace=None, stream=None):
+    """(dH, dW) of sum_t g_t loss_t; ``want`` says which to compute.  ``piece``:
+    classes whose gradient is held at once (0: chosen by the library)."""
+    p = linear_ce_for(H, W, ignore_index, piece)
+    _ce_common(H, W, target, lse, g)
+    dH = (_new(H, H.shape, H.dtype, stream) if dH is None else dH) if want[0] else None
+    dW = (_new(H, W.shape, H.dtype, stream) if dW is None else dW) if want[1] else None
+    _tensor(dH, "dH", H, H.dtype, H.shape)
+    _tensor(dW, "dW", H, H.dtype, W.shape)
+    workspace, size = _ce_workspace(p, 1, H, workspace, stream)
+    _run("fbob_linear_ce_bwd", H, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(target), _ptr(lse), _ptr(g), _ptr(dH),
+         _ptr(dW), _ptr(workspace), size)
+    return dH, dW
+
+
+def fbob_linear_ce_bob(H, W, target, lse, g, UH, UW, ignore_index=-100, piece=0, gH=None, gW=None, gg=None,
+                       want=(True, True, True), workspace=None, stream=None):
+    """(gH, gW, gg) = the vector-Jacobian product of (H, W, g) -> (dH, dW)
+    along (UH, UW), one of which may be None; ``want`` says which to compute."""
+    p = linear_ce_for(H, W, ignore_index, piece)
+    _ce_common(H, W, target, lse, g)
+    _tensor(UH, "UH", H, H.dtype, H.shape)
+    _tensor(UW, "UW", H, H.dtype, W.shape)
+    gH = (_new(H, H.shape, H.dtype, stream) if gH is None else gH) if want[0] else None
+    gW = (_new(H, W.shape, H.dtype, stream) if gW is None else gW) if want[1] else None
+    gg = (_new(H, H.shape[:1], torch.float32, stream) if gg is None else gg) if want[2] else None
+    _tensor(gH, "gH", H, H.dtype, H.shape)
+    _tensor(gW, "gW", H, H.dtype, W.shape)
+    _tensor(gg, "gg", H, torch.float32, H.shape[:1])
+    workspace, size = _ce_workspace(p, 2, H, workspace, stream)
+    _run("fbob_linear_ce_bob", H, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(target), _ptr(lse), _ptr(g), _ptr(UH),
+         _ptr(UW), _ptr(gH), _ptr(gW), _ptr(gg), _ptr(workspace), size)
+    return gH, gW, gg

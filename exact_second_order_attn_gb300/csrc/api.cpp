@@ -248,6 +248,8 @@ fbob_status fbob_device_status(cudaStream_t stream) {
     if ((e = cudaMemcpy(word, &zero, sizeof(zero), cudaMemcpyHostToDevice)) != cudaSuccess)
       return cuda_fail(e, "clear device status word");
     if (v & fbob::kErrTimeout) return fail(FBOB_ERR_TIMEOUT, "a device-side wait exceeded its time limit");
+    if (v & fbob::kErrTarget)
+      return fail(FBOB_ERR_INVALID_ARG, "a target of fbob_linear_ce_* was outside the vocabulary");
   }
   return FBOB_OK;
 }

@@ -1,5 +1,5 @@
 // C ABI of libfbob.so: the operators around the attention (rotary positions,
-// layer norm).  Argument validation and dispatch, as in api.cpp.
+// layer norm, the linear head's cross entropy).  Argument validation and dispatch, as in api.cpp.
 #include <cuda_runtime_api.h>
 #include <math.h>
 #include <string.h>
@@ -138,6 +138,59 @@ fbob_status zero_columns(const fbob_norm* p, void* const* outs, int n, cudaStrea
   return FBOB_OK;
 }
 
+fbob_status check_ce(const fbob_linear_ce* p) {
+  if (!p) return fail(FBOB_ERR_INVALID_ARG, "linear_ce descriptor is null");
+  const fbob_status st = check_dtype(p->dtype);
+  if (st != FBOB_OK) return st;
+  if (p->T < 0 || p->D <= 0 || p->V <= 0)
+    return fail(FBOB_ERR_INVALID_ARG, "bad sizes T=%d D=%d V=%d", p->T, p->D, p->V);
+  if (p->piece < 0) return fail(FBOB_ERR_INVALID_ARG, "piece is negative (%d)", p->piece);
+  if (p->T > (1 << 24) || p->D > (1 << 20) || p->V > (1 << 24))
+    return fail(FBOB_ERR_UNSUPPORTED, "T=%d D=%d V=%d exceed 2^24, 2^20, 2^24", p->T, p->D, p->V);
+  if ((long long)p->D * (p->T > p->V ? p->T : p->V) > (1ll << 40))
+    return fail(FBOB_ERR_UNSUPPORTED, "T=%d D=%d V=%d are too large", p->T, p->D, p->V);
+  return FBOB_OK;
+}
+
+fbob::CeArgs ce_args(const fbob_linear_ce* p) {
+  fbob::CeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.T = p->T, a.D = p->D, a.V = p->V, a.bf16 = p->dtype == FBOB_BF16, a.piece = p->piece, a.ignore = p->ignore_index;
+  return a;
+}
+
+fbob_status ce_run(const fbob::CeArgs& a, fbob::CePass pass, size_t have, const char* where, cudaStream_t stream) {
+  fbob_status st = check_workspace(a.ws, have, fbob::linear_ce_workspace(a, pass));
+  if (st != FBOB_OK) return st;
+  fbob::DevCtx c;
+  if ((st = fbob::make_ctx(&c)) != FBOB_OK) return st;
+  const cudaError_t e = fbob::linear_ce(a, pass, c, stream);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  return FBOB_OK;
+}
+
+// The head is read in place by 16-byte copies when it is bf16 and its rows
+// are 16-byte multiples.
+fbob_status check_head(const fbob_linear_ce* p, const void* W, const char* name) {
+  if (p->dtype == FBOB_BF16 && p->D % 8 == 0 && !aligned16(W))
+    return fail(FBOB_ERR_INVALID_ARG, "pointer %s is not 16-byte aligned", name);
+  return FBOB_OK;
+}
+
+fbob_status check_targets(const void* target) {
+  if ((reinterpret_cast<uintptr_t>(target) & 7u) != 0)
+    return fail(FBOB_ERR_INVALID_ARG, "pointer target is not aligned to its elements");
+  return FBOB_OK;
+}
+
+// With no tokens the head's gradient is zero.
+fbob_status zero_head(const fbob_linear_ce* p, void* dW, cudaStream_t stream) {
+  if (!dW) return FBOB_OK;
+  const cudaError_t e =
+      cudaMemsetAsync(dW, 0, (size_t)p->V * p->D * (p->dtype == FBOB_BF16 ? 2 : 4), stream);
+  return e == cudaSuccess ? FBOB_OK : cuda_fail(e, "linear_ce memset");
+}
+
 }  // namespace
 
 extern "C" {
@@ -272,6 +325,67 @@ fbob_status fbob_layer_norm_bob(const fbob_norm* p, const void* x, const void* w
   const cudaError_t e = fbob::layer_norm_bob(a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "layer_norm_bob launch");
   return FBOB_OK;
+}
+
+size_t fbob_linear_ce_workspace_bytes(const fbob_linear_ce* p, int pass) {
+  if (check_ce(p) != FBOB_OK || p->T == 0 || pass < 0 || pass > 2) return 0;
+  return fbob::linear_ce_workspace(ce_args(p), static_cast<fbob::CePass>(pass));
+}
+
+fbob_status fbob_linear_ce_fwd(const fbob_linear_ce* p, const void* H, const void* W, const long long* target,
+                               float* loss, float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  fbob_status st = check_ce(p);
+  if (st != FBOB_OK) return st;
+  if (p->T == 0) return FBOB_OK;
+  const Arg ps[] = {{H, "H", p->dtype, true},       {W, "W", p->dtype, true},     {target, "target", FBOB_FP32, true},
+                    {loss, "loss", FBOB_FP32, true}, {lse, "lse", FBOB_FP32, true}};
+  if ((st = check_args(ps, 5)) != FBOB_OK || (st = check_head(p, W, "W")) != FBOB_OK ||
+      (st = check_targets(target)) != FBOB_OK)
+    return st;
+  fbob::CeArgs a = ce_args(p);
+  a.H = H, a.W = W, a.target = target, a.loss = loss, a.lse_out = lse, a.ws = workspace;
+  return ce_run(a, fbob::CePass::kFwd, workspace_bytes, "linear_ce_fwd launch", stream);
+}
+
+fbob_status fbob_linear_ce_bwd(const fbob_linear_ce* p, const void* H, const void* W, const long long* target,
+                               const float* lse, const float* g, void* dH, void* dW, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+  fbob_status st = check_ce(p);
+  if (st != FBOB_OK) return st;
+  const bool some = p->T > 0;
+  const Arg ps[] = {{H, "H", p->dtype, some},      {W, "W", p->dtype, some},  {target, "target", FBOB_FP32, some},
+                    {lse, "lse", FBOB_FP32, some}, {g, "g", FBOB_FP32, some}, {dH, "dH", p->dtype, false},
+                    {dW, "dW", p->dtype, false}};
+  if ((st = check_args(ps, 7)) != FBOB_OK || (st = check_head(p, W, "W")) != FBOB_OK ||
+      (st = check_targets(target)) != FBOB_OK)
+    return st;
+  if (!some) return zero_head(p, dW, stream);
+  if (!dH && !dW) return FBOB_OK;
+  fbob::CeArgs a = ce_args(p);
+  a.H = H, a.W = W, a.target = target, a.lse = lse, a.g = g, a.dH = dH, a.dW = dW, a.ws = workspace;
+  return ce_run(a, fbob::CePass::kBwd, workspace_bytes, "linear_ce_bwd launch", stream);
+}
+
+fbob_status fbob_linear_ce_bob(const fbob_linear_ce* p, const void* H, const void* W, const long long* target,
+                               const float* lse, const float* g, const void* UH, const void* UW, void* gH, void* gW,
+                               float* gg, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  fbob_status st = check_ce(p);
+  if (st != FBOB_OK) return st;
+  const bool some = p->T > 0;
+  const Arg ps[] = {{H, "H", p->dtype, some},      {W, "W", p->dtype, some},  {target, "target", FBOB_FP32, some},
+                    {lse, "lse", FBOB_FP32, some}, {g, "g", FBOB_FP32, some}, {UH, "UH", p->dtype, false},
+                    {UW, "UW", p->dtype, false},   {gH, "gH", p->dtype, false}, {gW, "gW", p->dtype, false},
+                    {gg, "gg", FBOB_FP32, false}};
+  if ((st = check_args(ps, 10)) != FBOB_OK || (st = check_head(p, W, "W")) != FBOB_OK ||
+      (st = check_head(p, UW, "UW")) != FBOB_OK || (st = check_targets(target)) != FBOB_OK)
+    return st;
+  if (!UH && !UW) return fail(FBOB_ERR_INVALID_ARG, "pointers UH and UW are both null");
+  if (!some) return zero_head(p, gW, stream);
+  if (!gH && !gW && !gg) return FBOB_OK;
+  fbob::CeArgs a = ce_args(p);
+  a.H = H, a.W = W, a.target = target, a.lse = lse, a.g = g, a.UH = UH, a.UW = UW;
+  a.dH = gH, a.dW = gW, a.gg = gg, a.ws = workspace;
+  return ce_run(a, fbob::CePass::kBob, workspace_bytes, "linear_ce_bob launch", stream);
 }
 
 }  // extern "C"

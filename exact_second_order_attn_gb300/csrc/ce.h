@@ -1,0 +1,82 @@
+// Internal interface of the linear head's cross entropy: the tensor-core
+// product kernel (ce_gemm.cu) and the passes that call it (linear_ce.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime_api.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace fbob {
+namespace ce {
+
+constexpr int kTileM = 256;     // rows of a pair's tile (128 per block)
+constexpr int kTileN = 256;     // columns of a tile with one accumulator
+constexpr int kTileNDual = 128; // ... with two
+constexpr int kBK = 64;         // contraction per stage (128 bytes of bf16)
+constexpr int kPlanes = 3;      // bf16 terms that stand for one fp32 operand
+constexpr int kMaxMaps = 2 * kPlanes;
+constexpr int kMaxSegs = 18;
+
+// A product's operands: planes are bf16 matrices, a segment multiplies plane a
+// by plane b into accumulator acc.  The sum over the segments is the product.
+struct Seg {
+  uint8_t a, b, acc, pad;
+};
+
+// What becomes of an accumulator tile.
+enum Epilogue {
+  kStats,   // row maxima and sums of exponentials per 128 columns, target logits
+  kGrad,    // G = gs (p - onehot) as bf16 planes
+  kAlpha,   // (two accumulators z, b) row sums of p b, b at the target
+  kGrad2,   // (two accumulators) Z = gs p (b - alpha) and G, as bf16 planes
+  kSlab,    // fp32, optionally added to what is there
+  kOut      // scaled, in the output type
+};
+
+struct EpArgs {
+  // tokens (kStats .. kGrad2): rows of the tile
+  const int* target;      // [T]: column, or -1 where nothing is counted
+  const float* lse;       // [T]
+  const float* g;         // [T]
+  const float* gmax;      // [1]: gs = g / gmax
+  const float* alpha;     // [T]
+  float2* part;           // kStats: (max, sum) [parts][T], two parts per tile of columns
+  float* sums;            // kAlpha: row sums [parts][T], two parts per tile of columns
+  float* picked;          // [T]: z or b at the target
+  uint16_t* planes[2 * kPlanes];  // G planes [T][ld], then Z planes
+  int nplanes;            // per matrix
+  long long ld;
+  // kSlab, kOut
+  void* out;
+  long long out_ld, slab;  // elements between rows, between split slabs
+  int accumulate, out_bf16, out_vec;
+};
+
+struct GemmArgs {
+  CUtensorMap a[kMaxMaps], b[kMaxMaps];
+  Seg seg[kMaxSegs];
+  int nseg;
+  int K;                // contraction length
+  int splits;           // K is cut into this many slabs (kSlab)
+  int M, N;             // output rows and columns
+  int n_base;           // kStats..kGrad2: vocabulary index of column 0
+  int b0;               // offset into the rows of the matrices B is read from
+  EpArgs ep;
+  unsigned int* err;
+  unsigned long long wait_ns;
+  int stall;
+};
+
+// C = sum over segments of A_seg B_seg^T with A [M][K], B [N][K], then the
+// epilogue.  kSlab reads B and kOut reads both A and B from matrices stored
+// with the contraction outermost ([K][N], [K][M]).
+cudaError_t gemm(Epilogue ep, const GemmArgs& g, cudaStream_t s);
+
+// 2-D map of a bf16 matrix [rows][cols] with `ld` elements per row and a box
+// of box_rows x 64 columns, 128-byte swizzle.
+bool matrix_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows);
+
+}  // namespace ce
+}  // namespace fbob

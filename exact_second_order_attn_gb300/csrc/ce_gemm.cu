@@ -1,0 +1,508 @@
+// The matrix products of the linear head's cross entropy on the fifth
+// generation tensor cores, with the softmax work in the epilogue.
+//
+// C[256 x 256] = sum over segments of A_seg B_seg^T per pair of thread blocks
+// (cta_group::2): each block holds its 128 rows of A and its half of B's rows
+// of every 64-column stage, so a stage moves 32 KB per block for
+// 128 x 256 x 64 products, half of what a lone block would read from L2; the
+// accumulator's 128 rows x 256 columns lie in the block's tensor memory, two
+// of them, so the epilogue of one tile runs under the products of the next.
+// The kernels with two accumulators (z and b of the second order) use 128
+// columns each.
+//
+// Roles of a block's ten warps: 0-7 epilogue (thread = accumulator row, the two
+// warpgroups take half of the columns each), 8 TMA producer, 9 MMA issue (the
+// leader block's) and TMEM allocation.  Barriers: full[s] of the leader counts
+// both blocks' bytes; empty[s] and tile_full[b] are signalled in both blocks
+// by the MMAs' commit; tile_empty[b] of the leader counts the 16 epilogue
+// warps of the pair.  Every wait is bounded.  Blocks are persistent: pair i
+// takes tiles i, i + pairs, ...; tiles walk over 8 row tiles per column tile,
+// so that both operands are re-read from L2.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include "ce.h"
+#include "prof.h"
+#include "tc_pair.cuh"
+
+namespace fbob {
+namespace ce {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 320;
+constexpr int kEpWarps = 8;
+constexpr int kGroupM = 8;        // row tiles per raster group
+constexpr int kTmemCols = 512;
+constexpr int kBufCols = 256;     // accumulator columns per tile in flight
+constexpr uint64_t kDrainNs = 200000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int EP>
+struct Cfg {
+  static constexpr bool DUAL = EP == kAlpha || EP == kGrad2;
+  static constexpr bool A_MN = EP == kOut;
+  static constexpr bool B_MN = EP == kSlab || EP == kOut;
+  static constexpr int BN = DUAL ? kTileNDual : kTileN;
+  static constexpr int A_BYTES = 128 * kBK * 2;
+  static constexpr int B_BYTES = BN / 2 * kBK * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int NST = 196608 / STAGE;  // 6, or 8 with two accumulators
+  static constexpr int SMEM = NST * STAGE;
+  static_assert(SMEM + 1024 <= 232448, "shared memory budget");
+};
+
+struct Ctrl {
+  uint64_t full[8], empty[8], tile_full[2], tile_empty[2], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// A wait whose arrivals may come from the other block of the cluster.
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, const Waiter& w) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if ((it & 15u) == 0u) {
+      if (*w.abort) return false;
+      if (globaltimer_ns() - t0 > w.limit) {
+        *w.abort = 1;
+        atomicOr(w.err, kErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// e^x for the softmax: the difference is taken first, so that its rounding is
+// relative to it and not to the logit.
+__device__ __forceinline__ float ex(float z, float at) { return ex2((z - at) * kLog2e); }
+
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// 32 values as bf16 planes: plane k holds the rounding of what planes 0..k-1 left.
+__device__ __forceinline__ void store_planes(uint16_t* const* planes, int n, size_t at, float* v) {
+  for (int k = 0; k < n; ++k) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      const float2 f = __bfloat1622float2(h);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      v[2 * j] -= f.x;
+      v[2 * j + 1] -= f.y;
+    }
+    st_global_v8(planes[k] + at, w);
+    st_global_v8(planes[k] + at + 16, w + 8);
+  }
+}
+
+// The epilogue of one tile for this thread's row: `acc` is the TMEM address of
+// its first column (of accumulator 0), `row` the row in the output, n0 the
+// first column, part the index of this half tile's row statistics.
+template <int EP>
+__device__ __forceinline__ void epilogue(const GemmArgs& p, uint32_t acc, int row, int n0, int part, int split) {
+  const EpArgs& e = p.ep;
+  const bool live = row < p.M;
+  if constexpr (EP == kStats) {
+    const int y = live ? e.target[row] - p.n_base : -1;
+    float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      float v[32];
+      __syncwarp();  // the loads are warp-collective, the code between them is not
+      tmem_ld32(acc + c, v);
+      const int n = n0 + c;
+      if (y >= n && y < n + 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (n + j == y) e.picked[row] = v[j];
+        }
+      }
+      if (n + 32 > p.N) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = n + j < p.N ? v[j] : -INFINITY;
+      }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+      if (top > -INFINITY || top != top) {
+        float t = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) t += ex(v[j], top);
+        s = s * ex(m, top) + t;
+        m = top;
+      } else {  // nothing above -inf so far; a NaN among them still counts
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s += v[j] != v[j] ? v[j] : 0.f;
+      }
+    }
+    if (live) e.part[(size_t)part * p.M + row] = make_float2(m, s);
+  } else if constexpr (EP == kGrad) {
+    const int y = live ? e.target[row] : -1;
+    const float at = y >= 0 ? e.lse[row] : 0.f, gm = *e.gmax;
+    const float gs = y >= 0 && gm != 0.f ? e.g[row] / gm : 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      float v[32];
+      __syncwarp();  // the loads are warp-collective, the code between them is not
+      tmem_ld32(acc + c, v);
+      const int n = n0 + c, hit = y - p.n_base - n;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = y >= 0 ? gs * ex(v[j], at) : 0.f;
+      if (y >= 0 && hit >= 0 && hit < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] -= j == hit ? gs : 0.f;
+      }
+      if (live && n < e.ld) store_planes(e.planes, e.nplanes, (size_t)row * e.ld + n, v);
+    }
+  } else if constexpr (EP == kAlpha) {
+    const int y = live ? e.target[row] : -1;
+    const float at = y >= 0 ? e.lse[row] : 0.f;
+    float s = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+      float z[32], b[32];
+      __syncwarp();
+      tmem_ld32(acc + c, z);
+      tmem_ld32(acc + kTileNDual + c, b);
+      const int n = n0 + c, hit = y - p.n_base - n;
+      if (y >= 0 && hit >= 0 && hit < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j == hit) e.picked[row] = b[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s += n + j < p.N ? ex(z[j], at) * b[j] : 0.f;
+    }
+    if (live) e.sums[(size_t)part * p.M + row] = y >= 0 ? s : 0.f;
+  } else if constexpr (EP == kGrad2) {
+    const int y = live ? e.target[row] : -1;
+    const float at = y >= 0 ? e.lse[row] : 0.f, al = y >= 0 ? e.alpha[row] : 0.f, gm = *e.gmax;
+    const float gs = y >= 0 && gm != 0.f ? e.g[row] / gm : 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+      float z[32], b[32];
+      __syncwarp();
+      tmem_ld32(acc + c, z);
+      tmem_ld32(acc + kTileNDual + c, b);
+      const int n = n0 + c, hit = y - p.n_base - n;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        z[j] = y >= 0 ? gs * ex(z[j], at) : 0.f;
+        b[j] = y >= 0 ? z[j] * (b[j] - al) : 0.f;
+      }
+      if (y >= 0 && hit >= 0 && hit < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] -= j == hit ? gs : 0.f;
+      }
+      if (live && n < e.ld) {
+        store_planes(e.planes, e.nplanes, (size_t)row * e.ld + n, z);
+        store_planes(e.planes + kPlanes, e.nplanes, (size_t)row * e.ld + n, b);
+      }
+    }
+  } else if constexpr (EP == kSlab) {
+    float* out = static_cast<float*>(e.out) + (size_t)split * e.slab + (size_t)row * e.out_ld;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      float v[32];
+      __syncwarp();  // the loads are warp-collective, the code between them is not
+      tmem_ld32(acc + c, v);
+      const int n = n0 + c;
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {  // out_ld is a multiple of 4
+        if (live && n + j < e.out_ld) {
+          float4* o = reinterpret_cast<float4*>(out + n + j);
+          float4 f = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          if (e.accumulate) {
+            const float4 h = *o;
+            f.x += h.x, f.y += h.y, f.z += h.z, f.w += h.w;
+          }
+          *o = f;
+        }
+      }
+    }
+  } else {
+    const float gm = *e.gmax;
+    const size_t at = (size_t)row * e.out_ld;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      float v[32];
+      __syncwarp();  // the loads are warp-collective, the code between them is not
+      tmem_ld32(acc + c, v);
+      const int n = n0 + c;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] *= gm;
+      if (!live) {
+      } else if (e.out_bf16) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.out) + at + n;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          if (e.out_vec && n + j + 8 <= p.N) {
+            *reinterpret_cast<uint4*>(o + j) = make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
+                                                          pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              if (n + j + q < p.N) o[j + q] = __float2bfloat16_rn(v[j + q]);
+            }
+          }
+        }
+      } else {
+        float* o = static_cast<float*>(e.out) + at + n;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          if (e.out_vec && n + j + 4 <= p.N) {
+            *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (n + j + q < p.N) o[j + q] = v[j + q];
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+struct Tiles {
+  int mt, nt, splits, kb;  // row and column tiles, slabs, 64-column steps of K
+  __device__ __forceinline__ long long count() const { return (long long)mt * nt * splits; }
+  __device__ __forceinline__ void at(long long i, int& m, int& n, int& split) const {
+    const long long plane = (long long)mt * nt;
+    split = (int)(i / plane);
+    const long long r = i - split * plane;
+    const int first = (int)(r / ((long long)kGroupM * nt)) * kGroupM;
+    const int in = (int)(r - (long long)first * nt), rows = min(kGroupM, mt - first);
+    n = in / rows;
+    m = first + in - n * rows;
+  }
+  __device__ __forceinline__ int k_first(int split) const { return (int)((long long)kb * split / splits); }
+};
+
+template <int EP>
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs p) {
+  using C = Cfg<EP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Ctrl ctrl;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const uint32_t rank = cluster_rank();
+  const Tiles ts{(p.M + kTileM - 1) / kTileM, (p.N + C::BN - 1) / C::BN, p.splits, (p.K + kBK - 1) / kBK};
+  const long long total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (tid == 0) {
+    ctrl.abort_flag = 0;
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(&ctrl.full[s], 1);
+      mbar_init(&ctrl.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl.tile_full[b], 1);
+      mbar_init(&ctrl.tile_empty[b], 2 * kEpWarps);
+    }
+    mbar_init(&ctrl.drain, 1);
+    fence_mbar_init();
+    if ((smem_u32(smem) & 1023u) != 0u) {
+      ctrl.abort_flag = 1;
+      atomicOr(p.err, kErrTimeout);
+    }
+  }
+  if (warp == 9) {
+    tmem_alloc_pair(&ctrl.tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both blocks' barriers are initialised
+  tc_fence_after();
+  const uint32_t tb = ctrl.tmem_base;
+  const Waiter wt{&ctrl.abort_flag, p.err, p.wait_ns};
+  const bool live = ctrl.abort_flag == 0;
+  const uint32_t sm0 = smem_u32(smem);
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------ TMA
+    if (live && (tid & 31) == 0) {
+      long long it = 0;
+      bool ok = true;
+      for (long long t = pair; ok && t < total; t += pairs) {
+        int m, n, split;
+        ts.at(t, m, n, split);
+        const int row = m * kTileM + (int)rank * 128, col = n * C::BN + (int)rank * (C::BN / 2);
+        const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
+        for (int s = 0; ok && s < p.nseg; ++s) {
+          const CUtensorMap* ma = &p.a[p.seg[s].a];
+          const CUtensorMap* mb = &p.b[p.seg[s].b];
+          for (int k = k0; k < k1; ++k, ++it) {
+            const int st = (int)(it % C::NST);
+            if (!(ok = wait_cluster(&ctrl.empty[st], ((it / C::NST) & 1) ^ 1, wt))) break;
+            if (p.stall && it == 0) continue;  // test hook: nothing fills the first stage
+            const uint32_t bar = map_rank(smem_u32(&ctrl.full[st]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&ctrl.full[st], 2 * C::STAGE);
+            const uint32_t da = sm0 + st * C::STAGE, db = da + C::A_BYTES;
+            if (C::A_MN) {
+              tma_load_2d_pair(da, ma, bar, row, k * kBK);
+              tma_load_2d_pair(da + 8192, ma, bar, row + 64, k * kBK);
+            } else {
+              tma_load_2d_pair(da, ma, bar, k * kBK, row);
+            }
+            if (C::B_MN) {
+              tma_load_2d_pair(db, mb, bar, col, p.b0 + k * kBK);
+              tma_load_2d_pair(db + 8192, mb, bar, col + 64, p.b0 + k * kBK);
+            } else {
+              tma_load_2d_pair(db, mb, bar, k * kBK, p.b0 + col);
+            }
+          }
+        }
+      }
+      // The last use of each stage: on the leader its loads have landed, in both
+      // blocks the MMAs' arrivals have (on the give-up path after a limit), so
+      // nothing is in flight towards a block that has ended.
+      for (long long i = it > C::NST ? it - C::NST : 0; i < it; ++i) {
+        const int st = (int)(i % C::NST);
+        if (rank == 0 && !ok) mbar_wait_drain(&ctrl.full[st], (i / C::NST) & 1, kDrainNs);
+        if (ok) ok = wait_cluster(&ctrl.empty[st], (i / C::NST) & 1, wt);
+      }
+      if (!ok && rank != 0) {  // this block's loads count on the leader's barriers: give them time to land
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kDrainNs) {
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ MMA
+    if (live && rank == 0) {
+      constexpr uint32_t id = idesc_bf16(kTileM, C::BN, C::A_MN, C::B_MN);
+      constexpr uint32_t lbo_a = C::A_MN ? 8192 : 16, lbo_b = C::B_MN ? 8192 : 16;
+      constexpr uint32_t step_a = C::A_MN ? 2048 >> 4 : 32 >> 4, step_b = C::B_MN ? 2048 >> 4 : 32 >> 4;
+      long long it = 0;
+      int tile = 0;
+      bool ok = true;
+      for (long long t = pair; ok && t < total; t += pairs, ++tile) {
+        int m, n, split;
+        ts.at(t, m, n, split);
+        const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
+        const int buf = tile & 1;
+        ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_empty[buf], ((tile >> 1) & 1) ^ 1, wt));
+        tc_fence_after();
+        uint32_t started = 0;  // accumulators that hold a product already
+        for (int s = 0; ok && s < p.nseg; ++s) {
+          const uint32_t acc = p.seg[s].acc, d = tb + buf * kBufCols + acc * kTileNDual;
+          for (int k = k0; k < k1; ++k, ++it) {
+            const int st = (int)(it % C::NST);
+            ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.full[st], (it / C::NST) & 1, wt));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = desc_lo(sm0 + st * C::STAGE, lbo_a);
+            const uint32_t b = desc_lo(sm0 + st * C::STAGE + C::A_BYTES, lbo_b);
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_ss_pair(d, a + kk * step_a, b + kk * step_b, id, kk > 0 ? 1u : (started >> acc) & 1u);
+            started |= 1u << acc;
+            mma_commit_pair(&ctrl.empty[st]);
+          }
+        }
+        mma_commit_pair(&ctrl.tile_full[buf]);
+      }
+      mma_commit_pair(&ctrl.drain);  // the last MMA has read its operands
+      mbar_wait_drain(&ctrl.drain, 0, kDrainNs);
+    }
+  } else {
+    // ------------------------------------------------------------- epilogue
+    const int half = warp >> 2, r = (warp & 3) * 32 + (tid & 31);
+    const uint32_t lane = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t freed = map_rank(smem_u32(&ctrl.tile_empty[0]), 0);
+    int tile = 0;
+    for (long long t = pair; live && t < total; t += pairs, ++tile) {
+      int m, n, split;
+      ts.at(t, m, n, split);
+      const int buf = tile & 1;
+      // warp-uniform: the TMEM loads that follow are warp-collective
+      if (!__all_sync(0xffffffffu, wait_cluster(&ctrl.tile_full[buf], (tile >> 1) & 1, wt))) break;
+      tc_fence_after();
+      constexpr int H = C::BN / 2;
+      epilogue<EP>(p, tb + lane + buf * kBufCols + half * H, m * kTileM + (int)rank * 128 + r, n * C::BN + half * H,
+                   2 * n + half, split);
+      tc_fence_before();
+      __syncwarp();
+      if ((tid & 31) == 0) mbar_arrive_cluster(freed + buf * 8);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither block ends, or frees tensor memory, before the other is done
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc_pair(tb, kTmemCols);
+  }
+}
+
+template <int EP>
+cudaError_t launch(const GemmArgs& g, const char* name, cudaStream_t s) {
+  using C = Cfg<EP>;
+  auto kernel = gemm_kernel<EP>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (long long)((g.M + kTileM - 1) / kTileM) * ((g.N + C::BN - 1) / C::BN) * g.splits;
+  if (tiles == 0) return cudaSuccess;
+  const long long pairs = sm_count() / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  prof_begin(s, name);
+  e = cudaLaunchKernelEx(&cfg, kernel, g);
+  prof_end(s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t gemm(Epilogue ep, const GemmArgs& g, cudaStream_t s) {
+  switch (ep) {
+    case kStats: return launch<kStats>(g, "ce_stats", s);
+    case kGrad: return launch<kGrad>(g, "ce_grad", s);
+    case kAlpha: return launch<kAlpha>(g, "ce_alpha", s);
+    case kGrad2: return launch<kGrad2>(g, "ce_grad2", s);
+    case kSlab: return launch<kSlab>(g, "ce_hidden", s);
+    case kOut: return launch<kOut>(g, "ce_head", s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace ce
+}  // namespace fbob

@@ -75,8 +75,22 @@ struct NormArgs {
   float eps;
 };
 
+// Softmax cross entropy of a linear head: T tokens of D columns, V classes.
+struct CeArgs {
+  const void *H, *W, *UH, *UW;
+  const long long* target;
+  const float *lse, *g;
+  float *loss, *lse_out, *gg;
+  void *dH, *dW;  // or gH, gW
+  void* ws;
+  int T, D, V, bf16, piece;
+  long long ignore;
+};
+enum class CePass { kFwd, kBwd, kBob };
+
 // Status word bits.
 constexpr unsigned int kErrTimeout = 1u;
+constexpr unsigned int kErrTarget = 2u;  // a class index outside the vocabulary
 
 // errword.cu: device address of the status word on the current device.
 cudaError_t dev_status_word(unsigned int** ptr);
@@ -100,6 +114,10 @@ cudaError_t layer_norm_fwd(const NormArgs& a, cudaStream_t s);
 cudaError_t layer_norm_bwd(const NormArgs& a, cudaStream_t s);
 cudaError_t layer_norm_bob(const NormArgs& a, cudaStream_t s);
 size_t layer_norm_workspace_floats(long long rows, int D);  // of bwd (bob needs half)
+
+// linear_ce.cu
+size_t linear_ce_workspace(const CeArgs& a, CePass pass);
+cudaError_t linear_ce(const CeArgs& a, CePass pass, const DevCtx& c, cudaStream_t s);
 
 // bob_static.cu: the fixed (alpha, E) workspace of fbob_attn_bob_noalloc.
 size_t static_workspace_rows();           // capacity in query rows (B*H*N)

@@ -1,0 +1,507 @@
+// Softmax cross entropy of a linear head z = h W^T over a large vocabulary,
+// without keeping the logits: forward, gradients, and the gradients' own
+// vector-Jacobian product (formulas in fbob.h).
+//
+// Forward: one product whose epilogue reduces each 128 columns of a row to
+// (max, sum of exponentials) and picks the target's logit; a small kernel joins
+// them.  Gradients: for pieces of the vocabulary, the logits are formed again
+// and turned in the epilogue into G = (g / gmax) (p - onehot), kept as bf16 for
+// the piece only; then dH += G W and dW = gmax G^T H.  Second order: one pass
+// for alpha = sum p b, then the same with Z = (g / gmax) p (b - alpha) beside G.
+//
+// Dividing by gmax = max |g| (an fp32 factor of the results) keeps the target's
+// entry of G at p - 1 for a mean loss, where all g are equal: its rounding to
+// bf16 is then relative to p - 1 and not a systematic relative error of the
+// largest entry of every row.
+//
+// fp32 inputs stand as three bf16 terms each (8 bits of the value per term);
+// the six products of terms whose magnitudes reach 2^-16 of the first are
+// summed, smallest first, in fp32.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <string.h>
+
+#include "ce.h"
+#include "prof.h"
+
+namespace fbob {
+namespace ce {
+namespace {
+
+constexpr int kPairs = 76;                        // block pairs of a GB300, for the split rule
+constexpr size_t kPieceBytes = 512ull << 20;      // G (and Z) of one piece of the vocabulary
+constexpr int kPieceStep = 256;
+
+size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+// Piece width: all of V if its G fits kPieceBytes, else equal pieces that do
+// (at least 2048 columns, so that a piece's products keep the device busy).
+int piece_cols(const CeArgs& a, bool second) {
+  const size_t per = (size_t)a.T * 2 * (a.bf16 ? 1 : kPlanes) * (second ? 2 : 1);
+  size_t cols = a.piece > 0 ? (size_t)a.piece : kPieceBytes / (per ? per : 1);
+  cols = up(cols < 2048 && a.piece <= 0 ? 2048 : cols, kPieceStep);
+  const size_t whole = up(a.V, kPieceStep);
+  if (cols >= whole) return (int)whole;
+  const size_t n = (a.V + cols - 1) / cols;
+  return (int)up((a.V + n - 1) / n, kPieceStep);
+}
+
+// Slabs of the contraction over a piece in dH = G W.  Its output has few tiles
+// (T x D), so the contraction is cut until the tiles' last wave is nearly full;
+// each slab costs a write and a read of T x D floats, so no more than needed,
+// and at least eight 64-column steps remain in each.
+int hidden_splits(const CeArgs& a, int cols) {
+  const int tiles = ((a.T + kTileM - 1) / kTileM) * ((a.D + kTileN - 1) / kTileN);
+  const int most = (int)(up(cols, kBK) / kBK / 8);
+  int best = 1;
+  double best_eff = 0;
+  for (int s = 1; s <= most && s <= 64; ++s) {
+    const long long n = (long long)tiles * s;
+    const double eff = (double)n / (double)((n + kPairs - 1) / kPairs * kPairs);
+    if (eff > best_eff + 0.02) best = s, best_eff = eff;
+    if (best_eff > 0.9) break;
+  }
+  return best;
+}
+
+// Where everything lies in the workspace.
+struct Plan {
+  int np, Dp, ld, splits, stat_parts, alpha_parts;
+  bool copy_w;
+  size_t h, uh, w, uw, target, gmax, part, sums, picked, alpha, planes, slab, bytes;
+};
+
+Plan plan(const CeArgs& a, CePass pass) {
+  Plan p;
+  p.np = a.bf16 ? 1 : kPlanes;
+  p.Dp = (int)up(a.D, 8);
+  p.copy_w = !a.bf16 || a.D % 8 != 0;
+  p.stat_parts = 2 * ((a.V + kTileN - 1) / kTileN);
+  p.alpha_parts = 2 * ((a.V + kTileNDual - 1) / kTileNDual);
+  p.ld = pass == CePass::kFwd ? 0 : piece_cols(a, pass == CePass::kBob);
+  p.splits = pass == CePass::kFwd ? 1 : hidden_splits(a, p.ld);
+  size_t at = 0;
+  auto take = [&](bool want, size_t bytes) {
+    const size_t here = at;
+    if (want) at += up(bytes, 256);
+    return here;
+  };
+  const bool bwd = pass != CePass::kFwd, bob = pass == CePass::kBob;
+  const size_t T = a.T, V = a.V, row = (size_t)p.Dp * 2 * p.np;
+  p.h = take(true, T * row);
+  p.uh = take(bob, T * row);
+  p.w = take(p.copy_w, V * row);
+  p.uw = take(bob && p.copy_w, V * row);
+  p.target = take(true, T * 4);
+  p.gmax = take(true, 4);
+  p.picked = take(!bwd || bob, T * 4);
+  p.part = take(!bwd, T * p.stat_parts * sizeof(float2));
+  p.sums = take(bob, T * p.alpha_parts * 4);
+  p.alpha = take(bob, T * 4);
+  p.planes = take(bwd, T * p.ld * 2 * p.np * (bob ? 2 : 1));
+  p.slab = take(bwd, T * p.Dp * 4 * p.splits);
+  p.bytes = at;
+  return p;
+}
+
+// --- small kernels ---------------------------------------------------------------------------------
+
+// Rows of H (or UH), or of W (target null): bf16 planes [rows][Dp], zero in the
+// padding and in rows that are not counted (whatever those hold).  One thread
+// per 8 columns; the thread of a row's first columns also writes the row's
+// target as the products' epilogues read it: the column, -1 (ignored) or -2
+// (outside the vocabulary: reported in the status word).
+template <typename T>
+__global__ void __launch_bounds__(256)
+    planes_kernel(const T* x, const long long* target, long long ignore, int V, int* target_out, uint16_t* planes,
+                  long long rows, int D, int Dp, int np, bool vec, unsigned int* err) {
+  const int per = Dp / 8;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long r = i / per;
+  const int c = (int)(i - r * per) * 8;
+  if (r >= rows) return;
+  bool keep = true;
+  if (target) {
+    const long long y = target[r];
+    keep = y != ignore && y >= 0 && y < V;
+    if (target_out && c == 0) {
+      target_out[r] = keep ? (int)y : y == ignore ? -1 : -2;
+      if (!keep && y != ignore) atomicOr(err, kErrTarget);
+    }
+  }
+  float v[8];
+  const T* src = x + r * D + c;
+  if (!keep) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  } else if (vec) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 u = *reinterpret_cast<const uint4*>(src);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    } else {
+      const float4 f = *reinterpret_cast<const float4*>(src), g = *reinterpret_cast<const float4*>(src + 4);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w, v[4] = g.x, v[5] = g.y, v[6] = g.z, v[7] = g.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < D ? (float)src[j] : 0.f;
+  }
+  for (int k = 0; k < np; ++k) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      // an infinite value has no remainder (inf - inf would make one)
+      const float2 f = __bfloat1622float2(h);
+      v[2 * j] = isinf(f.x) ? 0.f : v[2 * j] - f.x;
+      v[2 * j + 1] = isinf(f.y) ? 0.f : v[2 * j + 1] - f.y;
+    }
+    *reinterpret_cast<uint4*>(planes + ((size_t)k * rows + r) * Dp + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// gmax = max |g| over the counted rows (1 if that is not finite), in one block.
+__global__ void __launch_bounds__(1024) gmax_kernel(const float* g, const long long* target, long long ignore, int V,
+                                                     int T, float* out) {
+  __shared__ float part[32];
+  float m = 0.f;
+  for (int t = threadIdx.x; t < T; t += blockDim.x) {
+    const long long y = target[t];
+    if (y != ignore && y >= 0 && y < V) m = fmaxf(m, fabsf(g[t]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    m = part[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (threadIdx.x == 0) *out = m < INFINITY ? m : 1.f;
+  }
+}
+
+// Sums over `parts` per-row partials, 32 rows per block and 8 (x 32 lanes)
+// threads per row: loss and lse (kStats), or alpha and gg (kAlpha).
+constexpr int kJoinRows = 32, kJoinWays = 16;
+
+__global__ void __launch_bounds__(kJoinRows* kJoinWays)
+    join_stats_kernel(const float2* part, int parts, const int* target, const float* picked, int T, float* loss,
+                      float* lse) {
+  __shared__ float2 sh[kJoinWays][kJoinRows];
+  const int t = blockIdx.x * kJoinRows + threadIdx.x;
+  float m = -INFINITY, s = 0.f;
+  if (t < T) {
+    for (int i = threadIdx.y; i < parts; i += kJoinWays) {
+      const float2 q = part[(size_t)i * T + t];
+      const float top = fmaxf(m, q.x);
+      if (top > -INFINITY) {
+        s = (m > -INFINITY ? s * expf(m - top) : s) + (q.x > -INFINITY ? q.y * expf(q.x - top) : q.y);
+        m = top;
+      } else {
+        s += q.y;
+      }
+    }
+  }
+  sh[threadIdx.y][threadIdx.x] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.y != 0 || t >= T) return;
+  float top = -INFINITY;
+  for (int w = 0; w < kJoinWays; ++w) top = fmaxf(top, sh[w][threadIdx.x].x);
+  s = 0.f;
+  for (int w = 0; w < kJoinWays; ++w) {
+    const float2 q = sh[w][threadIdx.x];
+    s += q.x > -INFINITY ? q.y * expf(q.x - top) : q.y;
+  }
+  const int y = target[t];
+  const float l = (top > -INFINITY ? top : 0.f) + logf(s);
+  lse[t] = y >= 0 ? l : 0.f;
+  loss[t] = y >= 0 ? l - picked[t] : y == -1 ? 0.f : NAN;
+}
+
+__global__ void __launch_bounds__(kJoinRows* kJoinWays)
+    join_alpha_kernel(const float* sums, int parts, const int* target, const float* picked, int T, float* alpha,
+                      float* gg) {
+  __shared__ float sh[kJoinWays][kJoinRows];
+  const int t = blockIdx.x * kJoinRows + threadIdx.x;
+  float s = 0.f;
+  if (t < T) {
+    for (int i = threadIdx.y; i < parts; i += kJoinWays) s += sums[(size_t)i * T + t];
+  }
+  sh[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y != 0 || t >= T) return;
+  s = 0.f;
+  for (int w = 0; w < kJoinWays; ++w) s += sh[w][threadIdx.x];
+  const bool keep = target[t] >= 0;
+  alpha[t] = keep ? s : 0.f;
+  if (gg) gg[t] = keep ? s - picked[t] : 0.f;
+}
+
+// out [T][D] = gmax * sum of the slabs [T][Dp]; zero in rows that are not counted.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    finish_kernel(const float* slab, int splits, long long stride, const int* target, const float* gmax, T* out, int D,
+                  int Dp, long long rows, bool vec) {
+  const int per = Dp / 4;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long r = i / per;
+  const int c = (int)(i - r * per) * 4;
+  if (r >= rows) return;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (target[r] >= 0) {
+    const float gm = *gmax;
+    for (int s = 0; s < splits; ++s) {
+      const float4 f = *reinterpret_cast<const float4*>(slab + s * stride + r * Dp + c);
+      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= gm;
+  }
+  T* o = out + r * D + c;
+  if (vec) {
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+      *reinterpret_cast<uint2*>(o) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c + j < D) o[j] = (T)v[j];
+    }
+  }
+}
+
+// --- the passes --------------------------------------------------------------------------------------
+
+#define CE_TRY(x)                                \
+  do {                                           \
+    const cudaError_t e_ = (x);                  \
+    if (e_ != cudaSuccess) return e_;            \
+  } while (0)
+
+bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+struct Run {
+  const CeArgs& a;
+  const DevCtx& c;
+  cudaStream_t s;
+  Plan p;
+  char* ws;
+  bool second;
+
+  template <typename T>
+  T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
+
+  cudaError_t make_planes(const void* x, bool tokens, int* target_out, uint16_t* out, long long rows) const {
+    const bool vec = a.D % 8 == 0 && aligned(x, 16);
+    const long long n = rows * (p.Dp / 8);
+    const unsigned blocks = (unsigned)((n + 255) / 256);
+    const long long* target = tokens ? a.target : nullptr;
+    prof_begin(s, "ce_operands");
+    if (a.bf16)
+      planes_kernel<<<blocks, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), target, a.ignore, a.V, target_out, out,
+                                           rows, a.D, p.Dp, p.np, vec, c.err);
+    else
+      planes_kernel<<<blocks, 256, 0, s>>>(static_cast<const float*>(x), target, a.ignore, a.V, target_out, out, rows,
+                                           a.D, p.Dp, p.np, vec, c.err);
+    prof_end(s);
+    return cudaGetLastError();
+  }
+
+  // H, W (and UH, UW) as the products read them.
+  cudaError_t operands() const {
+    CE_TRY(make_planes(a.H, true, at<int>(p.target), at<uint16_t>(p.h), a.T));
+    if (p.copy_w) CE_TRY(make_planes(a.W, false, nullptr, at<uint16_t>(p.w), a.V));
+    if (second) {
+      if (a.UH) CE_TRY(make_planes(a.UH, true, nullptr, at<uint16_t>(p.uh), a.T));
+      if (p.copy_w && a.UW) CE_TRY(make_planes(a.UW, false, nullptr, at<uint16_t>(p.uw), a.V));
+    }
+    if (a.g) {
+      prof_begin(s, "ce_gmax");
+      gmax_kernel<<<1, 1024, 0, s>>>(a.g, a.target, a.ignore, a.V, a.T, at<float>(p.gmax));
+      prof_end(s);
+      CE_TRY(cudaGetLastError());
+    }
+    return cudaSuccess;
+  }
+
+  GemmArgs base() const {
+    GemmArgs g;
+    memset(&g, 0, sizeof(g));
+    g.splits = 1;
+    g.err = c.err, g.wait_ns = c.wait_ns, g.stall = c.stall;
+    g.ep.target = at<int>(p.target), g.ep.lse = a.lse, g.ep.g = a.g, g.ep.gmax = at<float>(p.gmax);
+    return g;
+  }
+
+  // Maps of the planes of a [rows][D] operand (of the tokens, or of the head).
+  bool token_maps(CUtensorMap* m, size_t off, int box) const {
+    for (int k = 0; k < p.np; ++k)
+      if (!matrix_map(m + k, at<uint16_t>(off) + (size_t)k * a.T * p.Dp, a.T, p.Dp, p.Dp, box)) return false;
+    return true;
+  }
+  bool head_maps(CUtensorMap* m, const void* x, size_t off, int box) const {
+    for (int k = 0; k < p.np; ++k) {
+      const void* b = p.copy_w ? at<uint16_t>(off) + (size_t)k * a.V * p.Dp : x;
+      if (!matrix_map(m + k, b, a.V, p.Dp, p.Dp, box)) return false;
+    }
+    return true;
+  }
+  // Planes of G (which = 0) or Z (1) of a piece of `cols` columns.
+  uint16_t* piece_plane(int which, int k) const {
+    return at<uint16_t>(p.planes) + (size_t)(which * p.np + k) * a.T * p.ld;
+  }
+  bool piece_maps(CUtensorMap* m, int which, int cols, int box) const {
+    for (int k = 0; k < p.np; ++k)
+      if (!matrix_map(m + k, piece_plane(which, k), a.T, cols, p.ld, box)) return false;
+    return true;
+  }
+
+  // The products of planes of A operand `x` and B operand `y` (0 or 1 each),
+  // smallest first.
+  void products(GemmArgs& g, int x, int y, int acc) const {
+    static const uint8_t order[6][2] = {{0, 2}, {1, 1}, {2, 0}, {0, 1}, {1, 0}, {0, 0}};
+    for (int i = p.np == 1 ? 5 : 0; i < 6; ++i)
+      g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + order[i][0]), (uint8_t)(kPlanes * y + order[i][1]), (uint8_t)acc, 0};
+  }
+
+  // The logits (and, in the second order, b = UH W^T + H UW^T).
+  bool logits(GemmArgs& g, bool dual) const {
+    const int box = (dual ? kTileNDual : kTileN) / 2;
+    if (!token_maps(g.a, p.h, 128) || !head_maps(g.b, a.W, p.w, box)) return false;
+    products(g, 0, 0, 0);
+    if (dual) {
+      if (a.UH) {
+        if (!token_maps(g.a + kPlanes, p.uh, 128)) return false;
+        products(g, 1, 0, 1);
+      }
+      if (a.UW) {
+        if (!head_maps(g.b + kPlanes, a.UW, p.uw, box)) return false;
+        products(g, 0, 1, 1);
+      }
+    }
+    g.M = a.T, g.K = a.D;
+    return true;
+  }
+
+  cudaError_t stats() const {
+    GemmArgs g = base();
+    if (!logits(g, false)) return cudaErrorInvalidValue;
+    g.N = a.V;
+    g.ep.part = at<float2>(p.part), g.ep.picked = at<float>(p.picked);
+    CE_TRY(gemm(kStats, g, s));
+    prof_begin(s, "ce_join");
+    join_stats_kernel<<<(a.T + kJoinRows - 1) / kJoinRows, dim3(kJoinRows, kJoinWays), 0, s>>>(
+        at<float2>(p.part), p.stat_parts, at<int>(p.target), at<float>(p.picked), a.T, a.loss, a.lse_out);
+    prof_end(s);
+    return cudaGetLastError();
+  }
+
+  cudaError_t alpha() const {
+    GemmArgs g = base();
+    if (!logits(g, true)) return cudaErrorInvalidValue;
+    g.N = a.V;
+    g.ep.sums = at<float>(p.sums), g.ep.picked = at<float>(p.picked);
+    CE_TRY(gemm(kAlpha, g, s));
+    prof_begin(s, "ce_join");
+    join_alpha_kernel<<<(a.T + kJoinRows - 1) / kJoinRows, dim3(kJoinRows, kJoinWays), 0, s>>>(
+        at<float>(p.sums), p.alpha_parts, at<int>(p.target), at<float>(p.picked), a.T, at<float>(p.alpha), a.gg);
+    prof_end(s);
+    return cudaGetLastError();
+  }
+
+  // One piece of the vocabulary: columns c0 .. c0 + cols - 1.
+  cudaError_t piece(int c0, int cols, bool first) const {
+    GemmArgs g = base();
+    if (!logits(g, second)) return cudaErrorInvalidValue;
+    g.N = cols, g.n_base = g.b0 = c0;
+    g.ep.alpha = at<float>(p.alpha), g.ep.nplanes = p.np, g.ep.ld = p.ld;
+    for (int k = 0; k < p.np; ++k) {
+      g.ep.planes[k] = piece_plane(0, k);
+      if (second) g.ep.planes[kPlanes + k] = piece_plane(1, k);
+    }
+    CE_TRY(gemm(second ? kGrad2 : kGrad, g, s));
+    if (a.dH) {  // Z W + G UW, or G W
+      g = base();
+      if (!piece_maps(g.a, 0, cols, 128) || !head_maps(g.b, a.W, p.w, 64)) return cudaErrorInvalidValue;
+      if (second) {
+        if (!piece_maps(g.a + kPlanes, 1, cols, 128)) return cudaErrorInvalidValue;
+        products(g, 1, 0, 0);
+        if (a.UW) {
+          if (!head_maps(g.b + kPlanes, a.UW, p.uw, 64)) return cudaErrorInvalidValue;
+          products(g, 0, 1, 0);
+        }
+      } else {
+        products(g, 0, 0, 0);
+      }
+      g.M = a.T, g.N = a.D, g.K = cols, g.b0 = c0, g.splits = p.splits;
+      g.ep.out = at<float>(p.slab), g.ep.out_ld = p.Dp, g.ep.slab = (long long)a.T * p.Dp, g.ep.accumulate = !first;
+      CE_TRY(gemm(kSlab, g, s));
+    }
+    if (a.dW) {  // Z^T H + G^T UH, or G^T H
+      g = base();
+      if (!piece_maps(g.a, 0, cols, 64) || !token_maps(g.b, p.h, 64)) return cudaErrorInvalidValue;
+      if (second) {
+        if (!piece_maps(g.a + kPlanes, 1, cols, 64)) return cudaErrorInvalidValue;
+        products(g, 1, 0, 0);
+        if (a.UH) {
+          if (!token_maps(g.b + kPlanes, p.uh, 64)) return cudaErrorInvalidValue;
+          products(g, 0, 1, 0);
+        }
+      } else {
+        products(g, 0, 0, 0);
+      }
+      g.M = cols, g.N = a.D, g.K = a.T;
+      g.ep.out = static_cast<char*>(a.dW) + (size_t)c0 * a.D * (a.bf16 ? 2 : 4);
+      g.ep.out_ld = a.D, g.ep.out_bf16 = a.bf16;
+      g.ep.out_vec = a.D % (a.bf16 ? 8 : 4) == 0 && aligned(a.dW, 16);
+      CE_TRY(gemm(kOut, g, s));
+    }
+    return cudaSuccess;
+  }
+
+  cudaError_t finish() const {
+    if (!a.dH) return cudaSuccess;
+    const long long n = (long long)a.T * (p.Dp / 4);
+    const unsigned blocks = (unsigned)((n + 255) / 256);
+    const bool vec = a.D % 4 == 0 && aligned(a.dH, a.bf16 ? 8 : 16);
+    prof_begin(s, "ce_finish");
+    if (a.bf16)
+      finish_kernel<<<blocks, 256, 0, s>>>(at<float>(p.slab), p.splits, (long long)a.T * p.Dp, at<int>(p.target),
+                                           at<float>(p.gmax), static_cast<__nv_bfloat16*>(a.dH), a.D, p.Dp, a.T, vec);
+    else
+      finish_kernel<<<blocks, 256, 0, s>>>(at<float>(p.slab), p.splits, (long long)a.T * p.Dp, at<int>(p.target),
+                                           at<float>(p.gmax), static_cast<float*>(a.dH), a.D, p.Dp, a.T, vec);
+    prof_end(s);
+    return cudaGetLastError();
+  }
+};
+
+}  // namespace
+}  // namespace ce
+
+size_t linear_ce_workspace(const CeArgs& a, CePass pass) { return ce::plan(a, pass).bytes; }
+
+cudaError_t linear_ce(const CeArgs& a, CePass pass, const DevCtx& c, cudaStream_t s) {
+  const ce::Run r{a, c, s, ce::plan(a, pass), static_cast<char*>(a.ws), pass == CePass::kBob};
+  CE_TRY(r.operands());
+  if (pass == CePass::kFwd) return r.stats();
+  if (pass == CePass::kBob) CE_TRY(r.alpha());
+  if (!a.dH && !a.dW) return cudaSuccess;
+  for (int c0 = 0; c0 < a.V; c0 += r.p.ld)
+    CE_TRY(r.piece(c0, a.V - c0 < r.p.ld ? a.V - c0 : r.p.ld, c0 == 0));
+  return r.finish();
+}
+
+}  // namespace fbob

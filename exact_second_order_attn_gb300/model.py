@@ -1,7 +1,7 @@
 """PyTorch autograd integration of the operators around the attention.
 
-``rotary`` and ``layer_norm`` can be differentiated twice, like ``attention``,
-so that ``hvp`` passes through a model built of them.  Outputs and gradients
+``rotary``, ``layer_norm`` and ``linear_cross_entropy`` can be differentiated
+twice, like ``attention``, so that ``hvp`` passes through a model built of them.  Outputs and gradients
 have the inputs' dtypes; sums and statistics are fp32 inside the kernels.
 Third derivatives are not provided (rotary, a linear map, has all of them).
 
@@ -106,3 +106,53 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     return _Norm.apply(x, weight, bias, float(eps))
+
+
+class _CeBwd(torch.autograd.Function):
+    """(H, W, g) -> (dH, dW); its own backward is fbob_linear_ce_bob."""
+
+    @staticmethod
+    def forward(ctx, H, W, g, target, lse, ignore_index, want):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(H, W, g, target, lse)
+        ctx.ignore_index = ignore_index
+        return _model.fbob_linear_ce_bwd(H, W, target, lse, g, ignore_index, want=want)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, UH, UW):
+        H, W, g, target, lse = ctx.saved_tensors
+        want = ctx.needs_input_grad[:3]
+        if (UH is None and UW is None) or not any(want):
+            return None, None, None, None, None, None, None
+        UH, UW = (None if u is None else u.contiguous() for u in (UH, UW))
+        gH, gW, gg = _model.fbob_linear_ce_bob(H, W, target, lse, g, UH, UW, ctx.ignore_index, want=want)
+        return gH, gW, gg, None, None, None, None
+
+
+class _Ce(torch.autograd.Function):
+    """(H, W) -> loss per token; its backward is the differentiable _CeBwd."""
+
+    @staticmethod
+    def forward(ctx, H, W, target, ignore_index):
+        loss, lse = _model.fbob_linear_ce_fwd(H, W, target, ignore_index)
+        ctx.save_for_backward(H, W, target, lse)
+        ctx.ignore_index = ignore_index
+        return loss
+
+    @staticmethod
+    def backward(ctx, g):
+        H, W, target, lse = ctx.saved_tensors
+        dH, dW = _CeBwd.apply(H, W, g.contiguous(), target, lse, ctx.ignore_index, ctx.needs_input_grad[:2])
+        return dH, dW, None, None
+
+
+def linear_cross_entropy(H, W, target, ignore_index=-100):
+    """Losses [T] (fp32) of tokens H [T, D] under the logits H W^T of a head
+    W [V, D], twice differentiable in H and W; 0 where target [T] (int64) is
+    ``ignore_index``.  The logits are never stored.  A target outside [0, V)
+    that is not ``ignore_index`` gives a NaN loss and no gradient, and
+    ``device_status`` reports it."""
+    if not (H.is_contiguous() and W.is_contiguous() and target.is_contiguous()):
+        raise ValueError("H, W and target must be contiguous")
+    return _Ce.apply(H, W, target, int(ignore_index))

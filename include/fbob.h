@@ -319,10 +319,65 @@ fbob_status fbob_layer_norm_bob(const fbob_norm* p, const void* x, const void* w
                                 void* gx, void* gw, void* gdy,
                                 float* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* The cross entropy of a linear head: T tokens h of D columns, V classes. */
+typedef struct {
+  int T, D, V;
+  int dtype;               /* H, W, UH, UW and their gradients                */
+  long long ignore_index;  /* target of the tokens that are not counted       */
+  int piece;               /* classes whose gradient is held at once (rounded */
+                           /* up to 256); 0: as many as 512 MiB hold          */
+} fbob_linear_ce;
+
+/* Bytes of workspace of pass 0 (fwd), 1 (bwd) or 2 (bob); 0 for no tokens or
+ * a descriptor that the calls refuse. */
+size_t fbob_linear_ce_workspace_bytes(const fbob_linear_ce* p, int pass);
+
+/*
+ * Losses of the tokens under logits z = h W^T, which are never stored:
+ *   lse_t = log sum_v exp z_tv, loss_t = lse_t - z_t,target; both 0 where
+ *   target_t == ignore_index.  A target outside [0, V) that is not
+ *   ignore_index makes loss_t NaN, counts as ignored in every gradient and is
+ *   reported by fbob_device_status as FBOB_ERR_INVALID_ARG.
+ *   in : H [T, D], W [V, D] (W 16-byte aligned when bf16 with D a multiple
+ *        of 8), target [T] 64-bit
+ *   out: loss, lse [T] fp32
+ * Tokens that are not counted are never read into a sum, whatever H holds
+ * there.  fp32 inputs are multiplied as three bf16 terms each and lose
+ * nothing to about 2^-22.
+ */
+fbob_status fbob_linear_ce_fwd(const fbob_linear_ce* p, const void* H, const void* W,
+                               const long long* target, float* loss, float* lse,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Gradients of sum_t g_t loss_t: with p = exp(z - lse) and
+ * G = g (p - onehot(target)),
+ *   dH = G W, dW = G^T H; each optional.  G is formed for one piece of the
+ *   classes at a time, in bf16 for bf16 inputs.
+ *   in : as fbob_linear_ce_fwd, its lse, and g [T] fp32
+ */
+fbob_status fbob_linear_ce_bwd(const fbob_linear_ce* p, const void* H, const void* W,
+                               const long long* target, const float* lse, const float* g,
+                               void* dH, void* dW, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/*
+ * The vector-Jacobian product of (H, W, g) -> (dH, dW) along (UH, UW):
+ * gradients of <UH, dH> + <UW, dW>.  With b = UH W^T + H UW^T,
+ * alpha_t = sum_v p b and Z = g p (b - alpha),
+ *   gH = Z W + G UW, gW = Z^T H + G^T UH, gg_t = alpha_t - b_t,target;
+ * each optional; one of UH, UW may be null (zeros).
+ */
+fbob_status fbob_linear_ce_bob(const fbob_linear_ce* p, const void* H, const void* W,
+                               const long long* target, const float* lse, const float* g,
+                               const void* UH, const void* UW, void* gH, void* gW, float* gg,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /*
  * Device status: waits for `stream` to finish (this call DOES synchronise),
  * then returns FBOB_ERR_TIMEOUT if any kernel of this library on the current
- * device gave up on a bounded wait since the last call, else FBOB_OK (or
+ * device gave up on a bounded wait since the last call, FBOB_ERR_INVALID_ARG
+ * if fbob_linear_ce_* met a target outside its classes, else FBOB_OK (or
  * FBOB_ERR_CUDA if the synchronisation itself failed).  Clears the word.
  */
 fbob_status fbob_device_status(cudaStream_t stream);

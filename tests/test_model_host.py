@@ -127,3 +127,68 @@ def test_binding_refuses_host_tensors_types_and_shapes():
         fb.fbob_layer_norm_fwd(x.half())
     with pytest.raises(ValueError):
         fb.layer_norm(x.transpose(0, 1))
+
+
+def ce(T=4, D=64, V=50, dtype=_lib.BF16, ignore=-100, piece=0):
+    return _lib.LinearCe(T, D, V, dtype, ignore, piece)
+
+
+def ce_calls(lib, p, ptr=0x1000, drop=None, ws=0x100000, short=0):
+    ref = ctypes.byref(p) if p else None
+    def ptrs(n):
+        return [None if i == drop else ptr for i in range(n)]
+    def size(which):
+        return max(0, lib.fbob_linear_ce_workspace_bytes(ref, which) - short) if p else 0
+    return (lib.fbob_linear_ce_fwd(ref, *ptrs(5), ws, size(0), None),
+            lib.fbob_linear_ce_bwd(ref, *ptrs(7), ws, size(1), None),
+            lib.fbob_linear_ce_bob(ref, *ptrs(10), ws, size(2), None))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INVALID), (dict(D=0), INVALID), (dict(V=0), INVALID), (dict(V=-5), INVALID), (dict(piece=-1), INVALID),
+    (dict(dtype=3), INVALID), (dict(T=2 ** 24 + 1), UNSUPPORTED), (dict(V=2 ** 24 + 1), UNSUPPORTED),
+    (dict(D=2 ** 20 + 1), UNSUPPORTED), (dict(T=2 ** 22, D=2 ** 19), UNSUPPORTED),
+])
+def test_linear_ce_descriptor_refusals(lib, kw, status):
+    assert ce_calls(lib, ce(**kw)) == (status,) * 3
+    assert lib.fbob_linear_ce_workspace_bytes(ctypes.byref(ce(**kw)), 1) == 0
+
+
+def test_linear_ce_pointer_and_workspace_refusals(lib):
+    assert ce_calls(lib, None) == (INVALID,) * 3
+    assert ce_calls(lib, ce(), ptr=0x1001) == (INVALID,) * 3
+    assert ce_calls(lib, ce(), ptr=0x1004) == (INVALID,) * 3   # W off 16 bytes, targets off 8
+    for drop in range(5):
+        assert ce_calls(lib, ce(), drop=drop) == (INVALID,) * 3
+    assert ce_calls(lib, ce(), ws=0) == (WORKSPACE,) * 3
+    assert ce_calls(lib, ce(), ws=0x100008) == (WORKSPACE,) * 3
+    assert ce_calls(lib, ce(), short=1) == (WORKSPACE,) * 3
+    assert lib.fbob_linear_ce_workspace_bytes(None, 0) == 0
+    assert lib.fbob_linear_ce_workspace_bytes(ctypes.byref(ce()), 3) == 0
+    # nothing asked for, nothing launched
+    x, ref = ctypes.c_void_p(0x1000), ctypes.byref(ce())
+    assert lib.fbob_linear_ce_bwd(ref, x, x, x, x, x, None, None, None, 0, None) == _lib.OK
+    assert lib.fbob_linear_ce_bob(ref, x, x, x, x, x, x, x, None, None, None, None, 0, None) == _lib.OK
+    assert lib.fbob_linear_ce_bob(ref, x, x, x, x, x, None, None, x, x, x, x, 0, None) == INVALID
+
+
+def test_linear_ce_workspace_is_bounded_by_the_piece(lib):
+    """The workspace holds a piece of the classes, not all of them."""
+    def need(**kw):
+        return lib.fbob_linear_ce_workspace_bytes(ctypes.byref(ce(**kw)), 1)
+    big = dict(T=65536, D=64, V=200000)
+    assert need(**big) < 65536 * 200000 * 2 / 20
+    assert need(piece=256, **big) < need(piece=4096, **big) < need(**big)
+
+
+def test_linear_ce_binding_refuses_shapes_and_types():
+    H, W, y = torch.zeros(3, 8), torch.zeros(5, 8), torch.zeros(3, dtype=torch.int64)
+    for h, w in ((H[0], W), (H, W[:, :4]), (H, W[0])):
+        with pytest.raises(ValueError):
+            fb.fbob_linear_ce_fwd(h, w, y)
+    with pytest.raises(ValueError):
+        fb.fbob_linear_ce_fwd(H, W, y)   # host tensors
+    with pytest.raises(TypeError):
+        fb.fbob_linear_ce_fwd(H.half(), W, y)
+    with pytest.raises(ValueError):
+        fb.linear_cross_entropy(H.t().contiguous().t(), W, y)
