@@ -13,9 +13,15 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import LinearCe, Norm, Rotary, RotaryHeads, _check, _ptr, load
+from ._lib import LinearCe, Norm, Rotary, RotaryHeads, _check, load
 
 DTYPES = {torch.bfloat16: _lib.BF16, torch.float32: _lib.FP32}
+
+
+# The stream handle itself, without a Stream object around it (a call of the
+# smallest sizes is bound by the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _dtype(t):
@@ -25,11 +31,19 @@ def _dtype(t):
         raise TypeError(f"unsupported dtype {t.dtype}") from None
 
 
-def _tensor(t, name, like, dtype, shape=None):
+def _device(t, name):
+    """The index of the CUDA device that the call runs on."""
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
+        raise ValueError(f"{name}: all tensors must be on the same CUDA device")
+    return index
+
+
+def _tensor(t, name, index, dtype, shape=None):
     """Check one contiguous tensor argument (None passes)."""
     if t is None:
         return
-    if not t.is_cuda or t.device != like.device:
+    if t.get_device() != index:
         raise ValueError(f"{name}: all tensors must be on the same CUDA device")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -39,18 +53,19 @@ def _tensor(t, name, like, dtype, shape=None):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _run(entry, like, stream, *args):
-    """Call a launching entry point with ``like``'s device current."""
-    fn = getattr(load(), entry)
-    if torch.cuda.current_device() == like.device.index:
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        _check(fn(*args, ctypes.c_void_p(stream.cuda_stream)))
-        return
-    with torch.cuda.device(like.device):
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        _check(fn(*args, ctypes.c_void_p(stream.cuda_stream)))
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(fn, index, stream, *args):
+    """Call a launching entry point with device ``index`` current."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
 
 
 def _new(like, shape, dtype, stream):
@@ -62,6 +77,14 @@ def _new(like, shape, dtype, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _out(given, name, like, index, shape, dtype, stream):
+    """The given output, checked, or a new one."""
+    if given is None:
+        return _new(like, shape, dtype, stream)
+    _tensor(given, name, index, dtype, shape)
+    return given
+
+
 # --- rotary positions -----------------------------------------------------------------------------
 
 def fbob_rotary_frequencies(rotary: Rotary) -> list:
@@ -71,15 +94,30 @@ def fbob_rotary_frequencies(rotary: Rotary) -> list:
     return list(out)
 
 
-def _heads(t, name, like):
+def _heads(t, name, like, index):
     if t.dim() != 4:
         raise ValueError(f"{name} must be [B, H, N, d]")
-    if not t.is_cuda or t.device != like.device:
+    if t.get_device() != index:
         raise ValueError(f"{name}: all tensors must be on the same CUDA device")
     if t.dtype != like.dtype:
         raise TypeError(f"{name}: expected {like.dtype}, got {t.dtype}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] > 1:
         raise ValueError(f"{name}: the columns of a head must be contiguous")
+    return st[:3]
+
+
+def _rotary_side(x, y, name, like, index, stream):
+    """(description for the library, output) of one tensor."""
+    xs, shape = _heads(x, name, like, index), x.shape
+    if y is None:
+        y = _new(like, shape, like.dtype, stream)
+        ys = y.stride()[:3]
+    else:
+        ys = _heads(y, name + "o", like, index)
+        if y.shape != shape:
+            raise ValueError(f"{name}o: expected shape {tuple(shape)}, got {tuple(y.shape)}")
+    return RotaryHeads(x.data_ptr(), y.data_ptr(), shape[1], xs, ys), y
 
 
 def fbob_rotary_apply(rotary, Q, K=None, positions=None, offset=0, transpose=False, Qo=None, Ko=None, stream=None):
@@ -88,39 +126,36 @@ def fbob_rotary_apply(rotary, Q, K=None, positions=None, offset=0, transpose=Fal
     [B, H, N, d] if not given.  ``positions``: int32 or int64, [N] or [B, N],
     added to ``offset``; without them token n has position offset + n.
     ``transpose``: the map's transpose (gradients)."""
-    _heads(Q, "Q", Q)
-    dt = _dtype(Q)
-    B, H, N, d = Q.shape
-    pairs = [("Q", Q, _new(Q, Q.shape, Q.dtype, stream) if Qo is None else Qo)]
-    if K is not None:
-        _heads(K, "K", Q)
-        if K.shape[0] != B or K.shape[2:] != Q.shape[2:]:
+    if Q.dim() != 4:
+        raise ValueError("Q must be [B, H, N, d]")
+    dt, index = _dtype(Q), _device(Q, "Q")
+    B, _, N, d = Q.shape
+    side, Qo = _rotary_side(Q, Qo, "Q", Q, index, stream)
+    if K is None:
+        if Ko is not None:
+            raise ValueError("Ko without K")
+        sides, count = (RotaryHeads * 1)(side), 1
+    else:
+        if K.dim() != 4 or K.shape[0] != B or K.shape[2] != N or K.shape[3] != d:
             raise ValueError(f"K: expected shape ({B}, Hk, {N}, {d}), got {tuple(K.shape)}")
-        pairs.append(("K", K, _new(Q, K.shape, Q.dtype, stream) if Ko is None else Ko))
-    elif Ko is not None:
-        raise ValueError("Ko without K")
-    t = (RotaryHeads * len(pairs))()
-    for e, (name, x, y) in zip(t, pairs):
-        _heads(y, name + "o", Q)
-        if y.shape != x.shape:
-            raise ValueError(f"{name}o: expected shape {tuple(x.shape)}, got {tuple(y.shape)}")
-        e.x, e.y, e.H = x.data_ptr(), y.data_ptr(), x.shape[1]
-        e.x_stride[:], e.y_stride[:] = x.stride()[:3], y.stride()[:3]
-    size, step = 0, 0
+        other, Ko = _rotary_side(K, Ko, "K", Q, index, stream)
+        sides, count = (RotaryHeads * 2)(side, other), 2
+    at, size, step = None, 0, 0
     if positions is not None:
         if positions.dtype not in (torch.int32, torch.int64):
             raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-        if not positions.is_cuda or positions.device != Q.device:
+        if positions.get_device() != index:
             raise ValueError("positions: all tensors must be on the same CUDA device")
-        if tuple(positions.shape) not in ((N,), (B, N)):
+        if positions.shape != (N,) and positions.shape != (B, N):
             raise ValueError(f"positions: expected shape ({N},) or ({B}, {N}), got {tuple(positions.shape)}")
-        if N > 1 and positions.stride(-1) != 1:
+        st = positions.stride()
+        if st[-1] != 1 and N > 1:
             raise ValueError("positions must be contiguous")
-        size = positions.element_size()
-        step = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    _run("fbob_rotary_apply", Q, stream, ctypes.byref(rotary), B, N, d, dt, t, len(pairs), _ptr(positions), size, step,
-         int(offset), int(bool(transpose)))
-    return pairs[0][2] if K is None else (pairs[0][2], pairs[1][2])
+        at, size = positions.data_ptr(), positions.element_size()
+        step = st[0] if len(st) == 2 and B > 1 else 0
+    _run(load().fbob_rotary_apply, index, stream, rotary, B, N, d, dt, sides, count, at, size, step, int(offset),
+         int(bool(transpose)))
+    return Qo if K is None else (Qo, Ko)
 
 
 # --- layer norm -----------------------------------------------------------------------------------
@@ -145,39 +180,44 @@ def _weight_dtype(x, *ws):
     return x.dtype
 
 
-def _norm_workspace(p, x, need, workspace, stream):
+def _floats(workspace, need, x, index, stream):
+    """(pointer, bytes) of the given fp32 workspace or of a new one."""
     if workspace is None:
-        workspace = _new(x, (max(1, need) + 3) // 4, torch.float32, stream)
-    _tensor(workspace, "workspace", x, torch.float32)
-    return workspace
+        if need == 0:
+            return None, 0, None
+        workspace = _new(x, ((need + 3) // 4,), torch.float32, stream)
+    else:
+        _tensor(workspace, "workspace", index, torch.float32)
+    return workspace.data_ptr(), workspace.numel() * 4, workspace
 
 
 def fbob_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None, stream=None):
     """(y, mean, rstd) = layer norm over the last dimension of x (contiguous,
     any leading shape); mean and rstd are fp32 of the leading shape."""
     wt = _weight_dtype(x, weight, bias)
-    p = norm_for(x, wt, eps)
-    _tensor(x, "x", x, x.dtype)
-    _tensor(weight, "weight", x, wt, x.shape[-1:])
-    _tensor(bias, "bias", x, wt, x.shape[-1:])
-    y = _new(x, x.shape, x.dtype, stream) if y is None else y
-    mean = _new(x, x.shape[:-1], torch.float32, stream) if mean is None else mean
-    rstd = _new(x, x.shape[:-1], torch.float32, stream) if rstd is None else rstd
-    _tensor(y, "y", x, x.dtype, x.shape)
-    _tensor(mean, "mean", x, torch.float32, x.shape[:-1])
-    _tensor(rstd, "rstd", x, torch.float32, x.shape[:-1])
-    _run("fbob_layer_norm_fwd", x, stream, ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean),
-         _ptr(rstd))
+    p, index = norm_for(x, wt, eps), _device(x, "x")
+    shape = x.shape
+    rows, cols = shape[:-1], shape[-1:]
+    _tensor(x, "x", index, x.dtype)
+    _tensor(weight, "weight", index, wt, cols)
+    _tensor(bias, "bias", index, wt, cols)
+    y = _out(y, "y", x, index, shape, x.dtype, stream)
+    mean = _out(mean, "mean", x, index, rows, torch.float32, stream)
+    rstd = _out(rstd, "rstd", x, index, rows, torch.float32, stream)
+    _run(load().fbob_layer_norm_fwd, index, stream, p, x.data_ptr(), _p(weight), _p(bias), y.data_ptr(),
+         mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
 
 
-def _norm_common(x, weight, mean, rstd, dy):
-    _tensor(x, "x", x, x.dtype)
-    _tensor(mean, "mean", x, torch.float32, x.shape[:-1])
-    _tensor(rstd, "rstd", x, torch.float32, x.shape[:-1])
-    _tensor(dy, "dy", x, x.dtype, x.shape)
+def _norm_common(x, weight, mean, rstd, dy, index):
+    shape = x.shape
+    _tensor(x, "x", index, x.dtype)
+    _tensor(mean, "mean", index, torch.float32, shape[:-1])
+    _tensor(rstd, "rstd", index, torch.float32, shape[:-1])
+    _tensor(dy, "dy", index, x.dtype, shape)
     if weight is not None:
-        _tensor(weight, "weight", x, weight.dtype, x.shape[-1:])
+        _tensor(weight, "weight", index, weight.dtype, shape[-1:])
+    return shape, shape[-1:]
 
 
 def fbob_layer_norm_bwd(x, weight, mean, rstd, dy, dx=None, dw=None, db=None, want=(True, True, True),
@@ -186,21 +226,18 @@ def fbob_layer_norm_bwd(x, weight, mean, rstd, dy, dx=None, dw=None, db=None, wa
     (the others are None).  dw needs ``weight``; without one db has
     ``bias_dtype`` (default: x's)."""
     wt = weight.dtype if weight is not None else bias_dtype or x.dtype
-    p = norm_for(x, wt)
-    _norm_common(x, weight, mean, rstd, dy)
+    p, index = norm_for(x, wt), _device(x, "x")
+    shape, cols = _norm_common(x, weight, mean, rstd, dy, index)
     want = (want[0], want[1] and weight is not None, want[2])
-    dx = (_new(x, x.shape, x.dtype, stream) if dx is None else dx) if want[0] else None
-    dw = (_new(x, x.shape[-1:], wt, stream) if dw is None else dw) if want[1] else None
-    db = (_new(x, x.shape[-1:], wt, stream) if db is None else db) if want[2] else None
-    _tensor(dx, "dx", x, x.dtype, x.shape)
-    _tensor(dw, "dw", x, wt, x.shape[-1:])
-    _tensor(db, "db", x, wt, x.shape[-1:])
-    need = 0
+    dx = _out(dx, "dx", x, index, shape, x.dtype, stream) if want[0] else None
+    dw = _out(dw, "dw", x, index, cols, wt, stream) if want[1] else None
+    db = _out(db, "db", x, index, cols, wt, stream) if want[2] else None
+    lib, need = load(), 0
     if want[1] or want[2]:
-        need = fbob_layer_norm_workspace_bytes(p) // (1 if want[1] and want[2] else 2)
-    workspace = _norm_workspace(p, x, need, workspace, stream)
-    _run("fbob_layer_norm_bwd", x, stream, ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy),
-         _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace), ctypes.c_size_t(workspace.numel() * 4))
+        need = lib.fbob_layer_norm_workspace_bytes(p) // (1 if want[1] and want[2] else 2)
+    at, size, workspace = _floats(workspace, need, x, index, stream)
+    _run(lib.fbob_layer_norm_bwd, index, stream, p, x.data_ptr(), _p(weight), mean.data_ptr(), rstd.data_ptr(),
+         dy.data_ptr(), _p(dx), _p(dw), _p(db), at, size)
     return dx, dw, db
 
 
@@ -209,22 +246,20 @@ def fbob_layer_norm_bob(x, weight, mean, rstd, dy, ux, uw=None, ub=None, gx=None
     """(gx, gw, gdy) = the vector-Jacobian product of layer norm's backward
     along (ux, uw, ub); ``want`` says which to compute.  gw needs ``weight``."""
     wt = _weight_dtype(x, weight, uw, ub)
-    p = norm_for(x, wt)
-    _norm_common(x, weight, mean, rstd, dy)
-    _tensor(ux, "ux", x, x.dtype, x.shape)
-    _tensor(uw, "uw", x, wt, x.shape[-1:])
-    _tensor(ub, "ub", x, wt, x.shape[-1:])
+    p, index = norm_for(x, wt), _device(x, "x")
+    shape, cols = _norm_common(x, weight, mean, rstd, dy, index)
+    _tensor(ux, "ux", index, x.dtype, shape)
+    _tensor(uw, "uw", index, wt, cols)
+    _tensor(ub, "ub", index, wt, cols)
     want = (want[0], want[1] and weight is not None, want[2])
-    gx = (_new(x, x.shape, x.dtype, stream) if gx is None else gx) if want[0] else None
-    gw = (_new(x, x.shape[-1:], wt, stream) if gw is None else gw) if want[1] else None
-    gdy = (_new(x, x.shape, x.dtype, stream) if gdy is None else gdy) if want[2] else None
-    _tensor(gx, "gx", x, x.dtype, x.shape)
-    _tensor(gw, "gw", x, wt, x.shape[-1:])
-    _tensor(gdy, "gdy", x, x.dtype, x.shape)
-    workspace = _norm_workspace(p, x, fbob_layer_norm_workspace_bytes(p) // 2 if want[1] else 0, workspace, stream)
-    _run("fbob_layer_norm_bob", x, stream, ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy),
-         _ptr(ux), _ptr(uw), _ptr(ub), _ptr(gx), _ptr(gw), _ptr(gdy), _ptr(workspace),
-         ctypes.c_size_t(workspace.numel() * 4))
+    gx = _out(gx, "gx", x, index, shape, x.dtype, stream) if want[0] else None
+    gw = _out(gw, "gw", x, index, cols, wt, stream) if want[1] else None
+    gdy = _out(gdy, "gdy", x, index, shape, x.dtype, stream) if want[2] else None
+    lib = load()
+    need = lib.fbob_layer_norm_workspace_bytes(p) // 2 if want[1] else 0
+    at, size, workspace = _floats(workspace, need, x, index, stream)
+    _run(lib.fbob_layer_norm_bob, index, stream, p, x.data_ptr(), _p(weight), mean.data_ptr(), rstd.data_ptr(),
+         dy.data_ptr(), ux.data_ptr(), _p(uw), _p(ub), _p(gx), _p(gw), _p(gdy), at, size)
     return gx, gw, gdy
 
 
@@ -233,9 +268,10 @@ def fbob_layer_norm_bob(x, weight, mean, rstd, dy, ux, uw=None, ub=None, gx=None
 def linear_ce_for(H: torch.Tensor, W: torch.Tensor, ignore_index: int = -100, piece: int = 0) -> LinearCe:
     if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1]:
         raise ValueError(f"H [T, D] and W [V, D] are needed, got {tuple(H.shape)} and {tuple(W.shape)}")
-    if max(H.shape[0], W.shape[0], W.shape[1]) > 2 ** 31 - 1:
+    (T, D), V = H.shape, W.shape[0]
+    if max(T, D, V) > 2 ** 31 - 1:
         raise ValueError("sizes must fit 32 bits")
-    return LinearCe(H.shape[0], H.shape[1], W.shape[0], _dtype(H), int(ignore_index), int(piece))
+    return LinearCe(T, D, V, _dtype(H), int(ignore_index), int(piece))
 
 
 def fbob_linear_ce_workspace_bytes(p: LinearCe, which: int) -> int:
@@ -244,32 +280,34 @@ def fbob_linear_ce_workspace_bytes(p: LinearCe, which: int) -> int:
 
 
 def _ce_common(H, W, target, lse=None, g=None):
-    _tensor(H, "H", H, H.dtype)
-    _tensor(W, "W", H, H.dtype)
-    _tensor(target, "target", H, torch.int64, H.shape[:1])
-    _tensor(lse, "lse", H, torch.float32, H.shape[:1])
-    _tensor(g, "g", H, torch.float32, H.shape[:1])
+    index, rows = _device(H, "H"), H.shape[:1]
+    _tensor(H, "H", index, H.dtype)
+    _tensor(W, "W", index, H.dtype)
+    _tensor(target, "target", index, torch.int64, rows)
+    _tensor(lse, "lse", index, torch.float32, rows)
+    _tensor(g, "g", index, torch.float32, rows)
+    return index, rows
 
 
-def _ce_workspace(p, which, H, workspace, stream):
+def _bytes(p, which, workspace, H, index, stream):
+    """(pointer, bytes) of the given uint8 workspace or of a new one."""
     if workspace is None:
-        workspace = _new(H, (fbob_linear_ce_workspace_bytes(p, which),), torch.uint8, stream)
-    _tensor(workspace, "workspace", H, torch.uint8)
-    return workspace, ctypes.c_size_t(workspace.numel())
+        workspace = _new(H, (load().fbob_linear_ce_workspace_bytes(p, which),), torch.uint8, stream)
+    else:
+        _tensor(workspace, "workspace", index, torch.uint8)
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 def fbob_linear_ce_fwd(H, W, target, ignore_index=-100, loss=None, lse=None, workspace=None, stream=None):
     """(loss, lse) [T] fp32 of the tokens H [T, D] under logits H W^T, W [V, D];
     target [T] int64.  ``workspace``: uint8."""
     p = linear_ce_for(H, W, ignore_index)
-    _ce_common(H, W, target)
-    loss = _new(H, H.shape[:1], torch.float32, stream) if loss is None else loss
-    lse = _new(H, H.shape[:1], torch.float32, stream) if lse is None else lse
-    _tensor(loss, "loss", H, torch.float32, H.shape[:1])
-    _tensor(lse, "lse", H, torch.float32, H.shape[:1])
-    workspace, size = _ce_workspace(p, 0, H, workspace, stream)
-    _run("fbob_linear_ce_fwd", H, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(target), _ptr(loss), _ptr(lse),
-         _ptr(workspace), size)
+    index, rows = _ce_common(H, W, target)
+    loss = _out(loss, "loss", H, index, rows, torch.float32, stream)
+    lse = _out(lse, "lse", H, index, rows, torch.float32, stream)
+    at, size, workspace = _bytes(p, 0, workspace, H, index, stream)
+    _run(load().fbob_linear_ce_fwd, index, stream, p, H.data_ptr(), W.data_ptr(), target.data_ptr(), loss.data_ptr(),
+         lse.data_ptr(), at, size)
     return loss, lse
 
 
@@ -278,14 +316,12 @@ def fbob_linear_ce_bwd(H, W, target, lse, g, ignore_index=-100, piece=0, dH=None
     """(dH, dW) of sum_t g_t loss_t; ``want`` says which to compute.  ``piece``:
     classes whose gradient is held at once (0: chosen by the library)."""
     p = linear_ce_for(H, W, ignore_index, piece)
-    _ce_common(H, W, target, lse, g)
-    dH = (_new(H, H.shape, H.dtype, stream) if dH is None else dH) if want[0] else None
-    dW = (_new(H, W.shape, H.dtype, stream) if dW is None else dW) if want[1] else None
-    _tensor(dH, "dH", H, H.dtype, H.shape)
-    _tensor(dW, "dW", H, H.dtype, W.shape)
-    workspace, size = _ce_workspace(p, 1, H, workspace, stream)
-    _run("fbob_linear_ce_bwd", H, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(target), _ptr(lse), _ptr(g), _ptr(dH),
-         _ptr(dW), _ptr(workspace), size)
+    index, _ = _ce_common(H, W, target, lse, g)
+    dH = _out(dH, "dH", H, index, H.shape, H.dtype, stream) if want[0] else None
+    dW = _out(dW, "dW", H, index, W.shape, H.dtype, stream) if want[1] else None
+    at, size, workspace = _bytes(p, 1, workspace, H, index, stream)
+    _run(load().fbob_linear_ce_bwd, index, stream, p, H.data_ptr(), W.data_ptr(), target.data_ptr(), lse.data_ptr(),
+         g.data_ptr(), _p(dH), _p(dW), at, size)
     return dH, dW
 
 
@@ -294,16 +330,13 @@ def fbob_linear_ce_bob(H, W, target, lse, g, UH, UW, ignore_index=-100, piece=0,
     """(gH, gW, gg) = the vector-Jacobian product of (H, W, g) -> (dH, dW)
     along (UH, UW), one of which may be None; ``want`` says which to compute."""
     p = linear_ce_for(H, W, ignore_index, piece)
-    _ce_common(H, W, target, lse, g)
-    _tensor(UH, "UH", H, H.dtype, H.shape)
-    _tensor(UW, "UW", H, H.dtype, W.shape)
-    gH = (_new(H, H.shape, H.dtype, stream) if gH is None else gH) if want[0] else None
-    gW = (_new(H, W.shape, H.dtype, stream) if gW is None else gW) if want[1] else None
-    gg = (_new(H, H.shape[:1], torch.float32, stream) if gg is None else gg) if want[2] else None
-    _tensor(gH, "gH", H, H.dtype, H.shape)
-    _tensor(gW, "gW", H, H.dtype, W.shape)
-    _tensor(gg, "gg", H, torch.float32, H.shape[:1])
-    workspace, size = _ce_workspace(p, 2, H, workspace, stream)
-    _run("fbob_linear_ce_bob", H, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(target), _ptr(lse), _ptr(g), _ptr(UH),
-         _ptr(UW), _ptr(gH), _ptr(gW), _ptr(gg), _ptr(workspace), size)
+    index, rows = _ce_common(H, W, target, lse, g)
+    _tensor(UH, "UH", index, H.dtype, H.shape)
+    _tensor(UW, "UW", index, H.dtype, W.shape)
+    gH = _out(gH, "gH", H, index, H.shape, H.dtype, stream) if want[0] else None
+    gW = _out(gW, "gW", H, index, W.shape, H.dtype, stream) if want[1] else None
+    gg = _out(gg, "gg", H, index, rows, torch.float32, stream) if want[2] else None
+    at, size, workspace = _bytes(p, 2, workspace, H, index, stream)
+    _run(load().fbob_linear_ce_bob, index, stream, p, H.data_ptr(), W.data_ptr(), target.data_ptr(), lse.data_ptr(),
+         g.data_ptr(), _p(UH), _p(UW), _p(gH), _p(gW), _p(gg), at, size)
     return gH, gW, gg

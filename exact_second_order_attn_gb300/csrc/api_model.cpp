@@ -62,6 +62,23 @@ double theta(const fbob_rotary* r, int i) {
   return t;
 }
 
+// Frequencies as 64-bit fractions of a turn.  The last description's are kept
+// per host thread (a model rotates with one description; the powers would
+// cost more than the launch).
+const unsigned long long* fixed_frequencies(const fbob_rotary* r) {
+  thread_local fbob_rotary last = {};
+  thread_local unsigned long long freq[fbob::kRotaryMaxPairs];
+  const bool same = last.rot == r->rot && last.scaling == r->scaling && last.base == r->base &&
+                    last.factor == r->factor && last.original == r->original && last.slow == r->slow &&
+                    last.fast == r->fast;
+  if (!same) {
+    for (int i = 0; i < r->rot / 2; ++i)  // a turn's fraction is below 2^-2, since theta <= 1
+      freq[i] = (unsigned long long)ldexp(theta(r, i) / (2.0 * M_PI), 64);
+    last = *r;
+  }
+  return freq;
+}
+
 // Whether no two elements of [B, H, N, d] with these strides (last one 1)
 // share an address: each stride, from the smallest, steps over all that the
 // smaller ones reach.
@@ -244,10 +261,7 @@ fbob_status fbob_rotary_apply(const fbob_rotary* r, int B, int N, int d, int dty
       o.ys[i] = size[i] > 1 ? t[k].y_stride[i] : 0;
     }
   }
-  for (int i = 0; i < r->rot / 2; ++i) {
-    const double turns = theta(r, i) / (2.0 * M_PI);  // below 2^-2, since theta <= 1
-    a.freq[i] = (unsigned long long)ldexp(turns, 64);
-  }
+  memcpy(a.freq, fixed_frequencies(r), sizeof(unsigned long long) * (r->rot / 2));
   a.positions = positions, a.pos_bytes = position_bytes, a.pos_stride = position_stride, a.offset = offset;
   a.B = B, a.N = N, a.d = d, a.rot = r->rot;
   a.interleaved = r->interleaved != 0, a.transpose = transpose != 0, a.bf16 = dtype == FBOB_BF16;

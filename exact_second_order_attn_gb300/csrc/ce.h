@@ -17,19 +17,21 @@ constexpr int kTileNDual = 128; // ... with two
 constexpr int kBK = 64;         // contraction per stage (128 bytes of bf16)
 constexpr int kPlanes = 3;      // bf16 terms that stand for one fp32 operand
 constexpr int kMaxMaps = 2 * kPlanes;
-constexpr int kMaxSegs = 18;
+constexpr int kMaxSegs = 2 * 6;
 
 // A product's operands: planes are bf16 matrices, a segment multiplies plane a
-// by plane b into accumulator acc.  The sum over the segments is the product.
+// by plane b; the sum over the segments is the product.  With two accumulators
+// a segment stands for z += a[a] b[b] and b += a[kPlanes + a] b[b] +
+// a[a] b[kPlanes + b] (each term only if its second-order operand is there).
 struct Seg {
-  uint8_t a, b, acc, pad;
+  uint8_t a, b;
 };
 
 // What becomes of an accumulator tile.
 enum Epilogue {
   kStats,   // row maxima and sums of exponentials per 128 columns, target logits
   kGrad,    // G = gs (p - onehot) as bf16 planes
-  kAlpha,   // (two accumulators z, b) row sums of p b, b at the target
+  kAlpha,   // (two accumulators z, b) row sums of p b
   kGrad2,   // (two accumulators) Z = gs p (b - alpha) and G, as bf16 planes
   kSlab,    // fp32, optionally added to what is there
   kOut      // scaled, in the output type
@@ -44,9 +46,8 @@ struct EpArgs {
   const float* alpha;     // [T]
   float2* part;           // kStats: (max, sum) [parts][T], two parts per tile of columns
   float* sums;            // kAlpha: row sums [parts][T], two parts per tile of columns
-  float* picked;          // [T]: z or b at the target
+  float* picked;          // kStats: [T], z at the target
   uint16_t* planes[2 * kPlanes];  // G planes [T][ld], then Z planes
-  int nplanes;            // per matrix
   long long ld;
   // kSlab, kOut
   void* out;
@@ -58,6 +59,8 @@ struct GemmArgs {
   CUtensorMap a[kMaxMaps], b[kMaxMaps];
   Seg seg[kMaxSegs];
   int nseg;
+  int fp32;             // operands stand for fp32 (kPlanes planes, sums kept to fp32)
+  int has_ua, has_ub;   // two accumulators: which second-order operands are there
   int K;                // contraction length
   int splits;           // K is cut into this many slabs (kSlab)
   int M, N;             // output rows and columns

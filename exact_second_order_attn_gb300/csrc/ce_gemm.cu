@@ -8,7 +8,15 @@
 // accumulator's 128 rows x 256 columns lie in the block's tensor memory, two
 // of them, so the epilogue of one tile runs under the products of the next.
 // The kernels with two accumulators (z and b of the second order) use 128
-// columns each.
+// columns each, and their stages hold both operands of both sides (48 KB for
+// three products of 128 x 128 x 64, the same traffic per product).
+//
+// bf16 operands: a tile's whole contraction is one chain in the accumulator.
+// The tensor cores drop the bits of a step's sum below the accumulator's last
+// one, an error that grows with the chain (4e-6 of the result at 32,000 terms),
+// too much for fp32 operands: there a chain ends after kChainBlocks stages of
+// each plane product and the epilogue threads add the chains up in registers,
+// rounding to nearest.
 //
 // Roles of a block's ten warps: 0-7 epilogue (thread = accumulator row, the two
 // warpgroups take half of the columns each), 8 TMA producer, 9 MMA issue (the
@@ -41,6 +49,7 @@ constexpr int kTmemCols = 512;
 constexpr int kBufCols = 256;     // accumulator columns per tile in flight
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kChainBlocks = 4;   // 256 columns of the contraction
 
 template <int EP>
 struct Cfg {
@@ -50,8 +59,8 @@ struct Cfg {
   static constexpr int BN = DUAL ? kTileNDual : kTileN;
   static constexpr int A_BYTES = 128 * kBK * 2;
   static constexpr int B_BYTES = BN / 2 * kBK * 2;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int NST = 196608 / STAGE;  // 6, or 8 with two accumulators
+  static constexpr int STAGE = (A_BYTES + B_BYTES) * (DUAL ? 2 : 1);  // [A | B], or [A | UA | B | UB]
+  static constexpr int NST = 196608 / STAGE;  // 6, or 4 with two accumulators
   static constexpr int SMEM = NST * STAGE;
   static_assert(SMEM + 1024 <= 232448, "shared memory budget");
 };
@@ -106,8 +115,10 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* r) {
 }
 
 // 32 values as bf16 planes: plane k holds the rounding of what planes 0..k-1 left.
-__device__ __forceinline__ void store_planes(uint16_t* const* planes, int n, size_t at, float* v) {
-  for (int k = 0; k < n; ++k) {
+template <bool FP32>
+__device__ __forceinline__ void store_planes(uint16_t* const* planes, size_t at, float* v) {
+#pragma unroll
+  for (int k = 0; k < (FP32 ? kPlanes : 1); ++k) {
     uint32_t w[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -122,21 +133,37 @@ __device__ __forceinline__ void store_planes(uint16_t* const* planes, int n, siz
   }
 }
 
-// The epilogue of one tile for this thread's row: `acc` is the TMEM address of
-// its first column (of accumulator 0), `row` the row in the output, n0 the
+// 32 columns of an accumulator, from tensor memory or from the registers in
+// which its chains were added up (c is then a constant: unrolled loops).
+template <bool FP32>
+struct Acc {
+  uint32_t tmem;
+  const float* sum;
+  __device__ __forceinline__ void load(int tmem_col, int at, float* v) const {
+    if constexpr (FP32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = sum[at + j];
+    } else {
+      __syncwarp();  // the load is warp-collective, the code between loads is not
+      tmem_ld32(tmem + tmem_col, v);
+    }
+  }
+};
+
+// The epilogue of one tile for this thread's row: `row` in the output, n0 the
 // first column, part the index of this half tile's row statistics.
-template <int EP>
-__device__ __forceinline__ void epilogue(const GemmArgs& p, uint32_t acc, int row, int n0, int part, int split) {
+template <int EP, bool FP32>
+__device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc, int row, int n0, int part, int split) {
+  constexpr int kUnroll = FP32 ? 4 : 1;
   const EpArgs& e = p.ep;
   const bool live = row < p.M;
   if constexpr (EP == kStats) {
     const int y = live ? e.target[row] - p.n_base : -1;
     float m = -INFINITY, s = 0.f;
-#pragma unroll 1
+#pragma unroll kUnroll
     for (int c = 0; c < 128; c += 32) {
       float v[32];
-      __syncwarp();  // the loads are warp-collective, the code between them is not
-      tmem_ld32(acc + c, v);
+      acc.load(c, c, v);
       const int n = n0 + c;
       if (y >= n && y < n + 32) {
 #pragma unroll
@@ -167,11 +194,10 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, uint32_t acc, int ro
     const int y = live ? e.target[row] : -1;
     const float at = y >= 0 ? e.lse[row] : 0.f, gm = *e.gmax;
     const float gs = y >= 0 && gm != 0.f ? e.g[row] / gm : 0.f;
-#pragma unroll 1
+#pragma unroll kUnroll
     for (int c = 0; c < 128; c += 32) {
       float v[32];
-      __syncwarp();  // the loads are warp-collective, the code between them is not
-      tmem_ld32(acc + c, v);
+      acc.load(c, c, v);
       const int n = n0 + c, hit = y - p.n_base - n;
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = y >= 0 ? gs * ex(v[j], at) : 0.f;
@@ -179,25 +205,18 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, uint32_t acc, int ro
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] -= j == hit ? gs : 0.f;
       }
-      if (live && n < e.ld) store_planes(e.planes, e.nplanes, (size_t)row * e.ld + n, v);
+      if (live && n < e.ld) store_planes<FP32>(e.planes, (size_t)row * e.ld + n, v);
     }
   } else if constexpr (EP == kAlpha) {
     const int y = live ? e.target[row] : -1;
     const float at = y >= 0 ? e.lse[row] : 0.f;
     float s = 0.f;
-#pragma unroll 1
+#pragma unroll kUnroll
     for (int c = 0; c < 64; c += 32) {
       float z[32], b[32];
-      __syncwarp();
-      tmem_ld32(acc + c, z);
-      tmem_ld32(acc + kTileNDual + c, b);
-      const int n = n0 + c, hit = y - p.n_base - n;
-      if (y >= 0 && hit >= 0 && hit < 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j == hit) e.picked[row] = b[j];
-        }
-      }
+      acc.load(c, c, z);
+      acc.load(kTileNDual + c, 64 + c, b);
+      const int n = n0 + c;
 #pragma unroll
       for (int j = 0; j < 32; ++j) s += n + j < p.N ? ex(z[j], at) * b[j] : 0.f;
     }
@@ -206,12 +225,11 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, uint32_t acc, int ro
     const int y = live ? e.target[row] : -1;
     const float at = y >= 0 ? e.lse[row] : 0.f, al = y >= 0 ? e.alpha[row] : 0.f, gm = *e.gmax;
     const float gs = y >= 0 && gm != 0.f ? e.g[row] / gm : 0.f;
-#pragma unroll 1
+#pragma unroll kUnroll
     for (int c = 0; c < 64; c += 32) {
       float z[32], b[32];
-      __syncwarp();
-      tmem_ld32(acc + c, z);
-      tmem_ld32(acc + kTileNDual + c, b);
+      acc.load(c, c, z);
+      acc.load(kTileNDual + c, 64 + c, b);
       const int n = n0 + c, hit = y - p.n_base - n;
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
@@ -223,17 +241,16 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, uint32_t acc, int ro
         for (int j = 0; j < 32; ++j) z[j] -= j == hit ? gs : 0.f;
       }
       if (live && n < e.ld) {
-        store_planes(e.planes, e.nplanes, (size_t)row * e.ld + n, z);
-        store_planes(e.planes + kPlanes, e.nplanes, (size_t)row * e.ld + n, b);
+        store_planes<FP32>(e.planes, (size_t)row * e.ld + n, z);
+        store_planes<FP32>(e.planes + kPlanes, (size_t)row * e.ld + n, b);
       }
     }
   } else if constexpr (EP == kSlab) {
     float* out = static_cast<float*>(e.out) + (size_t)split * e.slab + (size_t)row * e.out_ld;
-#pragma unroll 1
+#pragma unroll kUnroll
     for (int c = 0; c < 128; c += 32) {
       float v[32];
-      __syncwarp();  // the loads are warp-collective, the code between them is not
-      tmem_ld32(acc + c, v);
+      acc.load(c, c, v);
       const int n = n0 + c;
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {  // out_ld is a multiple of 4
@@ -251,11 +268,10 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, uint32_t acc, int ro
   } else {
     const float gm = *e.gmax;
     const size_t at = (size_t)row * e.out_ld;
-#pragma unroll 1
+#pragma unroll kUnroll
     for (int c = 0; c < 128; c += 32) {
       float v[32];
-      __syncwarp();  // the loads are warp-collective, the code between them is not
-      tmem_ld32(acc + c, v);
+      acc.load(c, c, v);
       const int n = n0 + c;
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= gm;
@@ -307,7 +323,7 @@ struct Tiles {
   __device__ __forceinline__ int k_first(int split) const { return (int)((long long)kb * split / splits); }
 };
 
-template <int EP>
+template <int EP, bool FP32>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs p) {
   using C = Cfg<EP>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -346,10 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   const Waiter wt{&ctrl.abort_flag, p.err, p.wait_ns};
   const bool live = ctrl.abort_flag == 0;
   const uint32_t sm0 = smem_u32(smem);
+  // the steps of K up to which an accumulator chain that starts at kc runs
+  auto chain_end = [](int kc, int k1) { return FP32 ? min(kc + kChainBlocks, k1) : k1; };
 
   if (warp == 8) {
     // ------------------------------------------------------------------ TMA
     if (live && (tid & 31) == 0) {
+      const uint32_t stage_bytes = 2 * (C::DUAL ? C::A_BYTES * (1 + p.has_ua) + C::B_BYTES * (1 + p.has_ub) : C::STAGE);
       long long it = 0;
       bool ok = true;
       for (long long t = pair; ok && t < total; t += pairs) {
@@ -357,27 +376,34 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         ts.at(t, m, n, split);
         const int row = m * kTileM + (int)rank * 128, col = n * C::BN + (int)rank * (C::BN / 2);
         const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
-        for (int s = 0; ok && s < p.nseg; ++s) {
-          const CUtensorMap* ma = &p.a[p.seg[s].a];
-          const CUtensorMap* mb = &p.b[p.seg[s].b];
-          for (int k = k0; k < k1; ++k, ++it) {
-            const int st = (int)(it % C::NST);
-            if (!(ok = wait_cluster(&ctrl.empty[st], ((it / C::NST) & 1) ^ 1, wt))) break;
-            if (p.stall && it == 0) continue;  // test hook: nothing fills the first stage
-            const uint32_t bar = map_rank(smem_u32(&ctrl.full[st]), 0);
-            if (rank == 0) mbar_arrive_expect_tx(&ctrl.full[st], 2 * C::STAGE);
-            const uint32_t da = sm0 + st * C::STAGE, db = da + C::A_BYTES;
-            if (C::A_MN) {
-              tma_load_2d_pair(da, ma, bar, row, k * kBK);
-              tma_load_2d_pair(da + 8192, ma, bar, row + 64, k * kBK);
-            } else {
-              tma_load_2d_pair(da, ma, bar, k * kBK, row);
-            }
-            if (C::B_MN) {
-              tma_load_2d_pair(db, mb, bar, col, p.b0 + k * kBK);
-              tma_load_2d_pair(db + 8192, mb, bar, col + 64, p.b0 + k * kBK);
-            } else {
-              tma_load_2d_pair(db, mb, bar, k * kBK, p.b0 + col);
+        for (int kc = k0; ok && kc < k1; kc = chain_end(kc, k1)) {
+          const int ke = chain_end(kc, k1);
+          for (int s = 0; ok && s < p.nseg; ++s) {
+            const CUtensorMap* ma = &p.a[p.seg[s].a];
+            const CUtensorMap* mb = &p.b[p.seg[s].b];
+            for (int k = kc; k < ke; ++k, ++it) {
+              const int st = (int)(it % C::NST);
+              if (!(ok = wait_cluster(&ctrl.empty[st], ((it / C::NST) & 1) ^ 1, wt))) break;
+              if (p.stall && it == 0) continue;  // test hook: nothing fills the first stage
+              const uint32_t bar = map_rank(smem_u32(&ctrl.full[st]), 0);
+              if (rank == 0) mbar_arrive_expect_tx(&ctrl.full[st], stage_bytes);
+              const uint32_t da = sm0 + st * C::STAGE, db = da + (C::DUAL ? 2 : 1) * C::A_BYTES;
+              if (C::A_MN) {
+                tma_load_2d_pair(da, ma, bar, row, k * kBK);
+                tma_load_2d_pair(da + 8192, ma, bar, row + 64, k * kBK);
+              } else {
+                tma_load_2d_pair(da, ma, bar, k * kBK, row);
+              }
+              if (C::B_MN) {
+                tma_load_2d_pair(db, mb, bar, col, p.b0 + k * kBK);
+                tma_load_2d_pair(db + 8192, mb, bar, col + 64, p.b0 + k * kBK);
+              } else {
+                tma_load_2d_pair(db, mb, bar, k * kBK, p.b0 + col);
+              }
+              if (C::DUAL) {
+                if (p.has_ua) tma_load_2d_pair(da + C::A_BYTES, ma + kPlanes, bar, k * kBK, row);
+                if (p.has_ub) tma_load_2d_pair(db + C::B_BYTES, mb + kPlanes, bar, k * kBK, p.b0 + col);
+              }
             }
           }
         }
@@ -403,33 +429,48 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
       constexpr uint32_t lbo_a = C::A_MN ? 8192 : 16, lbo_b = C::B_MN ? 8192 : 16;
       constexpr uint32_t step_a = C::A_MN ? 2048 >> 4 : 32 >> 4, step_b = C::B_MN ? 2048 >> 4 : 32 >> 4;
       long long it = 0;
-      int tile = 0;
+      int chain = 0;  // accumulator buffers handed to the epilogue so far
       bool ok = true;
-      for (long long t = pair; ok && t < total; t += pairs, ++tile) {
+      for (long long t = pair; ok && t < total; t += pairs) {
         int m, n, split;
         ts.at(t, m, n, split);
         const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
-        const int buf = tile & 1;
-        ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_empty[buf], ((tile >> 1) & 1) ^ 1, wt));
-        tc_fence_after();
-        uint32_t started = 0;  // accumulators that hold a product already
-        for (int s = 0; ok && s < p.nseg; ++s) {
-          const uint32_t acc = p.seg[s].acc, d = tb + buf * kBufCols + acc * kTileNDual;
-          for (int k = k0; k < k1; ++k, ++it) {
-            const int st = (int)(it % C::NST);
-            ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.full[st], (it / C::NST) & 1, wt));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t a = desc_lo(sm0 + st * C::STAGE, lbo_a);
-            const uint32_t b = desc_lo(sm0 + st * C::STAGE + C::A_BYTES, lbo_b);
+        for (int kc = k0; ok && kc < k1; kc = chain_end(kc, k1), ++chain) {
+          const int ke = chain_end(kc, k1), buf = chain & 1;
+          ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_empty[buf], ((chain >> 1) & 1) ^ 1, wt));
+          tc_fence_after();
+          const uint32_t d = tb + buf * kBufCols;
+          for (int s = 0; ok && s < p.nseg; ++s) {
+            for (int k = kc; k < ke; ++k, ++it) {
+              const int st = (int)(it % C::NST);
+              ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.full[st], (it / C::NST) & 1, wt));
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t more = s > 0 || k > kc;  // the accumulator holds a product already
+              const uint32_t a = desc_lo(sm0 + st * C::STAGE, lbo_a);
+              const uint32_t b = desc_lo(sm0 + st * C::STAGE + (C::DUAL ? 2 : 1) * C::A_BYTES, lbo_b);
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_ss_pair(d, a + kk * step_a, b + kk * step_b, id, kk > 0 ? 1u : (started >> acc) & 1u);
-            started |= 1u << acc;
-            mma_commit_pair(&ctrl.empty[st]);
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                mma_ss_pair(d, a + kk * step_a, b + kk * step_b, id, kk > 0 ? 1u : more);
+              if (C::DUAL) {
+                if (p.has_ua) {
+#pragma unroll
+                  for (int kk = 0; kk < kBK / 16; ++kk)
+                    mma_ss_pair(d + kTileNDual, a + (C::A_BYTES >> 4) + kk * step_a, b + kk * step_b, id,
+                                kk > 0 ? 1u : more);
+                }
+                if (p.has_ub) {
+#pragma unroll
+                  for (int kk = 0; kk < kBK / 16; ++kk)
+                    mma_ss_pair(d + kTileNDual, a + kk * step_a, b + (C::B_BYTES >> 4) + kk * step_b, id,
+                                kk > 0 ? 1u : more | p.has_ua);
+                }
+              }
+              mma_commit_pair(&ctrl.empty[st]);
+            }
           }
+          mma_commit_pair(&ctrl.tile_full[buf]);
         }
-        mma_commit_pair(&ctrl.tile_full[buf]);
       }
       mma_commit_pair(&ctrl.drain);  // the last MMA has read its operands
       mbar_wait_drain(&ctrl.drain, 0, kDrainNs);
@@ -439,20 +480,46 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const int half = warp >> 2, r = (warp & 3) * 32 + (tid & 31);
     const uint32_t lane = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t freed = map_rank(smem_u32(&ctrl.tile_empty[0]), 0);
-    int tile = 0;
-    for (long long t = pair; live && t < total; t += pairs, ++tile) {
+    int chain = 0;
+    bool ok = live;
+    for (long long t = pair; ok && t < total; t += pairs) {
       int m, n, split;
       ts.at(t, m, n, split);
-      const int buf = tile & 1;
-      // warp-uniform: the TMEM loads that follow are warp-collective
-      if (!__all_sync(0xffffffffu, wait_cluster(&ctrl.tile_full[buf], (tile >> 1) & 1, wt))) break;
-      tc_fence_after();
       constexpr int H = C::BN / 2;
-      epilogue<EP>(p, tb + lane + buf * kBufCols + half * H, m * kTileM + (int)rank * 128 + r, n * C::BN + half * H,
-                   2 * n + half, split);
-      tc_fence_before();
-      __syncwarp();
-      if ((tid & 31) == 0) mbar_arrive_cluster(freed + buf * 8);
+      const int row = m * kTileM + (int)rank * 128 + r, n0 = n * C::BN + half * H;
+      if constexpr (FP32) {
+        float sum[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+        const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
+        for (int kc = k0; kc < k1; kc = chain_end(kc, k1), ++chain) {
+          const int buf = chain & 1;
+          if (!(ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float v[32];
+            // two accumulators: 64 columns of each
+            tmem_ld32(tb + lane + buf * kBufCols + half * H + (C::DUAL ? (q >> 1) * kTileNDual + (q & 1) * 32 : q * 32), v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[q * 32 + j] += v[j];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if ((tid & 31) == 0) mbar_arrive_cluster(freed + buf * 8);
+        }
+        if (ok) epilogue<EP, true>(p, Acc<true>{0, sum}, row, n0, 2 * n + half, split);
+      } else {
+        const int buf = chain & 1;
+        // warp-uniform: the TMEM loads that follow are warp-collective
+        if (!(ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
+        tc_fence_after();
+        epilogue<EP, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr}, row, n0, 2 * n + half, split);
+        tc_fence_before();
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive_cluster(freed + buf * 8);
+        ++chain;
+      }
     }
   }
   __syncwarp();
@@ -465,10 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   }
 }
 
-template <int EP>
-cudaError_t launch(const GemmArgs& g, const char* name, cudaStream_t s) {
+template <int EP, bool FP32>
+cudaError_t launch_as(const GemmArgs& g, const char* name, cudaStream_t s) {
   using C = Cfg<EP>;
-  auto kernel = gemm_kernel<EP>;
+  auto kernel = gemm_kernel<EP, FP32>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((g.M + kTileM - 1) / kTileM) * ((g.N + C::BN - 1) / C::BN) * g.splits;
@@ -488,6 +555,11 @@ cudaError_t launch(const GemmArgs& g, const char* name, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, kernel, g);
   prof_end(s);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int EP>
+cudaError_t launch(const GemmArgs& g, const char* name, cudaStream_t s) {
+  return g.fp32 ? launch_as<EP, true>(g, name, s) : launch_as<EP, false>(g, name, s);
 }
 
 }  // namespace

@@ -95,7 +95,7 @@ Plan plan(const CeArgs& a, CePass pass) {
   p.uw = take(bob && p.copy_w, V * row);
   p.target = take(true, T * 4);
   p.gmax = take(true, 4);
-  p.picked = take(!bwd || bob, T * 4);
+  p.picked = take(!bwd, T * 4);
   p.part = take(!bwd, T * p.stat_parts * sizeof(float2));
   p.sums = take(bob, T * p.alpha_parts * 4);
   p.alpha = take(bob, T * 4);
@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(1024) gmax_kernel(const float* g, const long l
   }
 }
 
-// Sums over `parts` per-row partials, 32 rows per block and 8 (x 32 lanes)
-// threads per row: loss and lse (kStats), or alpha and gg (kAlpha).
+// Sums over `parts` per-row partials, 32 rows per block, 16 threads per row:
+// loss and lse (kStats), or alpha and gg (kAlpha).
 constexpr int kJoinRows = 32, kJoinWays = 16;
 
 __global__ void __launch_bounds__(kJoinRows* kJoinWays)
@@ -226,23 +226,44 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWays)
   loss[t] = y >= 0 ? l - picked[t] : y == -1 ? 0.f : NAN;
 }
 
+// alpha, and gg = alpha - b at the target, with b's row summed here in fp32
+// (one warp per token): out of the tensor cores' chain it would carry 1e-6.
+template <typename T>
 __global__ void __launch_bounds__(kJoinRows* kJoinWays)
-    join_alpha_kernel(const float* sums, int parts, const int* target, const float* picked, int T, float* alpha,
-                      float* gg) {
+    join_alpha_kernel(const float* sums, int parts, const int* target, const T* H, const T* W, const T* UH, const T* UW,
+                      int T_, int D, float* alpha, float* gg) {
   __shared__ float sh[kJoinWays][kJoinRows];
+  __shared__ float total[kJoinRows];
   const int t = blockIdx.x * kJoinRows + threadIdx.x;
   float s = 0.f;
-  if (t < T) {
-    for (int i = threadIdx.y; i < parts; i += kJoinWays) s += sums[(size_t)i * T + t];
+  if (t < T_) {
+    for (int i = threadIdx.y; i < parts; i += kJoinWays) s += sums[(size_t)i * T_ + t];
   }
   sh[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y != 0 || t >= T) return;
-  s = 0.f;
-  for (int w = 0; w < kJoinWays; ++w) s += sh[w][threadIdx.x];
-  const bool keep = target[t] >= 0;
-  alpha[t] = keep ? s : 0.f;
-  if (gg) gg[t] = keep ? s - picked[t] : 0.f;
+  if (threadIdx.y == 0) {
+    s = 0.f;
+    for (int w = 0; w < kJoinWays; ++w) s += sh[w][threadIdx.x];
+    total[threadIdx.x] = s;
+    if (t < T_) alpha[t] = target[t] >= 0 ? s : 0.f;
+  }
+  __syncthreads();
+  if (!gg) return;
+  for (int i = threadIdx.y; i < kJoinRows; i += kJoinWays) {
+    const int r = blockIdx.x * kJoinRows + i;
+    if (r >= T_) break;
+    const int y = target[r];
+    float b = 0.f;
+    if (y >= 0) {
+      for (int c = threadIdx.x; c < D; c += 32) {
+        if (UH) b += (float)UH[(size_t)r * D + c] * (float)W[(size_t)y * D + c];
+        if (UW) b += (float)H[(size_t)r * D + c] * (float)UW[(size_t)y * D + c];
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+    if (threadIdx.x == 0) gg[r] = y >= 0 ? total[i] - b : 0.f;
+  }
 }
 
 // out [T][D] = gmax * sum of the slabs [T][Dp]; zero in rows that are not counted.
@@ -339,7 +360,7 @@ struct Run {
   GemmArgs base() const {
     GemmArgs g;
     memset(&g, 0, sizeof(g));
-    g.splits = 1;
+    g.splits = 1, g.fp32 = !a.bf16;
     g.err = c.err, g.wait_ns = c.wait_ns, g.stall = c.stall;
     g.ep.target = at<int>(p.target), g.ep.lse = a.lse, g.ep.g = a.g, g.ep.gmax = at<float>(p.gmax);
     return g;
@@ -370,26 +391,21 @@ struct Run {
 
   // The products of planes of A operand `x` and B operand `y` (0 or 1 each),
   // smallest first.
-  void products(GemmArgs& g, int x, int y, int acc) const {
+  void products(GemmArgs& g, int x, int y) const {
     static const uint8_t order[6][2] = {{0, 2}, {1, 1}, {2, 0}, {0, 1}, {1, 0}, {0, 0}};
     for (int i = p.np == 1 ? 5 : 0; i < 6; ++i)
-      g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + order[i][0]), (uint8_t)(kPlanes * y + order[i][1]), (uint8_t)acc, 0};
+      g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + order[i][0]), (uint8_t)(kPlanes * y + order[i][1])};
   }
 
   // The logits (and, in the second order, b = UH W^T + H UW^T).
   bool logits(GemmArgs& g, bool dual) const {
     const int box = (dual ? kTileNDual : kTileN) / 2;
     if (!token_maps(g.a, p.h, 128) || !head_maps(g.b, a.W, p.w, box)) return false;
-    products(g, 0, 0, 0);
+    products(g, 0, 0);
     if (dual) {
-      if (a.UH) {
-        if (!token_maps(g.a + kPlanes, p.uh, 128)) return false;
-        products(g, 1, 0, 1);
-      }
-      if (a.UW) {
-        if (!head_maps(g.b + kPlanes, a.UW, p.uw, box)) return false;
-        products(g, 0, 1, 1);
-      }
+      if (a.UH && !token_maps(g.a + kPlanes, p.uh, 128)) return false;
+      if (a.UW && !head_maps(g.b + kPlanes, a.UW, p.uw, box)) return false;
+      g.has_ua = a.UH != nullptr, g.has_ub = a.UW != nullptr;
     }
     g.M = a.T, g.K = a.D;
     return true;
@@ -412,13 +428,19 @@ struct Run {
     GemmArgs g = base();
     if (!logits(g, true)) return cudaErrorInvalidValue;
     g.N = a.V;
-    g.ep.sums = at<float>(p.sums), g.ep.picked = at<float>(p.picked);
+    g.ep.sums = at<float>(p.sums);
     CE_TRY(gemm(kAlpha, g, s));
     prof_begin(s, "ce_join");
-    join_alpha_kernel<<<(a.T + kJoinRows - 1) / kJoinRows, dim3(kJoinRows, kJoinWays), 0, s>>>(
-        at<float>(p.sums), p.alpha_parts, at<int>(p.target), at<float>(p.picked), a.T, at<float>(p.alpha), a.gg);
+    if (a.bf16) join_alpha<__nv_bfloat16>();
+    else join_alpha<float>();
     prof_end(s);
     return cudaGetLastError();
+  }
+  template <typename E>
+  void join_alpha() const {
+    join_alpha_kernel<E><<<(a.T + kJoinRows - 1) / kJoinRows, dim3(kJoinRows, kJoinWays), 0, s>>>(
+        at<float>(p.sums), p.alpha_parts, at<int>(p.target), static_cast<const E*>(a.H), static_cast<const E*>(a.W),
+        static_cast<const E*>(a.UH), static_cast<const E*>(a.UW), a.T, a.D, at<float>(p.alpha), a.gg);
   }
 
   // One piece of the vocabulary: columns c0 .. c0 + cols - 1.
@@ -426,7 +448,7 @@ struct Run {
     GemmArgs g = base();
     if (!logits(g, second)) return cudaErrorInvalidValue;
     g.N = cols, g.n_base = g.b0 = c0;
-    g.ep.alpha = at<float>(p.alpha), g.ep.nplanes = p.np, g.ep.ld = p.ld;
+    g.ep.alpha = at<float>(p.alpha), g.ep.ld = p.ld;
     for (int k = 0; k < p.np; ++k) {
       g.ep.planes[k] = piece_plane(0, k);
       if (second) g.ep.planes[kPlanes + k] = piece_plane(1, k);
@@ -437,13 +459,13 @@ struct Run {
       if (!piece_maps(g.a, 0, cols, 128) || !head_maps(g.b, a.W, p.w, 64)) return cudaErrorInvalidValue;
       if (second) {
         if (!piece_maps(g.a + kPlanes, 1, cols, 128)) return cudaErrorInvalidValue;
-        products(g, 1, 0, 0);
+        products(g, 1, 0);
         if (a.UW) {
           if (!head_maps(g.b + kPlanes, a.UW, p.uw, 64)) return cudaErrorInvalidValue;
-          products(g, 0, 1, 0);
+          products(g, 0, 1);
         }
       } else {
-        products(g, 0, 0, 0);
+        products(g, 0, 0);
       }
       g.M = a.T, g.N = a.D, g.K = cols, g.b0 = c0, g.splits = p.splits;
       g.ep.out = at<float>(p.slab), g.ep.out_ld = p.Dp, g.ep.slab = (long long)a.T * p.Dp, g.ep.accumulate = !first;
@@ -454,13 +476,13 @@ struct Run {
       if (!piece_maps(g.a, 0, cols, 64) || !token_maps(g.b, p.h, 64)) return cudaErrorInvalidValue;
       if (second) {
         if (!piece_maps(g.a + kPlanes, 1, cols, 64)) return cudaErrorInvalidValue;
-        products(g, 1, 0, 0);
+        products(g, 1, 0);
         if (a.UH) {
           if (!token_maps(g.b + kPlanes, p.uh, 64)) return cudaErrorInvalidValue;
-          products(g, 0, 1, 0);
+          products(g, 0, 1);
         }
       } else {
-        products(g, 0, 0, 0);
+        products(g, 0, 0);
       }
       g.M = cols, g.N = a.D, g.K = a.T;
       g.ep.out = static_cast<char*>(a.dW) + (size_t)c0 * a.D * (a.bf16 ? 2 : 4);

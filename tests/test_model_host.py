@@ -178,7 +178,7 @@ def test_linear_ce_workspace_is_bounded_by_the_piece(lib):
         return lib.fbob_linear_ce_workspace_bytes(ctypes.byref(ce(**kw)), 1)
     big = dict(T=65536, D=64, V=200000)
     assert need(**big) < 65536 * 200000 * 2 / 20
-    assert need(piece=256, **big) < need(piece=4096, **big) < need(**big)
+    assert need(piece=256, **big) < need(piece=2048, **big) < need(**big)
 
 
 def test_linear_ce_binding_refuses_shapes_and_types():
