@@ -287,7 +287,9 @@ fbob_status fbob_layer_norm_fwd(const fbob_norm* p, const void* x, const void* w
   if ((st = check_args(ps, 6)) != FBOB_OK) return st;
   fbob::NormArgs a = norm_args(p);
   a.x = x, a.w = w, a.b = b, a.y = y, a.mean = mean, a.rstd = rstd;
-  const cudaError_t e = fbob::layer_norm_fwd(a, stream);
+  fbob::DevCtx c;
+  if ((st = fbob::make_ctx(&c)) != FBOB_OK) return st;
+  const cudaError_t e = fbob::layer_norm_fwd(a, c, stream);
   if (e != cudaSuccess) return cuda_fail(e, "layer_norm_fwd launch");
   return FBOB_OK;
 }
@@ -312,7 +314,9 @@ fbob_status fbob_layer_norm_bwd(const fbob_norm* p, const void* x, const void* w
   fbob::NormArgs a = norm_args(p);
   a.x = x, a.w = w, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd), a.dy = dy;
   a.dx = dx, a.dw = dw, a.db = db, a.ws = workspace;
-  const cudaError_t e = fbob::layer_norm_bwd(a, stream);
+  fbob::DevCtx c;
+  if ((st = fbob::make_ctx(&c)) != FBOB_OK) return st;
+  const cudaError_t e = fbob::layer_norm_bwd(a, c, stream);
   if (e != cudaSuccess) return cuda_fail(e, "layer_norm_bwd launch");
   return FBOB_OK;
 }
@@ -336,7 +340,9 @@ fbob_status fbob_layer_norm_bob(const fbob_norm* p, const void* x, const void* w
   fbob::NormArgs a = norm_args(p);
   a.x = x, a.w = w, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd), a.dy = dy;
   a.ux = ux, a.uw = uw, a.ub = ub, a.gx = gx, a.gw = gw, a.gdy = gdy, a.ws = workspace;
-  const cudaError_t e = fbob::layer_norm_bob(a, stream);
+  fbob::DevCtx c;
+  if ((st = fbob::make_ctx(&c)) != FBOB_OK) return st;
+  const cudaError_t e = fbob::layer_norm_bob(a, c, stream);
   if (e != cudaSuccess) return cuda_fail(e, "layer_norm_bob launch");
   return FBOB_OK;
 }

@@ -110,9 +110,9 @@ cudaError_t tc_bob_cols_wide(const BobArgs& a, const DevCtx& c, cudaStream_t s);
 
 // rotary.cu, layer_norm_*.cu
 cudaError_t rotary(const RotaryArgs& a, cudaStream_t s);
-cudaError_t layer_norm_fwd(const NormArgs& a, cudaStream_t s);
-cudaError_t layer_norm_bwd(const NormArgs& a, cudaStream_t s);
-cudaError_t layer_norm_bob(const NormArgs& a, cudaStream_t s);
+cudaError_t layer_norm_fwd(const NormArgs& a, const DevCtx& c, cudaStream_t s);
+cudaError_t layer_norm_bwd(const NormArgs& a, const DevCtx& c, cudaStream_t s);
+cudaError_t layer_norm_bob(const NormArgs& a, const DevCtx& c, cudaStream_t s);
 size_t layer_norm_workspace_floats(long long rows, int D);  // of bwd (bob needs half)
 
 // linear_ce.cu

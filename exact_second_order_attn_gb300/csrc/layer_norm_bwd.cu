@@ -12,64 +12,107 @@ namespace fbob {
 namespace ln {
 namespace {
 
-template <typename T, typename WT, int VEC, int E, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : kWarps * 32)
+template <typename T, typename WT, int VEC, int E, int OWN, bool EVEN>
+__global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
     bwd_kernel(const T* x, const WT* w, const float* mean, const float* rstd, const T* dy, T* dx, float* dw_parts,
-               float* db_parts, long long rows, int D) {
-  extern __shared__ float sh[];
-  const Cols<VEC, E, BLOCK> c;
-  const long long step = BLOCK ? gridDim.x : (long long)gridDim.x * kWarps;
+               float* db_parts, long long rows, int D, int period, int stages, unsigned int* err,
+               unsigned long long wait_ns) {
+  constexpr int R = kRows<T, E, 2>, U = kUnits<VEC>;
+  using G = Ring<T, 2, R, VEC, OWN, EVEN>;
+  extern __shared__ __align__(16) char dyn[];
+  __shared__ typename G::Bars bars;
+  const T* const tensors[] = {x, dy};
+  char* const slots = dyn + (kStaged<OWN> && VEC > 1 && w ? Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0);
+  const G ring(tensors, rows, D, period, stages, slots, bars);
+  const Cols<VEC, E, OWN, EVEN> c(D, VEC == 1 ? 0 : ring.shift());
+  char* free = dyn;
+  const Weights<WT, VEC, E, OWN, EVEN> ww(w, free, c);
+  __syncthreads();
   const float inv = 1.f / (float)D;
-  float dw[E] = {}, db[E] = {};
-  for (long long r = BLOCK ? blockIdx.x : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows; r += step) {
-    Raw<T, VEC> vx[c.NV], vd[c.NV];
+  int flip = 0;
+  Unit<VEC> dw[c.NV][U], db[c.NV][U];
 #pragma unroll
-    for (int i = 0; i < c.NV; ++i) {
-      if (c.at(i) < D) {
-        vx[i].load(x + r * D + c.at(i));
-        vd[i].load(dy + r * D + c.at(i));
-      }
+  for (int i = 0; i < c.NV; ++i) {
+#pragma unroll
+    for (int e = 0; e < U; ++e) dw[i][e] = db[i][e] = all<VEC>(0.f);
+  }
+  float mu_next[R], rs_next[R];  // the rows' statistics, read one step ahead
+  auto statistics = [&](long long first) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const long long at = first + j * ring.period;
+      mu_next[j] = at < rows ? mean[at] : 0.f;
+      rs_next[j] = at < rows ? rstd[at] : 0.f;
     }
-    const float mu = mean[r], rs = rstd[r];
-    float s[2] = {0.f, 0.f};  // sums of a, a xh
+  };
+  long long r = ring.first;
+  statistics(r);
+  for (int k = 0; r < rows; ++k, r += ring.step) {
+    float mu[R], rs[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) mu[j] = mu_next[j], rs[j] = rs_next[j];
+    statistics(r + ring.step);
+    Raw<T, VEC> vx[R][c.NV], vd[R][c.NV];
+    if (!ring.wait(k, r, err, wait_ns)) return;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      ring.template read<E>(k, r, j, 0, vx[j], c);
+      ring.template read<E>(k, r, j, 1, vd[j], c);
+    }
+    if (OWN == kWarp) {
+      __syncwarp();  // the whole warp has read its slots
+      ring.fill(k + stages, r + stages * ring.step);
+    }
+    // columns outside the row hold dy = 0, so every term there is zero
+    float s[2 * R];  // sums of a, a xh
+    Unit<VEC> sa[R], sx[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) sa[j] = sx[j] = all<VEC>(0.f);
 #pragma unroll
     for (int i = 0; i < c.NV; ++i) {
-      if (c.at(i) < D) {
-        Raw<WT, VEC> q;
-        if (w) q.load(w + c.at(i));
+      if (!c.any(i)) continue;
+      Unit<VEC> q[U];
+      ww.load(i, q, 1.f, c);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (vx[i].get(j) - mu) * rs, g = vd[i].get(j);
-          const float a = w ? g * q.get(j) : g;
-          s[0] += a;
-          s[1] += a * xh;
-          dw[i * VEC + j] += g * xh;
-          db[i * VEC + j] += g;
+      for (int j = 0; j < R; ++j) {
+        const Unit<VEC> m = all<VEC>(-mu[j]), ir = all<VEC>(rs[j]);
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          const Unit<VEC> xh = (vx[j][i].unit(e) + m) * ir, g = vd[j][i].unit(e), a = g * q[e];
+          sa[j] = sa[j] + a;
+          sx[j] = mad(a, xh, sx[j]);
+          dw[i][e] = mad(g, xh, dw[i][e]);
+          db[i][e] = db[i][e] + g;
         }
       }
     }
-    row_sum<2, BLOCK>(s);
-    const float ma = s[0] * inv, max_ = s[1] * inv;
-    if (dx) {
 #pragma unroll
-      for (int i = 0; i < c.NV; ++i) {
-        if (c.at(i) < D) {
-          Raw<WT, VEC> q;
-          if (w) q.load(w + c.at(i));
-          float o[VEC];
+    for (int j = 0; j < R; ++j) s[2 * j] = total(sa[j]), s[2 * j + 1] = total(sx[j]);
+    row_sum<2 * R, OWN>(s, flip);
+    if (OWN != kWarp) ring.fill(k + stages, r + stages * ring.step);  // the sum's barrier followed every read
+    if (!dx) continue;
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float xh = (vx[i].get(j) - mu) * rs, g = vd[i].get(j);
-            o[j] = rs * ((w ? g * q.get(j) : g) - ma - xh * max_);
-          }
-          vd[i].set(o);
-          vd[i].store(dx + r * D + c.at(i));
+    for (int i = 0; i < c.NV; ++i) {
+      if (!c.any(i)) continue;
+      Unit<VEC> q[U];
+      ww.load(i, q, 1.f, c);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        vx[j][i].renew(), vd[j][i].renew();
+        const Unit<VEC> m = all<VEC>(-mu[j]), ir = all<VEC>(rs[j]);
+        const Unit<VEC> ma = all<VEC>(-s[2 * j] * inv), max_ = all<VEC>(-s[2 * j + 1] * inv);
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          const Unit<VEC> xh = (vx[j][i].unit(e) + m) * ir;
+          vd[j][i].put(e, ir * mad(xh, max_, mad(vd[j][i].unit(e), q[e], ma)));
         }
+        if (ring.live(r, j)) write<T, VEC, E, OWN, EVEN>(dx + (r + j * ring.period) * D, vd[j][i], i, c);
       }
     }
   }
-  if (dw_parts) write_column_sums<VEC, E, BLOCK>(dw, dw_parts + (size_t)blockIdx.x * D, D, sh);
-  if (db_parts) write_column_sums<VEC, E, BLOCK>(db, db_parts + (size_t)blockIdx.x * D, D, sh);
+  float* sh = reinterpret_cast<float*>(slots);  // every copy has been read
+  if (dw_parts) write_column_sums<VEC, E, OWN, EVEN>(dw, dw_parts + (size_t)blockIdx.x * D, sh, c);
+  if (db_parts) write_column_sums<VEC, E, OWN, EVEN>(db, db_parts + (size_t)blockIdx.x * D, sh, c);
 }
 
 constexpr int kRedCols = 32, kRedRows = 32;
@@ -98,21 +141,25 @@ __global__ void __launch_bounds__(kRedCols * kRedRows)
 }
 
 template <typename T, typename WT>
-cudaError_t launch(const NormArgs& a, cudaStream_t s) {
-  const bool vec = a.D % row::kFull<T> == 0 && all_aligned({a.x, a.w, a.dy, a.dx});
-  const Shape sh = shape(a.rows, a.D, kMaxParts);
+cudaError_t launch(const NormArgs& a, const DevCtx& ctx, cudaStream_t s) {
+  const Layout l = layout<T>(a.D, {a.x, a.dy, a.dx}, {a.w});
+  const Shape sh = shape(a.rows, l, kMaxParts);
   // dw's partial sums first where both are wanted
   float* dwp = a.dw ? a.ws : nullptr;
   float* dbp = a.db ? a.ws + (a.dw ? (size_t)sh.blocks * a.D : 0) : nullptr;
-  const int smem = sh.block ? 0 : kWarps * kWarpCols * (int)sizeof(float);
+  cudaError_t e_ = cudaSuccess;
   prof_begin(s, "layer_norm_bwd");
-  dispatch<T>(a.D, vec, [&](auto v, auto e, auto block) {
-    bwd_kernel<T, WT, v(), e(), block()><<<sh.blocks, sh.threads, smem, s>>>(
-        static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd, static_cast<const T*>(a.dy),
-        static_cast<T*>(a.dx), dwp, dbp, a.rows, a.D);
+  dispatch<T>(l, [&](auto v, auto e, auto own, auto even) {
+    auto kernel = bwd_kernel<T, WT, v(), e(), own(), even()>;
+    int smem = 0;
+    const int stages = ring_stages<T, WT, 2, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w, a.dw || a.db, &smem);
+    if ((e_ = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return;
+    kernel<<<sh.blocks, sh.threads, smem, s>>>(static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd,
+                                               static_cast<const T*>(a.dy), static_cast<T*>(a.dx), dwp, dbp, a.rows,
+                                               a.D, l.period, stages, ctx.err, ctx.wait_ns);
   });
   prof_end(s);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = e_ != cudaSuccess ? e_ : cudaGetLastError();
   if (e != cudaSuccess || (!a.dw && !a.db)) return e;
   return reduce_parts(a.ws, sh.blocks, a.D, a.dw ? a.dw : a.db, a.dw ? a.db : nullptr, a.wbf16, s);
 }
@@ -130,12 +177,16 @@ cudaError_t reduce_parts(const float* in, int parts, int D, void* out0, void* ou
 }  // namespace ln
 
 size_t layer_norm_workspace_floats(long long rows, int D) {
-  return 2 * (size_t)ln::shape(rows, D, ln::kMaxParts).blocks * D;
+  // a block per row at most, in whole periods (of up to 8 rows); rows above a
+  // warp's but below 2048 columns have up to 128 threads, twice as many blocks
+  const long long blocks = (rows + 7) / 8 * 8;
+  const int most = (D > ln::kWarpCols - 8 && D <= 2048 ? 2 : 1) * ln::kMaxParts;
+  return 2 * (size_t)(blocks < most ? blocks : most) * D;
 }
 
-cudaError_t layer_norm_bwd(const NormArgs& a, cudaStream_t s) {
-  if (!a.bf16) return ln::launch<float, float>(a, s);
-  return a.wbf16 ? ln::launch<row::bf16, row::bf16>(a, s) : ln::launch<row::bf16, float>(a, s);
+cudaError_t layer_norm_bwd(const NormArgs& a, const DevCtx& c, cudaStream_t s) {
+  if (!a.bf16) return ln::launch<float, float>(a, c, s);
+  return a.wbf16 ? ln::launch<row::bf16, row::bf16>(a, c, s) : ln::launch<row::bf16, float>(a, c, s);
 }
 
 }  // namespace fbob

@@ -89,6 +89,35 @@ def test_layer_norm_misaligned_equals_aligned():
         assert torch.equal(ref[k], got[k])
 
 
+@pytest.mark.parametrize("D,shift", [(769, 0), (769, 3), (1537, 1), (770, 2), (4099, 5), (8200, 1), (33, 7)])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("fp32", "fp32")])
+def test_layer_norm_rows_off_bounds_touch_nothing_else(D, shift, types):
+    """Rows off 16-byte bounds, all tensors shifted alike or each differently:
+    the values are right, and what surrounds the outputs stays."""
+    T = 37
+    t = make(T, D, *types, seed=D)
+    x = t["x"]
+
+    def place(v, s, fill=5.0):
+        flat = torch.full((v.numel() + 64,), fill, dtype=v.dtype, device="cuda")
+        out = flat[s:s + v.numel()].view(v.shape)
+        out.copy_(v)
+        return flat, out
+
+    for each in (False, True):
+        s = (lambda k: (shift + k) % 8) if each else (lambda k: shift)
+        u = {k: place(v, s(i))[1] for i, (k, v) in enumerate(t.items())}
+        outs = {k: place(torch.zeros_like(x), s(i)) for i, k in enumerate(("y", "dx", "gx", "gdy"))}
+        y, mean, rstd = fb.fbob_layer_norm_fwd(u["x"], u["w"], u["b"], EPS, y=outs["y"][1])
+        dx, dw, db = fb.fbob_layer_norm_bwd(u["x"], u["w"], mean, rstd, u["dy"], dx=outs["dx"][1])
+        gx, gw, gdy = fb.fbob_layer_norm_bob(u["x"], u["w"], mean, rstd, u["dy"], u["ux"], u["uw"], u["ub"],
+                                             gx=outs["gx"][1], gdy=outs["gdy"][1])
+        fb.device_status()
+        compare(t, dict(y=y, dx=dx, dw=dw, db=db, gx=gx, gw=gw, gdy=gdy))
+        for i, (k, (flat, view)) in enumerate(outs.items()):
+            assert (flat[:s(i)] == 5.0).all() and (flat[s(i) + view.numel():] == 5.0).all(), k
+
+
 def test_layer_norm_constant_rows_and_optional_arguments():
     """A row of equal elements has xh = 0 and r = eps^-1/2: y is the bias."""
     x = torch.full((3, 40), 2.5, device="cuda")
