@@ -108,7 +108,7 @@ def load():
     ll, sz = ctypes.c_longlong, ctypes.c_size_t
     lib.fbob_rotary_frequencies.argtypes = [ctypes.POINTER(Rotary), ctypes.POINTER(ctypes.c_double)]
     lib.fbob_rotary_frequencies.restype = st
-    lib.fbob_rotary_apply.argtypes = [ctypes.POINTER(Rotary), st, st, st, st, ctypes.POINTER(RotaryHeads), st, vp, st,
+    lib.fbob_rotary_apply.argtypes = [ctypes.POINTER(Rotary), st, st, st, st, vp, st, vp, st,
                                       ll, ll, st, vp]
     lib.fbob_rotary_apply.restype = st
     np = ctypes.POINTER(Norm)

@@ -9,11 +9,12 @@ allocator on that stream.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
 from . import _lib
-from ._lib import LinearCe, Norm, Rotary, RotaryHeads, _check, load
+from ._lib import LinearCe, Norm, Rotary, _check, load
 
 DTYPES = {torch.bfloat16: _lib.BF16, torch.float32: _lib.FP32}
 
@@ -94,17 +95,21 @@ def fbob_rotary_frequencies(rotary: Rotary) -> list:
     return list(out)
 
 
+# fbob_rotary_heads as the library lays it out (the fields of RotaryHeads)
+_HEADS = struct.Struct("@PPi6q")
+
+
 def _heads(t, name, like, index):
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [B, H, N, d]")
     if t.get_device() != index:
         raise ValueError(f"{name}: all tensors must be on the same CUDA device")
     if t.dtype != like.dtype:
         raise TypeError(f"{name}: expected {like.dtype}, got {t.dtype}")
     st = t.stride()
+    if len(st) != 4:
+        raise ValueError(f"{name} must be [B, H, N, d]")
     if st[3] != 1 and t.shape[3] > 1:
         raise ValueError(f"{name}: the columns of a head must be contiguous")
-    return st[:3]
+    return st
 
 
 def _rotary_side(x, y, name, like, index, stream):
@@ -112,12 +117,12 @@ def _rotary_side(x, y, name, like, index, stream):
     xs, shape = _heads(x, name, like, index), x.shape
     if y is None:
         y = _new(like, shape, like.dtype, stream)
-        ys = y.stride()[:3]
+        ys = y.stride()
     else:
         ys = _heads(y, name + "o", like, index)
         if y.shape != shape:
             raise ValueError(f"{name}o: expected shape {tuple(shape)}, got {tuple(y.shape)}")
-    return RotaryHeads(x.data_ptr(), y.data_ptr(), shape[1], xs, ys), y
+    return _HEADS.pack(x.data_ptr(), y.data_ptr(), shape[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2]), y
 
 
 def fbob_rotary_apply(rotary, Q, K=None, positions=None, offset=0, transpose=False, Qo=None, Ko=None, stream=None):
@@ -134,12 +139,12 @@ def fbob_rotary_apply(rotary, Q, K=None, positions=None, offset=0, transpose=Fal
     if K is None:
         if Ko is not None:
             raise ValueError("Ko without K")
-        sides, count = (RotaryHeads * 1)(side), 1
+        sides, count = side, 1
     else:
         if K.dim() != 4 or K.shape[0] != B or K.shape[2] != N or K.shape[3] != d:
             raise ValueError(f"K: expected shape ({B}, Hk, {N}, {d}), got {tuple(K.shape)}")
         other, Ko = _rotary_side(K, Ko, "K", Q, index, stream)
-        sides, count = (RotaryHeads * 2)(side, other), 2
+        sides, count = side + other, 2
     at, size, step = None, 0, 0
     if positions is not None:
         if positions.dtype not in (torch.int32, torch.int64):

@@ -38,10 +38,11 @@ enum Epilogue {
 };
 
 struct EpArgs {
-  // tokens (kStats .. kGrad2): rows of the tile
-  const int* target;      // [T]: column, or -1 where nothing is counted
-  const float* lse;       // [T]
-  const float* g;         // [T]
+  // tokens (kStats .. kGrad2): rows of the tile, counted tokens only
+  const int* index;       // [T]: the caller's row of each counted token
+  const int* target;      // [T]: its column
+  const float* lse;       // [T], the caller's rows
+  const float* g;         // [T], the caller's rows
   const float* gmax;      // [1]: gs = g / gmax
   const float* alpha;     // [T]
   float2* part;           // kStats: (max, sum) [parts][T], two parts per tile of columns
@@ -64,6 +65,11 @@ struct GemmArgs {
   int K;                // contraction length
   int splits;           // K is cut into this many slabs (kSlab)
   int M, N;             // output rows and columns
+  // The counted tokens lie in the first *count of T rows.  They are the rows of
+  // kStats .. kSlab (M = T at most) and the contraction of kOut (K = T at most);
+  // kGrad and kGrad2 also write zero rows up to token_steps() x 64, which kOut
+  // reads.
+  const int* count;
   int n_base;           // kStats..kGrad2: vocabulary index of column 0
   int b0;               // offset into the rows of the matrices B is read from
   EpArgs ep;
@@ -71,6 +77,10 @@ struct GemmArgs {
   unsigned long long wait_ns;
   int stall;
 };
+
+// Rows, in steps of the contraction, that hold n counted tokens (at least one
+// step, so that a sum over no tokens is written as zero).
+__host__ __device__ inline int token_steps(int n) { return n <= kBK ? 1 : (n + kBK - 1) / kBK; }
 
 // C = sum over segments of A_seg B_seg^T with A [M][K], B [N][K], then the
 // epilogue.  kSlab reads B and kOut reads both A and B from matrices stored

@@ -33,6 +33,7 @@
 #include <math.h>
 
 #include "ce.h"
+#include "launch.cuh"
 #include "prof.h"
 #include "tc_pair.cuh"
 
@@ -49,7 +50,7 @@ constexpr int kTmemCols = 512;
 constexpr int kBufCols = 256;     // accumulator columns per tile in flight
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kChainBlocks = 4;   // 256 columns of the contraction
+constexpr int kChainBlocks = 2;   // 128 columns of the contraction
 
 template <int EP>
 struct Cfg {
@@ -104,9 +105,14 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// e^x for the softmax: the difference is taken first, so that its rounding is
-// relative to it and not to the logit.
-__device__ __forceinline__ float ex(float z, float at) { return ex2((z - at) * kLog2e); }
+// e^(z - at) for the softmax: the difference is taken first, so that its
+// rounding is relative to it and not to the logit.  For bf16 operands the
+// special function unit's 2^x of a rounded product (error about 5e-7 at
+// z - at = -15) is far below the rounding of G; fp32 operands take expf.
+template <bool FP32>
+__device__ __forceinline__ float ex(float z, float at) {
+  return FP32 ? expf(z - at) : ex2((z - at) * kLog2e);
+}
 
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
@@ -153,12 +159,13 @@ struct Acc {
 // The epilogue of one tile for this thread's row: `row` in the output, n0 the
 // first column, part the index of this half tile's row statistics.
 template <int EP, bool FP32>
-__device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc, int row, int n0, int part, int split) {
+__device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc, int rows, int row, int n0, int part,
+                                         int split) {
   constexpr int kUnroll = FP32 ? 4 : 1;
   const EpArgs& e = p.ep;
-  const bool live = row < p.M;
+  const bool live = row < rows;
   if constexpr (EP == kStats) {
-    const int y = live ? e.target[row] - p.n_base : -1;
+    const int y = live ? e.target[row] : -1;
     float m = -INFINITY, s = 0.f;
 #pragma unroll kUnroll
     for (int c = 0; c < 128; c += 32) {
@@ -181,8 +188,8 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
       if (top > -INFINITY || top != top) {
         float t = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) t += ex(v[j], top);
-        s = s * ex(m, top) + t;
+        for (int j = 0; j < 32; ++j) t += ex<FP32>(v[j], top);
+        s = s * ex<FP32>(m, top) + t;
         m = top;
       } else {  // nothing above -inf so far; a NaN among them still counts
 #pragma unroll
@@ -191,25 +198,25 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
     }
     if (live) e.part[(size_t)part * p.M + row] = make_float2(m, s);
   } else if constexpr (EP == kGrad) {
-    const int y = live ? e.target[row] : -1;
-    const float at = y >= 0 ? e.lse[row] : 0.f, gm = *e.gmax;
-    const float gs = y >= 0 && gm != 0.f ? e.g[row] / gm : 0.f;
+    const int y = live ? e.target[row] : -1, own = live ? e.index[row] : 0;
+    const float at = live ? e.lse[own] : 0.f, gm = *e.gmax;
+    const float gs = live && gm != 0.f ? e.g[own] / gm : 0.f;
+    const bool stored = row < min(p.M, token_steps(rows) * kBK);  // rows past the tokens: zero
 #pragma unroll kUnroll
     for (int c = 0; c < 128; c += 32) {
       float v[32];
       acc.load(c, c, v);
       const int n = n0 + c, hit = y - p.n_base - n;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = y >= 0 ? gs * ex(v[j], at) : 0.f;
-      if (y >= 0 && hit >= 0 && hit < 32) {
+      for (int j = 0; j < 32; ++j) v[j] = live ? gs * ex<FP32>(v[j], at) : 0.f;
+      if (live && hit >= 0 && hit < 32) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] -= j == hit ? gs : 0.f;
       }
-      if (live && n < e.ld) store_planes<FP32>(e.planes, (size_t)row * e.ld + n, v);
+      if (stored && n < e.ld) store_planes<FP32>(e.planes, (size_t)row * e.ld + n, v);
     }
   } else if constexpr (EP == kAlpha) {
-    const int y = live ? e.target[row] : -1;
-    const float at = y >= 0 ? e.lse[row] : 0.f;
+    const float at = live ? e.lse[e.index[row]] : 0.f;
     float s = 0.f;
 #pragma unroll kUnroll
     for (int c = 0; c < 64; c += 32) {
@@ -218,13 +225,14 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
       acc.load(kTileNDual + c, 64 + c, b);
       const int n = n0 + c;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) s += n + j < p.N ? ex(z[j], at) * b[j] : 0.f;
+      for (int j = 0; j < 32; ++j) s += n + j < p.N ? ex<FP32>(z[j], at) * b[j] : 0.f;
     }
-    if (live) e.sums[(size_t)part * p.M + row] = y >= 0 ? s : 0.f;
+    if (live) e.sums[(size_t)part * p.M + row] = s;
   } else if constexpr (EP == kGrad2) {
-    const int y = live ? e.target[row] : -1;
-    const float at = y >= 0 ? e.lse[row] : 0.f, al = y >= 0 ? e.alpha[row] : 0.f, gm = *e.gmax;
-    const float gs = y >= 0 && gm != 0.f ? e.g[row] / gm : 0.f;
+    const int y = live ? e.target[row] : -1, own = live ? e.index[row] : 0;
+    const float at = live ? e.lse[own] : 0.f, al = live ? e.alpha[row] : 0.f, gm = *e.gmax;
+    const float gs = live && gm != 0.f ? e.g[own] / gm : 0.f;
+    const bool stored = row < min(p.M, token_steps(rows) * kBK);  // rows past the tokens: zero
 #pragma unroll kUnroll
     for (int c = 0; c < 64; c += 32) {
       float z[32], b[32];
@@ -233,14 +241,14 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
       const int n = n0 + c, hit = y - p.n_base - n;
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        z[j] = y >= 0 ? gs * ex(z[j], at) : 0.f;
-        b[j] = y >= 0 ? z[j] * (b[j] - al) : 0.f;
+        z[j] = live ? gs * ex<FP32>(z[j], at) : 0.f;
+        b[j] = live ? z[j] * (b[j] - al) : 0.f;
       }
-      if (y >= 0 && hit >= 0 && hit < 32) {
+      if (live && hit >= 0 && hit < 32) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) z[j] -= j == hit ? gs : 0.f;
       }
-      if (live && n < e.ld) {
+      if (stored && n < e.ld) {
         store_planes<FP32>(e.planes, (size_t)row * e.ld + n, z);
         store_planes<FP32>(e.planes + kPlanes, (size_t)row * e.ld + n, b);
       }
@@ -253,15 +261,15 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
       acc.load(c, c, v);
       const int n = n0 + c;
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {  // out_ld is a multiple of 4
+      for (int j = 0; j < 32; j += 8) {  // out_ld is a multiple of 8
         if (live && n + j < e.out_ld) {
-          float4* o = reinterpret_cast<float4*>(out + n + j);
-          float4 f = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          float* o = out + n + j;
           if (e.accumulate) {
-            const float4 h = *o;
-            f.x += h.x, f.y += h.y, f.z += h.z, f.w += h.w;
+            const float4 h = *reinterpret_cast<const float4*>(o), i = *reinterpret_cast<const float4*>(o + 4);
+            v[j] += h.x, v[j + 1] += h.y, v[j + 2] += h.z, v[j + 3] += h.w;
+            v[j + 4] += i.x, v[j + 5] += i.y, v[j + 6] += i.z, v[j + 7] += i.w;
           }
-          *o = f;
+          st_global_v8(o, reinterpret_cast<const uint32_t*>(v + j));
         }
       }
     }
@@ -279,13 +287,15 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
       } else if (e.out_bf16) {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.out) + at + n;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          if (e.out_vec && n + j + 8 <= p.N) {
-            *reinterpret_cast<uint4*>(o + j) = make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
-                                                          pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+        for (int j = 0; j < 32; j += 16) {
+          if (e.out_vec && n + j + 16 <= p.N) {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] = pack_bf16x2(v[j + 2 * q], v[j + 2 * q + 1]);
+            st_global_v8(o + j, w);
           } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 16; ++q) {
               if (n + j + q < p.N) o[j + q] = __float2bfloat16_rn(v[j + q]);
             }
           }
@@ -293,12 +303,12 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
       } else {
         float* o = static_cast<float*>(e.out) + at + n;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          if (e.out_vec && n + j + 4 <= p.N) {
-            *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        for (int j = 0; j < 32; j += 8) {
+          if (e.out_vec && n + j + 8 <= p.N) {
+            st_global_v8(o + j, reinterpret_cast<const uint32_t*>(v + j));
           } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 8; ++q) {
               if (n + j + q < p.N) o[j + q] = v[j + q];
             }
           }
@@ -330,8 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   __shared__ Ctrl ctrl;
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
-  const Tiles ts{(p.M + kTileM - 1) / kTileM, (p.N + C::BN - 1) / C::BN, p.splits, (p.K + kBK - 1) / kBK};
-  const long long total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  allow_next();
 
   if (tid == 0) {
     ctrl.abort_flag = 0;
@@ -362,6 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   const Waiter wt{&ctrl.abort_flag, p.err, p.wait_ns};
   const bool live = ctrl.abort_flag == 0;
   const uint32_t sm0 = smem_u32(smem);
+  wait_previous();
+  const int tokens = *p.count, written = min(p.M, token_steps(tokens) * kBK);
+  const int rows = EP == kOut ? p.M : tokens;                             // that hold results
+  const int tile_rows = EP == kGrad || EP == kGrad2 ? written : rows;     // that are worked on
+  const Tiles ts{(tile_rows + kTileM - 1) / kTileM, (p.N + C::BN - 1) / C::BN, p.splits,
+                 EP == kOut ? token_steps(tokens) : (p.K + kBK - 1) / kBK};
+  const long long total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   // the steps of K up to which an accumulator chain that starts at kc runs
   auto chain_end = [](int kc, int k1) { return FP32 ? min(kc + kChainBlocks, k1) : k1; };
 
@@ -508,13 +524,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           __syncwarp();
           if ((tid & 31) == 0) mbar_arrive_cluster(freed + buf * 8);
         }
-        if (ok) epilogue<EP, true>(p, Acc<true>{0, sum}, row, n0, 2 * n + half, split);
+        if (ok) epilogue<EP, true>(p, Acc<true>{0, sum}, rows, row, n0, 2 * n + half, split);
       } else {
         const int buf = chain & 1;
         // warp-uniform: the TMEM loads that follow are warp-collective
         if (!(ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
         tc_fence_after();
-        epilogue<EP, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr}, row, n0, 2 * n + half, split);
+        epilogue<EP, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr}, rows, row, n0, 2 * n + half,
+                            split);
         tc_fence_before();
         __syncwarp();
         if ((tid & 31) == 0) mbar_arrive_cluster(freed + buf * 8);
@@ -541,20 +558,10 @@ cudaError_t launch_as(const GemmArgs& g, const char* name, cudaStream_t s) {
   const long long tiles = (long long)((g.M + kTileM - 1) / kTileM) * ((g.N + C::BN - 1) / C::BN) * g.splits;
   if (tiles == 0) return cudaSuccess;
   const long long pairs = sm_count() / 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   prof_begin(s, name);
-  e = cudaLaunchKernelEx(&cfg, kernel, g);
+  e = chained(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kThreads), C::SMEM, 2, s, g);
   prof_end(s);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return e;
 }
 
 template <int EP>

@@ -2,6 +2,10 @@
 // without keeping the logits: forward, gradients, and the gradients' own
 // vector-Jacobian product (formulas in fbob.h).
 //
+// Tokens that are not counted cost nothing: a first kernel lists the others, and
+// every product works on the listed rows only (their number stays on the
+// device; launches are sized for all tokens, blocks without tiles end at once).
+//
 // Forward: one product whose epilogue reduces each 128 columns of a row to
 // (max, sum of exponentials) and picks the target's logit; a small kernel joins
 // them.  Gradients: for pieces of the vocabulary, the logits are formed again
@@ -23,6 +27,7 @@
 #include <string.h>
 
 #include "ce.h"
+#include "launch.cuh"
 #include "prof.h"
 
 namespace fbob {
@@ -69,7 +74,7 @@ int hidden_splits(const CeArgs& a, int cols) {
 struct Plan {
   int np, Dp, ld, splits, stat_parts, alpha_parts;
   bool copy_w;
-  size_t h, uh, w, uw, target, gmax, part, sums, picked, alpha, planes, slab, bytes;
+  size_t h, uh, w, uw, place, index, target, totals, part, sums, picked, alpha, planes, slab, bytes;
 };
 
 Plan plan(const CeArgs& a, CePass pass) {
@@ -93,8 +98,10 @@ Plan plan(const CeArgs& a, CePass pass) {
   p.uh = take(bob, T * row);
   p.w = take(p.copy_w, V * row);
   p.uw = take(bob && p.copy_w, V * row);
+  p.place = take(true, T * 4);
+  p.index = take(true, T * 4);
   p.target = take(true, T * 4);
-  p.gmax = take(true, 4);
+  p.totals = take(true, 8);
   p.picked = take(!bwd, T * 4);
   p.part = take(!bwd, T * p.stat_parts * sizeof(float2));
   p.sums = take(bob, T * p.alpha_parts * 4);
@@ -107,50 +114,122 @@ Plan plan(const CeArgs& a, CePass pass) {
 
 // --- small kernels ---------------------------------------------------------------------------------
 
-// Rows of H (or UH), or of W (target null): bf16 planes [rows][Dp], zero in the
-// padding and in rows that are not counted (whatever those hold).  One thread
-// per 8 columns; the thread of a row's first columns also writes the row's
-// target as the products' epilogues read it: the column, -1 (ignored) or -2
-// (outside the vocabulary: reported in the status word).
+// The counted tokens, in order: index[i] is the caller's row of the i-th one and
+// target[i] its column; place[r] is that i for row r, -1 if it is ignored, -2 if
+// its target is outside the vocabulary (reported in the status word).  Also
+// gmax = max |g| over them (1 if that is not finite).  One block: 4096 tokens
+// per round, a prefix sum over the warps' counts.
+struct Totals {
+  int count;
+  float gmax;
+};
+constexpr int kListThreads = 1024, kListItems = 4;
+
+__global__ void __launch_bounds__(kListThreads)
+    list_kernel(const long long* target, const float* g, long long ignore, int V, int T, int* place, int* index,
+                int* column, Totals* totals, unsigned int* err) {
+  allow_next();
+  wait_previous();
+  __shared__ int warp_n[32];
+  __shared__ float warp_m[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float m = 0.f;
+  int before = 0;  // counted tokens of the earlier rounds
+  bool wrong = false;
+  for (int t0 = 0; t0 < T; t0 += kListThreads * kListItems) {
+    long long y[kListItems];
+    bool keep[kListItems];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kListItems; ++i) {
+      const int t = t0 + threadIdx.x * kListItems + i;
+      y[i] = t < T ? target[t] : ignore;
+      keep[i] = y[i] != ignore && y[i] >= 0 && y[i] < V;
+      wrong |= !keep[i] && y[i] != ignore;
+      if (g && keep[i]) m = fmaxf(m, fabsf(g[t]));
+      n += keep[i];
+    }
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) warp_n[warp] = upto;
+    __syncthreads();
+    int mine = lane <= warp ? warp_n[lane] : 0, all = warp_n[lane];
+    if (lane == warp) mine = 0;  // the warps before this one
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    int at = before + mine + upto - n;
+#pragma unroll
+    for (int i = 0; i < kListItems; ++i) {
+      const int t = t0 + threadIdx.x * kListItems + i;
+      if (t < T) place[t] = keep[i] ? at : y[i] == ignore ? -1 : -2;
+      if (keep[i]) {
+        index[at] = t;
+        column[at] = (int)y[i];
+        ++at;
+      }
+    }
+    before += all;
+    __syncthreads();
+  }
+  if (wrong) atomicOr(err, kErrTarget);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) warp_m[warp] = m;
+  __syncthreads();
+  if (warp == 0) {
+    m = warp_m[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) *totals = Totals{before, m < INFINITY ? m : 1.f};
+  }
+}
+
+// bf16 planes [rows][Dp] of the counted rows of H or UH (index given; then zero
+// rows up to a whole step of the contraction), or of W; zero in the padding.
+// One thread per 8 columns.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    planes_kernel(const T* x, const long long* target, long long ignore, int V, int* target_out, uint16_t* planes,
-                  long long rows, int D, int Dp, int np, bool vec, unsigned int* err) {
+    planes_kernel(const T* x, const int* index, const Totals* totals, uint16_t* planes, long long rows, int D, int Dp,
+                  int np, int vec) {
+  allow_next();
+  wait_previous();
   const int per = Dp / 8;
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long r = i / per;
   const int c = (int)(i - r * per) * 8;
   if (r >= rows) return;
-  bool keep = true;
-  if (target) {
-    const long long y = target[r];
-    keep = y != ignore && y >= 0 && y < V;
-    if (target_out && c == 0) {
-      target_out[r] = keep ? (int)y : y == ignore ? -1 : -2;
-      if (!keep && y != ignore) atomicOr(err, kErrTarget);
-    }
-  }
+  const int count = index ? totals->count : 0;
+  if (index && r >= (long long)token_steps(count) * kBK) return;
   float v[8];
-  const T* src = x + r * D + c;
-  if (!keep) {
+  if (index && r >= count) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  } else if (vec) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 u = *reinterpret_cast<const uint4*>(src);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  } else {
+    const T* src = x + (index ? index[r] : r) * D + c;
+    if (vec) {
+      if constexpr (sizeof(T) == 2) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = __uint_as_float(w[j] << 16);
+          v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+      } else {
+        const float4 f = *reinterpret_cast<const float4*>(src), g = *reinterpret_cast<const float4*>(src + 4);
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w, v[4] = g.x, v[5] = g.y, v[6] = g.z, v[7] = g.w;
       }
     } else {
-      const float4 f = *reinterpret_cast<const float4*>(src), g = *reinterpret_cast<const float4*>(src + 4);
-      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w, v[4] = g.x, v[5] = g.y, v[6] = g.z, v[7] = g.w;
-    }
-  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < D ? (float)src[j] : 0.f;
+      for (int j = 0; j < 8; ++j) v[j] = c + j < D ? (float)src[j] : 0.f;
+    }
   }
   for (int k = 0; k < np; ++k) {
     uint32_t w[4];
@@ -167,40 +246,22 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// gmax = max |g| over the counted rows (1 if that is not finite), in one block.
-__global__ void __launch_bounds__(1024) gmax_kernel(const float* g, const long long* target, long long ignore, int V,
-                                                     int T, float* out) {
-  __shared__ float part[32];
-  float m = 0.f;
-  for (int t = threadIdx.x; t < T; t += blockDim.x) {
-    const long long y = target[t];
-    if (y != ignore && y >= 0 && y < V) m = fmaxf(m, fabsf(g[t]));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    m = part[threadIdx.x];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (threadIdx.x == 0) *out = m < INFINITY ? m : 1.f;
-  }
-}
-
 // Sums over `parts` per-row partials, 32 rows per block, 16 threads per row:
 // loss and lse (kStats), or alpha and gg (kAlpha).
 constexpr int kJoinRows = 32, kJoinWays = 16;
 
 __global__ void __launch_bounds__(kJoinRows* kJoinWays)
-    join_stats_kernel(const float2* part, int parts, const int* target, const float* picked, int T, float* loss,
+    join_stats_kernel(const float2* part, int parts, const int* place, const float* picked, int T, float* loss,
                       float* lse) {
+  allow_next();
+  wait_previous();
   __shared__ float2 sh[kJoinWays][kJoinRows];
   const int t = blockIdx.x * kJoinRows + threadIdx.x;
+  const int at = t < T ? place[t] : -1;
   float m = -INFINITY, s = 0.f;
-  if (t < T) {
+  if (at >= 0) {
     for (int i = threadIdx.y; i < parts; i += kJoinWays) {
-      const float2 q = part[(size_t)i * T + t];
+      const float2 q = part[(size_t)i * T + at];
       const float top = fmaxf(m, q.x);
       if (top > -INFINITY) {
         s = (m > -INFINITY ? s * expf(m - top) : s) + (q.x > -INFINITY ? q.y * expf(q.x - top) : q.y);
@@ -220,24 +281,26 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWays)
     const float2 q = sh[w][threadIdx.x];
     s += q.x > -INFINITY ? q.y * expf(q.x - top) : q.y;
   }
-  const int y = target[t];
   const float l = (top > -INFINITY ? top : 0.f) + logf(s);
-  lse[t] = y >= 0 ? l : 0.f;
-  loss[t] = y >= 0 ? l - picked[t] : y == -1 ? 0.f : NAN;
+  lse[t] = at >= 0 ? l : 0.f;
+  loss[t] = at >= 0 ? l - picked[at] : at == -1 ? 0.f : NAN;
 }
 
 // alpha, and gg = alpha - b at the target, with b's row summed here in fp32
 // (one warp per token): out of the tensor cores' chain it would carry 1e-6.
 template <typename T>
 __global__ void __launch_bounds__(kJoinRows* kJoinWays)
-    join_alpha_kernel(const float* sums, int parts, const int* target, const T* H, const T* W, const T* UH, const T* UW,
-                      int T_, int D, float* alpha, float* gg) {
+    join_alpha_kernel(const float* sums, int parts, const int* place, const int* column, const T* H, const T* W,
+                      const T* UH, const T* UW, int T_, int D, float* alpha, float* gg) {
+  allow_next();
+  wait_previous();
   __shared__ float sh[kJoinWays][kJoinRows];
   __shared__ float total[kJoinRows];
   const int t = blockIdx.x * kJoinRows + threadIdx.x;
+  const int at = t < T_ ? place[t] : -1;
   float s = 0.f;
-  if (t < T_) {
-    for (int i = threadIdx.y; i < parts; i += kJoinWays) s += sums[(size_t)i * T_ + t];
+  if (at >= 0) {
+    for (int i = threadIdx.y; i < parts; i += kJoinWays) s += sums[(size_t)i * T_ + at];
   }
   sh[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
@@ -245,16 +308,17 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWays)
     s = 0.f;
     for (int w = 0; w < kJoinWays; ++w) s += sh[w][threadIdx.x];
     total[threadIdx.x] = s;
-    if (t < T_) alpha[t] = target[t] >= 0 ? s : 0.f;
+    if (at >= 0) alpha[at] = s;
   }
   __syncthreads();
   if (!gg) return;
   for (int i = threadIdx.y; i < kJoinRows; i += kJoinWays) {
     const int r = blockIdx.x * kJoinRows + i;
     if (r >= T_) break;
-    const int y = target[r];
+    const int from = place[r];
     float b = 0.f;
-    if (y >= 0) {
+    if (from >= 0) {
+      const int y = column[from];
       for (int c = threadIdx.x; c < D; c += 32) {
         if (UH) b += (float)UH[(size_t)r * D + c] * (float)W[(size_t)y * D + c];
         if (UW) b += (float)H[(size_t)r * D + c] * (float)UW[(size_t)y * D + c];
@@ -262,25 +326,28 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWays)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
-    if (threadIdx.x == 0) gg[r] = y >= 0 ? total[i] - b : 0.f;
+    if (threadIdx.x == 0) gg[r] = from >= 0 ? total[i] - b : 0.f;
   }
 }
 
 // out [T][D] = gmax * sum of the slabs [T][Dp]; zero in rows that are not counted.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    finish_kernel(const float* slab, int splits, long long stride, const int* target, const float* gmax, T* out, int D,
-                  int Dp, long long rows, bool vec) {
+    finish_kernel(const float* slab, int splits, long long stride, const int* place, const Totals* totals, T* out,
+                  int D, int Dp, long long rows, int vec) {
+  allow_next();
+  wait_previous();
   const int per = Dp / 4;
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long r = i / per;
   const int c = (int)(i - r * per) * 4;
   if (r >= rows) return;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (target[r] >= 0) {
-    const float gm = *gmax;
+  const int at = place[r];
+  if (at >= 0) {
+    const float gm = totals->gmax;
     for (int s = 0; s < splits; ++s) {
-      const float4 f = *reinterpret_cast<const float4*>(slab + s * stride + r * Dp + c);
+      const float4 f = *reinterpret_cast<const float4*>(slab + s * stride + (long long)at * Dp + c);
       v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
     }
 #pragma unroll
@@ -324,35 +391,34 @@ struct Run {
   template <typename T>
   T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
 
-  cudaError_t make_planes(const void* x, bool tokens, int* target_out, uint16_t* out, long long rows) const {
-    const bool vec = a.D % 8 == 0 && aligned(x, 16);
+  template <typename E>
+  cudaError_t planes_of(const void* x, bool tokens, uint16_t* out, long long rows) const {
+    const int vec = a.D % 8 == 0 && aligned(x, 16);
     const long long n = rows * (p.Dp / 8);
-    const unsigned blocks = (unsigned)((n + 255) / 256);
-    const long long* target = tokens ? a.target : nullptr;
+    return chained(planes_kernel<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, 1, s, static_cast<const E*>(x),
+                   tokens ? at<int>(p.index) : nullptr, at<Totals>(p.totals), out, rows, a.D, p.Dp, p.np, vec);
+  }
+  cudaError_t make_planes(const void* x, bool tokens, size_t off) const {
     prof_begin(s, "ce_operands");
-    if (a.bf16)
-      planes_kernel<<<blocks, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), target, a.ignore, a.V, target_out, out,
-                                           rows, a.D, p.Dp, p.np, vec, c.err);
-    else
-      planes_kernel<<<blocks, 256, 0, s>>>(static_cast<const float*>(x), target, a.ignore, a.V, target_out, out, rows,
-                                           a.D, p.Dp, p.np, vec, c.err);
+    const long long rows = tokens ? a.T : a.V;
+    const cudaError_t e = a.bf16 ? planes_of<__nv_bfloat16>(x, tokens, at<uint16_t>(off), rows)
+                                 : planes_of<float>(x, tokens, at<uint16_t>(off), rows);
     prof_end(s);
-    return cudaGetLastError();
+    return e;
   }
 
-  // H, W (and UH, UW) as the products read them.
+  // The list of counted tokens, and H, W (UH, UW) as the products read them.
   cudaError_t operands() const {
-    CE_TRY(make_planes(a.H, true, at<int>(p.target), at<uint16_t>(p.h), a.T));
-    if (p.copy_w) CE_TRY(make_planes(a.W, false, nullptr, at<uint16_t>(p.w), a.V));
+    prof_begin(s, "ce_list");
+    const cudaError_t e = chained(list_kernel, dim3(1), dim3(kListThreads), 0, 1, s, a.target, a.g, a.ignore, a.V, a.T,
+                                  at<int>(p.place), at<int>(p.index), at<int>(p.target), at<Totals>(p.totals), c.err);
+    prof_end(s);
+    CE_TRY(e);
+    CE_TRY(make_planes(a.H, true, p.h));
+    if (p.copy_w) CE_TRY(make_planes(a.W, false, p.w));
     if (second) {
-      if (a.UH) CE_TRY(make_planes(a.UH, true, nullptr, at<uint16_t>(p.uh), a.T));
-      if (p.copy_w && a.UW) CE_TRY(make_planes(a.UW, false, nullptr, at<uint16_t>(p.uw), a.V));
-    }
-    if (a.g) {
-      prof_begin(s, "ce_gmax");
-      gmax_kernel<<<1, 1024, 0, s>>>(a.g, a.target, a.ignore, a.V, a.T, at<float>(p.gmax));
-      prof_end(s);
-      CE_TRY(cudaGetLastError());
+      if (a.UH) CE_TRY(make_planes(a.UH, true, p.uh));
+      if (p.copy_w && a.UW) CE_TRY(make_planes(a.UW, false, p.uw));
     }
     return cudaSuccess;
   }
@@ -362,7 +428,9 @@ struct Run {
     memset(&g, 0, sizeof(g));
     g.splits = 1, g.fp32 = !a.bf16;
     g.err = c.err, g.wait_ns = c.wait_ns, g.stall = c.stall;
-    g.ep.target = at<int>(p.target), g.ep.lse = a.lse, g.ep.g = a.g, g.ep.gmax = at<float>(p.gmax);
+    g.count = &at<Totals>(p.totals)->count;
+    g.ep.index = at<int>(p.index), g.ep.target = at<int>(p.target), g.ep.lse = a.lse, g.ep.g = a.g;
+    g.ep.gmax = &at<Totals>(p.totals)->gmax;
     return g;
   }
 
@@ -418,10 +486,11 @@ struct Run {
     g.ep.part = at<float2>(p.part), g.ep.picked = at<float>(p.picked);
     CE_TRY(gemm(kStats, g, s));
     prof_begin(s, "ce_join");
-    join_stats_kernel<<<(a.T + kJoinRows - 1) / kJoinRows, dim3(kJoinRows, kJoinWays), 0, s>>>(
-        at<float2>(p.part), p.stat_parts, at<int>(p.target), at<float>(p.picked), a.T, a.loss, a.lse_out);
+    const cudaError_t e = chained(join_stats_kernel, dim3((a.T + kJoinRows - 1) / kJoinRows),
+                                  dim3(kJoinRows, kJoinWays), 0, 1, s, at<float2>(p.part), p.stat_parts,
+                                  at<int>(p.place), at<float>(p.picked), a.T, a.loss, a.lse_out);
     prof_end(s);
-    return cudaGetLastError();
+    return e;
   }
 
   cudaError_t alpha() const {
@@ -431,16 +500,16 @@ struct Run {
     g.ep.sums = at<float>(p.sums);
     CE_TRY(gemm(kAlpha, g, s));
     prof_begin(s, "ce_join");
-    if (a.bf16) join_alpha<__nv_bfloat16>();
-    else join_alpha<float>();
+    const cudaError_t e = a.bf16 ? join_alpha<__nv_bfloat16>() : join_alpha<float>();
     prof_end(s);
-    return cudaGetLastError();
+    return e;
   }
   template <typename E>
-  void join_alpha() const {
-    join_alpha_kernel<E><<<(a.T + kJoinRows - 1) / kJoinRows, dim3(kJoinRows, kJoinWays), 0, s>>>(
-        at<float>(p.sums), p.alpha_parts, at<int>(p.target), static_cast<const E*>(a.H), static_cast<const E*>(a.W),
-        static_cast<const E*>(a.UH), static_cast<const E*>(a.UW), a.T, a.D, at<float>(p.alpha), a.gg);
+  cudaError_t join_alpha() const {
+    return chained(join_alpha_kernel<E>, dim3((a.T + kJoinRows - 1) / kJoinRows), dim3(kJoinRows, kJoinWays), 0, 1, s,
+                   at<float>(p.sums), p.alpha_parts, at<int>(p.place), at<int>(p.target), static_cast<const E*>(a.H),
+                   static_cast<const E*>(a.W), static_cast<const E*>(a.UH), static_cast<const E*>(a.UW), a.T, a.D,
+                   at<float>(p.alpha), a.gg);
   }
 
   // One piece of the vocabulary: columns c0 .. c0 + cols - 1.
@@ -487,7 +556,7 @@ struct Run {
       g.M = cols, g.N = a.D, g.K = a.T;
       g.ep.out = static_cast<char*>(a.dW) + (size_t)c0 * a.D * (a.bf16 ? 2 : 4);
       g.ep.out_ld = a.D, g.ep.out_bf16 = a.bf16;
-      g.ep.out_vec = a.D % (a.bf16 ? 8 : 4) == 0 && aligned(a.dW, 16);
+      g.ep.out_vec = a.D % (a.bf16 ? 16 : 8) == 0 && aligned(a.dW, 32);  // rows of 32-byte stores
       CE_TRY(gemm(kOut, g, s));
     }
     return cudaSuccess;
@@ -495,18 +564,18 @@ struct Run {
 
   cudaError_t finish() const {
     if (!a.dH) return cudaSuccess;
-    const long long n = (long long)a.T * (p.Dp / 4);
-    const unsigned blocks = (unsigned)((n + 255) / 256);
-    const bool vec = a.D % 4 == 0 && aligned(a.dH, a.bf16 ? 8 : 16);
     prof_begin(s, "ce_finish");
-    if (a.bf16)
-      finish_kernel<<<blocks, 256, 0, s>>>(at<float>(p.slab), p.splits, (long long)a.T * p.Dp, at<int>(p.target),
-                                           at<float>(p.gmax), static_cast<__nv_bfloat16*>(a.dH), a.D, p.Dp, a.T, vec);
-    else
-      finish_kernel<<<blocks, 256, 0, s>>>(at<float>(p.slab), p.splits, (long long)a.T * p.Dp, at<int>(p.target),
-                                           at<float>(p.gmax), static_cast<float*>(a.dH), a.D, p.Dp, a.T, vec);
+    const cudaError_t e = a.bf16 ? finish_as<__nv_bfloat16>() : finish_as<float>();
     prof_end(s);
-    return cudaGetLastError();
+    return e;
+  }
+  template <typename E>
+  cudaError_t finish_as() const {
+    const long long n = (long long)a.T * (p.Dp / 4);
+    const int vec = a.D % 4 == 0 && aligned(a.dH, 4 * sizeof(E));
+    return chained(finish_kernel<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, 1, s, at<float>(p.slab), p.splits,
+                   (long long)a.T * p.Dp, at<int>(p.place), at<Totals>(p.totals), static_cast<E*>(a.dH), a.D, p.Dp,
+                   (long long)a.T, vec);
   }
 };
 

@@ -145,6 +145,14 @@ def test_linear_ce_all_ignored_and_no_tokens():
     assert gH.shape == (0, 64) and (gW == 0).all() and gg.shape == (0,)
 
 
+@pytest.mark.parametrize("T,counted", [(9000, 8999), (9000, 1), (5000, 64), (4097, 65), (300, 256), (300, 257)])
+def test_linear_ce_counts_of_tokens(T, counted):
+    """Lists of counted tokens over several rounds, and at the steps' edges."""
+    order = torch.randperm(T, generator=torch.Generator().manual_seed(T))
+    t = make(T, 16, 40, "bf16", seed=counted, ignored=order[counted:].tolist())
+    compare(t, chain(t))
+
+
 @pytest.mark.parametrize("wrong", [-1, 50, 2 ** 40])
 def test_linear_ce_target_outside_the_classes(wrong):
     t = make(9, 64, 50, "bf16", seed=2)
