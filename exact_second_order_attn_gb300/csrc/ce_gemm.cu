@@ -318,19 +318,32 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
   }
 }
 
+// Fewer than 2^31 tiles (the sizes are checked): 32-bit arithmetic throughout,
+// since a division of 64 bits costs the issuing threads more than a product.
 struct Tiles {
   int mt, nt, splits, kb;  // row and column tiles, slabs, 64-column steps of K
-  __device__ __forceinline__ long long count() const { return (long long)mt * nt * splits; }
-  __device__ __forceinline__ void at(long long i, int& m, int& n, int& split) const {
-    const long long plane = (long long)mt * nt;
-    split = (int)(i / plane);
-    const long long r = i - split * plane;
-    const int first = (int)(r / ((long long)kGroupM * nt)) * kGroupM;
-    const int in = (int)(r - (long long)first * nt), rows = min(kGroupM, mt - first);
+  __device__ __forceinline__ int count() const { return mt * nt * splits; }
+  __device__ __forceinline__ int split(int i) const { return splits == 1 ? 0 : i / (mt * nt); }
+  __device__ __forceinline__ void at(int i, int& m, int& n) const {
+    const int r = splits == 1 ? i : i % (mt * nt);
+    const int first = r / (kGroupM * nt) * kGroupM;
+    const int in = r - first * nt, rows = min(kGroupM, mt - first);
     n = in / rows;
     m = first + in - n * rows;
   }
-  __device__ __forceinline__ int k_first(int split) const { return (int)((long long)kb * split / splits); }
+  __device__ __forceinline__ int k_first(int split) const {
+    return splits == 1 ? split * kb : (int)((long long)kb * split / splits);
+  }
+};
+
+// A place in the ring of stages and its pass over the ring.
+template <int NST>
+struct Place {
+  int s = 0;
+  uint32_t pass = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == NST) s = 0, pass ^= 1;
+  }
 };
 
 template <int EP, bool FP32>
@@ -377,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   const int tile_rows = EP == kGrad || EP == kGrad2 ? written : rows;     // that are worked on
   const Tiles ts{(tile_rows + kTileM - 1) / kTileM, (p.N + C::BN - 1) / C::BN, p.splits,
                  EP == kOut ? token_steps(tokens) : (p.K + kBK - 1) / kBK};
-  const long long total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   // the steps of K up to which an accumulator chain that starts at kc runs
   auto chain_end = [](int kc, int k1) { return FP32 ? min(kc + kChainBlocks, k1) : k1; };
 
@@ -385,11 +398,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     // ------------------------------------------------------------------ TMA
     if (live && (tid & 31) == 0) {
       const uint32_t stage_bytes = 2 * (C::DUAL ? C::A_BYTES * (1 + p.has_ua) + C::B_BYTES * (1 + p.has_ub) : C::STAGE);
-      long long it = 0;
+      Place<C::NST> at;
+      long long issued = 0;
       bool ok = true;
-      for (long long t = pair; ok && t < total; t += pairs) {
-        int m, n, split;
-        ts.at(t, m, n, split);
+      for (int t = pair; ok && t < total; t += pairs) {
+        int m, n;
+        ts.at(t, m, n);
+        const int split = ts.split(t);
         const int row = m * kTileM + (int)rank * 128, col = n * C::BN + (int)rank * (C::BN / 2);
         const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
         for (int kc = k0; ok && kc < k1; kc = chain_end(kc, k1)) {
@@ -397,10 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           for (int s = 0; ok && s < p.nseg; ++s) {
             const CUtensorMap* ma = &p.a[p.seg[s].a];
             const CUtensorMap* mb = &p.b[p.seg[s].b];
-            for (int k = kc; k < ke; ++k, ++it) {
-              const int st = (int)(it % C::NST);
-              if (!(ok = wait_cluster(&ctrl.empty[st], ((it / C::NST) & 1) ^ 1, wt))) break;
-              if (p.stall && it == 0) continue;  // test hook: nothing fills the first stage
+            for (int k = kc; k < ke; ++k, ++issued, at.next()) {
+              const int st = at.s;
+              if (!(ok = mbar_wait(&ctrl.empty[st], at.pass ^ 1, wt))) break;
+              if (p.stall && issued == 0) continue;  // test hook: nothing fills the first stage
               const uint32_t bar = map_rank(smem_u32(&ctrl.full[st]), 0);
               if (rank == 0) mbar_arrive_expect_tx(&ctrl.full[st], stage_bytes);
               const uint32_t da = sm0 + st * C::STAGE, db = da + (C::DUAL ? 2 : 1) * C::A_BYTES;
@@ -427,10 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
       // The last use of each stage: on the leader its loads have landed, in both
       // blocks the MMAs' arrivals have (on the give-up path after a limit), so
       // nothing is in flight towards a block that has ended.
-      for (long long i = it > C::NST ? it - C::NST : 0; i < it; ++i) {
+      for (long long i = issued > C::NST ? issued - C::NST : 0; i < issued; ++i) {
         const int st = (int)(i % C::NST);
         if (rank == 0 && !ok) mbar_wait_drain(&ctrl.full[st], (i / C::NST) & 1, kDrainNs);
-        if (ok) ok = wait_cluster(&ctrl.empty[st], (i / C::NST) & 1, wt);
+        if (ok) ok = mbar_wait(&ctrl.empty[st], (i / C::NST) & 1, wt);
       }
       if (!ok && rank != 0) {  // this block's loads count on the leader's barriers: give them time to land
         const uint64_t t0 = globaltimer_ns();
@@ -444,12 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
       constexpr uint32_t id = idesc_bf16(kTileM, C::BN, C::A_MN, C::B_MN);
       constexpr uint32_t lbo_a = C::A_MN ? 8192 : 16, lbo_b = C::B_MN ? 8192 : 16;
       constexpr uint32_t step_a = C::A_MN ? 2048 >> 4 : 32 >> 4, step_b = C::B_MN ? 2048 >> 4 : 32 >> 4;
-      long long it = 0;
+      Place<C::NST> at;
       int chain = 0;  // accumulator buffers handed to the epilogue so far
       bool ok = true;
-      for (long long t = pair; ok && t < total; t += pairs) {
-        int m, n, split;
-        ts.at(t, m, n, split);
+      for (int t = pair; ok && t < total; t += pairs) {
+        const int split = ts.split(t);
         const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
         for (int kc = k0; ok && kc < k1; kc = chain_end(kc, k1), ++chain) {
           const int ke = chain_end(kc, k1), buf = chain & 1;
@@ -457,9 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           tc_fence_after();
           const uint32_t d = tb + buf * kBufCols;
           for (int s = 0; ok && s < p.nseg; ++s) {
-            for (int k = kc; k < ke; ++k, ++it) {
-              const int st = (int)(it % C::NST);
-              ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.full[st], (it / C::NST) & 1, wt));
+            for (int k = kc; k < ke; ++k, at.next()) {
+              const int st = at.s;
+              ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.full[st], at.pass, wt));
               if (!ok) break;
               tc_fence_after();
               const uint32_t more = s > 0 || k > kc;  // the accumulator holds a product already
@@ -498,9 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const uint32_t freed = map_rank(smem_u32(&ctrl.tile_empty[0]), 0);
     int chain = 0;
     bool ok = live;
-    for (long long t = pair; ok && t < total; t += pairs) {
-      int m, n, split;
-      ts.at(t, m, n, split);
+    for (int t = pair; ok && t < total; t += pairs) {
+      int m, n;
+      ts.at(t, m, n);
+      const int split = ts.split(t);
       constexpr int H = C::BN / 2;
       const int row = m * kTileM + (int)rank * 128 + r, n0 = n * C::BN + half * H;
       if constexpr (FP32) {
@@ -510,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
         for (int kc = k0; kc < k1; kc = chain_end(kc, k1), ++chain) {
           const int buf = chain & 1;
-          if (!(ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
           tc_fence_after();
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -528,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
       } else {
         const int buf = chain & 1;
         // warp-uniform: the TMEM loads that follow are warp-collective
-        if (!(ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
         tc_fence_after();
         epilogue<EP, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr}, rows, row, n0, 2 * n + half,
                             split);

@@ -117,13 +117,13 @@ Plan plan(const CeArgs& a, CePass pass) {
 // The counted tokens, in order: index[i] is the caller's row of the i-th one and
 // target[i] its column; place[r] is that i for row r, -1 if it is ignored, -2 if
 // its target is outside the vocabulary (reported in the status word).  Also
-// gmax = max |g| over them (1 if that is not finite).  One block: 4096 tokens
+// gmax = max |g| over them (1 if that is not finite).  One block: 8192 tokens
 // per round, a prefix sum over the warps' counts.
 struct Totals {
   int count;
   float gmax;
 };
-constexpr int kListThreads = 1024, kListItems = 4;
+constexpr int kListThreads = 1024, kListItems = 8;
 
 __global__ void __launch_bounds__(kListThreads)
     list_kernel(const long long* target, const float* g, long long ignore, int V, int T, int* place, int* index,
@@ -137,43 +137,46 @@ __global__ void __launch_bounds__(kListThreads)
   int before = 0;  // counted tokens of the earlier rounds
   bool wrong = false;
   for (int t0 = 0; t0 < T; t0 += kListThreads * kListItems) {
+    // item i of this thread: row i of the 32-token rows of its warp
+    const int first = t0 + warp * 32 * kListItems + lane;
     long long y[kListItems];
-    bool keep[kListItems];
-    int n = 0;
+    float w[kListItems];
+    unsigned kept[kListItems];
+    int n = 0;  // counted tokens of the warp
 #pragma unroll
     for (int i = 0; i < kListItems; ++i) {
-      const int t = t0 + threadIdx.x * kListItems + i;
+      const int t = first + 32 * i;
       y[i] = t < T ? target[t] : ignore;
-      keep[i] = y[i] != ignore && y[i] >= 0 && y[i] < V;
-      wrong |= !keep[i] && y[i] != ignore;
-      if (g && keep[i]) m = fmaxf(m, fabsf(g[t]));
-      n += keep[i];
+      w[i] = g && t < T ? fabsf(g[t]) : 0.f;
     }
-    int upto = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
+    for (int i = 0; i < kListItems; ++i) {
+      const bool keep = y[i] != ignore && y[i] >= 0 && y[i] < V;
+      wrong |= !keep && y[i] != ignore;
+      if (keep) m = fmaxf(m, w[i]);
+      kept[i] = __ballot_sync(0xffffffffu, keep);
+      n += __popc(kept[i]);
     }
-    if (lane == 31) warp_n[warp] = upto;
+    if (lane == 0) warp_n[warp] = n;
     __syncthreads();
-    int mine = lane <= warp ? warp_n[lane] : 0, all = warp_n[lane];
-    if (lane == warp) mine = 0;  // the warps before this one
+    int mine = lane < warp ? warp_n[lane] : 0, all = warp_n[lane];  // of the warps before, of all
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       mine += __shfl_xor_sync(0xffffffffu, mine, o);
       all += __shfl_xor_sync(0xffffffffu, all, o);
     }
-    int at = before + mine + upto - n;
+    int at = before + mine;
 #pragma unroll
     for (int i = 0; i < kListItems; ++i) {
-      const int t = t0 + threadIdx.x * kListItems + i;
-      if (t < T) place[t] = keep[i] ? at : y[i] == ignore ? -1 : -2;
-      if (keep[i]) {
-        index[at] = t;
-        column[at] = (int)y[i];
-        ++at;
+      const int t = first + 32 * i;
+      const bool keep = kept[i] >> lane & 1u;
+      const int to = at + __popc(kept[i] & ((1u << lane) - 1u));
+      if (t < T) place[t] = keep ? to : y[i] == ignore ? -1 : -2;
+      if (keep) {
+        index[to] = t;
+        column[to] = (int)y[i];
       }
+      at += __popc(kept[i]);
     }
     before += all;
     __syncthreads();
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(256)
 
 // Sums over `parts` per-row partials, 32 rows per block, 16 threads per row:
 // loss and lse (kStats), or alpha and gg (kAlpha).
-constexpr int kJoinRows = 32, kJoinWays = 16;
+constexpr int kJoinRows = 32, kJoinWays = 16, kJoinLoads = 8;
 
 __global__ void __launch_bounds__(kJoinRows* kJoinWays)
     join_stats_kernel(const float2* part, int parts, const int* place, const float* picked, int T, float* loss,
@@ -260,15 +263,20 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWays)
   const int at = t < T ? place[t] : -1;
   float m = -INFINITY, s = 0.f;
   if (at >= 0) {
-    for (int i = threadIdx.y; i < parts; i += kJoinWays) {
-      const float2 q = part[(size_t)i * T + at];
-      const float top = fmaxf(m, q.x);
-      if (top > -INFINITY) {
-        s = (m > -INFINITY ? s * expf(m - top) : s) + (q.x > -INFINITY ? q.y * expf(q.x - top) : q.y);
-        m = top;
-      } else {
-        s += q.y;
+    for (int i0 = threadIdx.y; i0 < parts; i0 += kJoinWays * kJoinLoads) {
+      float2 q[kJoinLoads];  // loads first: their latency would be paid one by one
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < kJoinLoads; ++u) {
+        const int i = i0 + u * kJoinWays;
+        q[u] = i < parts ? part[(size_t)i * T + at] : make_float2(-INFINITY, 0.f);
       }
+#pragma unroll
+      for (int u = 0; u < kJoinLoads; ++u) top = fmaxf(top, q[u].x);
+      if (m > -INFINITY) s *= expf(m - top);
+#pragma unroll
+      for (int u = 0; u < kJoinLoads; ++u) s += q[u].x > -INFINITY ? q[u].y * expf(q[u].x - top) : q[u].y;
+      m = top;
     }
   }
   sh[threadIdx.y][threadIdx.x] = make_float2(m, s);
@@ -300,7 +308,16 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWays)
   const int at = t < T_ ? place[t] : -1;
   float s = 0.f;
   if (at >= 0) {
-    for (int i = threadIdx.y; i < parts; i += kJoinWays) s += sums[(size_t)i * T_ + at];
+    for (int i0 = threadIdx.y; i0 < parts; i0 += kJoinWays * kJoinLoads) {
+      float q[kJoinLoads];
+#pragma unroll
+      for (int u = 0; u < kJoinLoads; ++u) {
+        const int i = i0 + u * kJoinWays;
+        q[u] = i < parts ? sums[(size_t)i * T_ + at] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kJoinLoads; ++u) s += q[u];
+    }
   }
   sh[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
@@ -319,6 +336,7 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWays)
     float b = 0.f;
     if (from >= 0) {
       const int y = column[from];
+#pragma unroll 4
       for (int c = threadIdx.x; c < D; c += 32) {
         if (UH) b += (float)UH[(size_t)r * D + c] * (float)W[(size_t)y * D + c];
         if (UW) b += (float)H[(size_t)r * D + c] * (float)UW[(size_t)y * D + c];
@@ -346,9 +364,14 @@ __global__ void __launch_bounds__(256)
   const int at = place[r];
   if (at >= 0) {
     const float gm = totals->gmax;
-    for (int s = 0; s < splits; ++s) {
-      const float4 f = *reinterpret_cast<const float4*>(slab + s * stride + (long long)at * Dp + c);
-      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+      float4 f[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        f[u] = s0 + u < splits ? *reinterpret_cast<const float4*>(slab + (s0 + u) * stride + (long long)at * Dp + c)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[0] += f[u].x, v[1] += f[u].y, v[2] += f[u].z, v[3] += f[u].w;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= gm;
