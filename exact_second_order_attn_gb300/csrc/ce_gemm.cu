@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
   if (warp == 8) {
     // ------------------------------------------------------------------ TMA
-    if (live && (tid & 31) == 0) {
+    if (live) {  // the whole warp runs the loop; one lane issues (elect.sync)
+      const uint32_t full0 = map_rank(smem_u32(&ctrl.full[0]), 0);
       const uint32_t stage_bytes = 2 * (C::DUAL ? C::A_BYTES * (1 + p.has_ua) + C::B_BYTES * (1 + p.has_ub) : C::STAGE);
       Place<C::NST> at;
       long long issued = 0;
@@ -414,10 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const CUtensorMap* mb = &p.b[p.seg[s].b];
             for (int k = kc; k < ke; ++k, ++issued, at.next()) {
               const int st = at.s;
-              if (!(ok = mbar_wait(&ctrl.empty[st], at.pass ^ 1, wt))) break;
+              if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.empty[st], at.pass ^ 1, wt)))) break;
               if (p.stall && issued == 0) continue;  // test hook: nothing fills the first stage
-              const uint32_t bar = map_rank(smem_u32(&ctrl.full[st]), 0);
-              if (rank == 0) mbar_arrive_expect_tx(&ctrl.full[st], stage_bytes);
+              const uint32_t bar = full0 + 8 * st;
+              if (rank == 0) mbar_expect_tx_w(&ctrl.full[st], stage_bytes);
               const uint32_t da = sm0 + st * C::STAGE, db = da + (C::DUAL ? 2 : 1) * C::A_BYTES;
               if (C::A_MN) {
                 tma_load_2d_pair(da, ma, bar, row, k * kBK);
