@@ -48,16 +48,15 @@ struct EpArgs {
   float2* part;           // kStats: (max, sum) [parts][T], two parts per tile of columns
   float* sums;            // kAlpha: row sums [parts][T], two parts per tile of columns
   float* picked;          // kStats: [T], z at the target
-  uint16_t* planes[2 * kPlanes];  // G planes [T][ld], then Z planes
-  long long ld;
   // kSlab, kOut
   void* out;
   long long out_ld, slab;  // elements between rows, between split slabs
-  int accumulate, out_bf16, out_vec;
+  int accumulate, out_bf16, out_map;  // out_map: bf16 results leave through GemmArgs::c[0]
 };
 
 struct GemmArgs {
   CUtensorMap a[kMaxMaps], b[kMaxMaps];
+  CUtensorMap c[kMaxMaps];  // store_map()s: kGrad, kGrad2: G planes, then Z planes; kOut: the output
   Seg seg[kMaxSegs];
   int nseg;
   int fp32;             // operands stand for fp32 (kPlanes planes, sums kept to fp32)
@@ -90,6 +89,9 @@ cudaError_t gemm(Epilogue ep, const GemmArgs& g, cudaStream_t s);
 // 2-D map of a bf16 matrix [rows][cols] with `ld` elements per row and a box
 // of box_rows x 64 columns, 128-byte swizzle.
 bool matrix_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows);
+
+// The same matrix as the epilogue stores it: boxes of 32 x 32, 64-byte swizzle.
+bool store_map(CUtensorMap* m, void* base, long long rows, long long cols, long long ld);
 
 }  // namespace ce
 }  // namespace fbob

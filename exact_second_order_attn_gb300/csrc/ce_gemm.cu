@@ -50,6 +50,7 @@ constexpr int kTmemCols = 512;
 constexpr int kBufCols = 256;     // accumulator columns per tile in flight
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kBoxBytes = 32 * 32 * 2;  // an outgoing box: a warp's 32 rows x 32 columns of bf16
 constexpr int kChainBlocks = 2;   // 128 columns of the contraction
 
 template <int EP>
@@ -62,7 +63,8 @@ struct Cfg {
   static constexpr int B_BYTES = BN / 2 * kBK * 2;
   static constexpr int STAGE = (A_BYTES + B_BYTES) * (DUAL ? 2 : 1);  // [A | B], or [A | UA | B | UB]
   static constexpr int NST = 196608 / STAGE;  // 6, or 4 with two accumulators
-  static constexpr int SMEM = NST * STAGE;
+  static constexpr int OUT_OFF = NST * STAGE;  // the epilogue warps' outgoing boxes
+  static constexpr int SMEM = OUT_OFF + kEpWarps * 2 * kBoxBytes;
   static_assert(SMEM + 1024 <= 232448, "shared memory budget");
 };
 
@@ -120,9 +122,43 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* r) {
                : "memory");
 }
 
+// An epilogue warp's way out for bf16 results: 32 rows x 32 columns (lane =
+// row) go to shared memory with the 64-byte swizzle and leave as one bulk tensor
+// store, clipped at the matrix's ends (a box starts inside it); two boxes take
+// turns.  Stored from the
+// registers, a row per lane, the same bytes cost the load-store unit 32 lines
+// per instruction and bound the G kernel (8,300 of 8,800 cycles per tile).
+struct Outbox {
+  uint32_t smem;  // this warp's two boxes
+  int turn;
+  __device__ __forceinline__ void put(const CUtensorMap* map, int x, int y, const uint32_t (&w)[16]) {
+    const uint32_t lane = threadIdx.x & 31, box = smem + turn * kBoxBytes;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();  // the box's earlier content has left
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c)
+      st_shared_v4(box + lane * 64 + ((c ^ ((lane >> 1) & 3u)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2],
+                   w[4 * c + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile(
+          "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+          "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+          "r"(box), "r"(x), "r"(y)
+          : "memory");
+    }
+    turn ^= 1;
+  }
+  // Everything has been written (the lane that issued the stores).
+  __device__ __forceinline__ void drain() const {
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+};
+
 // 32 values as bf16 planes: plane k holds the rounding of what planes 0..k-1 left.
 template <bool FP32>
-__device__ __forceinline__ void store_planes(uint16_t* const* planes, size_t at, float* v) {
+__device__ __forceinline__ void store_planes(Outbox& out, const CUtensorMap* maps, int x, int y, float* v) {
 #pragma unroll
   for (int k = 0; k < (FP32 ? kPlanes : 1); ++k) {
     uint32_t w[16];
@@ -134,8 +170,7 @@ __device__ __forceinline__ void store_planes(uint16_t* const* planes, size_t at,
       v[2 * j] -= f.x;
       v[2 * j + 1] -= f.y;
     }
-    st_global_v8(planes[k] + at, w);
-    st_global_v8(planes[k] + at + 16, w + 8);
+    out.put(maps + k, x, y, w);
   }
 }
 
@@ -159,11 +194,12 @@ struct Acc {
 // The epilogue of one tile for this thread's row: `row` in the output, n0 the
 // first column, part the index of this half tile's row statistics.
 template <int EP, bool FP32>
-__device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc, int rows, int row, int n0, int part,
-                                         int split) {
+__device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc, Outbox& out, int rows, int row, int n0,
+                                         int part, int split) {
   constexpr int kUnroll = FP32 ? 4 : 1;
   const EpArgs& e = p.ep;
   const bool live = row < rows;
+  const int box_row = row - (int)(threadIdx.x & 31);  // of the warp's first row
   if constexpr (EP == kStats) {
     const int y = live ? e.target[row] : -1;
     float m = -INFINITY, s = 0.f;
@@ -201,7 +237,6 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
     const int y = live ? e.target[row] : -1, own = live ? e.index[row] : 0;
     const float at = live ? e.lse[own] : 0.f, gm = *e.gmax;
     const float gs = live && gm != 0.f ? e.g[own] / gm : 0.f;
-    const bool stored = row < min(p.M, token_steps(rows) * kBK);  // rows past the tokens: zero
 #pragma unroll kUnroll
     for (int c = 0; c < 128; c += 32) {
       float v[32];
@@ -213,7 +248,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] -= j == hit ? gs : 0.f;
       }
-      if (stored && n < e.ld) store_planes<FP32>(e.planes, (size_t)row * e.ld + n, v);
+      if (box_row < p.M && n < p.N) store_planes<FP32>(out, p.c, n, box_row, v);  // rows past the tokens: zero
     }
   } else if constexpr (EP == kAlpha) {
     const float at = live ? e.lse[e.index[row]] : 0.f;
@@ -232,7 +267,6 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
     const int y = live ? e.target[row] : -1, own = live ? e.index[row] : 0;
     const float at = live ? e.lse[own] : 0.f, al = live ? e.alpha[row] : 0.f, gm = *e.gmax;
     const float gs = live && gm != 0.f ? e.g[own] / gm : 0.f;
-    const bool stored = row < min(p.M, token_steps(rows) * kBK);  // rows past the tokens: zero
 #pragma unroll kUnroll
     for (int c = 0; c < 64; c += 32) {
       float z[32], b[32];
@@ -248,13 +282,13 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
 #pragma unroll
         for (int j = 0; j < 32; ++j) z[j] -= j == hit ? gs : 0.f;
       }
-      if (stored && n < e.ld) {
-        store_planes<FP32>(e.planes, (size_t)row * e.ld + n, z);
-        store_planes<FP32>(e.planes + kPlanes, (size_t)row * e.ld + n, b);
+      if (box_row < p.M && n < p.N) {  // rows past the tokens: zero
+        store_planes<FP32>(out, p.c, n, box_row, z);
+        store_planes<FP32>(out, p.c + kPlanes, n, box_row, b);
       }
     }
   } else if constexpr (EP == kSlab) {
-    float* out = static_cast<float*>(e.out) + (size_t)split * e.slab + (size_t)row * e.out_ld;
+    float* slab = static_cast<float*>(e.out) + (size_t)split * e.slab + (size_t)row * e.out_ld;
 #pragma unroll kUnroll
     for (int c = 0; c < 128; c += 32) {
       float v[32];
@@ -263,7 +297,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {  // out_ld is a multiple of 8
         if (live && n + j < e.out_ld) {
-          float* o = out + n + j;
+          float* o = slab + n + j;
           if (e.accumulate) {
             const float4 h = *reinterpret_cast<const float4*>(o), i = *reinterpret_cast<const float4*>(o + 4);
             v[j] += h.x, v[j + 1] += h.y, v[j + 2] += h.z, v[j + 3] += h.w;
@@ -283,28 +317,24 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
       const int n = n0 + c;
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= gm;
-      if (!live) {
+      if (!FP32 && e.out_map) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        if (box_row < p.M && n < p.N) out.put(p.c, n, box_row, w);
+      } else if (!live) {
       } else if (e.out_bf16) {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.out) + at + n;
 #pragma unroll
-        for (int j = 0; j < 32; j += 16) {
-          if (e.out_vec && n + j + 16 <= p.N) {
-            uint32_t w[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] = pack_bf16x2(v[j + 2 * q], v[j + 2 * q + 1]);
-            st_global_v8(o + j, w);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              if (n + j + q < p.N) o[j + q] = __float2bfloat16_rn(v[j + q]);
-            }
-          }
+        for (int j = 0; j < 32; ++j) {
+          if (n + j < p.N) o[j] = __float2bfloat16_rn(v[j]);
         }
       } else {
         float* o = static_cast<float*>(e.out) + at + n;
+        const bool whole = (reinterpret_cast<uintptr_t>(e.out) & 31) == 0 && e.out_ld % 8 == 0;
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
-          if (e.out_vec && n + j + 8 <= p.N) {
+          if (whole && n + j + 8 <= p.N) {
             st_global_v8(o + j, reinterpret_cast<const uint32_t*>(v + j));
           } else {
 #pragma unroll
@@ -511,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const int half = warp >> 2, r = (warp & 3) * 32 + (tid & 31);
     const uint32_t lane = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t freed = map_rank(smem_u32(&ctrl.tile_empty[0]), 0);
+    Outbox out{sm0 + C::OUT_OFF + warp * 2 * kBoxBytes, 0};
     int chain = 0;
     bool ok = live;
     for (int t = pair; ok && t < total; t += pairs) {
@@ -540,13 +571,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           __syncwarp();
           if ((tid & 31) == 0) mbar_arrive_cluster(freed + buf * 8);
         }
-        if (ok) epilogue<EP, true>(p, Acc<true>{0, sum}, rows, row, n0, 2 * n + half, split);
+        if (ok) epilogue<EP, true>(p, Acc<true>{0, sum}, out, rows, row, n0, 2 * n + half, split);
       } else {
         const int buf = chain & 1;
         // warp-uniform: the TMEM loads that follow are warp-collective
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
         tc_fence_after();
-        epilogue<EP, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr}, rows, row, n0, 2 * n + half,
+        epilogue<EP, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr}, out, rows, row, n0, 2 * n + half,
                             split);
         tc_fence_before();
         __syncwarp();
@@ -554,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         ++chain;
       }
     }
+    out.drain();
   }
   __syncwarp();
   tc_fence_before();

@@ -540,10 +540,10 @@ struct Run {
     GemmArgs g = base();
     if (!logits(g, second)) return cudaErrorInvalidValue;
     g.N = cols, g.n_base = g.b0 = c0;
-    g.ep.alpha = at<float>(p.alpha), g.ep.ld = p.ld;
+    g.ep.alpha = at<float>(p.alpha);
     for (int k = 0; k < p.np; ++k) {
-      g.ep.planes[k] = piece_plane(0, k);
-      if (second) g.ep.planes[kPlanes + k] = piece_plane(1, k);
+      if (!store_map(g.c + k, piece_plane(0, k), a.T, cols, p.ld)) return cudaErrorInvalidValue;
+      if (second && !store_map(g.c + kPlanes + k, piece_plane(1, k), a.T, cols, p.ld)) return cudaErrorInvalidValue;
     }
     CE_TRY(gemm(second ? kGrad2 : kGrad, g, s));
     if (a.dH) {  // Z W + G UW, or G W
@@ -579,7 +579,9 @@ struct Run {
       g.M = cols, g.N = a.D, g.K = a.T;
       g.ep.out = static_cast<char*>(a.dW) + (size_t)c0 * a.D * (a.bf16 ? 2 : 4);
       g.ep.out_ld = a.D, g.ep.out_bf16 = a.bf16;
-      g.ep.out_vec = a.D % (a.bf16 ? 16 : 8) == 0 && aligned(a.dW, 32);  // rows of 32-byte stores
+      // bulk stores want 16-byte rows; a piece's rows end with a tile's, or with W's
+      g.ep.out_map = a.bf16 && a.D % 8 == 0 && aligned(a.dW, 16);
+      if (g.ep.out_map && !store_map(g.c, g.ep.out, cols, a.D, a.D)) return cudaErrorInvalidValue;
       CE_TRY(gemm(kOut, g, s));
     }
     return cudaSuccess;

@@ -39,16 +39,28 @@ bool make_bf16_map(CUtensorMap* m, const void* base, int BH, int N, int D, int r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool ce::matrix_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows) {
+namespace {
+
+bool map_2d(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows, int box_cols,
+            CUtensorMapSwizzle swizzle) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool ce::matrix_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows) {
+  return map_2d(m, base, rows, cols, ld, box_rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool ce::store_map(CUtensorMap* m, void* base, long long rows, long long cols, long long ld) {
+  return map_2d(m, base, rows, cols, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace fbob
