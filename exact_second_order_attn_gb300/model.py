@@ -75,7 +75,7 @@ class _NormBwd(torch.autograd.Function):
         want = ctx.needs_input_grad[:3]
         if (ux is None and uw is None and ub is None) or not any(want):
             return None, None, None, None, None, None, None
-        wt = _model._weight_dtype(x, w, uw, ub)
+        wt = next((u.dtype for u in (w, uw, ub) if u is not None), x.dtype)
         ux = torch.zeros_like(x) if ux is None else ux.contiguous()
         uw, ub = (None if u is None else u.to(wt).contiguous() for u in (uw, ub))
         gx, gw, gdy = _model.fbob_layer_norm_bob(x, w, mean, rstd, dy, ux, uw, ub, want=want)

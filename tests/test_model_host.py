@@ -19,12 +19,6 @@ def lib():
     return _lib.load()
 
 
-def test_packed_heads_match_the_structure():
-    from exact_second_order_attn_gb300 import _model
-    e = _lib.RotaryHeads(11, 22, 3, (4, 5, 6), (7, 8, 9))
-    assert bytes(e) == _model._HEADS.pack(11, 22, 3, 4, 5, 6, 7, 8, 9)
-
-
 def rotary_call(lib, r, B=1, N=4, d=8, dtype=0, H=2, count=1, x=0x1000, y=0x2000, xs=None, ys=None, positions=None,
                 size=8, step=0):
     t = (_lib.RotaryHeads * 2)()
