@@ -52,9 +52,11 @@ constexpr uint64_t kDrainNs = 200000000ull;
 enum Owner { kWarp, kBlock256, kBlock512 };
 template <int OWN>
 constexpr int kMaxThreads = OWN == kBlock512 ? 512 : 256;
-// Blocks of 512 threads read the weights in place: staging would not fit.
-template <int OWN>
-constexpr bool kStaged = OWN != kBlock512;
+// Weights are staged in shared memory where the rows lie off 16-byte bounds
+// (blocks of 512 threads never take such rows as vectors) and read in place
+// otherwise: staging costs a launch of few rows 4 us.
+template <int VEC, bool EVEN>
+constexpr bool kStaged = VEC > 1 && !EVEN;
 
 // Rows taken at a time: N tensors' rows of E elements in at most 48 registers.
 template <typename T, int E, int N>
@@ -284,7 +286,7 @@ struct Weights {
   static __host__ __device__ int bytes(int D) { return (D + 2 * 8) * (int)sizeof(WT) / 16 * 16 + 16; }
   __device__ __forceinline__ Weights(const WT* src, char*& dyn, const C& c) {
     p = src;
-    if (!src || !kStaged<OWN> || VEC == 1) return;
+    if (!src || !kStaged<VEC, EVEN>) return;
     WT* q = reinterpret_cast<WT*>(dyn);
     dyn += bytes(c.D);
     const int span = (c.D + c.shift + VEC - 1) / VEC * VEC;
@@ -395,11 +397,10 @@ inline Layout layout(int D, std::initializer_list<const void*> tensors, std::ini
   bool same = true;  // the optional ones may be null
   for (const void* p : tensors) same = same && (!p || (reinterpret_cast<uintptr_t>(p) & 15) == at);
   const int bytes = D * (int)sizeof(T);
-  const bool even = at == 0 && bytes % 16 == 0;
-  // weights that are not staged are read in whole vectors from where they lie
-  bool in_place = even;
-  for (const void* p : weights) in_place = in_place && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-  if (!same || (!in_place && D + row::kFull<T> > 4096)) return Layout{false, false, 1, D};
+  // even rows read the weights in whole vectors from where they lie
+  bool even = at == 0 && bytes % 16 == 0;
+  for (const void* p : weights) even = even && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+  if (!same || (!even && D + row::kFull<T> > 4096)) return Layout{false, false, 1, D};
   int period = 1;
   while (period * bytes % 16 != 0) period *= 2;
   return Layout{true, even, period, even ? D : D + row::kFull<T> - 1};
@@ -434,7 +435,9 @@ inline void dispatch(const Layout& l, F&& f) {
   constexpr int V = row::kFull<T>;
   auto with = [&](auto e, auto own) {
     if (l.even) f(std::integral_constant<int, V>{}, e, own, std::true_type{});
-    else if (!l.vec) f(std::integral_constant<int, 1>{}, e, own, std::false_type{});
+    // tensors that are shifted differently: the widest kernel of a warp serves all its rows
+    else if (!l.vec) f(std::integral_constant<int, 1>{}, std::integral_constant<int, own() == kWarp ? 32 : e()>{}, own,
+                       std::false_type{});
     // rows off the bounds with more than 4096 columns never come as vectors
     else if constexpr (own() != kBlock512) f(std::integral_constant<int, V>{}, e, own, std::false_type{});
   };
@@ -454,7 +457,7 @@ template <typename T, typename WT, int N, int VEC, int E, int OWN, bool EVEN>
 inline int ring_stages(int D, long long rows, const Layout& l, const Shape& sh, int nw, bool sums, int* smem) {
   constexpr int R = kRows<T, E, N>;
   using G = Ring<T, N, R, VEC, OWN, EVEN>;
-  const int fixed = kStaged<OWN> && VEC > 1 ? nw * Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0;
+  const int fixed = kStaged<VEC, EVEN> ? nw * Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0;
   const int per = G::kOwners * N * R * G::slot_bytes(D);
   int s = (kRingMemory / (kResident<T, E, OWN> * blocks_per_max(sh.threads)) - fixed) / per;
   if (s > kMaxStages) s = kMaxStages;

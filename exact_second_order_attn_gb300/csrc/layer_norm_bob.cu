@@ -17,6 +17,7 @@
 #include <initializer_list>
 #include <type_traits>
 
+#include "launch.cuh"
 #include "layer_norm.cuh"
 
 namespace fbob {
@@ -31,10 +32,12 @@ __global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
   constexpr int R = kRows<T, E, 3>, U = kUnits<VEC>;
   using G = Ring<T, 3, R, VEC, OWN, EVEN>;
   extern __shared__ __align__(16) char dyn[];
+  allow_next();
+  wait_previous();
   __shared__ typename G::Bars bars;
   const T* const tensors[] = {x, dy, u};
   char* const slots =
-      dyn + (kStaged<OWN> && VEC > 1 ? ((w != nullptr) + (uw != nullptr) + (ub != nullptr)) * Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0);
+      dyn + (kStaged<VEC, EVEN> ? ((w != nullptr) + (uw != nullptr) + (ub != nullptr)) * Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0);
   const G ring(tensors, rows, D, period, stages, slots, bars);
   const Cols<VEC, E, OWN, EVEN> c(D, VEC == 1 ? 0 : ring.shift());
   char* free = dyn;
@@ -157,11 +160,7 @@ cudaError_t launch(const NormArgs& a, const DevCtx& ctx, cudaStream_t s) {
     int smem = 0;
     const int stages = ring_stages<T, WT, 3, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w + !!a.uw + !!a.ub, a.gw != nullptr, &smem);
     if ((e_ = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return;
-    kernel<<<sh.blocks, sh.threads, smem, s>>>(
-        static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd, static_cast<const T*>(a.dy),
-        static_cast<const T*>(a.ux), static_cast<const WT*>(a.uw), static_cast<const WT*>(a.ub),
-        static_cast<T*>(a.gx), static_cast<T*>(a.gdy), a.gw ? a.ws : nullptr, a.rows, a.D, l.period, stages, ctx.err,
-        ctx.wait_ns);
+    e_ = chained(kernel, dim3(sh.blocks), dim3(sh.threads), smem, 1, s, static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd, static_cast<const T*>(a.dy), static_cast<const T*>(a.ux), static_cast<const WT*>(a.uw), static_cast<const WT*>(a.ub), static_cast<T*>(a.gx), static_cast<T*>(a.gdy), a.gw ? a.ws : nullptr, a.rows, a.D, l.period, stages, ctx.err, ctx.wait_ns);
   });
   prof_end(s);
   const cudaError_t e = e_ != cudaSuccess ? e_ : cudaGetLastError();

@@ -6,6 +6,7 @@
 #include <initializer_list>
 #include <type_traits>
 
+#include "launch.cuh"
 #include "layer_norm.cuh"
 
 namespace fbob {
@@ -20,9 +21,11 @@ __global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
   constexpr int R = kRows<T, E, 2>, U = kUnits<VEC>;
   using G = Ring<T, 2, R, VEC, OWN, EVEN>;
   extern __shared__ __align__(16) char dyn[];
+  allow_next();
+  wait_previous();
   __shared__ typename G::Bars bars;
   const T* const tensors[] = {x, dy};
-  char* const slots = dyn + (kStaged<OWN> && VEC > 1 && w ? Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0);
+  char* const slots = dyn + (kStaged<VEC, EVEN> && w ? Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0);
   const G ring(tensors, rows, D, period, stages, slots, bars);
   const Cols<VEC, E, OWN, EVEN> c(D, VEC == 1 ? 0 : ring.shift());
   char* free = dyn;
@@ -119,13 +122,21 @@ constexpr int kRedCols = 32, kRedRows = 32;
 
 __global__ void __launch_bounds__(kRedCols * kRedRows)
     reduce_kernel(const float* in, int parts, int D, void* out0, void* out1, int out_bf16) {
+  allow_next();
+  wait_previous();
   __shared__ float sh[kRedRows][kRedCols + 1];
   void* out = blockIdx.y == 0 ? out0 : out1;
   const int col = blockIdx.x * kRedCols + threadIdx.x;
   float t = 0.f;
   if (col < D) {
     const float* src = in + (size_t)blockIdx.y * parts * D + col;
-    for (int r = threadIdx.y; r < parts; r += kRedRows) t += src[(size_t)r * D];
+    for (int r0 = threadIdx.y; r0 < parts; r0 += 4 * kRedRows) {
+      float q[4];  // loads first: their latency would be paid one by one
+#pragma unroll
+      for (int u = 0; u < 4; ++u) q[u] = r0 + u * kRedRows < parts ? src[(size_t)(r0 + u * kRedRows) * D] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) t += q[u];
+    }
   }
   sh[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
@@ -154,9 +165,7 @@ cudaError_t launch(const NormArgs& a, const DevCtx& ctx, cudaStream_t s) {
     int smem = 0;
     const int stages = ring_stages<T, WT, 2, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w, a.dw || a.db, &smem);
     if ((e_ = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return;
-    kernel<<<sh.blocks, sh.threads, smem, s>>>(static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd,
-                                               static_cast<const T*>(a.dy), static_cast<T*>(a.dx), dwp, dbp, a.rows,
-                                               a.D, l.period, stages, ctx.err, ctx.wait_ns);
+    e_ = chained(kernel, dim3(sh.blocks), dim3(sh.threads), smem, 1, s, static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd, static_cast<const T*>(a.dy), static_cast<T*>(a.dx), dwp, dbp, a.rows, a.D, l.period, stages, ctx.err, ctx.wait_ns);
   });
   prof_end(s);
   const cudaError_t e = e_ != cudaSuccess ? e_ : cudaGetLastError();
@@ -168,10 +177,10 @@ cudaError_t launch(const NormArgs& a, const DevCtx& ctx, cudaStream_t s) {
 
 cudaError_t reduce_parts(const float* in, int parts, int D, void* out0, void* out1, bool out_bf16, cudaStream_t s) {
   prof_begin(s, "layer_norm_columns");
-  reduce_kernel<<<dim3((D + kRedCols - 1) / kRedCols, out1 ? 2 : 1), dim3(kRedCols, kRedRows), 0, s>>>(
-      in, parts, D, out0, out1, out_bf16);
+  const cudaError_t e = chained(reduce_kernel, dim3((D + kRedCols - 1) / kRedCols, out1 ? 2 : 1),
+                                dim3(kRedCols, kRedRows), 0, 1, s, in, parts, D, out0, out1, (int)out_bf16);
   prof_end(s);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace ln

@@ -3,6 +3,7 @@
 #include <initializer_list>
 #include <type_traits>
 
+#include "launch.cuh"
 #include "layer_norm.cuh"
 
 namespace fbob {
@@ -16,9 +17,11 @@ __global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
   constexpr int R = kRows<T, E, 1>, U = kUnits<VEC>;
   using G = Ring<T, 1, R, VEC, OWN, EVEN>;
   extern __shared__ __align__(16) char dyn[];
+  allow_next();
+  wait_previous();
   __shared__ typename G::Bars bars;
   const T* const tensors[] = {x};
-  const int fixed = kStaged<OWN> && VEC > 1 ? ((w != nullptr) + (b != nullptr)) * Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0;
+  const int fixed = kStaged<VEC, EVEN> ? ((w != nullptr) + (b != nullptr)) * Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0;
   const G ring(tensors, rows, D, period, stages, dyn + fixed, bars);
   const Cols<VEC, E, OWN, EVEN> c(D, VEC == 1 ? 0 : ring.shift());
   char* free = dyn;
@@ -116,9 +119,7 @@ cudaError_t launch(const NormArgs& a, const DevCtx& ctx, cudaStream_t s) {
     int smem = 0;
     const int stages = ring_stages<T, WT, 1, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w + !!a.b, false, &smem);
     if ((e_ = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return;
-    kernel<<<sh.blocks, sh.threads, smem, s>>>(static_cast<const T*>(a.x), static_cast<const WT*>(a.w),
-                                               static_cast<const WT*>(a.b), static_cast<T*>(a.y), a.mean, a.rstd,
-                                               a.rows, a.D, a.eps, l.period, stages, ctx.err, ctx.wait_ns);
+    e_ = chained(kernel, dim3(sh.blocks), dim3(sh.threads), smem, 1, s, static_cast<const T*>(a.x), static_cast<const WT*>(a.w), static_cast<const WT*>(a.b), static_cast<T*>(a.y), a.mean, a.rstd, a.rows, a.D, a.eps, l.period, stages, ctx.err, ctx.wait_ns);
   });
   prof_end(s);
   return e_ != cudaSuccess ? e_ : cudaGetLastError();
