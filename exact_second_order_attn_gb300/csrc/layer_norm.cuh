@@ -290,10 +290,19 @@ struct Weights {
     WT* q = reinterpret_cast<WT*>(dyn);
     dyn += bytes(c.D);
     const int span = (c.D + c.shift + VEC - 1) / VEC * VEC;
-    for (int i = threadIdx.x; i < span; i += blockDim.x) {
-      const int col = i - c.shift;
-      if (col >= 0 && col < c.D) q[i] = src[col];
-      else q[i] = (WT)0.f;
+    for (int i0 = threadIdx.x; i0 < span; i0 += 8 * blockDim.x) {
+      WT v[8];  // loads first: their latency would be paid one by one
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int col = i0 + u * (int)blockDim.x - c.shift;
+        v[u] = (WT)0.f;
+        if (col >= 0 && col < c.D) v[u] = src[col];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * (int)blockDim.x;
+        if (i < span) q[i] = v[u];
+      }
     }
     p = q + c.shift;
   }
