@@ -559,7 +559,10 @@ struct Run {
       } else {
         products(g, 0, 0);
       }
-      g.M = a.T, g.N = a.D, g.K = cols, g.b0 = c0, g.splits = p.splits;
+      g.M = a.T, g.N = a.D, g.K = cols, g.b0 = c0;
+      // every slab gets at least one step: a short last piece adds to the first slabs only
+      const int steps = (cols + kBK - 1) / kBK;
+      g.splits = p.splits < steps ? p.splits : steps;
       g.ep.out = at<float>(p.slab), g.ep.out_ld = p.Dp, g.ep.slab = (long long)a.T * p.Dp, g.ep.accumulate = !first;
       CE_TRY(gemm(kSlab, g, s));
     }

@@ -109,6 +109,15 @@ def test_linear_ce_pieces(dtype):
         assert torch.equal(got["dW"], whole["dW"]) and torch.equal(got["gW"], whole["gW"])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V,piece", [(5121, 1280), (5 * 1280, 1280), (20481, 5120), (2049, 2048)])
+def test_linear_ce_short_last_piece(dtype, V, piece):
+    """A last piece of one class, after pieces whose contraction is cut into
+    several slabs."""
+    t = make(9, 32, V, dtype, seed=V)
+    compare(t, chain(t, piece=piece))
+
+
 def test_linear_ce_peaked_rows():
     """Targets that hold nearly all of the probability, and others none."""
     t = make(150, 128, 700, "bf16", seed=21, spread=12.0)
