@@ -62,7 +62,8 @@ struct GemmArgs {
   int fp32;             // operands stand for fp32 (kPlanes planes, sums kept to fp32)
   int has_ua, has_ub;   // two accumulators: which second-order operands are there
   int K;                // contraction length
-  int splits;           // K is cut into this many slabs (kSlab)
+  int splits;           // K is cut into at most this many slabs (kSlab)
+  const int* slabs;     // the number wanted, on the device (kSlab)
   int M, N;             // output rows and columns
   // The counted tokens lie in the first *count of T rows.  They are the rows of
   // kStats .. kSlab (M = T at most) and the contraction of kOut (K = T at most);

@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   const int tokens = *p.count, written = min(p.M, token_steps(tokens) * kBK);
   const int rows = EP == kOut ? p.M : tokens;                             // that hold results
   const int tile_rows = EP == kGrad || EP == kGrad2 ? written : rows;     // that are worked on
-  const Tiles ts{(tile_rows + kTileM - 1) / kTileM, (p.N + C::BN - 1) / C::BN, p.splits,
+  const Tiles ts{(tile_rows + kTileM - 1) / kTileM, (p.N + C::BN - 1) / C::BN, EP == kSlab ? min(p.splits, *p.slabs) : 1,
                  EP == kOut ? token_steps(tokens) : (p.K + kBK - 1) / kBK};
   const int total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   // the steps of K up to which an accumulator chain that starts at kc runs

