@@ -1,7 +1,8 @@
 """GB300 (sm_103a) exact attention backward-over-backward.
 
 The compute lives in ``libfbob.so`` (hand-written CUDA behind the C ABI in
-``include/fbob.h``); this package is its ctypes binding.  Build the library
+``include/fbob.h``); this package is its binding (ctypes for the attention, a
+compiled module for the operators around it).  Build the library
 with ``exact_second_order_attn_gb300.build.build()``.
 """
 from ._lib import (  # noqa: F401

@@ -60,6 +60,7 @@ struct GemmArgs {
   Seg seg[kMaxSegs];
   int nseg;
   int fp32;             // operands stand for fp32 (kPlanes planes, sums kept to fp32)
+  int planes;           // of G and of Z that kGrad and kGrad2 store
   int has_ua, has_ub;   // two accumulators: which second-order operands are there
   int K;                // contraction length
   int splits;           // K is cut into at most this many slabs (kSlab)

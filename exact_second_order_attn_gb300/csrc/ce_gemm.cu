@@ -158,9 +158,10 @@ struct Outbox {
 
 // 32 values as bf16 planes: plane k holds the rounding of what planes 0..k-1 left.
 template <bool FP32>
-__device__ __forceinline__ void store_planes(Outbox& out, const CUtensorMap* maps, int x, int y, float* v) {
-#pragma unroll
-  for (int k = 0; k < (FP32 ? kPlanes : 1); ++k) {
+__device__ __forceinline__ void store_planes(Outbox& out, const CUtensorMap* maps, int n, int x, int y, float* v) {
+  // (fp32 unrolled; bf16 has one plane, two for few tokens)
+#pragma unroll(FP32 ? kPlanes : 1)
+  for (int k = 0; k < (FP32 ? kPlanes : n); ++k) {
     uint32_t w[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -248,7 +249,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] -= j == hit ? gs : 0.f;
       }
-      if (box_row < p.M && n < p.N) store_planes<FP32>(out, p.c, n, box_row, v);  // rows past the tokens: zero
+      if (box_row < p.M && n < p.N) store_planes<FP32>(out, p.c, p.planes, n, box_row, v);  // rows past the tokens: zero
     }
   } else if constexpr (EP == kAlpha) {
     const float at = live ? e.lse[e.index[row]] : 0.f;
@@ -283,8 +284,8 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
         for (int j = 0; j < 32; ++j) z[j] -= j == hit ? gs : 0.f;
       }
       if (box_row < p.M && n < p.N) {  // rows past the tokens: zero
-        store_planes<FP32>(out, p.c, n, box_row, z);
-        store_planes<FP32>(out, p.c + kPlanes, n, box_row, b);
+        store_planes<FP32>(out, p.c, p.planes, n, box_row, z);
+        store_planes<FP32>(out, p.c + kPlanes, p.planes, n, box_row, b);
       }
     }
   } else if constexpr (EP == kSlab) {

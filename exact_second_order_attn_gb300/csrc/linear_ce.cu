@@ -16,7 +16,10 @@
 // Dividing by gmax = max |g| (an fp32 factor of the results) keeps the target's
 // entry of G at p - 1 for a mean loss, where all g are equal: its rounding to
 // bf16 is then relative to p - 1 and not a systematic relative error of the
-// largest entry of every row.
+// largest entry of every row.  The roundings average out over many tokens; with
+// few a row of dW hangs on one or two of them (4 tokens: 1.6 times the error of a
+// result rounded once; 24: 1.05 times), so up to kExactTokens G and Z keep two
+// bf16 terms (2^-17): 14 us of 127 at 24 tokens x 50,257 classes x 768.
 //
 // fp32 inputs stand as three bf16 terms each (8 bits of the value per term);
 // the six products of terms whose magnitudes reach 2^-16 of the first are
@@ -37,13 +40,17 @@ namespace {
 constexpr int kPairs = 76;                        // block pairs of a GB300, for the split rule
 constexpr size_t kPieceBytes = 512ull << 20;      // G (and Z) of one piece of the vocabulary
 constexpr int kPieceStep = 256;
+constexpr int kExactTokens = 16;                  // G and Z in two bf16 terms up to here (bf16 inputs)
 
 size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+// bf16 terms of G and of Z.
+int grad_planes(const CeArgs& a) { return !a.bf16 ? kPlanes : a.T <= kExactTokens ? 2 : 1; }
 
 // Piece width: all of V if its G fits kPieceBytes, else equal pieces that do
 // (at least 2048 columns, so that a piece's products keep the device busy).
 int piece_cols(const CeArgs& a, bool second) {
-  const size_t per = (size_t)a.T * 2 * (a.bf16 ? 1 : kPlanes) * (second ? 2 : 1);
+  const size_t per = (size_t)a.T * 2 * grad_planes(a) * (second ? 2 : 1);
   size_t cols = a.piece > 0 ? (size_t)a.piece : kPieceBytes / (per ? per : 1);
   cols = up(cols < 2048 && a.piece <= 0 ? 2048 : cols, kPieceStep);
   const size_t whole = up(a.V, kPieceStep);
@@ -73,7 +80,7 @@ struct Totals {
 
 // Where everything lies in the workspace.
 struct Plan {
-  int np, Dp, ld, splits, stat_parts, alpha_parts;
+  int np, gp, Dp, ld, splits, stat_parts, alpha_parts;
   bool copy_w;
   size_t h, uh, w, uw, place, index, target, totals, part, sums, picked, alpha, planes, slab, bytes;
 };
@@ -81,6 +88,7 @@ struct Plan {
 Plan plan(const CeArgs& a, CePass pass) {
   Plan p;
   p.np = a.bf16 ? 1 : kPlanes;
+  p.gp = grad_planes(a);
   p.Dp = (int)up(a.D, 8);
   p.copy_w = !a.bf16 || a.D % 8 != 0;
   p.stat_parts = 2 * ((a.V + kTileN - 1) / kTileN);
@@ -107,7 +115,7 @@ Plan plan(const CeArgs& a, CePass pass) {
   p.part = take(!bwd, T * p.stat_parts * sizeof(float2));
   p.sums = take(bob, T * p.alpha_parts * 4);
   p.alpha = take(bob, T * 4);
-  p.planes = take(bwd, T * p.ld * 2 * p.np * (bob ? 2 : 1));
+  p.planes = take(bwd, T * p.ld * 2 * p.gp * (bob ? 2 : 1));
   p.slab = take(bwd, T * p.Dp * 4 * p.splits);
   p.bytes = at;
   return p;
@@ -206,28 +214,46 @@ __global__ void __launch_bounds__(kListThreads)
   }
 }
 
-// bf16 planes [rows][Dp] of the counted rows of H or UH (index given; then zero
-// rows up to a whole step of the contraction), or of W; zero in the padding.
-// One thread per 8 columns.
+// bf16 planes [np][rows][Dp] of up to four operands in one launch: of the counted
+// rows of H and UH (then zero rows up to a whole step of the contraction), and of
+// W and UW where they are not read in place; zero in the padding.  One thread per
+// 8 columns; an operand's blocks start at first_block.
+struct Operand {
+  const void* x;
+  uint16_t* planes;
+  long long rows;
+  unsigned first_block;
+  int tokens, vec;
+};
+struct Operands {
+  Operand o[4];
+  int n;
+};
+
 template <typename T>
 __global__ void __launch_bounds__(256)
-    planes_kernel(const T* x, const int* index, const Totals* totals, uint16_t* planes, long long rows, int D, int Dp,
-                  int np, int vec) {
+    planes_kernel(const __grid_constant__ Operands all, const int* index, const Totals* totals, int D, int Dp, int np) {
   allow_next();
   wait_previous();
+  int which = 0;
+  while (which + 1 < all.n && blockIdx.x >= all.o[which + 1].first_block) ++which;
+  const Operand& o = all.o[which];
+  const long long rows = o.rows;
+  uint16_t* const planes = o.planes;
+  const bool vec = o.vec;
   const int per = Dp / 8;
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long i = (long long)(blockIdx.x - o.first_block) * blockDim.x + threadIdx.x;
   const long long r = i / per;
   const int c = (int)(i - r * per) * 8;
   if (r >= rows) return;
-  const int count = index ? totals->count : 0;
-  if (index && r >= (long long)token_steps(count) * kBK) return;
+  const int count = o.tokens ? totals->count : 0;
+  if (o.tokens && r >= (long long)token_steps(count) * kBK) return;
   float v[8];
-  if (index && r >= count) {
+  if (o.tokens && r >= count) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
   } else {
-    const T* src = x + (index ? index[r] : r) * D + c;
+    const T* src = static_cast<const T*>(o.x) + (o.tokens ? index[r] : r) * D + c;
     if (vec) {
       if constexpr (sizeof(T) == 2) {
         const uint4 u = *reinterpret_cast<const uint4*>(src);
@@ -427,22 +453,6 @@ struct Run {
   template <typename T>
   T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
 
-  template <typename E>
-  cudaError_t planes_of(const void* x, bool tokens, uint16_t* out, long long rows) const {
-    const int vec = a.D % 8 == 0 && aligned(x, 16);
-    const long long n = rows * (p.Dp / 8);
-    return chained(planes_kernel<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, 1, s, static_cast<const E*>(x),
-                   tokens ? at<int>(p.index) : nullptr, at<Totals>(p.totals), out, rows, a.D, p.Dp, p.np, vec);
-  }
-  cudaError_t make_planes(const void* x, bool tokens, size_t off) const {
-    prof_begin(s, "ce_operands");
-    const long long rows = tokens ? a.T : a.V;
-    const cudaError_t e = a.bf16 ? planes_of<__nv_bfloat16>(x, tokens, at<uint16_t>(off), rows)
-                                 : planes_of<float>(x, tokens, at<uint16_t>(off), rows);
-    prof_end(s);
-    return e;
-  }
-
   // The list of counted tokens, and H, W (UH, UW) as the products read them.
   cudaError_t operands() const {
     prof_begin(s, "ce_list");
@@ -451,19 +461,32 @@ struct Run {
                                   p.splits, c.err);
     prof_end(s);
     CE_TRY(e);
-    CE_TRY(make_planes(a.H, true, p.h));
-    if (p.copy_w) CE_TRY(make_planes(a.W, false, p.w));
-    if (second) {
-      if (a.UH) CE_TRY(make_planes(a.UH, true, p.uh));
-      if (p.copy_w && a.UW) CE_TRY(make_planes(a.UW, false, p.uw));
-    }
-    return cudaSuccess;
+    Operands o;
+    o.n = 0;
+    long long blocks = 0;
+    auto add = [&](const void* x, bool tokens, size_t off) {
+      if (!x) return;
+      const long long rows = tokens ? a.T : a.V;
+      o.o[o.n++] = Operand{x, at<uint16_t>(off), rows, (unsigned)blocks, tokens, a.D % 8 == 0 && aligned(x, 16)};
+      blocks += (rows * (p.Dp / 8) + 255) / 256;
+    };
+    add(a.H, true, p.h);
+    if (second) add(a.UH, true, p.uh);
+    if (p.copy_w) add(a.W, false, p.w);
+    if (p.copy_w && second) add(a.UW, false, p.uw);
+    prof_begin(s, "ce_operands");
+    const cudaError_t f = a.bf16 ? chained(planes_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(256), 0, 1, s, o,
+                                           at<int>(p.index), at<Totals>(p.totals), a.D, p.Dp, p.np)
+                                 : chained(planes_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, 1, s, o,
+                                           at<int>(p.index), at<Totals>(p.totals), a.D, p.Dp, p.np);
+    prof_end(s);
+    return f;
   }
 
   GemmArgs base() const {
     GemmArgs g;
     memset(&g, 0, sizeof(g));
-    g.splits = 1, g.fp32 = !a.bf16;
+    g.splits = 1, g.fp32 = !a.bf16, g.planes = p.gp;
     g.err = c.err, g.wait_ns = c.wait_ns, g.stall = c.stall;
     g.count = &at<Totals>(p.totals)->count, g.slabs = &at<Totals>(p.totals)->slabs;
     g.ep.index = at<int>(p.index), g.ep.target = at<int>(p.target), g.ep.lse = a.lse, g.ep.g = a.g;
@@ -486,27 +509,30 @@ struct Run {
   }
   // Planes of G (which = 0) or Z (1) of a piece of `cols` columns.
   uint16_t* piece_plane(int which, int k) const {
-    return at<uint16_t>(p.planes) + (size_t)(which * p.np + k) * a.T * p.ld;
+    return at<uint16_t>(p.planes) + (size_t)(which * p.gp + k) * a.T * p.ld;
   }
   bool piece_maps(CUtensorMap* m, int which, int cols, int box) const {
-    for (int k = 0; k < p.np; ++k)
+    for (int k = 0; k < p.gp; ++k)
       if (!matrix_map(m + k, piece_plane(which, k), a.T, cols, p.ld, box)) return false;
     return true;
   }
 
-  // The products of planes of A operand `x` and B operand `y` (0 or 1 each),
-  // smallest first.
-  void products(GemmArgs& g, int x, int y) const {
-    static const uint8_t order[6][2] = {{0, 2}, {1, 1}, {2, 0}, {0, 1}, {1, 0}, {0, 0}};
-    for (int i = p.np == 1 ? 5 : 0; i < 6; ++i)
-      g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + order[i][0]), (uint8_t)(kPlanes * y + order[i][1])};
+  // The products of the na terms of A operand `x` and the np terms of B operand
+  // `y` (0 or 1 each) that reach 2^-16 of the first, smallest first.
+  void products(GemmArgs& g, int x, int y, int na) const {
+    for (int order = 2; order >= 0; --order) {
+      for (int i = order; i >= 0; --i) {
+        if (i < na && order - i < p.np)
+          g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + i), (uint8_t)(kPlanes * y + order - i)};
+      }
+    }
   }
 
   // The logits (and, in the second order, b = UH W^T + H UW^T).
   bool logits(GemmArgs& g, bool dual) const {
     const int box = (dual ? kTileNDual : kTileN) / 2;
     if (!token_maps(g.a, p.h, 128) || !head_maps(g.b, a.W, p.w, box)) return false;
-    products(g, 0, 0);
+    products(g, 0, 0, p.np);
     if (dual) {
       if (a.UH && !token_maps(g.a + kPlanes, p.uh, 128)) return false;
       if (a.UW && !head_maps(g.b + kPlanes, a.UW, p.uw, box)) return false;
@@ -555,7 +581,7 @@ struct Run {
     if (!logits(g, second)) return cudaErrorInvalidValue;
     g.N = cols, g.n_base = g.b0 = c0;
     g.ep.alpha = at<float>(p.alpha);
-    for (int k = 0; k < p.np; ++k) {
+    for (int k = 0; k < p.gp; ++k) {
       if (!store_map(g.c + k, piece_plane(0, k), a.T, cols, p.ld)) return cudaErrorInvalidValue;
       if (second && !store_map(g.c + kPlanes + k, piece_plane(1, k), a.T, cols, p.ld)) return cudaErrorInvalidValue;
     }
@@ -565,13 +591,13 @@ struct Run {
       if (!piece_maps(g.a, 0, cols, 128) || !head_maps(g.b, a.W, p.w, 64)) return cudaErrorInvalidValue;
       if (second) {
         if (!piece_maps(g.a + kPlanes, 1, cols, 128)) return cudaErrorInvalidValue;
-        products(g, 1, 0);
+        products(g, 1, 0, p.gp);
         if (a.UW) {
           if (!head_maps(g.b + kPlanes, a.UW, p.uw, 64)) return cudaErrorInvalidValue;
-          products(g, 0, 1);
+          products(g, 0, 1, p.gp);
         }
       } else {
-        products(g, 0, 0);
+        products(g, 0, 0, p.gp);
       }
       g.M = a.T, g.N = a.D, g.K = cols, g.b0 = c0;
       // every slab gets at least one step: a short last piece adds to the first slabs only
@@ -585,13 +611,13 @@ struct Run {
       if (!piece_maps(g.a, 0, cols, 64) || !token_maps(g.b, p.h, 64)) return cudaErrorInvalidValue;
       if (second) {
         if (!piece_maps(g.a + kPlanes, 1, cols, 64)) return cudaErrorInvalidValue;
-        products(g, 1, 0);
+        products(g, 1, 0, p.gp);
         if (a.UH) {
           if (!token_maps(g.b + kPlanes, p.uh, 64)) return cudaErrorInvalidValue;
-          products(g, 0, 1);
+          products(g, 0, 1, p.gp);
         }
       } else {
-        products(g, 0, 0);
+        products(g, 0, 0, p.gp);
       }
       g.M = cols, g.N = a.D, g.K = a.T;
       g.ep.out = static_cast<char*>(a.dW) + (size_t)c0 * a.D * (a.bf16 ? 2 : 4);
