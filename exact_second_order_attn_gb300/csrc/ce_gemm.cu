@@ -74,12 +74,13 @@ struct Ctrl {
   int abort_flag;
 };
 
-// A wait whose arrivals may come from the other block of the cluster.
+// A wait whose arrivals may come from the other block of the cluster (with
+// mbar_arrive_relaxed).
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -181,6 +182,7 @@ template <bool FP32>
 struct Acc {
   uint32_t tmem;
   const float* sum;
+  uint32_t freed;  // the leader's tile_empty barrier of this accumulator
   __device__ __forceinline__ void load(int tmem_col, int at, float* v) const {
     if constexpr (FP32) {
 #pragma unroll
@@ -190,6 +192,14 @@ struct Acc {
       tmem_ld32(tmem + tmem_col, v);
     }
   }
+  // The warp has read its part: the accumulator may be written again.
+  __device__ __forceinline__ void done() const {
+    if constexpr (!FP32) {
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive_relaxed(freed);
+    }
+  }
 };
 
 // The epilogue of one tile for this thread's row: `row` in the output, n0 the
@@ -197,7 +207,7 @@ struct Acc {
 template <int EP, bool FP32>
 __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc, Outbox& out, int rows, int row, int n0,
                                          int part, int split) {
-  constexpr int kUnroll = FP32 ? 4 : 1;
+  constexpr int W = Cfg<EP>::BN / 2, kUnroll = FP32 ? 4 : 1;  // columns of this thread (of each accumulator)
   const EpArgs& e = p.ep;
   const bool live = row < rows;
   const int box_row = row - (int)(threadIdx.x & 31);  // of the warp's first row
@@ -205,9 +215,10 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
     const int y = live ? e.target[row] : -1;
     float m = -INFINITY, s = 0.f;
 #pragma unroll kUnroll
-    for (int c = 0; c < 128; c += 32) {
+    for (int c = 0; c < W; c += 32) {
       float v[32];
       acc.load(c, c, v);
+      if (c + 32 == W) acc.done();
       const int n = n0 + c;
       if (y >= n && y < n + 32) {
 #pragma unroll
@@ -239,9 +250,10 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
     const float at = live ? e.lse[own] : 0.f, gm = *e.gmax;
     const float gs = live && gm != 0.f ? e.g[own] / gm : 0.f;
 #pragma unroll kUnroll
-    for (int c = 0; c < 128; c += 32) {
+    for (int c = 0; c < W; c += 32) {
       float v[32];
       acc.load(c, c, v);
+      if (c + 32 == W) acc.done();
       const int n = n0 + c, hit = y - p.n_base - n;
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = live ? gs * ex<FP32>(v[j], at) : 0.f;
@@ -255,10 +267,11 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
     const float at = live ? e.lse[e.index[row]] : 0.f;
     float s = 0.f;
 #pragma unroll kUnroll
-    for (int c = 0; c < 64; c += 32) {
+    for (int c = 0; c < W; c += 32) {
       float z[32], b[32];
       acc.load(c, c, z);
-      acc.load(kTileNDual + c, 64 + c, b);
+      acc.load(kTileNDual + c, W + c, b);
+      if (c + 32 == W) acc.done();
       const int n = n0 + c;
 #pragma unroll
       for (int j = 0; j < 32; ++j) s += n + j < p.N ? ex<FP32>(z[j], at) * b[j] : 0.f;
@@ -269,10 +282,11 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
     const float at = live ? e.lse[own] : 0.f, al = live ? e.alpha[row] : 0.f, gm = *e.gmax;
     const float gs = live && gm != 0.f ? e.g[own] / gm : 0.f;
 #pragma unroll kUnroll
-    for (int c = 0; c < 64; c += 32) {
+    for (int c = 0; c < W; c += 32) {
       float z[32], b[32];
       acc.load(c, c, z);
-      acc.load(kTileNDual + c, 64 + c, b);
+      acc.load(kTileNDual + c, W + c, b);
+      if (c + 32 == W) acc.done();
       const int n = n0 + c, hit = y - p.n_base - n;
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
@@ -291,9 +305,10 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
   } else if constexpr (EP == kSlab) {
     float* slab = static_cast<float*>(e.out) + (size_t)split * e.slab + (size_t)row * e.out_ld;
 #pragma unroll kUnroll
-    for (int c = 0; c < 128; c += 32) {
+    for (int c = 0; c < W; c += 32) {
       float v[32];
       acc.load(c, c, v);
+      if (c + 32 == W) acc.done();
       const int n = n0 + c;
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {  // out_ld is a multiple of 8
@@ -312,9 +327,10 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc
     const float gm = *e.gmax;
     const size_t at = (size_t)row * e.out_ld;
 #pragma unroll kUnroll
-    for (int c = 0; c < 128; c += 32) {
+    for (int c = 0; c < W; c += 32) {
       float v[32];
       acc.load(c, c, v);
+      if (c + 32 == W) acc.done();
       const int n = n0 + c;
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= gm;
@@ -570,19 +586,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           }
           tc_fence_before();
           __syncwarp();
-          if ((tid & 31) == 0) mbar_arrive_cluster(freed + buf * 8);
+          if ((tid & 31) == 0) mbar_arrive_relaxed(freed + buf * 8);
         }
-        if (ok) epilogue<EP, true>(p, Acc<true>{0, sum}, out, rows, row, n0, 2 * n + half, split);
+        if (ok) epilogue<EP, true>(p, Acc<true>{0, sum, 0}, out, rows, row, n0, 2 * n + half, split);
       } else {
         const int buf = chain & 1;
         // warp-uniform: the TMEM loads that follow are warp-collective
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
         tc_fence_after();
-        epilogue<EP, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr}, out, rows, row, n0, 2 * n + half,
+        epilogue<EP, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr, freed + buf * 8}, out, rows, row, n0, 2 * n + half,
                             split);
-        tc_fence_before();
-        __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive_cluster(freed + buf * 8);
         ++chain;
       }
     }
