@@ -18,8 +18,9 @@
 // each plane product and the epilogue threads add the chains up in registers,
 // rounding to nearest.
 //
-// Roles of a block's ten warps: 0-7 epilogue (thread = accumulator row, the two
-// warpgroups take half of the columns each), 8 TMA producer, 9 MMA issue (the
+// Roles of a block's eleven warps: 0-7 epilogue (thread = accumulator row, the
+// two warpgroups take half of the columns each), 8 and 10 TMA producers of A and
+// of B (one warp for both: G kernel 3 % slower), 9 MMA issue (the
 // leader block's) and TMEM allocation.  Barriers: full[s] of the leader counts
 // both blocks' bytes; empty[s] and tile_full[b] are signalled in both blocks
 // by the MMAs' commit; tile_empty[b] of the leader counts the 16 epilogue
@@ -43,7 +44,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kEpWarps = 8;
 constexpr int kGroupM = 8;        // row tiles per raster group
 constexpr int kTmemCols = 512;
@@ -441,8 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   // the steps of K up to which an accumulator chain that starts at kc runs
   auto chain_end = [](int kc, int k1) { return FP32 ? min(kc + kChainBlocks, k1) : k1; };
 
-  if (warp == 8) {
-    // ------------------------------------------------------------------ TMA
+  if (warp == 8 || warp == 10) {
+    // ------------------------------------------- TMA: warp 8 loads A, warp 10 loads B
+    const bool is_a = warp == 8;
     if (live) {  // the whole warp runs the loop; one lane issues (elect.sync)
       const uint32_t full0 = map_rank(smem_u32(&ctrl.full[0]), 0);
       const uint32_t stage_bytes = 2 * (C::DUAL ? C::A_BYTES * (1 + p.has_ua) + C::B_BYTES * (1 + p.has_ub) : C::STAGE);
@@ -465,23 +467,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
               if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.empty[st], at.pass ^ 1, wt)))) break;
               if (p.stall && issued == 0) continue;  // test hook: nothing fills the first stage
               const uint32_t bar = full0 + 8 * st;
-              if (rank == 0) mbar_expect_tx_w(&ctrl.full[st], stage_bytes);
               const uint32_t da = sm0 + st * C::STAGE, db = da + (C::DUAL ? 2 : 1) * C::A_BYTES;
-              if (C::A_MN) {
-                tma_load_2d_pair(da, ma, bar, row, k * kBK);
-                tma_load_2d_pair(da + 8192, ma, bar, row + 64, k * kBK);
+              if (is_a) {
+                if (rank == 0) mbar_expect_tx_w(&ctrl.full[st], stage_bytes);
+                if (C::A_MN) {
+                  tma_load_2d_pair(da, ma, bar, row, k * kBK);
+                  tma_load_2d_pair(da + 8192, ma, bar, row + 64, k * kBK);
+                } else {
+                  tma_load_2d_pair(da, ma, bar, k * kBK, row);
+                }
+                if (C::DUAL && p.has_ua) tma_load_2d_pair(da + C::A_BYTES, ma + kPlanes, bar, k * kBK, row);
               } else {
-                tma_load_2d_pair(da, ma, bar, k * kBK, row);
-              }
-              if (C::B_MN) {
-                tma_load_2d_pair(db, mb, bar, col, p.b0 + k * kBK);
-                tma_load_2d_pair(db + 8192, mb, bar, col + 64, p.b0 + k * kBK);
-              } else {
-                tma_load_2d_pair(db, mb, bar, k * kBK, p.b0 + col);
-              }
-              if (C::DUAL) {
-                if (p.has_ua) tma_load_2d_pair(da + C::A_BYTES, ma + kPlanes, bar, k * kBK, row);
-                if (p.has_ub) tma_load_2d_pair(db + C::B_BYTES, mb + kPlanes, bar, k * kBK, p.b0 + col);
+                if (C::B_MN) {
+                  tma_load_2d_pair(db, mb, bar, col, p.b0 + k * kBK);
+                  tma_load_2d_pair(db + 8192, mb, bar, col + 64, p.b0 + k * kBK);
+                } else {
+                  tma_load_2d_pair(db, mb, bar, k * kBK, p.b0 + col);
+                }
+                if (C::DUAL && p.has_ub) tma_load_2d_pair(db + C::B_BYTES, mb + kPlanes, bar, k * kBK, p.b0 + col);
               }
             }
           }
