@@ -360,34 +360,48 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int& flip) {
   for (int k = 0; k < K; ++k) v[k] = P == 1 ? mine : __shfl_sync(0xffffffffu, mine, k * G);
 }
 
-// Each block adds up its rows' contributions to a column sum in registers
-// (acc); this writes the block's own total to out[D], summed over its warps in
-// a fixed order.  sh: kWarps x D floats (unused when a block owns a row).
-template <int VEC, int E, int OWN, bool EVEN>
-__device__ __forceinline__ void write_column_sums(const Unit<VEC> (&acc)[E / VEC][kUnits<VEC>], float* out, float* sh,
+// Each block adds up its rows' contributions to N column sums in registers
+// (acc); this writes the block's own totals to out[n][D] (null: not wanted),
+// summed over its warps in a fixed order.  sh: N x kWarps x D floats (unused when
+// a block owns a row).
+template <int N, int VEC, int E, int OWN, bool EVEN>
+__device__ __forceinline__ void write_column_sums(const Unit<VEC> (&acc)[N][E / VEC][kUnits<VEC>],
+                                                  float* const (&out)[N], float* sh,
                                                   const Cols<VEC, E, OWN, EVEN>& c) {
-  float* to = OWN != kWarp ? out : sh + (threadIdx.x >> 5) * c.D;
   if (OWN == kWarp) __syncthreads();
 #pragma unroll
-  for (int i = 0; i < c.NV; ++i) {
+  for (int n = 0; n < N; ++n) {
+    if (!out[n]) continue;
+    float* to = OWN != kWarp ? out[n] : sh + (n * kWarps + (threadIdx.x >> 5)) * c.D;
 #pragma unroll
-    for (int j = 0; j < kUnits<VEC>; ++j) {
-      if constexpr (VEC == 1) {
-        if (c.any(i)) to[c.at(i)] = acc[i][0];
-      } else {
-        const float2 f = row::parts(acc[i][j]);
-        if (c.has(i, 2 * j)) to[c.at(i) + 2 * j] = f.x;
-        if (c.has(i, 2 * j + 1)) to[c.at(i) + 2 * j + 1] = f.y;
+    for (int i = 0; i < c.NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < kUnits<VEC>; ++j) {
+        if constexpr (VEC == 1) {
+          if (c.any(i)) to[c.at(i)] = acc[n][i][0];
+        } else {
+          const float2 f = row::parts(acc[n][i][j]);
+          if constexpr (EVEN) {
+            if (c.any(i)) *reinterpret_cast<float2*>(to + c.at(i) + 2 * j) = f;
+          } else {
+            if (c.has(i, 2 * j)) to[c.at(i) + 2 * j] = f.x;
+            if (c.has(i, 2 * j + 1)) to[c.at(i) + 2 * j + 1] = f.y;
+          }
+        }
       }
     }
   }
   if constexpr (OWN == kWarp) {
     __syncthreads();
-    for (int col = threadIdx.x; col < c.D; col += blockDim.x) {
-      float t = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) t += sh[w * c.D + col];
-      out[col] = t;
+    for (int n = 0; n < N; ++n) {
+      if (!out[n]) continue;
+      for (int col = threadIdx.x; col < c.D; col += blockDim.x) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) t += sh[(n * kWarps + w) * c.D + col];
+        out[n][col] = t;
+      }
     }
   }
 }
@@ -463,7 +477,7 @@ inline void dispatch(const Layout& l, F&& f) {
 // Ring depth of a launch, and its dynamic shared memory: the staged weights
 // (nw vectors), then the ring or, after it, the warps' column sums.
 template <typename T, typename WT, int N, int VEC, int E, int OWN, bool EVEN>
-inline int ring_stages(int D, long long rows, const Layout& l, const Shape& sh, int nw, bool sums, int* smem) {
+inline int ring_stages(int D, long long rows, const Layout& l, const Shape& sh, int nw, int sums, int* smem) {
   constexpr int R = kRows<T, E, N>;
   using G = Ring<T, N, R, VEC, OWN, EVEN>;
   const int fixed = kStaged<VEC, EVEN> ? nw * Weights<WT, VEC, E, OWN, EVEN>::bytes(D) : 0;
@@ -474,7 +488,7 @@ inline int ring_stages(int D, long long rows, const Layout& l, const Shape& sh, 
   const long long each = (rows + owners - 1) / owners;
   if (s > each) s = (int)each;
   if (s < 1) s = 1;
-  const int need = sums && OWN == kWarp ? kWarps * D * (int)sizeof(float) : 0;
+  const int need = OWN == kWarp ? sums * kWarps * D * (int)sizeof(float) : 0;
   *smem = fixed + (s * per > need ? s * per : need);
   return s;
 }

@@ -45,11 +45,11 @@ __global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
   __syncthreads();
   const float inv = 1.f / (float)D;
   int flip = 0;
-  Unit<VEC> gw[c.NV][U];
+  Unit<VEC> gw[1][c.NV][U];
 #pragma unroll
   for (int i = 0; i < c.NV; ++i) {
 #pragma unroll
-    for (int e = 0; e < U; ++e) gw[i][e] = all<VEC>(0.f);
+    for (int e = 0; e < U; ++e) gw[0][i][e] = all<VEC>(0.f);
   }
   float mu_next[R], rs_next[R];  // the rows' statistics, read one step ahead
   auto statistics = [&](long long first) {
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
           const Unit<VEC> xh = (vx[j][i].unit(e) + m) * ir, g = vd[j][i].unit(e), uu = vu[j][i].unit(e);
           const Unit<VEC> pu = ir * mad(xh, n_mux, uu + n_mu);  // r P u
           const Unit<VEC> h = mad(uu, r_max, g * mad(qw[e], r_mux, qu[e]));
-          gw[i][e] = mad(pu, g, gw[i][e]);
+          gw[0][i][e] = mad(pu, g, gw[0][i][e]);
           vx[j][i].put(e, ir * mad(xh, n_mhx, h + n_mh));
           vd[j][i].put(e, mad(qw[e], pu, mad(qu[e], xh, qb[e])));
         }
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
       }
     }
   }
-  if (gw_parts)  // every copy has been read
-    write_column_sums<VEC, E, OWN, EVEN>(gw, gw_parts + (size_t)blockIdx.x * D, reinterpret_cast<float*>(slots), c);
+  float* const parts[] = {gw_parts ? gw_parts + (size_t)blockIdx.x * D : nullptr};
+  write_column_sums<1, VEC, E, OWN, EVEN>(gw, parts, reinterpret_cast<float*>(slots), c);  // every copy has been read
 }
 
 template <typename T, typename WT>
@@ -158,7 +158,7 @@ cudaError_t launch(const NormArgs& a, const DevCtx& ctx, cudaStream_t s) {
   dispatch<T>(l, [&](auto v, auto e, auto own, auto even) {
     auto kernel = bob_kernel<T, WT, v(), e(), own(), even()>;
     int smem = 0;
-    const int stages = ring_stages<T, WT, 3, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w + !!a.uw + !!a.ub, a.gw != nullptr, &smem);
+    const int stages = ring_stages<T, WT, 3, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w + !!a.uw + !!a.ub, a.gw ? 1 : 0, &smem);
     if ((e_ = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return;
     e_ = chained(kernel, dim3(sh.blocks), dim3(sh.threads), smem, 1, s, static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd, static_cast<const T*>(a.dy), static_cast<const T*>(a.ux), static_cast<const WT*>(a.uw), static_cast<const WT*>(a.ub), static_cast<T*>(a.gx), static_cast<T*>(a.gdy), a.gw ? a.ws : nullptr, a.rows, a.D, l.period, stages, ctx.err, ctx.wait_ns);
   });

@@ -33,11 +33,11 @@ __global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
   __syncthreads();
   const float inv = 1.f / (float)D;
   int flip = 0;
-  Unit<VEC> dw[c.NV][U], db[c.NV][U];
+  Unit<VEC> sums[2][c.NV][U];  // of dw, db
 #pragma unroll
   for (int i = 0; i < c.NV; ++i) {
 #pragma unroll
-    for (int e = 0; e < U; ++e) dw[i][e] = db[i][e] = all<VEC>(0.f);
+    for (int e = 0; e < U; ++e) sums[0][i][e] = sums[1][i][e] = all<VEC>(0.f);
   }
   float mu_next[R], rs_next[R];  // the rows' statistics, read one step ahead
   auto statistics = [&](long long first) {
@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
           const Unit<VEC> xh = (vx[j][i].unit(e) + m) * ir, g = vd[j][i].unit(e), a = g * q[e];
           sa[j] = sa[j] + a;
           sx[j] = mad(a, xh, sx[j]);
-          dw[i][e] = mad(g, xh, dw[i][e]);
-          db[i][e] = db[i][e] + g;
+          sums[0][i][e] = mad(g, xh, sums[0][i][e]);
+          sums[1][i][e] = sums[1][i][e] + g;
         }
       }
     }
@@ -113,9 +113,9 @@ __global__ void __launch_bounds__(kMaxThreads<OWN>, kResident<T, E, OWN>)
       }
     }
   }
-  float* sh = reinterpret_cast<float*>(slots);  // every copy has been read
-  if (dw_parts) write_column_sums<VEC, E, OWN, EVEN>(dw, dw_parts + (size_t)blockIdx.x * D, sh, c);
-  if (db_parts) write_column_sums<VEC, E, OWN, EVEN>(db, db_parts + (size_t)blockIdx.x * D, sh, c);
+  float* const parts[] = {dw_parts ? dw_parts + (size_t)blockIdx.x * D : nullptr,
+                          db_parts ? db_parts + (size_t)blockIdx.x * D : nullptr};
+  write_column_sums<2, VEC, E, OWN, EVEN>(sums, parts, reinterpret_cast<float*>(slots), c);  // every copy has been read
 }
 
 constexpr int kRedCols = 32, kRedRows = 32;
@@ -163,7 +163,7 @@ cudaError_t launch(const NormArgs& a, const DevCtx& ctx, cudaStream_t s) {
   dispatch<T>(l, [&](auto v, auto e, auto own, auto even) {
     auto kernel = bwd_kernel<T, WT, v(), e(), own(), even()>;
     int smem = 0;
-    const int stages = ring_stages<T, WT, 2, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w, a.dw || a.db, &smem);
+    const int stages = ring_stages<T, WT, 2, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w, a.dw || a.db ? 2 : 0, &smem);
     if ((e_ = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return;
     e_ = chained(kernel, dim3(sh.blocks), dim3(sh.threads), smem, 1, s, static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd, static_cast<const T*>(a.dy), static_cast<T*>(a.dx), dwp, dbp, a.rows, a.D, l.period, stages, ctx.err, ctx.wait_ns);
   });
