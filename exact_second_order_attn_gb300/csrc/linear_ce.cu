@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= gm;
   }
+  if (c >= D) return;  // the slabs' padding
   T* o = out + r * D + c;
   if (vec) {
     if constexpr (sizeof(T) == 2) {

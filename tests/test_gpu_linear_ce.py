@@ -92,11 +92,20 @@ def test_linear_ce_against_oracle(T, D, V, dtype):
     compare(t, chain(t))
 
 
-@pytest.mark.parametrize("D", [1, 3, 7, 65, 130])
+@pytest.mark.parametrize("D", [1, 3, 4, 7, 12, 36, 65, 130, 396])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_linear_ce_odd_widths(D, dtype):
+    """Widths that the padding rounds up: right values, nothing written past
+    the outputs."""
     t = make(37, D, 301, dtype, seed=D)
     compare(t, chain(t))
+    _, lse = fb.fbob_linear_ce_fwd(t["H"], t["W"], t["target"])
+    flat = [torch.full((x.numel() + 64,), 9.0, dtype=x.dtype, device="cuda") for x in (t["H"], t["W"])]
+    dH, dW = (f[:x.numel()].view(x.shape) for f, x in zip(flat, (t["H"], t["W"])))
+    fb.fbob_linear_ce_bwd(t["H"], t["W"], t["target"], lse, t["g"], dH=dH, dW=dW)
+    fb.fbob_linear_ce_bob(t["H"], t["W"], t["target"], lse, t["g"], t["UH"], t["UW"], gH=dH, gW=dW)
+    for f in flat:
+        assert (f[-64:] == 9.0).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
