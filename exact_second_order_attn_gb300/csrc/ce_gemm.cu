@@ -11,12 +11,14 @@
 // columns each, and their stages hold both operands of both sides (48 KB for
 // three products of 128 x 128 x 64, the same traffic per product).
 //
-// bf16 operands: a tile's whole contraction is one chain in the accumulator.
 // The tensor cores drop the bits of a step's sum below the accumulator's last
-// one, an error that grows with the chain (4e-6 of the result at 32,000 terms),
-// too much for fp32 operands: there a chain ends after kChainBlocks stages of
-// each plane product and the epilogue threads add the chains up in registers,
-// rounding to nearest.
+// one, an error that grows with the chain of steps (4e-6 of the result at 32,000
+// terms).  That is too much for fp32 operands, and for the fp32 results of bf16
+// ones (losses, alpha: 1e-6 to 4e-6 at D above 500).  There a chain ends after
+// kChainBlocks stages of each plane product (bf16: 512 columns, at 8 % of the
+// kernel's time; 256 would cost 20 %) and the epilogue threads add the chains up
+// in registers, rounding to nearest.  What is rounded to bf16 anyway
+// has one chain.
 //
 // Roles of a block's eleven warps: 0-7 epilogue (thread = accumulator row, the
 // two warpgroups take half of the columns each), 8 and 10 TMA producers of A and
@@ -27,6 +29,12 @@
 // warps of the pair.  Every wait is bounded.  Blocks are persistent: pair i
 // takes tiles i, i + pairs, ...; tiles walk over 8 row tiles per column tile,
 // so that both operands are re-read from L2.
+//
+// Measured at 4096 tokens x 32,768 classes x 768 (206 GFLOP a product, burst
+// clock): logits with statistics 118 us, with G 122 us (1695 TFLOP/s), G W 113 us
+// (1825), G^T H 124 us (five waves of tiles); three products of alpha 325 us
+// (1900).  Bound by the tensor cores; a tile of K = 768 takes 6,900 cycles where
+// its MMAs need 6,144, since stages come at 64 bytes per cycle and multiprocessor.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -52,7 +60,12 @@ constexpr int kBufCols = 256;     // accumulator columns per tile in flight
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kBoxBytes = 32 * 32 * 2;  // an outgoing box: a warp's 32 rows x 32 columns of bf16
-constexpr int kChainBlocks = 2;   // 128 columns of the contraction
+// Whether a tile's contraction is cut into chains that are added up in
+// registers, and the chains' length in steps of 64 columns.
+template <int EP, bool FP32>
+constexpr bool kHeld = FP32 || EP == kStats || EP == kAlpha;
+template <bool FP32>
+constexpr int kChainBlocks = FP32 ? 2 : 8;
 
 template <int EP>
 struct Cfg {
@@ -179,13 +192,13 @@ __device__ __forceinline__ void store_planes(Outbox& out, const CUtensorMap* map
 
 // 32 columns of an accumulator, from tensor memory or from the registers in
 // which its chains were added up (c is then a constant: unrolled loops).
-template <bool FP32>
+template <bool HELD>
 struct Acc {
   uint32_t tmem;
   const float* sum;
   uint32_t freed;  // the leader's tile_empty barrier of this accumulator
   __device__ __forceinline__ void load(int tmem_col, int at, float* v) const {
-    if constexpr (FP32) {
+    if constexpr (HELD) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = sum[at + j];
     } else {
@@ -195,7 +208,7 @@ struct Acc {
   }
   // The warp has read its part: the accumulator may be written again.
   __device__ __forceinline__ void done() const {
-    if constexpr (!FP32) {
+    if constexpr (!HELD) {
       tc_fence_before();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive_relaxed(freed);
@@ -206,9 +219,9 @@ struct Acc {
 // The epilogue of one tile for this thread's row: `row` in the output, n0 the
 // first column, part the index of this half tile's row statistics.
 template <int EP, bool FP32>
-__device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<FP32>& acc, Outbox& out, int rows, int row, int n0,
+__device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<kHeld<EP, FP32>>& acc, Outbox& out, int rows, int row, int n0,
                                          int part, int split) {
-  constexpr int W = Cfg<EP>::BN / 2, kUnroll = FP32 ? 4 : 1;  // columns of this thread (of each accumulator)
+  constexpr int W = Cfg<EP>::BN / 2, kUnroll = kHeld<EP, FP32> ? 4 : 1;  // columns of this thread (of each accumulator)
   const EpArgs& e = p.ep;
   const bool live = row < rows;
   const int box_row = row - (int)(threadIdx.x & 31);  // of the warp's first row
@@ -440,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                  EP == kOut ? token_steps(tokens) : (p.K + kBK - 1) / kBK};
   const int total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   // the steps of K up to which an accumulator chain that starts at kc runs
-  auto chain_end = [](int kc, int k1) { return FP32 ? min(kc + kChainBlocks, k1) : k1; };
+  auto chain_end = [](int kc, int k1) { return kHeld<EP, FP32> ? min(kc + kChainBlocks<FP32>, k1) : k1; };
 
   if (warp == 8 || warp == 10) {
     // ------------------------------------------- TMA: warp 8 loads A, warp 10 loads B
@@ -570,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
       const int split = ts.split(t);
       constexpr int H = C::BN / 2;
       const int row = m * kTileM + (int)rank * 128 + r, n0 = n * C::BN + half * H;
-      if constexpr (FP32) {
+      if constexpr (kHeld<EP, FP32>) {
         float sum[128];
 #pragma unroll
         for (int j = 0; j < 128; ++j) sum[j] = 0.f;
@@ -591,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           __syncwarp();
           if ((tid & 31) == 0) mbar_arrive_relaxed(freed + buf * 8);
         }
-        if (ok) epilogue<EP, true>(p, Acc<true>{0, sum, 0}, out, rows, row, n0, 2 * n + half, split);
+        if (ok) epilogue<EP, FP32>(p, Acc<true>{0, sum, 0}, out, rows, row, n0, 2 * n + half, split);
       } else {
         const int buf = chain & 1;
         // warp-uniform: the TMEM loads that follow are warp-collective

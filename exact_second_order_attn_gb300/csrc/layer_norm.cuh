@@ -22,6 +22,10 @@
 // way: its vectors then hold the same columns in every row, and the weights are
 // staged once, shifted, in shared memory.  Only vectors at a row's ends are
 // handled element by element.
+//
+// Measured (bf16, copy rate 6.79 TB/s): 32,768 x 4096 forward 87 us, 6.2 TB/s,
+// backward 137 us, 5.9 TB/s, at about half of the issue slots; 8192 x 768 7 and
+// 12 us, of which the launch and the first loads are half.
 #pragma once
 
 #include <cuda_runtime.h>
