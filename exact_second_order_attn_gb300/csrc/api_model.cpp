@@ -162,8 +162,8 @@ fbob_status check_ce(const fbob_linear_ce* p) {
   if (p->T < 0 || p->D <= 0 || p->V <= 0)
     return fail(FBOB_ERR_INVALID_ARG, "bad sizes T=%d D=%d V=%d", p->T, p->D, p->V);
   if (p->piece < 0) return fail(FBOB_ERR_INVALID_ARG, "piece is negative (%d)", p->piece);
-  if (p->T > (1 << 24) || p->D > (1 << 20) || p->V > (1 << 24))
-    return fail(FBOB_ERR_UNSUPPORTED, "T=%d D=%d V=%d exceed 2^24, 2^20, 2^24", p->T, p->D, p->V);
+  if (p->T > (1 << 24) || p->D > (1 << 15) || p->V > (1 << 24))
+    return fail(FBOB_ERR_UNSUPPORTED, "T=%d D=%d V=%d exceed 2^24, 2^15, 2^24", p->T, p->D, p->V);
   // fewer than 2^31 tiles of 256 x 128 logits
   if ((long long)p->D * (p->T > p->V ? p->T : p->V) > (1ll << 40) || (long long)p->T * p->V > (1ll << 45))
     return fail(FBOB_ERR_UNSUPPORTED, "T=%d D=%d V=%d are too large", p->T, p->D, p->V);

@@ -17,8 +17,10 @@
 // ones (losses, alpha: 1e-6 to 4e-6 at D above 500).  There a chain ends after
 // kChainBlocks stages of each plane product (bf16: 512 columns, at 8 % of the
 // kernel's time; 256 would cost 20 %) and the epilogue threads add the chains up
-// in registers, rounding to nearest.  What is rounded to bf16 anyway
-// has one chain.
+// in registers, rounding to nearest.  The gradients' sums, which are rounded to
+// bf16, run over tokens or classes without limit: where those are more than
+// 16,384 their chains end there (1,024 steps, 3e-5; shorter sums keep the plain
+// epilogue, 10 us of 119 at 24 tokens).  G, rounded to bf16, has one chain over D.
 //
 // Roles of a block's eleven warps: 0-7 epilogue (thread = accumulator row, the
 // two warpgroups take half of the columns each), 8 and 10 TMA producers of A and
@@ -62,10 +64,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kBoxBytes = 32 * 32 * 2;  // an outgoing box: a warp's 32 rows x 32 columns of bf16
 // Whether a tile's contraction is cut into chains that are added up in
 // registers, and the chains' length in steps of 64 columns.
+// LONG: kSlab and kOut of bf16 operands with more than kLongBlocks steps.
+constexpr int kLongBlocks = 256;
+template <int EP, bool FP32, bool LONG>
+constexpr bool kHeld = FP32 || LONG || EP == kStats || EP == kAlpha;
 template <int EP, bool FP32>
-constexpr bool kHeld = FP32 || EP == kStats || EP == kAlpha;
-template <bool FP32>
-constexpr int kChainBlocks = FP32 ? 2 : 8;
+constexpr int kChainBlocks = FP32 ? 2 : EP == kStats || EP == kAlpha ? 8 : kLongBlocks;
 
 template <int EP>
 struct Cfg {
@@ -218,10 +222,10 @@ struct Acc {
 
 // The epilogue of one tile for this thread's row: `row` in the output, n0 the
 // first column, part the index of this half tile's row statistics.
-template <int EP, bool FP32>
-__device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<kHeld<EP, FP32>>& acc, Outbox& out, int rows, int row, int n0,
+template <int EP, bool FP32, bool HELD>
+__device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<HELD>& acc, Outbox& out, int rows, int row, int n0,
                                          int part, int split) {
-  constexpr int W = Cfg<EP>::BN / 2, kUnroll = kHeld<EP, FP32> ? 4 : 1;  // columns of this thread (of each accumulator)
+  constexpr int W = Cfg<EP>::BN / 2, kUnroll = HELD ? 4 : 1;  // columns of this thread (of each accumulator)
   const EpArgs& e = p.ep;
   const bool live = row < rows;
   const int box_row = row - (int)(threadIdx.x & 31);  // of the warp's first row
@@ -407,9 +411,10 @@ struct Place {
   }
 };
 
-template <int EP, bool FP32>
+template <int EP, bool FP32, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs p) {
   using C = Cfg<EP>;
+  constexpr bool HELD = kHeld<EP, FP32, LONG>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Ctrl ctrl;
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                  EP == kOut ? token_steps(tokens) : (p.K + kBK - 1) / kBK};
   const int total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   // the steps of K up to which an accumulator chain that starts at kc runs
-  auto chain_end = [](int kc, int k1) { return kHeld<EP, FP32> ? min(kc + kChainBlocks<FP32>, k1) : k1; };
+  auto chain_end = [](int kc, int k1) { return HELD ? min(kc + kChainBlocks<EP, FP32>, k1) : k1; };
 
   if (warp == 8 || warp == 10) {
     // ------------------------------------------- TMA: warp 8 loads A, warp 10 loads B
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
       const int split = ts.split(t);
       constexpr int H = C::BN / 2;
       const int row = m * kTileM + (int)rank * 128 + r, n0 = n * C::BN + half * H;
-      if constexpr (kHeld<EP, FP32>) {
+      if constexpr (HELD) {
         float sum[128];
 #pragma unroll
         for (int j = 0; j < 128; ++j) sum[j] = 0.f;
@@ -604,13 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           __syncwarp();
           if ((tid & 31) == 0) mbar_arrive_relaxed(freed + buf * 8);
         }
-        if (ok) epilogue<EP, FP32>(p, Acc<true>{0, sum, 0}, out, rows, row, n0, 2 * n + half, split);
+        if (ok) epilogue<EP, FP32, true>(p, Acc<true>{0, sum, 0}, out, rows, row, n0, 2 * n + half, split);
       } else {
         const int buf = chain & 1;
         // warp-uniform: the TMEM loads that follow are warp-collective
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
         tc_fence_after();
-        epilogue<EP, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr, freed + buf * 8}, out, rows, row, n0, 2 * n + half,
+        epilogue<EP, FP32, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr, freed + buf * 8}, out, rows, row, n0, 2 * n + half,
                             split);
         ++chain;
       }
@@ -627,10 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   }
 }
 
-template <int EP, bool FP32>
+template <int EP, bool FP32, bool LONG>
 cudaError_t launch_as(const GemmArgs& g, const char* name, cudaStream_t s) {
   using C = Cfg<EP>;
-  auto kernel = gemm_kernel<EP, FP32>;
+  auto kernel = gemm_kernel<EP, FP32, LONG>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((g.M + kTileM - 1) / kTileM) * ((g.N + C::BN - 1) / C::BN) * g.splits;
@@ -644,7 +649,11 @@ cudaError_t launch_as(const GemmArgs& g, const char* name, cudaStream_t s) {
 
 template <int EP>
 cudaError_t launch(const GemmArgs& g, const char* name, cudaStream_t s) {
-  return g.fp32 ? launch_as<EP, true>(g, name, s) : launch_as<EP, false>(g, name, s);
+  if (g.fp32) return launch_as<EP, true, false>(g, name, s);
+  if constexpr (EP == kSlab || EP == kOut) {
+    if (g.K > kLongBlocks * kBK) return launch_as<EP, false, true>(g, name, s);
+  }
+  return launch_as<EP, false, false>(g, name, s);
 }
 
 }  // namespace

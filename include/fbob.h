@@ -321,7 +321,7 @@ fbob_status fbob_layer_norm_bob(const fbob_norm* p, const void* x, const void* w
 
 /* The cross entropy of a linear head: T tokens h of D columns, V classes. */
 typedef struct {
-  int T, D, V;
+  int T, D, V;             /* up to 2^24, 2^15, 2^24, and T V up to 2^45      */
   int dtype;               /* H, W, UH, UW and their gradients                */
   long long ignore_index;  /* target of the tokens that are not counted       */
   int piece;               /* classes whose gradient is held at once (rounded */

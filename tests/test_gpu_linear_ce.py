@@ -85,7 +85,7 @@ def compare(t, got):
 
 @pytest.mark.parametrize("T,D,V", [(1, 8, 1), (1, 16, 2), (3, 64, 127), (128, 64, 128), (129, 72, 129), (255, 128, 255),
                                    (256, 256, 256), (257, 320, 257), (300, 768, 1000), (24, 768, 5003), (2, 1032, 513),
-                                   (700, 40, 600)])
+                                   (700, 40, 600), (5, 16, 40007)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_linear_ce_against_oracle(T, D, V, dtype):
     t = make(T, D, V, dtype, seed=T + V, ignored=range(0, T, 5) if T > 1 else ())
@@ -165,7 +165,7 @@ def test_linear_ce_all_ignored_and_no_tokens():
     assert gH.shape == (0, 64) and (gW == 0).all() and gg.shape == (0,)
 
 
-@pytest.mark.parametrize("T,counted", [(9000, 8999), (9000, 1), (5000, 64), (4097, 65), (300, 256), (300, 257)])
+@pytest.mark.parametrize("T,counted", [(9000, 8999), (9000, 1), (40000, 39000), (5000, 64), (4097, 65), (300, 256), (300, 257)])
 def test_linear_ce_counts_of_tokens(T, counted):
     """Lists of counted tokens over several rounds, and at the steps' edges."""
     order = torch.randperm(T, generator=torch.Generator().manual_seed(T))
