@@ -15,9 +15,9 @@
 // one, an error that grows with the chain of steps (4e-6 of the result at 32,000
 // terms).  That is too much for fp32 operands, and for the fp32 results of bf16
 // ones (losses, alpha: 1e-6 to 4e-6 at D above 500).  There a chain ends after
-// kChainBlocks stages of each plane product (bf16: 512 columns, at 8 % of the
-// kernel's time; 256 would cost 20 %) and the epilogue threads add the chains up
-// in registers, rounding to nearest.  The gradients' sums, which are rounded to
+// kChainBlocks stages of each plane product (bf16: 768 columns, 2 % of the
+// kernel's time; 512 cost 8 %, 256 20 %) and the epilogue threads add the chains
+// up in registers, rounding to nearest.  The gradients' sums, which are rounded to
 // bf16, run over tokens or classes without limit: where those are more than
 // 16,384 their chains end there (1,024 steps, 3e-5; shorter sums keep the plain
 // epilogue, 10 us of 119 at 24 tokens).  G, rounded to bf16, has one chain over D.
@@ -32,11 +32,11 @@
 // takes tiles i, i + pairs, ...; tiles walk over 8 row tiles per column tile,
 // so that both operands are re-read from L2.
 //
-// Measured at 4096 tokens x 32,768 classes x 768 (206 GFLOP a product, burst
-// clock): logits with statistics 118 us, with G 122 us (1695 TFLOP/s), G W 113 us
-// (1825), G^T H 124 us (five waves of tiles); three products of alpha 325 us
-// (1900).  Bound by the tensor cores; a tile of K = 768 takes 6,900 cycles where
-// its MMAs need 6,144, since stages come at 64 bytes per cycle and multiprocessor.
+// Measured on 7,373 counted tokens x 50,257 classes x 768 (569 GFLOP a product,
+// burst clock): logits with statistics 314 us (1,810 TFLOP/s), with G 350, G W 353,
+// G^T H 312 us; half as many tokens, alpha's three products 536 us.  Bound by the
+// tensor cores; a tile of K = 768 takes 6,900 cycles where its MMAs need 6,144,
+// since stages come at 64 bytes per cycle and multiprocessor.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -69,7 +69,7 @@ constexpr int kLongBlocks = 256;
 template <int EP, bool FP32, bool LONG>
 constexpr bool kHeld = FP32 || LONG || EP == kStats || EP == kAlpha;
 template <int EP, bool FP32>
-constexpr int kChainBlocks = FP32 ? 2 : EP == kStats || EP == kAlpha ? 8 : kLongBlocks;
+constexpr int kChainBlocks = FP32 ? 2 : EP == kStats || EP == kAlpha ? 12 : kLongBlocks;
 
 template <int EP>
 struct Cfg {

@@ -22,8 +22,8 @@
 // bf16 terms (2^-17): 14 us of 127 at 24 tokens x 50,257 classes x 768.
 //
 // Measured: 8192 tokens (a tenth ignored) x 50,257 classes x 768, bf16, forward
-// and gradients 1.38 ms in a burst (1.58 ms under the power cap), 4096 with the
-// second order 2.59 (2.72) ms; 24 tokens 107 us, bound by reading and writing W
+// and gradients 1.37 ms in a burst (1.58 ms under the power cap), 4096 with the
+// second order 2.60 (2.72) ms; 24 tokens 109 us, bound by reading and writing W
 // and dW and by eight launches; fp32 1021 x 32,003 x 512 602 us.
 //
 // fp32 inputs stand as three bf16 terms each (8 bits of the value per term);
