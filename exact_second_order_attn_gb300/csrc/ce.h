@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime_api.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "internal.h"
@@ -78,6 +79,16 @@ struct GemmArgs {
   unsigned long long wait_ns;
   int stall;
 };
+
+// The slabs are read and written 32 bytes at a time and every part of the plan
+// starts a multiple of 256 bytes after the workspace's base.  Callers' workspaces
+// are 16-byte aligned, so the base is the next 256-byte bound; the slack for it
+// is part of the size that callers are told.
+constexpr size_t kWorkspaceAlign = 256;
+constexpr size_t kWorkspaceSlack = kWorkspaceAlign - 16;
+inline void* workspace_base(void* ws) {
+  return reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(ws) + kWorkspaceAlign - 1) & ~(uintptr_t)(kWorkspaceAlign - 1));
+}
 
 // Rows, in steps of the contraction, that hold n counted tokens (at least one
 // step, so that a sum over no tokens is written as zero).

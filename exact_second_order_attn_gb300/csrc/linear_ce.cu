@@ -103,7 +103,7 @@ Plan plan(const CeArgs& a, CePass pass) {
   size_t at = 0;
   auto take = [&](bool want, size_t bytes) {
     const size_t here = at;
-    if (want) at += up(bytes, 256);
+    if (want) at += up(bytes, kWorkspaceAlign);
     return here;
   };
   const bool bwd = pass != CePass::kFwd, bob = pass == CePass::kBob;
@@ -656,10 +656,11 @@ struct Run {
 }  // namespace
 }  // namespace ce
 
-size_t linear_ce_workspace(const CeArgs& a, CePass pass) { return ce::plan(a, pass).bytes; }
+size_t linear_ce_workspace(const CeArgs& a, CePass pass) { return ce::plan(a, pass).bytes + ce::kWorkspaceSlack; }
 
 cudaError_t linear_ce(const CeArgs& a, CePass pass, const DevCtx& c, cudaStream_t s) {
-  const ce::Run r{a, c, s, ce::plan(a, pass), static_cast<char*>(a.ws), pass == CePass::kBob};
+  const ce::Run r{a, c, s, ce::plan(a, pass), static_cast<char*>(ce::workspace_base(a.ws)),
+                  pass == CePass::kBob};
   CE_TRY(r.operands());
   if (pass == CePass::kFwd) return r.stats();
   if (pass == CePass::kBob) CE_TRY(r.alpha());

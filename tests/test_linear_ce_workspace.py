@@ -1,0 +1,41 @@
+"""Where the linear head's passes place their parts in a workspace: callers
+may start it on any 16-byte bound, the kernels access it 32 bytes at a time."""
+
+import ctypes
+
+import pytest
+
+from exact_second_order_attn_gb300 import _lib
+from exact_second_order_attn_gb300.build import build
+from native_helpers import compiled
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    lib = compiled(str(tmp_path_factory.mktemp("ws")), """
+        #include "ce.h"
+        extern "C" unsigned long long base(unsigned long long ws) {
+          return reinterpret_cast<uintptr_t>(fbob::ce::workspace_base(reinterpret_cast<void*>(ws)));
+        }
+        extern "C" unsigned long long slack() { return fbob::ce::kWorkspaceSlack; }
+    """)
+    for f in (lib.base, lib.slack):
+        f.restype = ctypes.c_ulonglong
+    lib.base.argtypes = [ctypes.c_ulonglong]
+    return lib
+
+
+def test_base_is_aligned_and_within_the_slack(host):
+    for ws in range(1 << 20, (1 << 20) + 512, 16):
+        base = host.base(ws)
+        assert base % 256 == 0 and 0 <= base - ws <= host.slack()
+
+
+@pytest.mark.parametrize("shape", [(1, 8, 1), (37, 65, 301), (24, 768, 5003), (8192, 768, 50257)])
+@pytest.mark.parametrize("dtype", [_lib.BF16, _lib.FP32])
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_the_size_that_callers_are_told_holds_the_slack(host, shape, dtype, which):
+    """The parts are whole multiples of 256 bytes; the slack comes on top."""
+    build()
+    need = _lib.load().fbob_linear_ce_workspace_bytes(ctypes.byref(_lib.LinearCe(*shape, dtype, -100, 0)), which)
+    assert need % 256 == host.slack() and need > host.slack()
