@@ -31,6 +31,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "prof.h"
 #include "rowvec.cuh"
 #include "tc_ptx.cuh"
@@ -71,6 +72,11 @@ constexpr int kRows = N * E * (int)sizeof(T) / 4 <= 8 ? 4 : N * E * (int)sizeof(
 template <typename T, int E, int OWN>
 constexpr int kResident = OWN == kBlock512 || E * (int)sizeof(T) > 64 ? 1 : 2;
 constexpr int kRingMemory = 200 * 1024;
+// The dynamic shared memory that every kernel is allowed.  The allowance belongs
+// to the kernel, not to the launch, and host threads may launch one kernel for
+// different sizes at once, so it is one number for all of them: a ring and staged
+// weights take 200 KB at most, static arrays 4.1 KB of the 227 KB of a block.
+constexpr int kDynamicMemory = 220 * 1024;
 inline int blocks_per_max(int threads) { return threads < 256 ? 256 / threads : 1; }
 
 // Where a block's rows lie against 16-byte bounds, and this thread's columns:
@@ -495,6 +501,14 @@ inline int ring_stages(int D, long long rows, const Layout& l, const Shape& sh, 
   const int need = OWN == kWarp ? sums * kWarps * D * (int)sizeof(float) : 0;
   *smem = fixed + (s * per > need ? s * per : need);
   return s;
+}
+
+// Launches one of the kernels with `smem` bytes of dynamic shared memory.
+template <typename... P, typename... A>
+inline cudaError_t launch_rows(void (*kernel)(P...), const Shape& sh, int smem, cudaStream_t s, A... args) {
+  if (smem > kDynamicMemory) return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynamicMemory);
+  return e != cudaSuccess ? e : chained(kernel, dim3(sh.blocks), dim3(sh.threads), smem, 1, s, args...);
 }
 
 // Blocks of 256 threads of the kernels that reduce over rows (one partial sum

@@ -164,8 +164,7 @@ cudaError_t launch(const NormArgs& a, const DevCtx& ctx, cudaStream_t s) {
     auto kernel = bwd_kernel<T, WT, v(), e(), own(), even()>;
     int smem = 0;
     const int stages = ring_stages<T, WT, 2, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w, a.dw || a.db ? 2 : 0, &smem);
-    if ((e_ = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return;
-    e_ = chained(kernel, dim3(sh.blocks), dim3(sh.threads), smem, 1, s, static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd, static_cast<const T*>(a.dy), static_cast<T*>(a.dx), dwp, dbp, a.rows, a.D, l.period, stages, ctx.err, ctx.wait_ns);
+    e_ = launch_rows(kernel, sh, smem, s, static_cast<const T*>(a.x), static_cast<const WT*>(a.w), a.mean, a.rstd, static_cast<const T*>(a.dy), static_cast<T*>(a.dx), dwp, dbp, a.rows, a.D, l.period, stages, ctx.err, ctx.wait_ns);
   });
   prof_end(s);
   const cudaError_t e = e_ != cudaSuccess ? e_ : cudaGetLastError();

@@ -118,8 +118,7 @@ cudaError_t launch(const NormArgs& a, const DevCtx& ctx, cudaStream_t s) {
     auto kernel = fwd_kernel<T, WT, v(), e(), own(), even()>;
     int smem = 0;
     const int stages = ring_stages<T, WT, 1, v(), e(), own(), even()>(a.D, a.rows, l, sh, !!a.w + !!a.b, false, &smem);
-    if ((e_ = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return;
-    e_ = chained(kernel, dim3(sh.blocks), dim3(sh.threads), smem, 1, s, static_cast<const T*>(a.x), static_cast<const WT*>(a.w), static_cast<const WT*>(a.b), static_cast<T*>(a.y), a.mean, a.rstd, a.rows, a.D, a.eps, l.period, stages, ctx.err, ctx.wait_ns);
+    e_ = launch_rows(kernel, sh, smem, s, static_cast<const T*>(a.x), static_cast<const WT*>(a.w), static_cast<const WT*>(a.b), static_cast<T*>(a.y), a.mean, a.rstd, a.rows, a.D, a.eps, l.period, stages, ctx.err, ctx.wait_ns);
   });
   prof_end(s);
   return e_ != cudaSuccess ? e_ : cudaGetLastError();
