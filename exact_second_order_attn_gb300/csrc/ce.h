@@ -19,6 +19,10 @@ constexpr int kBK = 64;         // contraction per stage (128 bytes of bf16)
 constexpr int kPlanes = 3;      // bf16 terms that stand for one fp32 operand
 constexpr int kMaxMaps = 2 * kPlanes;
 constexpr int kMaxSegs = 2 * 6;
+// bf16 operands: up to this many counted tokens G and Z keep two bf16 terms.  The
+// second ones have room for that many tokens' rows (whole steps) only.
+constexpr int kExactTokens = 16;
+constexpr int kLowRows = kBK;
 
 // A product's operands: planes are bf16 matrices, a segment multiplies plane a
 // by plane b; the sum over the segments is the product.  With two accumulators
@@ -59,9 +63,8 @@ struct GemmArgs {
   CUtensorMap a[kMaxMaps], b[kMaxMaps];
   CUtensorMap c[kMaxMaps];  // store_map()s: kGrad, kGrad2: G planes, then Z planes; kOut: the output
   Seg seg[kMaxSegs];
-  int nseg;
+  int nseg, nlow;       // the first nlow are left out if more than kExactTokens tokens count
   int fp32;             // operands stand for fp32 (kPlanes planes, sums kept to fp32)
-  int planes;           // of G and of Z that kGrad and kGrad2 store
   int has_ua, has_ub;   // two accumulators: which second-order operands are there
   int K;                // contraction length
   int splits;           // K is cut into at most this many slabs (kSlab)

@@ -175,10 +175,11 @@ struct Outbox {
   }
 };
 
-// 32 values as bf16 planes: plane k holds the rounding of what planes 0..k-1 left.
+// 32 values as bf16 planes (n of them, or kPlanes): plane k holds the rounding of
+// what planes 0..k-1 left.
 template <bool FP32>
 __device__ __forceinline__ void store_planes(Outbox& out, const CUtensorMap* maps, int n, int x, int y, float* v) {
-  // (fp32 unrolled; bf16 has one plane, two for few tokens)
+  // (fp32 unrolled; bf16 has one plane, two where few tokens count)
 #pragma unroll(FP32 ? kPlanes : 1)
   for (int k = 0; k < (FP32 ? kPlanes : n); ++k) {
     uint32_t w[16];
@@ -224,11 +225,12 @@ struct Acc {
 // first column, part the index of this half tile's row statistics.
 template <int EP, bool FP32, bool HELD>
 __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<HELD>& acc, Outbox& out, int rows, int row, int n0,
-                                         int part, int split) {
+                                         int part, int split, bool few) {
   constexpr int W = Cfg<EP>::BN / 2, kUnroll = HELD ? 4 : 1;  // columns of this thread (of each accumulator)
   const EpArgs& e = p.ep;
   const bool live = row < rows;
   const int box_row = row - (int)(threadIdx.x & 31);  // of the warp's first row
+  const int planes = !FP32 && few && box_row < kLowRows ? 2 : 1;  // of bf16 G and Z
   if constexpr (EP == kStats) {
     const int y = live ? e.target[row] : -1;
     float m = -INFINITY, s = 0.f;
@@ -279,7 +281,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<HELD>& acc
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] -= j == hit ? gs : 0.f;
       }
-      if (box_row < p.M && n < p.N) store_planes<FP32>(out, p.c, p.planes, n, box_row, v);  // rows past the tokens: zero
+      if (box_row < p.M && n < p.N) store_planes<FP32>(out, p.c, planes, n, box_row, v);  // rows past the tokens: zero
     }
   } else if constexpr (EP == kAlpha) {
     const float at = live ? e.lse[e.index[row]] : 0.f;
@@ -316,8 +318,8 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const Acc<HELD>& acc
         for (int j = 0; j < 32; ++j) z[j] -= j == hit ? gs : 0.f;
       }
       if (box_row < p.M && n < p.N) {  // rows past the tokens: zero
-        store_planes<FP32>(out, p.c, p.planes, n, box_row, z);
-        store_planes<FP32>(out, p.c + kPlanes, p.planes, n, box_row, b);
+        store_planes<FP32>(out, p.c, planes, n, box_row, z);
+        store_planes<FP32>(out, p.c + kPlanes, planes, n, box_row, b);
       }
     }
   } else if constexpr (EP == kSlab) {
@@ -454,6 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   const int tokens = *p.count, written = min(p.M, token_steps(tokens) * kBK);
   const int rows = EP == kOut ? p.M : tokens;                             // that hold results
   const int tile_rows = EP == kGrad || EP == kGrad2 ? written : rows;     // that are worked on
+  const bool few = tokens <= kExactTokens;
+  const int seg0 = few ? 0 : p.nlow;
   const Tiles ts{(tile_rows + kTileM - 1) / kTileM, (p.N + C::BN - 1) / C::BN, EP == kSlab ? min(p.splits, *p.slabs) : 1,
                  EP == kOut ? token_steps(tokens) : (p.K + kBK - 1) / kBK};
   const int total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
         for (int kc = k0; ok && kc < k1; kc = chain_end(kc, k1)) {
           const int ke = chain_end(kc, k1);
-          for (int s = 0; ok && s < p.nseg; ++s) {
+          for (int s = seg0; ok && s < p.nseg; ++s) {
             const CUtensorMap* ma = &p.a[p.seg[s].a];
             const CUtensorMap* mb = &p.b[p.seg[s].b];
             for (int k = kc; k < ke; ++k, ++issued, at.next()) {
@@ -539,13 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_empty[buf], ((chain >> 1) & 1) ^ 1, wt));
           tc_fence_after();
           const uint32_t d = tb + buf * kBufCols;
-          for (int s = 0; ok && s < p.nseg; ++s) {
+          for (int s = seg0; ok && s < p.nseg; ++s) {
             for (int k = kc; k < ke; ++k, at.next()) {
               const int st = at.s;
               ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.full[st], at.pass, wt));
               if (!ok) break;
               tc_fence_after();
-              const uint32_t more = s > 0 || k > kc;  // the accumulator holds a product already
+              const uint32_t more = s > seg0 || k > kc;  // the accumulator holds a product already
               const uint32_t a = desc_lo(sm0 + st * C::STAGE, lbo_a);
               const uint32_t b = desc_lo(sm0 + st * C::STAGE + (C::DUAL ? 2 : 1) * C::A_BYTES, lbo_b);
 #pragma unroll
@@ -609,14 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           __syncwarp();
           if ((tid & 31) == 0) mbar_arrive_relaxed(freed + buf * 8);
         }
-        if (ok) epilogue<EP, FP32, true>(p, Acc<true>{0, sum, 0}, out, rows, row, n0, 2 * n + half, split);
+        if (ok) epilogue<EP, FP32, true>(p, Acc<true>{0, sum, 0}, out, rows, row, n0, 2 * n + half, split, few);
       } else {
         const int buf = chain & 1;
         // warp-uniform: the TMEM loads that follow are warp-collective
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
         tc_fence_after();
         epilogue<EP, FP32, false>(p, Acc<false>{tb + lane + buf * kBufCols + half * H, nullptr, freed + buf * 8}, out, rows, row, n0, 2 * n + half,
-                            split);
+                            split, few);
         ++chain;
       }
     }

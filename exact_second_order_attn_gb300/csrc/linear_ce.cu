@@ -18,8 +18,9 @@
 // bf16 is then relative to p - 1 and not a systematic relative error of the
 // largest entry of every row.  The roundings average out over many tokens; with
 // few a row of dW hangs on one or two of them (4 tokens: 1.6 times the error of a
-// result rounded once; 24: 1.05 times), so up to kExactTokens G and Z keep two
-// bf16 terms (2^-17): 14 us of 127 at 24 tokens x 50,257 classes x 768.
+// result rounded once; 24: 1.05 times), so up to kExactTokens counted ones G and Z
+// keep two bf16 terms (2^-17): 14 us of 127 at 24 tokens x 50,257 classes x 768.
+// How many count is known on the device, so the kernels choose.
 //
 // Measured: 8192 tokens (a tenth ignored) x 50,257 classes x 768, bf16, forward
 // and gradients 1.37 ms in a burst (1.58 ms under the power cap), 4096 with the
@@ -45,17 +46,22 @@ namespace {
 constexpr int kPairs = 76;                        // block pairs of a GB300, for the split rule
 constexpr size_t kPieceBytes = 512ull << 20;      // G (and Z) of one piece of the vocabulary
 constexpr int kPieceStep = 256;
-constexpr int kExactTokens = 16;                  // G and Z in two bf16 terms up to here (bf16 inputs)
 
 size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 
-// bf16 terms of G and of Z.
-int grad_planes(const CeArgs& a) { return !a.bf16 ? kPlanes : a.T <= kExactTokens ? 2 : 1; }
+// bf16 planes of G and of Z, and the rows that plane k has room for.
+int grad_planes(const CeArgs& a) { return a.bf16 ? 2 : kPlanes; }
+long long plane_rows(const CeArgs& a, int k) { return a.bf16 && k > 0 && a.T > kLowRows ? kLowRows : a.T; }
+long long plane_rows_to(const CeArgs& a, int k) {  // of the planes before k
+  long long n = 0;
+  for (int i = 0; i < k; ++i) n += plane_rows(a, i);
+  return n;
+}
 
 // Piece width: all of V if its G fits kPieceBytes, else equal pieces that do
 // (at least 2048 columns, so that a piece's products keep the device busy).
 int piece_cols(const CeArgs& a, bool second) {
-  const size_t per = (size_t)a.T * 2 * grad_planes(a) * (second ? 2 : 1);
+  const size_t per = (size_t)plane_rows_to(a, grad_planes(a)) * 2 * (second ? 2 : 1);
   size_t cols = a.piece > 0 ? (size_t)a.piece : kPieceBytes / (per ? per : 1);
   cols = up(cols < 2048 && a.piece <= 0 ? 2048 : cols, kPieceStep);
   const size_t whole = up(a.V, kPieceStep);
@@ -120,7 +126,7 @@ Plan plan(const CeArgs& a, CePass pass) {
   p.part = take(!bwd, T * p.stat_parts * sizeof(float2));
   p.sums = take(bob, T * p.alpha_parts * 4);
   p.alpha = take(bob, T * 4);
-  p.planes = take(bwd, T * p.ld * 2 * p.gp * (bob ? 2 : 1));
+  p.planes = take(bwd, (size_t)plane_rows_to(a, p.gp) * p.ld * 2 * (bob ? 2 : 1));
   p.slab = take(bwd, T * p.Dp * 4 * p.splits);
   p.bytes = at;
   return p;
@@ -492,7 +498,7 @@ struct Run {
   GemmArgs base() const {
     GemmArgs g;
     memset(&g, 0, sizeof(g));
-    g.splits = 1, g.fp32 = !a.bf16, g.planes = p.gp;
+    g.splits = 1, g.fp32 = !a.bf16;
     g.err = c.err, g.wait_ns = c.wait_ns, g.stall = c.stall;
     g.count = &at<Totals>(p.totals)->count, g.slabs = &at<Totals>(p.totals)->slabs;
     g.ep.index = at<int>(p.index), g.ep.target = at<int>(p.target), g.ep.lse = a.lse, g.ep.g = a.g;
@@ -515,30 +521,38 @@ struct Run {
   }
   // Planes of G (which = 0) or Z (1) of a piece of `cols` columns.
   uint16_t* piece_plane(int which, int k) const {
-    return at<uint16_t>(p.planes) + (size_t)(which * p.gp + k) * a.T * p.ld;
+    return at<uint16_t>(p.planes) + (size_t)(which * plane_rows_to(a, p.gp) + plane_rows_to(a, k)) * p.ld;
   }
   bool piece_maps(CUtensorMap* m, int which, int cols, int box) const {
     for (int k = 0; k < p.gp; ++k)
-      if (!matrix_map(m + k, piece_plane(which, k), a.T, cols, p.ld, box)) return false;
+      if (!matrix_map(m + k, piece_plane(which, k), plane_rows(a, k), cols, p.ld, box)) return false;
     return true;
   }
 
-  // The products of the na terms of A operand `x` and the np terms of B operand
-  // `y` (0 or 1 each) that reach 2^-16 of the first, smallest first.
-  void products(GemmArgs& g, int x, int y, int na) const {
-    for (int order = 2; order >= 0; --order) {
-      for (int i = order; i >= 0; --i) {
-        if (i < na && order - i < p.np)
-          g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + i), (uint8_t)(kPlanes * y + order - i)};
-      }
+  // The products of the terms of A operand `x` and B operand `y` (0 or 1 each),
+  // np of each, that reach 2^-16 of the first, smallest first.
+  void products(GemmArgs& g, int x, int y) const {
+    for (int order = p.np - 1; order >= 0; --order) {
+      for (int i = order; i >= 0; --i)
+        g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + i), (uint8_t)(kPlanes * y + order - i)};
     }
+  }
+  // The same with A operands of pieces: G (x = 0), or Z (1) and, with an operand
+  // of its own, G.  The second terms of bf16's G and Z go first.
+  void piece_products(GemmArgs& g, bool both) const {
+    const int xs[2] = {second ? 1 : 0, 0}, n = both ? 2 : 1;
+    for (int i = 0; i < n && p.np < p.gp; ++i) {
+      g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * xs[i] + 1), (uint8_t)(kPlanes * i)};
+      ++g.nlow;
+    }
+    for (int i = 0; i < n; ++i) products(g, xs[i], i);
   }
 
   // The logits (and, in the second order, b = UH W^T + H UW^T).
   bool logits(GemmArgs& g, bool dual) const {
     const int box = (dual ? kTileNDual : kTileN) / 2;
     if (!token_maps(g.a, p.h, 128) || !head_maps(g.b, a.W, p.w, box)) return false;
-    products(g, 0, 0, p.np);
+    products(g, 0, 0);
     if (dual) {
       if (a.UH && !token_maps(g.a + kPlanes, p.uh, 128)) return false;
       if (a.UW && !head_maps(g.b + kPlanes, a.UW, p.uw, box)) return false;
@@ -588,8 +602,9 @@ struct Run {
     g.N = cols, g.n_base = g.b0 = c0;
     g.ep.alpha = at<float>(p.alpha);
     for (int k = 0; k < p.gp; ++k) {
-      if (!store_map(g.c + k, piece_plane(0, k), a.T, cols, p.ld)) return cudaErrorInvalidValue;
-      if (second && !store_map(g.c + kPlanes + k, piece_plane(1, k), a.T, cols, p.ld)) return cudaErrorInvalidValue;
+      const long long rows = plane_rows(a, k);
+      if (!store_map(g.c + k, piece_plane(0, k), rows, cols, p.ld)) return cudaErrorInvalidValue;
+      if (second && !store_map(g.c + kPlanes + k, piece_plane(1, k), rows, cols, p.ld)) return cudaErrorInvalidValue;
     }
     CE_TRY(gemm(second ? kGrad2 : kGrad, g, s));
     if (a.dH) {  // Z W + G UW, or G W
@@ -597,14 +612,9 @@ struct Run {
       if (!piece_maps(g.a, 0, cols, 128) || !head_maps(g.b, a.W, p.w, 64)) return cudaErrorInvalidValue;
       if (second) {
         if (!piece_maps(g.a + kPlanes, 1, cols, 128)) return cudaErrorInvalidValue;
-        products(g, 1, 0, p.gp);
-        if (a.UW) {
-          if (!head_maps(g.b + kPlanes, a.UW, p.uw, 64)) return cudaErrorInvalidValue;
-          products(g, 0, 1, p.gp);
-        }
-      } else {
-        products(g, 0, 0, p.gp);
+        if (a.UW && !head_maps(g.b + kPlanes, a.UW, p.uw, 64)) return cudaErrorInvalidValue;
       }
+      piece_products(g, second && a.UW);
       g.M = a.T, g.N = a.D, g.K = cols, g.b0 = c0;
       // every slab gets at least one step: a short last piece adds to the first slabs only
       const int steps = (cols + kBK - 1) / kBK;
@@ -617,14 +627,9 @@ struct Run {
       if (!piece_maps(g.a, 0, cols, 64) || !token_maps(g.b, p.h, 64)) return cudaErrorInvalidValue;
       if (second) {
         if (!piece_maps(g.a + kPlanes, 1, cols, 64)) return cudaErrorInvalidValue;
-        products(g, 1, 0, p.gp);
-        if (a.UH) {
-          if (!token_maps(g.b + kPlanes, p.uh, 64)) return cudaErrorInvalidValue;
-          products(g, 0, 1, p.gp);
-        }
-      } else {
-        products(g, 0, 0, p.gp);
+        if (a.UH && !token_maps(g.b + kPlanes, p.uh, 64)) return cudaErrorInvalidValue;
       }
+      piece_products(g, second && a.UH);
       g.M = cols, g.N = a.D, g.K = a.T;
       g.ep.out = static_cast<char*>(a.dW) + (size_t)c0 * a.D * (a.bf16 ? 2 : 4);
       g.ep.out_ld = a.D, g.ep.out_bf16 = a.bf16;

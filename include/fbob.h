@@ -353,7 +353,8 @@ fbob_status fbob_linear_ce_fwd(const fbob_linear_ce* p, const void* H, const voi
  * Gradients of sum_t g_t loss_t: with p = exp(z - lse) and
  * G = g (p - onehot(target)),
  *   dH = G W, dW = G^T H; each optional.  G is formed for one piece of the
- *   classes at a time, in bf16 for bf16 inputs.
+ *   classes at a time, in bf16 for bf16 inputs (in two bf16 terms where up to
+ *   16 tokens are counted, whatever T is).
  *   in : as fbob_linear_ce_fwd, its lse, and g [T] fp32
  */
 fbob_status fbob_linear_ce_bwd(const fbob_linear_ce* p, const void* H, const void* W,
