@@ -97,6 +97,14 @@ inline void* workspace_base(void* ws) {
 // step, so that a sum over no tokens is written as zero).
 __host__ __device__ inline int token_steps(int n) { return n <= kBK ? 1 : (n + kBK - 1) / kBK; }
 
+// Sums of kSlab and kOut over K terms of each of nseg segments (those of low
+// terms not counted: 2^-8 of the others, they come first, while the accumulator is
+// as small).  Above 16,384 terms in all a chain of the tensor cores ends after
+// long_chain() steps of every segment, again 16,384 terms.
+constexpr int kLongTerms = 16384;
+__host__ __device__ inline int long_chain(int nseg) { return kLongTerms / kBK / nseg; }
+__host__ __device__ inline bool long_sum(int K, int nseg) { return (long long)K * nseg > kLongTerms; }
+
 // C = sum over segments of A_seg B_seg^T with A [M][K], B [N][K], then the
 // epilogue.  kSlab reads B and kOut reads both A and B from matrices stored
 // with the contraction outermost ([K][N], [K][M]).

@@ -19,8 +19,9 @@
 // kernel's time; 512 cost 8 %, 256 20 %) and the epilogue threads add the chains
 // up in registers, rounding to nearest.  The gradients' sums, which are rounded to
 // bf16, run over tokens or classes without limit: where those are more than
-// 16,384 their chains end there (1,024 steps, 3e-5; shorter sums keep the plain
-// epilogue, 10 us of 119 at 24 tokens).  G, rounded to bf16, has one chain over D.
+// 16,384, both products of the second order counted, their chains end there (1,024
+// steps, 3e-5; shorter sums keep the plain epilogue, 10 us of 119 at 24 tokens).
+// G, rounded to bf16, has one chain over D.
 //
 // Roles of a block's eleven warps: 0-7 epilogue (thread = accumulator row, the
 // two warpgroups take half of the columns each), 8 and 10 TMA producers of A and
@@ -64,12 +65,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kBoxBytes = 32 * 32 * 2;  // an outgoing box: a warp's 32 rows x 32 columns of bf16
 // Whether a tile's contraction is cut into chains that are added up in
 // registers, and the chains' length in steps of 64 columns.
-// LONG: kSlab and kOut of bf16 operands with more than kLongBlocks steps.
-constexpr int kLongBlocks = 256;
+// LONG: kSlab and kOut of bf16 operands where long_sum(); chains of long_chain().
 template <int EP, bool FP32, bool LONG>
 constexpr bool kHeld = FP32 || LONG || EP == kStats || EP == kAlpha;
-template <int EP, bool FP32>
-constexpr int kChainBlocks = FP32 ? 2 : EP == kStats || EP == kAlpha ? 12 : kLongBlocks;
+template <bool FP32>
+constexpr int kChainBlocks = FP32 ? 2 : 12;
 
 template <int EP>
 struct Cfg {
@@ -462,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                  EP == kOut ? token_steps(tokens) : (p.K + kBK - 1) / kBK};
   const int total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   // the steps of K up to which an accumulator chain that starts at kc runs
-  auto chain_end = [](int kc, int k1) { return HELD ? min(kc + kChainBlocks<EP, FP32>, k1) : k1; };
+  const int chain_steps = LONG ? long_chain(p.nseg - p.nlow) : kChainBlocks<FP32>;
+  auto chain_end = [chain_steps](int kc, int k1) { return HELD ? min(kc + chain_steps, k1) : k1; };
 
   if (warp == 8 || warp == 10) {
     // ------------------------------------------- TMA: warp 8 loads A, warp 10 loads B
@@ -655,7 +656,7 @@ template <int EP>
 cudaError_t launch(const GemmArgs& g, const char* name, cudaStream_t s) {
   if (g.fp32) return launch_as<EP, true, false>(g, name, s);
   if constexpr (EP == kSlab || EP == kOut) {
-    if (g.K > kLongBlocks * kBK) return launch_as<EP, false, true>(g, name, s);
+    if (long_sum(g.K, g.nseg - g.nlow)) return launch_as<EP, false, true>(g, name, s);
   }
   return launch_as<EP, false, false>(g, name, s);
 }
