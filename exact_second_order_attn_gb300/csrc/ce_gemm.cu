@@ -15,13 +15,15 @@
 // one, an error that grows with the chain of steps (4e-6 of the result at 32,000
 // terms).  That is too much for fp32 operands, and for the fp32 results of bf16
 // ones (losses, alpha: 1e-6 to 4e-6 at D above 500).  There a chain ends after
-// kChainBlocks stages of each plane product (bf16: 768 columns, 2 % of the
-// kernel's time; 512 cost 8 %, 256 20 %) and the epilogue threads add the chains
-// up in registers, rounding to nearest.  The gradients' sums, which are rounded to
-// bf16, run over tokens or classes without limit: where those are more than
-// 16,384, both products of the second order counted, their chains end there (1,024
-// steps, 3e-5; shorter sums keep the plain epilogue, 10 us of 119 at 24 tokens).
-// G, rounded to bf16, has one chain over D.
+// kChainBlocks stages of each plane product (bf16: 512 columns) and the epilogue
+// threads add the chains up in registers, rounding to nearest.  Shorter chains cost
+// time and longer ones bits (D = 768: 256 columns 20 % of these kernels' time, 512
+// 6 %, the whole width 2 %; of drawn cases of all widths 0.06, 0.09 and 0.7 % are
+// further off than 1e-6 and 1.5 times an fp32 sum).  The gradients' sums, which
+// are rounded to bf16, run over tokens or classes without limit: where those are
+// more than 16,384, both products of the second order counted, their chains end
+// there (1,024 steps, 3e-5; shorter sums keep the plain epilogue, 10 us of 119 at
+// 24 tokens).  G, rounded to bf16, has one chain over D.
 //
 // Roles of a block's eleven warps: 0-7 epilogue (thread = accumulator row, the
 // two warpgroups take half of the columns each), 8 and 10 TMA producers of A and
@@ -34,8 +36,8 @@
 // so that both operands are re-read from L2.
 //
 // Measured on 7,373 counted tokens x 50,257 classes x 768 (569 GFLOP a product,
-// burst clock): logits with statistics 314 us (1,810 TFLOP/s), with G 350, G W 353,
-// G^T H 312 us; half as many tokens, alpha's three products 536 us.  Bound by the
+// burst clock): logits with statistics 332 us (1,710 TFLOP/s), with G 350, G W 353,
+// G^T H 312 us; half as many tokens, alpha's three products 563 us.  Bound by the
 // tensor cores; a tile of K = 768 takes 6,900 cycles where its MMAs need 6,144,
 // since stages come at 64 bytes per cycle and multiprocessor.
 #include <cuda.h>
@@ -69,7 +71,7 @@ constexpr int kBoxBytes = 32 * 32 * 2;  // an outgoing box: a warp's 32 rows x 3
 template <int EP, bool FP32, bool LONG>
 constexpr bool kHeld = FP32 || LONG || EP == kStats || EP == kAlpha;
 template <bool FP32>
-constexpr int kChainBlocks = FP32 ? 2 : 12;
+constexpr int kChainBlocks = FP32 ? 2 : 8;
 
 template <int EP>
 struct Cfg {
