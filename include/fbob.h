@@ -325,7 +325,11 @@ typedef struct {
   int dtype;               /* H, W, UH, UW and their gradients                */
   long long ignore_index;  /* target of the tokens that are not counted       */
   int piece;               /* classes whose gradient is held at once (rounded */
-                           /* up to 256); 0: as many as 512 MiB hold          */
+                           /* up to 256); 0: as many as 512 MiB hold, but at  */
+                           /* least 2048, which take T x 4 KiB in bf16, T x   */
+                           /* 12 KiB in fp32 and twice that in the second     */
+                           /* order: above 512 MiB from 131,072 tokens (bf16, */
+                           /* first order) on                                 */
 } fbob_linear_ce;
 
 /* Bytes of workspace of pass 0 (fwd), 1 (bwd) or 2 (bob); 0 for no tokens or

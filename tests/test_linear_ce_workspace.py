@@ -39,3 +39,25 @@ def test_the_size_that_callers_are_told_holds_the_slack(host, shape, dtype, whic
     build()
     need = _lib.load().fbob_linear_ce_workspace_bytes(ctypes.byref(_lib.LinearCe(*shape, dtype, -100, 0)), which)
     assert need % 256 == host.slack() and need > host.slack()
+
+
+@pytest.mark.parametrize("T", [60000, 131072, 262144, 1 << 20])
+@pytest.mark.parametrize("dtype", [_lib.BF16, _lib.FP32])
+@pytest.mark.parametrize("which", [1, 2])
+def test_the_classes_that_are_held_by_default(T, dtype, which):
+    """As many as 512 MiB hold, but at least 2048, in equal pieces.  (One slab of
+    dH's sums at this width, so that the piece alone changes the size.)"""
+    build()
+
+    def need(piece):
+        return _lib.load().fbob_linear_ce_workspace_bytes(
+            ctypes.byref(_lib.LinearCe(T, 2048, 128256, dtype, -100, piece)), which)
+
+    terms = 3 if dtype == _lib.FP32 else 1
+    room = (need(512) - need(256)) // 256  # bytes of a class
+    assert T * 2 * terms * which <= room <= T * 2 * terms * which + 256
+    cols = max(2048, (512 << 20) // room)
+    cols = -(-128256 // -(-128256 // (-(-cols // 256) * 256)))
+    cols = -(-cols // 256) * 256
+    assert need(0) == need(256) + (cols - 256) * room
+    assert cols * room <= max(512 << 20, 2048 * room) + 256 * room
