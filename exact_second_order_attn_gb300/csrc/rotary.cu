@@ -4,10 +4,11 @@
 //
 // Angles.  The kernel holds each frequency as a 64-bit fixed-point fraction of
 // a turn, F_i = theta_i / (2 pi) * 2^64, so pos * F_i mod 2^64 is the angle
-// modulo a full turn with no range reduction: its error is pos * 2^-65 turns
-// from F_i's rounding and pos * theta_i / (2 pi) * 2^-53 from theta_i's, far
-// below fp32 at any 32-bit position.  The top 32 bits, read as a signed
-// fraction x in [-1, 1) of half a turn, go to sincospif(x).
+// modulo a full turn with no range reduction.  What is left is theta_i's own
+// rounding, below pos * 2^-52 radians (2e-10 at position 2^20, 5e-7 at 2^31, where
+// it reaches an fp32 result's), and pos * 2^-64 turns from cutting F_i off.  The
+// top 32 bits, read as a signed fraction x in [-1, 1) of half a turn, go to
+// sincospif(x).
 //
 // Work split.  A thread owns one chunk of a token's head row (two vectors of
 // VEC elements whose pairs it holds whole) and walks over a group of heads,
