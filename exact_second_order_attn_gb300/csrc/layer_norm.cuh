@@ -30,6 +30,7 @@
 
 #include <cuda_runtime.h>
 
+#include "copy_bounds.h"
 #include "internal.h"
 #include "launch.cuh"
 #include "prof.h"
@@ -124,7 +125,7 @@ struct Ring {
 #pragma unroll
     for (int k = 0; k < N; ++k) base[k] = reinterpret_cast<const char*>(x[k]);
     rows = n, stages = S, row_bytes = D * (int)sizeof(T), slot = slot_bytes(D), period = EVEN ? 1 : P;
-    edge = (15 + row_bytes) / row_bytes;
+    edge = copy_edge(row_bytes);
     first = ((long long)(blockIdx.x / period) * kOwners + owner) * R * period + blockIdx.x % period;
     step = (long long)(gridDim.x / period) * kOwners * R * period;
     smem = tc::smem_u32(dyn) + owner * S * N * R * slot;
@@ -147,20 +148,10 @@ struct Ring {
   }
   __device__ __forceinline__ bool live(long long r, int j) const { return r + j * period < rows; }
 
-  // Rows so near the tensor's ends that their copies' bounds may move inwards.
-  __device__ __forceinline__ bool at_end(long long r) const { return r < edge || r >= rows - edge; }
-
-  // Bounds of the bytes that the copy for row r of tensor b brings: the row's,
-  // moved outwards to 16 bytes within the tensor and inwards at its ends.
+  __device__ __forceinline__ bool at_end(long long r) const { return copy_at_end(r, rows, edge); }
+  // Bounds of the bytes that the copy for row r of tensor b brings.
   __device__ __forceinline__ void bounds(const char* b, long long r, uintptr_t& lo, uintptr_t& hi) const {
-    const uintptr_t start = reinterpret_cast<uintptr_t>(b), at = start + r * row_bytes, mask = ~(uintptr_t)15;
-    lo = at & mask;
-    hi = (at + row_bytes + 15) & mask;
-    if (at_end(r)) {
-      lo = max(lo, (start + 15) & mask);
-      hi = min(hi, (start + (uintptr_t)(rows * row_bytes)) & mask);
-      if (hi < lo) hi = lo;
-    }
+    copy_bounds(reinterpret_cast<uintptr_t>(b), rows, row_bytes, edge, r, lo, hi);
   }
 
   __device__ __forceinline__ void copy(uint32_t dst, uintptr_t src, uint32_t bytes, uint64_t* bar) const {
