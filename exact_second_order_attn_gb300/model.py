@@ -15,6 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _model
+from ._lib import Rotary
 
 
 def _rows(t):
@@ -55,7 +56,8 @@ def rotary(r, Q, K=None, positions=None, offset=0):
     say); the results are contiguous, as ``attention`` takes them.
     ``positions``: int32 or int64, [N] or [B, N], added to ``offset``; without
     them token n has position offset + n."""
-    out = _Rotary.apply(Q, K, positions, r, int(offset), False)
+    # the backward turns by the description as it is now, whatever becomes of r
+    out = _Rotary.apply(Q, K, positions, Rotary.from_buffer_copy(r), int(offset), False)
     return out[0] if K is None else out
 
 
