@@ -110,6 +110,14 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
     return _Norm.apply(x, weight, bias, float(eps))
 
 
+def _head(w):
+    """A head (or its cotangent) where the kernels read it in place: bf16 rows
+    of whole 16 bytes have to start on 16 (a view of a flat vector need not)."""
+    off = (w is not None and w.dtype == torch.bfloat16 and w.dim() == 2 and w.shape[1] % 8 == 0
+           and w.data_ptr() % 16 != 0)
+    return w.clone() if off else w
+
+
 class _CeBwd(torch.autograd.Function):
     """(H, W, g) -> (dH, dW); its own backward is fbob_linear_ce_bob."""
 
@@ -118,7 +126,7 @@ class _CeBwd(torch.autograd.Function):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(H, W, g, target, lse)
         ctx.ignore_index = ignore_index
-        return _model.fbob_linear_ce_bwd(H, W, target, lse, g, ignore_index, want=want)
+        return _model.fbob_linear_ce_bwd(H, _head(W), target, lse, g, ignore_index, want=want)
 
     @staticmethod
     @once_differentiable
@@ -128,7 +136,7 @@ class _CeBwd(torch.autograd.Function):
         if (UH is None and UW is None) or not any(want):
             return None, None, None, None, None, None, None
         UH, UW = (None if u is None else u.contiguous() for u in (UH, UW))
-        gH, gW, gg = _model.fbob_linear_ce_bob(H, W, target, lse, g, UH, UW, ctx.ignore_index, want=want)
+        gH, gW, gg = _model.fbob_linear_ce_bob(H, _head(W), target, lse, g, UH, _head(UW), ctx.ignore_index, want=want)
         return gH, gW, gg, None, None, None, None
 
 
@@ -137,7 +145,7 @@ class _Ce(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, H, W, target, ignore_index):
-        loss, lse = _model.fbob_linear_ce_fwd(H, W, target, ignore_index)
+        loss, lse = _model.fbob_linear_ce_fwd(H, _head(W), target, ignore_index)
         ctx.save_for_backward(H, W, target, lse)
         ctx.ignore_index = ignore_index
         return loss
