@@ -44,6 +44,11 @@ def _call(name, stream, *args):
     f = getattr(_ext or _bind(), name)
     if stream is None:
         return f(*args)
+    for a in args:
+        if isinstance(a, torch.Tensor):  # the binding holds the others to the first one's device
+            if stream.device != a.device:
+                raise ValueError(f"stream: of {stream.device}, the tensors are on {a.device}")
+            break
     with torch.cuda.stream(stream):
         return f(*args)
 
