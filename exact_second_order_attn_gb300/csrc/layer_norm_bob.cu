@@ -13,6 +13,10 @@
 //   m(h)    = m(uw dy) - r (m(a) m(u xh) + m(u) m(a xh))
 //   m(h xh) = m(uw dy xh) - 2 r m(a xh) m(u xh)
 //   m(P u a) = m(u a) - m(u) m(a) - m(u xh) m(a xh).
+// The differences cancel where u and a have a common level L times their spread;
+// so does P u, and forming it first and then its product's mean, for one more
+// reduction, is as badly off: errors of gx relative to its size, D = 768, level 1
+// / 10 / 100: 1.4e-6 / 1.3e-4 / 1.4e-2 here, 1.0e-6 / 0.8e-4 / 0.9e-2 that way.
 // One read of x, dy and u; one write of gx and gdy.
 #include <initializer_list>
 #include <type_traits>

@@ -16,11 +16,16 @@
 // Dividing by gmax = max |g| (an fp32 factor of the results) keeps the target's
 // entry of G at p - 1 for a mean loss, where all g are equal: its rounding to
 // bf16 is then relative to p - 1 and not a systematic relative error of the
-// largest entry of every row.  The roundings average out over many tokens; with
-// few a row of dW hangs on one or two of them (4 tokens: 1.6 times the error of a
-// result rounded once; 24: 1.05 times), so up to kExactTokens counted ones G and Z
-// keep two bf16 terms (2^-17): 14 us of 127 at 24 tokens x 50,257 classes x 768.
-// How many count is known on the device, so the kernels choose.
+// largest entry of every row.  With unequal g it is one: against 64 bits dH and dW
+// are 1.34 times as far off as a result that is rounded once (rows 2.7 times at
+// most; 1.01 and 1.65 with equal g; 24 to 4096 tokens x 8000 classes x 768, g of
+// 0.1 to 1), what a gradient of the logits kept in bf16 costs.  A second term of G
+// for every token would cost two more products beside the step's four.  The
+// roundings average out over many tokens; with few a row of dW hangs on one or two
+// of them (4 tokens: 1.6 times the error of a result rounded once; 24: 1.05 times),
+// so up to kExactTokens counted ones G and Z keep two bf16 terms (2^-17): 14 us of
+// 127 at 24 tokens x 50,257 classes x 768.  How many count is known on the device,
+// so the kernels choose.
 //
 // Measured: 8192 tokens (a tenth ignored) x 50,257 classes x 768, bf16, forward
 // and gradients 1.37 ms in a burst (1.58 ms under the power cap), 4096 with the
