@@ -69,7 +69,9 @@ long long plane_rows_to(const CeArgs& a, int k) {  // of the planes before k
 // fewer leave the device idle (262,144 tokens x 8192 classes x 768, backward: 54 ms
 // with 256 columns, 15.6 with 1024, 9.4 with 2048, 6.9 with 4096).
 int piece_cols(const CeArgs& a, bool second) {
-  const size_t per = (size_t)plane_rows_to(a, grad_planes(a)) * 2 * (second ? 2 : 1);
+  // (kLowRows rows beside more tokens' are not counted: 128 bytes of a class)
+  const size_t rows = a.bf16 && a.T > kLowRows ? a.T : plane_rows_to(a, grad_planes(a));
+  const size_t per = rows * 2 * (second ? 2 : 1);
   size_t cols = a.piece > 0 ? (size_t)a.piece : kPieceBytes / (per ? per : 1);
   cols = up(cols < kPieceLeast && a.piece <= 0 ? kPieceLeast : cols, kPieceStep);
   const size_t whole = up(a.V, kPieceStep);

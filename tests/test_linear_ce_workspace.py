@@ -61,3 +61,13 @@ def test_the_classes_that_are_held_by_default(T, dtype, which):
     cols = -(-cols // 256) * 256
     assert need(0) == need(256) + (cols - 256) * room
     assert cols * room <= max(512 << 20, 2048 * room) + 256 * room
+
+
+@pytest.mark.parametrize("T,V,which", [(8192, 32768, 1), (4096, 32768, 2), (65536, 4096, 1), (131072, 2048, 1)])
+def test_classes_that_just_fit_are_one_piece(T, V, which):
+    """T x V x 2 bytes of 512 MiB: the second terms' rows of a few tokens do not
+    make two pieces of them."""
+    build()
+    a, b = (_lib.load().fbob_linear_ce_workspace_bytes(ctypes.byref(_lib.LinearCe(T, 2048, V, _lib.BF16, -100, piece)),
+                                                       which) for piece in (0, V))
+    assert a == b
