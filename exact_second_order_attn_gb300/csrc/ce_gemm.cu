@@ -38,8 +38,8 @@
 // Measured on 7,373 counted tokens x 50,257 classes x 768 (569 GFLOP a product,
 // burst clock): logits with statistics 332 us (1,710 TFLOP/s), with G 350, G W 353,
 // G^T H 312 us; half as many tokens, alpha's three products 563 us.  Bound by the
-// tensor cores; a tile of K = 768 takes 6,900 cycles where its MMAs need 6,144,
-// since stages come at 64 bytes per cycle and multiprocessor.
+// tensor cores; a tile of K = 768 in one chain takes 6,900 cycles where its MMAs
+// need 6,144, since stages come at 64 bytes per cycle and multiprocessor.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -28,9 +28,9 @@
 // so the kernels choose.
 //
 // Measured: 8192 tokens (a tenth ignored) x 50,257 classes x 768, bf16, forward
-// and gradients 1.37 ms in a burst (1.58 ms under the power cap), 4096 with the
-// second order 2.60 (2.72) ms; 24 tokens 109 us, bound by reading and writing W
-// and dW and by eight launches; fp32 1021 x 32,003 x 512 602 us.
+// and gradients 1.40 ms in a burst (1.60 ms under the power cap), 4096 with the
+// second order 2.65 (2.77) ms; 24 tokens 109 us, bound by reading and writing W
+// and dW and by ten launches; fp32 1021 x 32,003 x 512 610 us.
 //
 // fp32 inputs stand as three bf16 terms each (8 bits of the value per term);
 // the six products of terms whose magnitudes reach 2^-16 of the first are
