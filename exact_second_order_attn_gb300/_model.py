@@ -53,11 +53,11 @@ def _call(name, stream, *args):
         return f(*args)
 
 
-def _dtype(t):
+def _code(dtype):
     try:
-        return DTYPES[t.dtype]
+        return DTYPES[dtype]
     except KeyError:
-        raise TypeError(f"unsupported dtype {t.dtype}") from None
+        raise TypeError(f"unsupported dtype {dtype}") from None
 
 
 # --- rotary positions -----------------------------------------------------------------------------
@@ -83,10 +83,8 @@ def fbob_rotary_apply(rotary, Q, K=None, positions=None, offset=0, transpose=Fal
 def norm_for(x: torch.Tensor, weight_dtype: torch.dtype, eps: float = 0.0) -> Norm:
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
-    if weight_dtype not in DTYPES:
-        raise TypeError(f"unsupported dtype {weight_dtype}")
     D = x.shape[-1]
-    return Norm(x.numel() // D if D else 0, D, _dtype(x), DTYPES[weight_dtype], float(eps))
+    return Norm(x.numel() // D if D else 0, D, _code(x.dtype), _code(weight_dtype), float(eps))
 
 
 def fbob_layer_norm_workspace_bytes(p: Norm) -> int:
@@ -105,7 +103,7 @@ def fbob_layer_norm_bwd(x, weight, mean, rstd, dy, dx=None, dw=None, db=None, wa
     (the others are None).  dw needs ``weight``; without one db has
     ``bias_dtype`` (default: x's)."""
     return _call("layer_norm_bwd", stream, x, weight, mean, rstd, dy, dx, dw, db, *want,
-                 None if bias_dtype is None else DTYPES[bias_dtype], workspace)
+                 None if bias_dtype is None else _code(bias_dtype), workspace)
 
 
 def fbob_layer_norm_bob(x, weight, mean, rstd, dy, ux, uw=None, ub=None, gx=None, gw=None, gdy=None,
@@ -123,7 +121,7 @@ def linear_ce_for(H: torch.Tensor, W: torch.Tensor, ignore_index: int = -100, pi
     (T, D), V = H.shape, W.shape[0]
     if max(T, D, V) > 2 ** 31 - 1:
         raise ValueError("sizes must fit 32 bits")
-    return LinearCe(T, D, V, _dtype(H), int(ignore_index), int(piece))
+    return LinearCe(T, D, V, _code(H.dtype), int(ignore_index), int(piece))
 
 
 def fbob_linear_ce_workspace_bytes(p: LinearCe, which: int) -> int:
