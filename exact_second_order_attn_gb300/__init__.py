@@ -12,9 +12,10 @@ from ._lib import (  # noqa: F401
     fbob_profile_report, fbob_set_wait_limit_ns, load, problem_for,
 )
 from ._model import (  # noqa: F401
-    LinearCe, Norm, Rotary, fbob_layer_norm_bob, fbob_layer_norm_bwd, fbob_layer_norm_fwd,
+    ACTIVATIONS, Dropout, Linear, LinearCe, Norm, Rotary, fbob_dropout_apply, fbob_layer_norm_bob, fbob_layer_norm_bwd, fbob_layer_norm_fwd,
     fbob_layer_norm_workspace_bytes, fbob_linear_ce_bob, fbob_linear_ce_bwd, fbob_linear_ce_fwd,
-    fbob_linear_ce_workspace_bytes, fbob_rotary_apply, fbob_rotary_frequencies, linear_ce_for, norm_for,
+    fbob_linear_ce_workspace_bytes, fbob_linear_bob, fbob_linear_bwd, fbob_linear_fwd, fbob_linear_workspace_bytes,
+    fbob_rotary_apply, fbob_rotary_frequencies, linear_ce_for, linear_for, norm_for,
 )
 from .autograd import attention, hvp  # noqa: F401
-from .model import layer_norm, linear_cross_entropy, rotary  # noqa: F401
+from .model import dropout, layer_norm, linear, linear_cross_entropy, rotary  # noqa: F401

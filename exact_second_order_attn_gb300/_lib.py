@@ -28,6 +28,7 @@ FUNCTIONS = (
     "fbob_rotary_frequencies", "fbob_rotary_apply",
     "fbob_layer_norm_workspace_bytes", "fbob_layer_norm_fwd", "fbob_layer_norm_bwd", "fbob_layer_norm_bob",
     "fbob_linear_ce_workspace_bytes", "fbob_linear_ce_fwd", "fbob_linear_ce_bwd", "fbob_linear_ce_bob",
+    "fbob_dropout_apply", "fbob_linear_workspace_bytes", "fbob_linear_fwd", "fbob_linear_bwd", "fbob_linear_bob",
 )
 
 
@@ -73,6 +74,25 @@ class LinearCe(ctypes.Structure):
     """fbob_linear_ce: T tokens of D columns, V classes."""
     _fields_ = [("T", ctypes.c_int), ("D", ctypes.c_int), ("V", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("ignore_index", ctypes.c_longlong), ("piece", ctypes.c_int)]
+
+
+class Dropout(ctypes.Structure):
+    """fbob_dropout: elements dropped with probability ``p`` (to 2^-16), as the
+    generator's ``seed`` and ``offset`` say (include/fbob.h has the mask's
+    definition); calls with different offsets have independent masks."""
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_ulonglong), ("offset", ctypes.c_ulonglong)]
+
+    def __init__(self, p, seed=0, offset=0):
+        super().__init__(p, seed % 2 ** 64, offset % 2 ** 64)
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+class Linear(ctypes.Structure):
+    """fbob_linear: T tokens of K columns, N outputs."""
+    _fields_ = [("T", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("activation", ctypes.c_int)]
 
 
 class FbobError(RuntimeError):
@@ -129,6 +149,17 @@ def load():
     lib.fbob_linear_ce_bwd.restype = st
     lib.fbob_linear_ce_bob.argtypes = [ce] + [vp] * 11 + [sz, vp]
     lib.fbob_linear_ce_bob.restype = st
+    dp, lp = ctypes.POINTER(Dropout), ctypes.POINTER(Linear)
+    lib.fbob_dropout_apply.argtypes = [dp, vp, ll, st, st] + [vp] * 4
+    lib.fbob_dropout_apply.restype = st
+    lib.fbob_linear_workspace_bytes.argtypes = [lp, dp, st]
+    lib.fbob_linear_workspace_bytes.restype = sz
+    lib.fbob_linear_fwd.argtypes = [lp, dp] + [vp] * 8 + [sz, vp]
+    lib.fbob_linear_fwd.restype = st
+    lib.fbob_linear_bwd.argtypes = [lp, dp] + [vp] * 9 + [sz, vp]
+    lib.fbob_linear_bwd.restype = st
+    lib.fbob_linear_bob.argtypes = [lp, dp] + [vp] * 13 + [sz, vp]
+    lib.fbob_linear_bob.restype = st
     lib.fbob_device_status.argtypes = [vp]
     lib.fbob_device_status.restype = st
     lib.fbob_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]

@@ -15,7 +15,7 @@ import importlib
 import torch
 
 from . import _lib
-from ._lib import LinearCe, Norm, Rotary, _check, load
+from ._lib import ACTIVATIONS, Dropout, Linear, LinearCe, Norm, Rotary, _check, load  # noqa: F401
 
 DTYPES = {torch.bfloat16: _lib.BF16, torch.float32: _lib.FP32}
 
@@ -147,3 +147,65 @@ def fbob_linear_ce_bob(H, W, target, lse, g, UH, UW, ignore_index=-100, piece=0,
     """(gH, gW, gg) = the vector-Jacobian product of (H, W, g) -> (dH, dW)
     along (UH, UW), one of which may be None; ``want`` says which to compute."""
     return _call("linear_ce_bob", stream, H, W, target, lse, g, UH, UW, ignore_index, piece, gH, gW, gg, *want, workspace)
+
+
+# --- linear layers and dropout ----------------------------------------------------------------------
+
+def _activation(name):
+    try:
+        return ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}") from None
+
+
+def linear_for(x: torch.Tensor, W: torch.Tensor, activation: str = "none") -> Linear:
+    if x.dim() < 1 or W.dim() != 2 or x.shape[-1] != W.shape[1]:
+        raise ValueError(f"x [..., K] and W [N, K] are needed, got {tuple(x.shape)} and {tuple(W.shape)}")
+    N, K = W.shape
+    T = x.numel() // K if K else 0
+    if max(T, K, N) > 2 ** 31 - 1:
+        raise ValueError("sizes must fit 32 bits")
+    return Linear(T, K, N, _code(x.dtype), _activation(activation))
+
+
+def fbob_linear_workspace_bytes(p: Linear, which: int, dropout: Dropout | None = None) -> int:
+    """Bytes of workspace of the forward (0), backward (1) or its product (2)."""
+    return int(load().fbob_linear_workspace_bytes(ctypes.byref(p), None if dropout is None else ctypes.byref(dropout),
+                                                  which))
+
+
+def fbob_dropout_apply(dropout, x, residual=None, counter=None, y=None, stream=None):
+    """y = residual + m x with the mask m that ``dropout`` (a ``Dropout``)
+    describes; rows are the last dimension of x (contiguous, any leading
+    shape).  ``counter``: one int64 element on the device, added to the offset
+    when the call runs.  The gradient of x is the same call on y's."""
+    return _call("dropout_apply", stream, dropout, x, residual, counter, y)
+
+
+def fbob_linear_fwd(x, W, bias=None, residual=None, activation="none", dropout=None, counter=None, keep=True, y=None,
+                    z=None, workspace=None, stream=None):
+    """(y, z): y = residual + m a(z), z = x W^T + bias, of x [..., K]
+    (contiguous) and W [N, K]; bias [N] and residual [..., N] are optional.
+    ``activation``: "none", "relu", "gelu", "gelu_tanh" or "silu".  ``dropout``
+    (a ``Dropout``) and ``counter``: as for fbob_dropout_apply.  z, which the
+    calls below take, is None for "none" or with ``keep`` false.
+    ``workspace``: uint8."""
+    return _call("linear_fwd", stream, x, W, bias, residual, _activation(activation), dropout, counter, keep, y, z,
+                 workspace)
+
+
+def fbob_linear_bwd(x, W, z, dy, activation="none", dropout=None, counter=None, dx=None, dW=None, db=None,
+                    want=(True, True, True), workspace=None, stream=None):
+    """(dx, dW, db) of a linear layer; ``want`` says which to compute (the
+    others are None).  The residual's gradient is dy."""
+    return _call("linear_bwd", stream, x, W, z, dy, _activation(activation), dropout, counter, dx, dW, db, *want,
+                 workspace)
+
+
+def fbob_linear_bob(x, W, z, dy, ux, uW, ub=None, activation="none", dropout=None, counter=None, gx=None, gW=None,
+                    gb=None, gdy=None, want=(True, True, True, True), workspace=None, stream=None):
+    """(gx, gW, gb, gdy) = the vector-Jacobian product of
+    (x, W, bias, dy) -> (dx, dW, db) along (ux, uW, ub), where ub and one of
+    ux and uW may be None; ``want`` says which to compute."""
+    return _call("linear_bob", stream, x, W, z, dy, ux, uW, ub, _activation(activation), dropout, counter, gx, gW, gb,
+                 gdy, *want, workspace)

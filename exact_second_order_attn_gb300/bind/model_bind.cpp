@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
+#include <vector>
 
 #include "fbob.h"
 
@@ -439,6 +440,156 @@ PyObject* linear_ce_bob(PyObject* const* a, Py_ssize_t n) {
   return tuple_of(gH, gW, gg);
 }
 
+// --- linear layers and dropout ----------------------------------------------------------------------
+
+// A dropout's description (None: none), held while the call runs.
+struct Drop {
+  Py_buffer b;
+  const fbob_dropout* p = nullptr;
+  explicit Drop(PyObject* o) {
+    if (o == Py_None) return;
+    if (!PyObject_CheckBuffer(o)) raise(PyExc_TypeError, "dropout", "a Dropout description is needed");
+    if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) throw Raised{};
+    if (b.len != (Py_ssize_t)sizeof(fbob_dropout)) {
+      PyBuffer_Release(&b);
+      raise(PyExc_TypeError, "dropout", "a Dropout description is needed");
+    }
+    p = static_cast<const fbob_dropout*>(b.buf);
+  }
+  ~Drop() {
+    if (p) PyBuffer_Release(&b);
+  }
+};
+
+const long long* counter_of(PyObject* o, int device) {
+  const Tensor* t = tensor(o, "counter", true);
+  if (!t) return nullptr;
+  check(t, "counter", device, ScalarType::Long, std::nullopt);
+  if (t->numel() != 1) raise(PyExc_ValueError, "counter", "one element is needed");
+  return static_cast<const long long*>(t->data_ptr());
+}
+
+// (dropout, x, residual, counter, y)
+PyObject* dropout_apply(PyObject* const* a, Py_ssize_t n) {
+  count(n, 5);
+  const Drop drop(a[0]);
+  if (!drop.p) raise(PyExc_TypeError, "dropout", "a Dropout description is needed");
+  const Tensor& x = *tensor(a[1], "x");
+  const Tensor* r = tensor(a[2], "residual", true);
+  if (x.dim() < 1) raise(PyExc_ValueError, "x", "must have at least one dimension");
+  const int64_t D = x.size(-1);
+  if (D > INT_MAX) raise(PyExc_ValueError, "x", "sizes must fit 32 bits");
+  const int dtype = dtype_code(x, "x"), device = device_of(x, "x");
+  check(&x, "x", device, x.scalar_type(), std::nullopt);
+  check(r, "residual", device, x.scalar_type(), x.sizes());
+  const long long* counter = counter_of(a[3], device);
+  Launch at(device);
+  const std::optional<Tensor> y = output(a[4], "y", x, device, x.sizes(), x.scalar_type());
+  done(fbob_dropout_apply(drop.p, counter, D ? x.numel() / D : 0, (int)D, dtype, ptr(&x), ptr(r), ptr(y), at.stream));
+  return wrapped(y);
+}
+
+// What the calls of a linear layer share: x [..., K] and W [N, K], checked.
+struct Layer {
+  fbob_linear p;
+  int device;
+  ScalarType type;
+  std::vector<int64_t> out;  // [..., N]
+
+  Layer(const Tensor& x, const Tensor& W, PyObject* activation) {
+    if (x.dim() < 1 || W.dim() != 2 || x.size(-1) != W.size(1)) {
+      PyErr_Format(PyExc_ValueError, "x [..., K] and W [N, K] are needed, got %s and %s", text(x.sizes()).c_str(),
+                   text(W.sizes()).c_str());
+      throw Raised{};
+    }
+    const int64_t K = x.size(-1), T = K ? x.numel() / K : 0;
+    if (T > INT_MAX || K > INT_MAX || W.size(0) > INT_MAX) raise(PyExc_ValueError, "x, W", "sizes must fit 32 bits");
+    type = x.scalar_type();
+    p.T = (int)T, p.K = (int)K, p.N = (int)W.size(0), p.dtype = dtype_code(x, "x");
+    p.activation = (int)integer(activation, "activation");
+    device = device_of(x, "x");
+    check(&x, "x", device, type, std::nullopt);
+    check(&W, "W", device, type, std::nullopt);
+    out.assign(x.sizes().begin(), x.sizes().end());
+    out.back() = p.N;
+  }
+  at::IntArrayRef bias(const Tensor& W) const { return W.sizes().slice(0, 1); }
+};
+
+// (x, W, bias, residual, activation, dropout, counter, keep, y, z, workspace)
+PyObject* linear_fwd(PyObject* const* a, Py_ssize_t n) {
+  count(n, 11);
+  const Tensor &x = *tensor(a[0], "x"), &W = *tensor(a[1], "W");
+  const Tensor *b = tensor(a[2], "bias", true), *r = tensor(a[3], "residual", true);
+  const Layer l(x, W, a[4]);
+  const Drop drop(a[5]);
+  check(b, "bias", l.device, l.type, l.bias(W));
+  check(r, "residual", l.device, l.type, l.out);
+  const long long* counter = counter_of(a[6], l.device);
+  const bool keep = flag(a[7]) && l.p.activation != FBOB_ACT_NONE;
+  Launch at(l.device);
+  const std::optional<Tensor> y = output(a[8], "y", x, l.device, l.out, l.type);
+  std::optional<Tensor> z;
+  if (keep) z = output(a[9], "z", x, l.device, l.out, l.type);
+  const auto ws = workspace_of(a[10], x, l.device, fbob_linear_workspace_bytes(&l.p, drop.p, 0), ScalarType::Byte);
+  done(fbob_linear_fwd(&l.p, drop.p, counter, ptr(&x), ptr(&W), ptr(b), ptr(r), ptr(y), ptr(z), ptr(ws), bytes_of(ws),
+                       at.stream));
+  return tuple_of(y, z);
+}
+
+const Tensor* check_layer(const Layer& l, PyObject* z, const Tensor& dy) {
+  const Tensor* t = l.p.activation == FBOB_ACT_NONE ? nullptr : tensor(z, "z");
+  check(t, "z", l.device, l.type, l.out);
+  check(&dy, "dy", l.device, l.type, l.out);
+  return t;
+}
+
+// (x, W, z, dy, activation, dropout, counter, dx, dW, db, want dx, want dW, want db, workspace)
+PyObject* linear_bwd(PyObject* const* a, Py_ssize_t n) {
+  count(n, 14);
+  const Tensor &x = *tensor(a[0], "x"), &W = *tensor(a[1], "W"), &dy = *tensor(a[3], "dy");
+  const Layer l(x, W, a[4]);
+  const Tensor* z = check_layer(l, a[2], dy);
+  const Drop drop(a[5]);
+  const long long* counter = counter_of(a[6], l.device);
+  const bool want_dx = flag(a[10]), want_dW = flag(a[11]), want_db = flag(a[12]);
+  Launch at(l.device);
+  std::optional<Tensor> dx, dW, db;
+  if (want_dx) dx = output(a[7], "dx", x, l.device, x.sizes(), l.type);
+  if (want_dW) dW = output(a[8], "dW", x, l.device, W.sizes(), l.type);
+  if (want_db) db = output(a[9], "db", x, l.device, l.bias(W), l.type);
+  const auto ws = workspace_of(a[13], x, l.device, fbob_linear_workspace_bytes(&l.p, drop.p, 1), ScalarType::Byte);
+  done(fbob_linear_bwd(&l.p, drop.p, counter, ptr(&x), ptr(&W), ptr(z), ptr(&dy), ptr(dx), ptr(dW), ptr(db), ptr(ws),
+                       bytes_of(ws), at.stream));
+  return tuple_of(dx, dW, db);
+}
+
+// (x, W, z, dy, ux, uW, ub, activation, dropout, counter, gx, gW, gb, gdy, want gx, want gW, want gb, want gdy,
+// workspace)
+PyObject* linear_bob(PyObject* const* a, Py_ssize_t n) {
+  count(n, 19);
+  const Tensor &x = *tensor(a[0], "x"), &W = *tensor(a[1], "W"), &dy = *tensor(a[3], "dy");
+  const Tensor *ux = tensor(a[4], "ux", true), *uW = tensor(a[5], "uW", true), *ub = tensor(a[6], "ub", true);
+  const Layer l(x, W, a[7]);
+  const Tensor* z = check_layer(l, a[2], dy);
+  check(ux, "ux", l.device, l.type, x.sizes());
+  check(uW, "uW", l.device, l.type, W.sizes());
+  check(ub, "ub", l.device, l.type, l.bias(W));
+  const Drop drop(a[8]);
+  const long long* counter = counter_of(a[9], l.device);
+  const bool want_gx = flag(a[14]), want_gW = flag(a[15]), want_gb = flag(a[16]), want_gdy = flag(a[17]);
+  Launch at(l.device);
+  std::optional<Tensor> gx, gW, gb, gdy;
+  if (want_gx) gx = output(a[10], "gx", x, l.device, x.sizes(), l.type);
+  if (want_gW) gW = output(a[11], "gW", x, l.device, W.sizes(), l.type);
+  if (want_gb) gb = output(a[12], "gb", x, l.device, l.bias(W), l.type);
+  if (want_gdy) gdy = output(a[13], "gdy", x, l.device, l.out, l.type);
+  const auto ws = workspace_of(a[18], x, l.device, fbob_linear_workspace_bytes(&l.p, drop.p, 2), ScalarType::Byte);
+  done(fbob_linear_bob(&l.p, drop.p, counter, ptr(&x), ptr(&W), ptr(z), ptr(&dy), ptr(ux), ptr(uW), ptr(ub), ptr(gx),
+                       ptr(gW), ptr(gb), ptr(gdy), ptr(ws), bytes_of(ws), at.stream));
+  return tuple_of(gx, gW, gb, gdy);
+}
+
 // C++ and torch errors become Python's; none crosses into the interpreter.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -460,7 +611,8 @@ PyObject* set_check(PyObject*, PyObject* f) {
 #define ENTRY(f) {#f, (PyCFunction)(void (*)(void))entry<f>, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {
     ENTRY(rotary_apply),   ENTRY(layer_norm_fwd), ENTRY(layer_norm_bwd), ENTRY(layer_norm_bob),
-    ENTRY(linear_ce_fwd),  ENTRY(linear_ce_bwd),  ENTRY(linear_ce_bob),  {"set_check", set_check, METH_O, nullptr},
+    ENTRY(linear_ce_fwd),  ENTRY(linear_ce_bwd),  ENTRY(linear_ce_bob),  ENTRY(dropout_apply),
+    ENTRY(linear_fwd),     ENTRY(linear_bwd),     ENTRY(linear_bob),     {"set_check", set_check, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fbob_model", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,5 +1,5 @@
 // C ABI of libfbob.so: the operators around the attention (rotary positions,
-// layer norm, the linear head's cross entropy).  Argument validation and dispatch, as in api.cpp.
+// layer norm, the linear head's cross entropy, linear layers, dropout).  Argument validation and dispatch, as in api.cpp.
 #include <cuda_runtime_api.h>
 #include <math.h>
 #include <string.h>
@@ -209,6 +209,76 @@ fbob_status zero_head(const fbob_linear_ce* p, void* dW, cudaStream_t stream) {
   return e == cudaSuccess ? FBOB_OK : cuda_fail(e, "linear_ce memset");
 }
 
+// Elements dropped of 65,536 and the others' factor; none for a null description.
+fbob_status check_dropout(const fbob_dropout* d, const long long* counter, fbob::DropArgs* out) {
+  memset(out, 0, sizeof(*out));
+  out->scale = 1.f;
+  if (!d) {
+    if (counter) return fail(FBOB_ERR_INVALID_ARG, "a counter without a dropout");
+    return FBOB_OK;
+  }
+  if (!(d->p >= 0.0 && d->p <= 1.0)) return fail(FBOB_ERR_INVALID_ARG, "p must be in [0, 1] (got %g)", d->p);
+  if ((reinterpret_cast<uintptr_t>(counter) & 7u) != 0)
+    return fail(FBOB_ERR_INVALID_ARG, "pointer counter is not aligned to its elements");
+  out->dropped = (unsigned)nearbyint(65536.0 * d->p);  // (halves to even)
+  out->scale = out->dropped < 65536u ? (float)(65536.0 / (65536u - out->dropped)) : 0.f;
+  out->seed = d->seed, out->offset = d->offset, out->counter = counter;
+  return FBOB_OK;
+}
+
+fbob_status check_linear(const fbob_linear* p) {
+  if (!p) return fail(FBOB_ERR_INVALID_ARG, "linear descriptor is null");
+  const fbob_status st = check_dtype(p->dtype);
+  if (st != FBOB_OK) return st;
+  if (p->activation < FBOB_ACT_NONE || p->activation > FBOB_ACT_SILU)
+    return fail(FBOB_ERR_INVALID_ARG, "unknown activation %d", p->activation);
+  if (p->T < 0 || p->K <= 0 || p->N <= 0)
+    return fail(FBOB_ERR_INVALID_ARG, "bad sizes T=%d K=%d N=%d", p->T, p->K, p->N);
+  if (p->T > (1 << 24) || p->K > (1 << 20) || p->N > (1 << 20))
+    return fail(FBOB_ERR_UNSUPPORTED, "T=%d K=%d N=%d exceed 2^24, 2^20, 2^20", p->T, p->K, p->N);
+  const long long most = 1ll << 40;
+  if ((long long)p->T * p->K > most || (long long)p->T * p->N > most || (long long)p->N * p->K > most)
+    return fail(FBOB_ERR_UNSUPPORTED, "T=%d K=%d N=%d are too large", p->T, p->K, p->N);
+  return FBOB_OK;
+}
+
+fbob::LinearArgs linear_args(const fbob_linear* p, const fbob::DropArgs& drop) {
+  fbob::LinearArgs a;
+  memset(&a, 0, sizeof(a));
+  a.T = p->T, a.K = p->K, a.N = p->N, a.bf16 = p->dtype == FBOB_BF16, a.act = p->activation, a.drop = drop;
+  return a;
+}
+
+// Operands of the products are read in place by 16-byte copies where they are bf16
+// and their rows (of `cols`) are 16-byte multiples.
+fbob_status check_operands(const fbob_linear* p, const Arg* a, const int* cols, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (p->dtype == FBOB_BF16 && cols[i] % 8 == 0 && !aligned16(a[i].p))
+      return fail(FBOB_ERR_INVALID_ARG, "pointer %s is not 16-byte aligned", a[i].name);
+  }
+  return FBOB_OK;
+}
+
+fbob_status linear_run(const fbob::LinearArgs& a, fbob::LinearPass pass, size_t have, const char* where,
+                       cudaStream_t stream) {
+  fbob_status st = check_workspace(a.ws, have, fbob::linear_workspace(a, pass));
+  if (st != FBOB_OK) return st;
+  fbob::DevCtx c;
+  if ((st = fbob::make_ctx(&c)) != FBOB_OK) return st;
+  const cudaError_t e = fbob::linear(a, pass, c, stream);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  return FBOB_OK;
+}
+
+// Gradients of weights over no tokens are zero.
+fbob_status zero_weights(const fbob_linear* p, void* dW, void* db, cudaStream_t stream) {
+  const size_t e = p->dtype == FBOB_BF16 ? 2 : 4;
+  cudaError_t r = cudaSuccess;
+  if (dW) r = cudaMemsetAsync(dW, 0, (size_t)p->N * p->K * e, stream);
+  if (r == cudaSuccess && db) r = cudaMemsetAsync(db, 0, (size_t)p->N * e, stream);
+  return r == cudaSuccess ? FBOB_OK : cuda_fail(r, "linear memset");
+}
+
 }  // namespace
 
 extern "C" {
@@ -407,6 +477,94 @@ fbob_status fbob_linear_ce_bob(const fbob_linear_ce* p, const void* H, const voi
   a.H = H, a.W = W, a.target = target, a.lse = lse, a.g = g, a.UH = UH, a.UW = UW;
   a.dH = gH, a.dW = gW, a.gg = gg, a.ws = workspace;
   return ce_run(a, fbob::CePass::kBob, workspace_bytes, "linear_ce_bob launch", stream);
+}
+
+fbob_status fbob_dropout_apply(const fbob_dropout* d, const long long* counter, long long rows, int D, int dtype,
+                               const void* x, const void* r, void* y, cudaStream_t stream) {
+  fbob::DropoutArgs a;
+  memset(&a, 0, sizeof(a));
+  fbob_status st = check_dtype(dtype);
+  if (st != FBOB_OK) return st;
+  if (!d) return fail(FBOB_ERR_INVALID_ARG, "dropout descriptor is null");
+  if ((st = check_dropout(d, counter, &a.drop)) != FBOB_OK) return st;
+  if (rows < 0 || D <= 0) return fail(FBOB_ERR_INVALID_ARG, "bad sizes rows=%lld D=%d", rows, D);
+  if (rows >= (1ll << 32) || D >= 0x7fffffff - 8 || (double)rows * D > (double)(1ll << 40))
+    return fail(FBOB_ERR_UNSUPPORTED, "%lld rows of %d are too large", rows, D);
+  if (rows == 0) return FBOB_OK;
+  const Arg ps[] = {{x, "x", dtype, true}, {r, "r", dtype, false}, {y, "y", dtype, true}};
+  if ((st = check_args(ps, 3)) != FBOB_OK) return st;
+  a.x = x, a.r = r, a.y = y, a.rows = rows, a.D = D, a.bf16 = dtype == FBOB_BF16;
+  const cudaError_t e = fbob::dropout(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "dropout launch");
+  return FBOB_OK;
+}
+
+size_t fbob_linear_workspace_bytes(const fbob_linear* p, const fbob_dropout* dropout, int pass) {
+  fbob::DropArgs drop;
+  if (check_linear(p) != FBOB_OK || p->T == 0 || check_dropout(dropout, nullptr, &drop) != FBOB_OK || pass < 0 || pass > 2)
+    return 0;
+  return fbob::linear_workspace(linear_args(p, drop), static_cast<fbob::LinearPass>(pass));
+}
+
+fbob_status fbob_linear_fwd(const fbob_linear* p, const fbob_dropout* dropout, const long long* counter, const void* x,
+                            const void* W, const void* b, const void* r, void* y, void* z, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
+  fbob::DropArgs drop;
+  fbob_status st = check_linear(p);
+  if (st != FBOB_OK || (st = check_dropout(dropout, counter, &drop)) != FBOB_OK) return st;
+  if (p->T == 0) return FBOB_OK;
+  const Arg ps[] = {{x, "x", p->dtype, true},  {W, "W", p->dtype, true}, {b, "b", p->dtype, false},
+                    {r, "r", p->dtype, false}, {y, "y", p->dtype, true}, {z, "z", p->dtype, false}};
+  const int cols[] = {p->K, p->K};
+  if ((st = check_args(ps, 6)) != FBOB_OK || (st = check_operands(p, ps, cols, 2)) != FBOB_OK) return st;
+  fbob::LinearArgs a = linear_args(p, drop);
+  a.x = x, a.W = W, a.b = b, a.r = r, a.y = y, a.z_out = z, a.ws = workspace;
+  return linear_run(a, fbob::LinearPass::kFwd, workspace_bytes, "linear_fwd launch", stream);
+}
+
+fbob_status fbob_linear_bwd(const fbob_linear* p, const fbob_dropout* dropout, const long long* counter, const void* x,
+                            const void* W, const void* z, const void* dy, void* dx, void* dW, void* db, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
+  fbob::DropArgs drop;
+  fbob_status st = check_linear(p);
+  if (st != FBOB_OK || (st = check_dropout(dropout, counter, &drop)) != FBOB_OK) return st;
+  const bool some = p->T > 0;
+  const Arg ps[] = {{x, "x", p->dtype, some},    {W, "W", p->dtype, some},
+                    {dy, "dy", p->dtype, some},  {z, "z", p->dtype, some && p->activation != FBOB_ACT_NONE},
+                    {dx, "dx", p->dtype, false}, {dW, "dW", p->dtype, false},
+                    {db, "db", p->dtype, false}};
+  const int cols[] = {p->K, p->K, p->N};
+  if ((st = check_args(ps, 7)) != FBOB_OK || (st = check_operands(p, ps, cols, 3)) != FBOB_OK) return st;
+  if (!some) return zero_weights(p, dW, db, stream);
+  if (!dx && !dW && !db) return FBOB_OK;
+  fbob::LinearArgs a = linear_args(p, drop);
+  a.x = x, a.W = W, a.z = z, a.dy = dy, a.dx = dx, a.dW = dW, a.db = db, a.ws = workspace;
+  return linear_run(a, fbob::LinearPass::kBwd, workspace_bytes, "linear_bwd launch", stream);
+}
+
+fbob_status fbob_linear_bob(const fbob_linear* p, const fbob_dropout* dropout, const long long* counter, const void* x,
+                            const void* W, const void* z, const void* dy, const void* ux, const void* uW, const void* ub,
+                            void* gx, void* gW, void* gb, void* gdy, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  fbob::DropArgs drop;
+  fbob_status st = check_linear(p);
+  if (st != FBOB_OK || (st = check_dropout(dropout, counter, &drop)) != FBOB_OK) return st;
+  const bool some = p->T > 0;
+  const Arg ps[] = {{x, "x", p->dtype, some},    {W, "W", p->dtype, some},
+                    {dy, "dy", p->dtype, some},  {ux, "ux", p->dtype, false},
+                    {uW, "uW", p->dtype, false}, {z, "z", p->dtype, some && p->activation != FBOB_ACT_NONE},
+                    {ub, "ub", p->dtype, false}, {gx, "gx", p->dtype, false},
+                    {gW, "gW", p->dtype, false}, {gb, "gb", p->dtype, false},
+                    {gdy, "gdy", p->dtype, false}};
+  const int cols[] = {p->K, p->K, p->N, p->K, p->K};
+  if ((st = check_args(ps, 11)) != FBOB_OK || (st = check_operands(p, ps, cols, 5)) != FBOB_OK) return st;
+  if (!ux && !uW) return fail(FBOB_ERR_INVALID_ARG, "pointers ux and uW are both null");
+  if (!some) return zero_weights(p, gW, gb, stream);
+  if (!gx && !gW && !gb && !gdy) return FBOB_OK;
+  fbob::LinearArgs a = linear_args(p, drop);
+  a.x = x, a.W = W, a.z = z, a.dy = dy, a.ux = ux, a.uW = uW, a.ub = ub;
+  a.dx = gx, a.dW = gW, a.db = gb, a.gdy = gdy, a.ws = workspace;
+  return linear_run(a, fbob::LinearPass::kBob, workspace_bytes, "linear_bob launch", stream);
 }
 
 }  // extern "C"

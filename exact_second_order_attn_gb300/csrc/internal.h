@@ -88,6 +88,35 @@ struct CeArgs {
 };
 enum class CePass { kFwd, kBwd, kBob };
 
+// Dropout: `dropped` of 65,536 elements; 0 is none.
+struct DropArgs {
+  unsigned long long seed, offset;
+  const long long* counter;  // null, or added to the offset, on the device
+  unsigned int dropped;
+  float scale;
+};
+
+// y = r + m x over rows of D elements; r may be null, y may be x or r.
+struct DropoutArgs {
+  const void *x, *r;
+  void* y;
+  long long rows;
+  int D, bf16;
+  DropArgs drop;
+};
+
+enum { kActNone, kActRelu, kActGelu, kActGeluTanh, kActSilu };
+
+// Linear layer: T rows of K columns, N outputs.
+struct LinearArgs {
+  const void *x, *W, *b, *r, *z, *dy, *ux, *uW, *ub;
+  void *y, *z_out, *dx, *dW, *db, *gdy;  // or gx, gW, gb
+  void* ws;
+  int T, K, N, bf16, act;
+  DropArgs drop;
+};
+enum class LinearPass { kFwd, kBwd, kBob };
+
 // Status word bits.
 constexpr unsigned int kErrTimeout = 1u;
 constexpr unsigned int kErrTarget = 2u;  // a class index outside the vocabulary
@@ -118,6 +147,11 @@ size_t layer_norm_workspace_floats(long long rows, int D);  // of bwd (bob needs
 // linear_ce.cu
 size_t linear_ce_workspace(const CeArgs& a, CePass pass);
 cudaError_t linear_ce(const CeArgs& a, CePass pass, const DevCtx& c, cudaStream_t s);
+
+// dropout.cu, linear.cu
+cudaError_t dropout(const DropoutArgs& a, cudaStream_t s);
+size_t linear_workspace(const LinearArgs& a, LinearPass pass);
+cudaError_t linear(const LinearArgs& a, LinearPass pass, const DevCtx& c, cudaStream_t s);
 
 // bob_static.cu: the fixed (alpha, E) workspace of fbob_attn_bob_noalloc.
 size_t static_workspace_rows();           // capacity in query rows (B*H*N)

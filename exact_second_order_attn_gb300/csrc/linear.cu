@@ -1,0 +1,573 @@
+// Linear layers y = r + m a(x W^T + b): forward, gradients, and the gradients' own
+// vector-Jacobian product (formulas in fbob.h; products in linear_gemm.cuh).
+//
+// Forward: one product whose epilogue adds the bias, applies activation and
+// dropout and adds the residual; a training forward also keeps z in the tensors'
+// type (bf16: off by 2^-9 of z, so dz by 2^-9 |z a''|, less than dz's own rounding).
+// Gradients: dz = m dy a'(z) once (with its column sums, in fp32), then dx = dz W
+// and dW = dz^T x; without activation and dropout dz is dy itself.  Second order: one
+// product for t whose epilogue turns it into gdy, q and dz, then gx = q W + dz uW and
+// gW = q^T x + dz^T ux, each one product over two segments.
+//
+// dz and q are rounded to bf16 for the products of bf16 tensors, which costs as much
+// as the rounding of the result (errors of 1.4 half steps); with up to kExactTokens
+// tokens a row of dW hangs on a few of them, and they keep two bf16 terms.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <string.h>
+
+#include "activation.cuh"
+#include "ce.h"
+#include "dropout.cuh"
+#include "launch.cuh"
+#include "linear.h"
+#include "prof.h"
+#include "vec8.cuh"
+
+namespace fbob {
+namespace lin {
+namespace {
+
+using ce::matrix_map;
+using ce::store_map;
+
+size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+constexpr int kPairs = 76;                     // block pairs of a GB300, for the rule below
+constexpr size_t kSlabBytes = 512ull << 20;    // slabs of a product
+constexpr long long kLongTerms = 16384;        // bf16 sums above end their chains there
+
+// Tile width and slabs of a product of M x N outputs over `steps` steps of the
+// contraction in each of nseg segments.
+struct Shape {
+  int tile_n, splits;
+};
+
+// The estimated time in cycles decides.  Per step of a tile 575 cycles (256 columns)
+// or 400 (128: as much of A is loaded for half the products), per wave of tiles 1,000
+// for the hand-over; slabs cost a write and a read of fp32 at 3,500 bytes a cycle and
+// a launch.
+Shape choose(long long M, long long N, int steps, int nseg, bool slabs, bool narrow_only) {
+  auto cost = [&](int tile, int s) {
+    const long long tiles = ((M + kTileM - 1) / kTileM) * ((N + tile - 1) / tile) * s;
+    const double waves = (double)((tiles + kPairs - 1) / kPairs);
+    const double each = (double)((steps + s - 1) / s) * nseg * (tile == 256 ? 575. : 400.) + 1000.;
+    return waves * each + (s > 1 ? 4000. + 8. * (double)M * (double)N * s / 3500. : 0.);
+  };
+  Shape best{narrow_only ? 128 : 256, 1};
+  double least = cost(best.tile_n, 1);
+  if (cost(128, 1) < least) best = Shape{128, 1}, least = cost(128, 1);
+  const size_t slab = (size_t)M * up(N, 8) * 4;
+  for (int s = 2; slabs && s <= 64 && s <= steps && slab * s <= kSlabBytes; ++s) {
+    if (cost(256, s) < least) best = Shape{256, s}, least = cost(256, s);
+  }
+  return best;
+}
+
+// Where everything lies in the workspace, and the products' shapes.
+struct Plan {
+  int np, zp;  // bf16 terms of an operand; of dz and q
+  int Kp, Np;
+  bool copy_k, copy_n;  // [.][K] and [.][N] operands are not read in place
+  bool own_dz;          // dz is not dy itself
+  bool curved;          // a'' is not zero
+  Shape fwd, sec, dx, dw;
+  int sum_rows, sum_parts;
+  size_t x, W, ux, uW, dz, q, sums, slab, bytes;
+};
+
+int steps_of(long long n) { return (int)((n + kBK - 1) / kBK); }
+
+Plan plan(const LinearArgs& a, LinearPass pass) {
+  Plan p;
+  const bool bwd = pass == LinearPass::kBwd, bob = pass == LinearPass::kBob;
+  p.np = a.bf16 ? 1 : kPlanes;
+  p.Kp = (int)up(a.K, 8), p.Np = (int)up(a.N, 8);
+  p.copy_k = !a.bf16 || a.K % 8 != 0, p.copy_n = !a.bf16 || a.N % 8 != 0;
+  p.own_dz = p.copy_n || a.act != kActNone || a.drop.dropped != 0;
+  p.curved = a.act != kActNone && a.act != kActRelu;
+  p.zp = !a.bf16 ? kPlanes : p.own_dz && a.T <= kExactTokens ? 2 : 1;
+  const int one = a.bf16 ? 1 : 6, back = a.bf16 ? p.zp : 6, two = bob && p.curved ? 2 : 1;
+  const bool held = !a.bf16;
+  p.fwd = choose(a.T, a.N, steps_of(a.K), one, true, held || a.K > kLongTerms);
+  p.sec = choose(a.T, a.N, steps_of(a.K), 2 * one, false, held || 2ll * a.K > kLongTerms);
+  p.dx = choose(a.T, a.K, steps_of(a.N), back * two, true, false);
+  p.dw = choose(a.N, a.K, steps_of(a.T), back * two, true, false);
+  // rows of a block of dz_kernel: as many blocks as fill the device six times
+  const long long across = (p.Np + 255) / 256;
+  p.sum_rows = (int)up((size_t)((long long)a.T * across / (152 * 6) + 1), 8);
+  p.sum_parts = (int)((a.T + p.sum_rows - 1) / p.sum_rows);
+  const size_t parts = bob && (a.T + 31) / 32 > p.sum_parts ? (a.T + 31) / 32 : p.sum_parts;
+  size_t at = 0;
+  auto take = [&](bool want, size_t bytes) {
+    const size_t here = at;
+    if (want) at += up(bytes, ce::kWorkspaceAlign);
+    return here;
+  };
+  const size_t T = a.T, K = p.Kp, N = p.Np, e = 2 * (size_t)p.np;
+  p.x = take(p.copy_k, T * K * e);
+  p.W = take(p.copy_k, (size_t)a.N * K * e);
+  p.ux = take(bob && p.copy_k, T * K * e);
+  p.uW = take(bob && p.copy_k, (size_t)a.N * K * e);
+  p.dz = take((bwd || bob) && p.own_dz, T * N * 2 * p.zp);
+  p.q = take(bob && p.curved, T * N * 2 * p.zp);
+  p.sums = take(bwd || (bob && p.curved), parts * N * 4);
+  const size_t f = p.fwd.splits > 1 ? p.fwd.splits * T * N * 4 : 0;
+  const size_t d = p.dx.splits > 1 ? p.dx.splits * T * K * 4 : 0;
+  const size_t w = p.dw.splits > 1 ? p.dw.splits * (size_t)a.N * K * 4 : 0;
+  p.slab = take(true, pass == LinearPass::kFwd ? f : d > w ? d : w);
+  p.bytes = at;
+  return p;
+}
+
+// --- small kernels ---------------------------------------------------------------------------------
+
+// n values of v as np bf16 planes of `stride` elements.
+__device__ __forceinline__ void store_planes8(uint16_t* to, size_t stride, int np, float* v) {
+  for (int k = 0; k < np; ++k) {
+    const uint4 w = bf16x8(v);
+    const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // an infinite value has no remainder (inf - inf would make one)
+      const float lo = __uint_as_float(h[j] << 16), hi = __uint_as_float(h[j] & 0xffff0000u);
+      v[2 * j] = isinf(lo) ? 0.f : v[2 * j] - lo;
+      v[2 * j + 1] = isinf(hi) ? 0.f : v[2 * j + 1] - hi;
+    }
+    *reinterpret_cast<uint4*>(to + k * stride) = w;
+  }
+}
+
+// bf16 planes [np][rows][Kp] of up to four [rows][K] operands in one launch, zero in
+// the padding.  One thread per 8 columns; an operand's blocks start at first.
+struct Operand {
+  const void* x;
+  uint16_t* planes;
+  long long rows;
+  unsigned first;
+  int vec;
+};
+struct Operands {
+  Operand o[4];
+  int n;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    operands_kernel(const __grid_constant__ Operands all, int K, int Kp, int np) {
+  allow_next();
+  wait_previous();
+  int which = 0;
+  while (which + 1 < all.n && blockIdx.x >= all.o[which + 1].first) ++which;
+  const Operand& o = all.o[which];
+  const int per = Kp / 8;
+  const long long i = (long long)(blockIdx.x - o.first) * blockDim.x + threadIdx.x, r = i / per;
+  const int c = (int)(i - r * per) * 8;
+  if (r >= o.rows) return;
+  float v[8];
+  const T* src = static_cast<const T*>(o.x) + r * K + c;
+  if (o.vec)
+    load8<T, true>(src, 8, v);
+  else
+    load8<T, false>(src, K - c, v);
+  store_planes8(o.planes + (size_t)r * Kp + c, (size_t)o.rows * Kp, np, v);
+}
+
+// dz = m dy a'(z) as np bf16 planes [np][T][Np] (0: not wanted), and its column sums
+// per block of `rows_each` rows [parts][Np] (sums may be null).  A warp takes a row of
+// 256 columns at a time, a lane eight of them.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+    dz_kernel(const T* dy, const T* z, DropArgs da, int act, int rows, int N, int Np, int rows_each, uint16_t* planes,
+              int np, float* sums) {
+  allow_next();
+  wait_previous();
+  __shared__ float part[8][256];
+  const Dropper drop(da);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 256 + lane * 8;
+  const int r0 = blockIdx.y * rows_each, r1 = min(r0 + rows_each, rows);
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+  if (c < Np) {
+    for (int ra = r0 + warp; ra < r1; ra += 16) {
+      float g[2][8], s[2][8];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = ra + 8 * u;
+        if (r >= r1) break;
+        load8<T, VEC>(dy + (size_t)r * N + c, N - c, g[u]);
+        if (z) load8<T, VEC>(z + (size_t)r * N + c, N - c, s[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = ra + 8 * u;
+        if (r >= r1) break;
+        if (z) {
+          act_slopes<sizeof(T) == 4, false, 8>(act, s[u], nullptr);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[u][j] *= s[u][j];
+        }
+        if (drop.on) drop.apply8((uint32_t)(c >> 3), (uint32_t)r, g[u]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += g[u][j];
+        if (np) store_planes8(planes + (size_t)r * Np + c, (size_t)rows * Np, np, g[u]);
+      }
+    }
+  }
+  if (!sums) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[warp][lane * 8 + j] = sum[j];
+  __syncthreads();
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n < Np) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += part[w][threadIdx.x];
+    sums[(size_t)blockIdx.y * Np + n] = t;
+  }
+}
+
+// out [N] = sum over the parts [parts][Np], in their order per way: 32 columns and 16
+// ways per block.
+template <typename T>
+__global__ void __launch_bounds__(512) columns_kernel(const float* sums, int parts, int N, int Np, T* out) {
+  allow_next();
+  wait_previous();
+  __shared__ float sh[16][32];
+  const int n = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.f;
+  if (n < N) {
+    for (int i0 = threadIdx.y; i0 < parts; i0 += 16 * 8) {
+      float q[8];  // loads first: their latency would be paid one by one
+#pragma unroll
+      for (int u = 0; u < 8; ++u) q[u] = i0 + 16 * u < parts ? sums[(size_t)(i0 + 16 * u) * Np + n] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += q[u];
+    }
+  }
+  sh[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y != 0 || n >= N) return;
+  s = 0.f;
+  for (int w = 0; w < 16; ++w) s += sh[w][threadIdx.x];
+  out[n] = (T)s;
+}
+
+// out [rows][N] = the sum of the slabs [splits][rows][Np]; with `fwd` the forward's
+// epilogue on it.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+    slabs_kernel(const float* slab, int splits, long long rows, int N, int Np, T* out, bool fwd, const T* bias,
+                 const T* r, T* z, int act, DropArgs da) {
+  allow_next();
+  wait_previous();
+  const Dropper drop(da);
+  const int per = Np / 8;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, row = i / per;
+  const int c = (int)(i - row * per) * 8, n = N - c;
+  if (row >= rows) return;
+  const size_t stride = (size_t)rows * Np, at = (size_t)row * Np + c, to = (size_t)row * N + c;
+  float v[8], w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  for (int s0 = 0; s0 < splits; s0 += 4) {
+    float f[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (s0 + u < splits) load8<float, true>(slab + (s0 + u) * stride + at, 8, f[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += s0 + u < splits ? f[u][j] : 0.f;
+    }
+  }
+  if (fwd) {
+    if (bias) {
+      load8<T, false>(bias + c, n, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += w[j];
+    }
+    if (z) store8<T, VEC>(z + to, n, v);
+    act_values<sizeof(T) == 4, 8>(act, v);
+    if (drop.on) drop.apply8((uint32_t)(c >> 3), (uint32_t)row, v);
+    if (r) {
+      load8<T, VEC>(r + to, n, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += w[j];
+    }
+  }
+  store8<T, VEC>(out + to, n, v);
+}
+
+// --- the passes --------------------------------------------------------------------------------------
+
+#define LIN_TRY(x)                    \
+  do {                                \
+    const cudaError_t e_ = (x);       \
+    if (e_ != cudaSuccess) return e_; \
+  } while (0)
+
+struct Run {
+  const LinearArgs& a;
+  const DevCtx& c;
+  cudaStream_t s;
+  Plan p;
+  char* ws;
+
+  template <typename T>
+  T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
+  size_t element() const { return a.bf16 ? 2 : 4; }
+
+  template <typename... P, typename... A>
+  cudaError_t run(const char* name, void (*kernel)(P...), dim3 grid, dim3 block, A... args) const {
+    prof_begin(s, name);
+    const cudaError_t e = chained(kernel, grid, block, 0, 1, s, args...);
+    prof_end(s);
+    return e;
+  }
+
+  // Planes of the [.][K] operands that are not read in place.
+  cudaError_t operands(const void* x, const void* W, const void* ux, const void* uW) const {
+    if (!p.copy_k) return cudaSuccess;
+    Operands o;
+    o.n = 0;
+    long long blocks = 0;
+    auto add = [&](const void* v, long long rows, size_t off) {
+      if (!v) return;
+      o.o[o.n++] = Operand{v, at<uint16_t>(off), rows, (unsigned)blocks, a.K % 8 == 0 && aligned(v, 16)};
+      blocks += (rows * (p.Kp / 8) + 255) / 256;
+    };
+    add(x, a.T, p.x), add(W, a.N, p.W), add(ux, a.T, p.ux), add(uW, a.N, p.uW);
+    if (o.n == 0) return cudaSuccess;
+    const dim3 grid((unsigned)blocks);
+    return a.bf16 ? run("linear_operands", operands_kernel<__nv_bfloat16>, grid, dim3(256), o, a.K, p.Kp, p.np)
+                  : run("linear_operands", operands_kernel<float>, grid, dim3(256), o, a.K, p.Kp, p.np);
+  }
+
+  GemmArgs base(long long M, long long N, long long K) const {
+    GemmArgs g;
+    memset(&g, 0, sizeof(g));
+    g.M = (int)M, g.N = (int)N, g.K = (int)K, g.splits = 1, g.fp32 = !a.bf16;
+    g.err = c.err, g.wait_ns = c.wait_ns, g.stall = c.stall;
+    return g;
+  }
+  // Chains of fp32 operands are 128 columns of each plane product; long sums of bf16
+  // ones end theirs every 16,384 terms.
+  void chains(GemmArgs& g) const {
+    if (!a.bf16) {
+      g.chain = 2;
+      return;
+    }
+    const long long terms = ((long long)g.K + g.splits - 1) / g.splits * g.nseg;
+    g.chain = terms > kLongTerms ? (int)(kLongTerms / kBK / g.nseg) : 0;
+  }
+
+  // Maps of the planes of a [rows][K] operand, boxes of `box` rows x 64 columns.
+  bool maps(CUtensorMap* m, const void* in, size_t off, long long rows, int box) const {
+    for (int k = 0; k < p.np; ++k) {
+      const void* b = p.copy_k ? at<uint16_t>(off) + (size_t)k * rows * p.Kp : in;
+      if (!matrix_map(m + k, b, rows, p.Kp, p.Kp, box)) return false;
+    }
+    return true;
+  }
+  // ... of dz (or q): [T][N].
+  bool z_maps(CUtensorMap* m, bool q, int box) const {
+    for (int k = 0; k < p.zp; ++k) {
+      const void* b = !q && !p.own_dz ? a.dy : at<uint16_t>(q ? p.q : p.dz) + (size_t)k * a.T * p.Np;
+      if (!matrix_map(m + k, b, a.T, p.Np, p.Np, box)) return false;
+    }
+    return true;
+  }
+  bool z_stores(CUtensorMap* m, bool q) const {
+    for (int k = 0; k < p.zp; ++k) {
+      if (!store_map(m + k, at<uint16_t>(q ? p.q : p.dz) + (size_t)k * a.T * p.Np, a.T, a.N, p.Np)) return false;
+    }
+    return true;
+  }
+
+  // The products of na terms of A operand x and the terms of B operand y (0 or 1
+  // each): of fp32 those that reach 2^-16 of the first; smallest first.
+  void products(GemmArgs& g, int x, int y, int na) const {
+    auto add = [&](int i, int j) { g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + i), (uint8_t)(kPlanes * y + j)}; };
+    if (a.bf16) {
+      for (int i = na - 1; i >= 0; --i) add(i, 0);
+      return;
+    }
+    for (int order = kPlanes - 1; order >= 0; --order) {
+      for (int i = order; i >= 0; --i) add(i, order - i);
+    }
+  }
+
+  bool mapped(const void* t) const { return !t || aligned(t, 16); }
+
+  // y and z from x and W.
+  cudaError_t forward() const {
+    if (a.T <= kRowsTokens) return rows(a, s);
+    LIN_TRY(operands(a.x, a.W, nullptr, nullptr));
+    GemmArgs g = base(a.T, a.N, a.K);
+    const Shape sh = p.fwd;
+    g.splits = sh.splits;
+    products(g, 0, 0, 1);
+    chains(g);
+    if (!maps(g.a, a.x, p.x, a.T, 128) || !maps(g.b, a.W, p.W, a.N, sh.tile_n / 2)) return cudaErrorInvalidValue;
+    if (sh.splits > 1) {
+      g.ep.slab = at<float>(p.slab), g.ep.ld = p.Np;
+      LIN_TRY(gemm_slab(kNT, g, s));
+      return slabs(sh.splits, a.T, a.N, a.y, true);
+    }
+    EpArgs& e = g.ep;
+    e.bias = a.b, e.in0 = a.r, e.out0 = a.y, e.out1 = a.z_out, e.in_ld = a.N, e.act = a.act, e.drop = a.drop;
+    const bool whole = a.bf16 && a.N % 8 == 0;
+    e.in_map = whole && mapped(a.r), e.out_map = whole && mapped(a.y) && mapped(a.z_out);
+    if (e.in_map && a.r && !store_map(g.in, const_cast<void*>(a.r), a.T, a.N, a.N)) return cudaErrorInvalidValue;
+    if (e.out_map && (!store_map(g.out, a.y, a.T, a.N, a.N) ||
+                      (a.z_out && !store_map(g.out + 1, a.z_out, a.T, a.N, a.N))))
+      return cudaErrorInvalidValue;
+    return gemm_forward(sh.tile_n, g, s);
+  }
+
+  cudaError_t slabs(int splits, long long rows, int N, void* out, bool fwd) const {
+    return a.bf16 ? slabs_as<__nv_bfloat16>(splits, rows, N, out, fwd) : slabs_as<float>(splits, rows, N, out, fwd);
+  }
+  template <typename E>
+  cudaError_t slabs_as(int splits, long long rows, int N, void* out, bool fwd) const {
+    const int Np = (int)up(N, 8);
+    const bool vec = N % 8 == 0 && aligned(out, 16) && (!fwd || (mapped(a.r) && mapped(a.z_out)));
+    const dim3 grid((unsigned)((rows * (Np / 8) + 255) / 256));
+    return run("linear_slabs", vec ? slabs_kernel<E, true> : slabs_kernel<E, false>, grid, dim3(256), at<float>(p.slab),
+               splits, rows, N, Np, static_cast<E*>(out), fwd, static_cast<const E*>(a.b), static_cast<const E*>(a.r),
+               static_cast<E*>(a.z_out), a.act, a.drop);
+  }
+
+  // dz and its column sums out of dy and z.
+  cudaError_t make_dz(bool planes, bool sums) const {
+    if (!planes && !sums) return cudaSuccess;
+    return a.bf16 ? make_dz_as<__nv_bfloat16>(planes, sums) : make_dz_as<float>(planes, sums);
+  }
+  template <typename E>
+  cudaError_t make_dz_as(bool planes, bool sums) const {
+    const E* z = a.act == kActNone ? nullptr : static_cast<const E*>(a.z);
+    const bool vec = a.N % 8 == 0 && aligned(a.dy, 16) && mapped(z);
+    return run("linear_dz", vec ? dz_kernel<E, true> : dz_kernel<E, false>, dim3((p.Np + 255) / 256, p.sum_parts),
+               dim3(256), static_cast<const E*>(a.dy), z, a.drop, a.act, a.T, a.N, p.Np, p.sum_rows,
+               at<uint16_t>(p.dz), planes ? p.zp : 0, sums ? at<float>(p.sums) : nullptr);
+  }
+  cudaError_t columns(int parts, void* out) const {
+    const dim3 grid((a.N + 31) / 32), block(32, 16);
+    return a.bf16 ? run("linear_columns", columns_kernel<__nv_bfloat16>, grid, block, at<float>(p.sums), parts, a.N,
+                        p.Np, static_cast<__nv_bfloat16*>(out))
+                  : run("linear_columns", columns_kernel<float>, grid, block, at<float>(p.sums), parts, a.N, p.Np,
+                        static_cast<float*>(out));
+  }
+
+  // dx [T, K] = q W + dz uW, or dW [N, K] = q^T x + dz^T ux; either term may be absent
+  // (the backward's has dz with the first operand).
+  cudaError_t gradient(Layout layout, Shape sh, void* out, const void* u, size_t u_off, const void* v, size_t v_off) const {
+    const bool dw = layout == kTN;
+    const long long rows_a = dw ? a.N : a.T, over = dw ? a.T : a.N, rows_b = dw ? a.T : a.N;
+    GemmArgs g = base(rows_a, a.K, over);
+    const int box_a = dw ? kBK : 128;
+    if (u) {  // with q
+      if (!z_maps(g.a, true, box_a) || !maps(g.b, u, u_off, rows_b, kBK)) return cudaErrorInvalidValue;
+      products(g, 0, 0, p.zp);
+    }
+    if (v) {  // with dz
+      if (!z_maps(g.a + kPlanes, false, box_a) || !maps(g.b + kPlanes, v, v_off, rows_b, kBK)) return cudaErrorInvalidValue;
+      products(g, 1, 1, p.zp);
+    }
+    if (g.nseg == 0) return cudaMemsetAsync(out, 0, (size_t)rows_a * a.K * element(), s);
+    g.splits = sh.splits;
+    chains(g);
+    if (sh.splits > 1) {
+      g.ep.slab = at<float>(p.slab), g.ep.ld = p.Kp;
+      LIN_TRY(gemm_slab(layout, g, s));
+      return slabs(sh.splits, rows_a, a.K, out, false);
+    }
+    g.ep.out0 = out, g.ep.in_ld = a.K;
+    g.ep.out_map = a.bf16 && a.K % 8 == 0 && aligned(out, 16);
+    if (g.ep.out_map && !store_map(g.out, out, rows_a, a.K, a.K)) return cudaErrorInvalidValue;
+    return gemm_out(layout, sh.tile_n, g, s);
+  }
+
+  cudaError_t backward() const {
+    LIN_TRY(operands(a.dW ? a.x : nullptr, a.dx ? a.W : nullptr, nullptr, nullptr));
+    LIN_TRY(make_dz(p.own_dz && (a.dx || a.dW), a.db != nullptr));
+    if (a.db) LIN_TRY(columns(p.sum_parts, a.db));
+    if (a.dx) LIN_TRY(gradient(kNN, p.dx, a.dx, nullptr, 0, a.W, p.W));
+    if (a.dW) LIN_TRY(gradient(kTN, p.dw, a.dW, nullptr, 0, a.x, p.x));
+    return cudaSuccess;
+  }
+
+  // dx, dW, db here are gx, gW, gb.
+  cudaError_t second() const {
+    const bool want_q = p.curved && (a.dx || a.dW || a.db);
+    const bool want_dz = (a.dx && a.uW) || (a.dW && a.ux);
+    const bool product = a.gdy || want_q;
+    LIN_TRY(operands((product && a.uW) || (want_q && a.dW) ? a.x : nullptr,
+                     (product && a.ux) || (want_q && a.dx) ? a.W : nullptr, a.ux, a.uW));
+    if (product) {
+      GemmArgs g = base(a.T, a.N, a.K);
+      const int box = p.sec.tile_n / 2;
+      if (a.ux) {
+        if (!maps(g.a, a.ux, p.ux, a.T, 128) || !maps(g.b, a.W, p.W, a.N, box)) return cudaErrorInvalidValue;
+        products(g, 0, 0, 1);
+      }
+      if (a.uW) {
+        if (!maps(g.a + kPlanes, a.x, p.x, a.T, 128) || !maps(g.b + kPlanes, a.uW, p.uW, a.N, box))
+          return cudaErrorInvalidValue;
+        products(g, 1, 1, 1);
+      }
+      chains(g);
+      EpArgs& e = g.ep;
+      e.bias = a.ub, e.act = a.act, e.drop = a.drop, e.in_ld = a.N, e.ld = p.Np;
+      e.q_planes = want_q && (a.dx || a.dW) ? p.zp : 0;
+      e.dz_planes = want_dz && p.own_dz ? p.zp : 0;
+      e.sums = want_q && a.db ? at<float>(p.sums) : nullptr;
+      e.in0 = a.act == kActNone ? nullptr : a.z;
+      e.in1 = want_q || e.dz_planes ? a.dy : nullptr;
+      e.out0 = a.gdy;
+      const bool whole = a.bf16 && a.N % 8 == 0;
+      e.in_map = whole && mapped(e.in0) && mapped(e.in1), e.out_map = whole && mapped(a.gdy);
+      if (e.in_map && ((e.in0 && !store_map(g.in, const_cast<void*>(e.in0), a.T, a.N, a.N)) ||
+                       (e.in1 && !store_map(g.in + 1, const_cast<void*>(e.in1), a.T, a.N, a.N))))
+        return cudaErrorInvalidValue;
+      if (e.out_map && a.gdy && !store_map(g.out, a.gdy, a.T, a.N, a.N)) return cudaErrorInvalidValue;
+      if ((e.q_planes && !z_stores(g.out + 2, true)) || (e.dz_planes && !z_stores(g.out + 2 + kPlanes, false)))
+        return cudaErrorInvalidValue;
+      LIN_TRY(gemm_second(p.sec.tile_n, g, s));
+      if (e.sums) LIN_TRY(columns((a.T + 31) / 32, a.db));
+    } else if (want_dz && p.own_dz) {
+      LIN_TRY(make_dz(true, false));
+    }
+    if (a.db && !p.curved) LIN_TRY(cudaMemsetAsync(a.db, 0, a.N * element(), s));
+    const bool q = p.curved;
+    if (a.dx) LIN_TRY(gradient(kNN, p.dx, a.dx, q ? a.W : nullptr, p.W, a.uW, p.uW));
+    if (a.dW) LIN_TRY(gradient(kTN, p.dw, a.dW, q ? a.x : nullptr, p.x, a.ux, p.ux));
+    return cudaSuccess;
+  }
+};
+
+}  // namespace
+}  // namespace lin
+
+size_t linear_workspace(const LinearArgs& a, LinearPass pass) {
+  if (pass == LinearPass::kFwd && a.T <= lin::kRowsTokens) return 0;
+  const size_t n = lin::plan(a, pass).bytes;
+  return n ? n + ce::kWorkspaceSlack : 0;
+}
+
+cudaError_t linear(const LinearArgs& a, LinearPass pass, const DevCtx& c, cudaStream_t s) {
+  const lin::Run r{a, c, s, lin::plan(a, pass), static_cast<char*>(ce::workspace_base(a.ws))};
+  switch (pass) {
+    case LinearPass::kFwd: return r.forward();
+    case LinearPass::kBwd: return r.backward();
+    case LinearPass::kBob: return r.second();
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fbob

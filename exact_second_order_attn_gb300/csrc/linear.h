@@ -1,0 +1,81 @@
+// Internal interface of linear layers: the tensor-core product kernel
+// (linear_gemm.cu), the product of a few tokens (linear_rows.cu) and the passes
+// that call them (linear.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace fbob {
+namespace lin {
+
+constexpr int kTileM = 256;  // rows of a pair's tile (128 per block)
+constexpr int kBK = 64;      // contraction per stage (128 bytes of bf16)
+constexpr int kPlanes = 3;   // bf16 terms that stand for one fp32 operand
+constexpr int kMaxSegs = 12;
+// bf16 operands: up to this many tokens dz and q keep two bf16 terms.
+constexpr int kExactTokens = 16;
+
+// A segment multiplies plane a by plane b; the sum over the segments is the product.
+struct Seg {
+  uint8_t a, b;
+};
+
+// How A [M, K] and B [N, K] are stored.
+enum Layout {
+  kNT,  // A [M][K], B [N][K]
+  kNN,  // A [M][K], B [K][N]
+  kTN   // A [K][M], B [K][N]
+};
+// What becomes of an accumulator tile.
+enum Epilogue {
+  kForward,  // y = r + m a(v + bias), and z = v + bias
+  kSecond,   // v + bias = t: gdy, q, dz and q's column sums
+  kOut,      // in the output type
+  kSlab      // fp32
+};
+
+struct EpArgs {
+  const void *bias;         // [N], or null
+  const void *in0, *in1;    // kForward: r, -; kSecond: z, dy (null: absent)
+  void *out0, *out1;        // kForward: y, z; kSecond: gdy; kOut: the output (null: not wanted)
+  float* slab;              // kSlab: [splits][M][ld]
+  float* sums;              // kSecond: column sums of q [rows / 32][ld], or null
+  long long ld, in_ld;      // of the slabs and sums; of the inputs and outputs (elements)
+  int in_map, out_map;      // inputs and outputs move through the maps (bf16)
+  int q_planes, dz_planes;  // bf16 terms of q and dz (0: not wanted), stored through out[2], out[5]
+  int act;
+  DropArgs drop;
+};
+
+struct GemmArgs {
+  CUtensorMap a[2 * kPlanes], b[2 * kPlanes];
+  CUtensorMap in[2];                // store_map()s of in0, in1
+  CUtensorMap out[2 + 2 * kPlanes];  // of out0, out1, q's planes, dz's planes
+  Seg seg[kMaxSegs];
+  int nseg, fp32;
+  int M, N, K, splits;
+  int chain;  // steps of K after which a chain of the tensor cores ends (0: never)
+  EpArgs ep;
+  unsigned int* err;
+  unsigned long long wait_ns;
+  int stall;
+};
+
+// C = sum over segments of A_seg B_seg^T, then the epilogue; tiles of kTileM x
+// tile_n (128 or 256).  Splits are at most the steps of K.
+cudaError_t gemm_forward(int tile_n, const GemmArgs& g, cudaStream_t s);  // kNT, kForward
+cudaError_t gemm_second(int tile_n, const GemmArgs& g, cudaStream_t s);   // kNT, kSecond
+cudaError_t gemm_out(Layout layout, int tile_n, const GemmArgs& g, cudaStream_t s);  // kNN, kTN
+cudaError_t gemm_slab(Layout layout, const GemmArgs& g, cudaStream_t s);
+
+// y (and z) of up to kRowsTokens tokens without tensor cores (linear_rows.cu).
+constexpr int kRowsTokens = 16;
+cudaError_t rows(const LinearArgs& a, cudaStream_t s);
+
+}  // namespace lin
+}  // namespace fbob

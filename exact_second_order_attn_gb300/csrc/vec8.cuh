@@ -1,0 +1,56 @@
+// Eight neighbouring elements of a row as fp32, in 16-byte accesses (VEC: the
+// caller has checked addresses and that all eight are there) or one by one, `n` of
+// them at most.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace fbob {
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* p, int n, float* v) {
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? (float)p[j] : 0.f;
+  } else if constexpr (sizeof(T) == 2) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  } else {
+    const float4 f = *reinterpret_cast<const float4*>(p), g = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w, v[4] = g.x, v[5] = g.y, v[6] = g.z, v[7] = g.w;
+  }
+}
+
+// Eight values as bf16 pairs.
+__device__ __forceinline__ uint4 bf16x8(const float* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* p, int n, const float* v) {
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < n) p[j] = (T)v[j];
+    }
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(p) = bf16x8(v);
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+}  // namespace fbob

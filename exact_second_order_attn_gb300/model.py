@@ -1,9 +1,9 @@
 """PyTorch autograd integration of the operators around the attention.
 
-``rotary``, ``layer_norm`` and ``linear_cross_entropy`` can be differentiated
+``rotary``, ``layer_norm``, ``linear``, ``dropout`` and ``linear_cross_entropy`` can be differentiated
 twice, like ``attention``, so that ``hvp`` passes through a model built of them.  Outputs and gradients
 have the inputs' dtypes; sums and statistics are fp32 inside the kernels.
-Third derivatives are not provided (rotary, a linear map, has all of them).
+Third derivatives are not provided (rotary and dropout, linear maps, have all of them).
 
 Every computation runs in the library; this module only moves tensors between
 autograd and the binding.
@@ -15,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _model
-from ._lib import Rotary
+from ._lib import Dropout, Rotary
 
 
 def _rows(t):
@@ -111,9 +111,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
 
 
 def _head(w):
-    """A head (or its cotangent) where the kernels read it in place: bf16 rows
-    of whole 16 bytes have to start on 16 (a view of a flat vector need not)."""
-    off = (w is not None and w.dtype == torch.bfloat16 and w.dim() == 2 and w.shape[1] % 8 == 0
+    """A head (or another operand of a product, or its cotangent) where the kernels
+    read it in place: bf16 rows of whole 16 bytes have to start on 16 (a view of a
+    flat vector need not)."""
+    off = (w is not None and w.dtype == torch.bfloat16 and w.dim() >= 1 and w.shape[-1] % 8 == 0
            and w.data_ptr() % 16 != 0)
     return w.clone() if off else w
 
@@ -166,3 +167,88 @@ def linear_cross_entropy(H, W, target, ignore_index=-100):
     if not (H.is_contiguous() and W.is_contiguous() and target.is_contiguous()):
         raise ValueError("H, W and target must be contiguous")
     return _Ce.apply(H, W, target, int(ignore_index))
+
+
+class _Dropout(torch.autograd.Function):
+    """(x, residual) -> residual + m x; the backward is the same map of x."""
+
+    @staticmethod
+    def forward(ctx, x, residual, counter, d):
+        ctx.save_for_backward(counter)
+        ctx.d = d
+        return _model.fbob_dropout_apply(d, x, residual, counter)
+
+    @staticmethod
+    def backward(ctx, g):
+        (counter,) = ctx.saved_tensors
+        dx = _Dropout.apply(g.contiguous(), None, counter, ctx.d) if ctx.needs_input_grad[0] else None
+        return dx, (g if ctx.needs_input_grad[1] else None), None, None
+
+
+def dropout(d, x, residual=None, counter=None):
+    """residual + m x with the mask m that ``d`` (a ``Dropout``) describes, which
+    is drawn again for the gradients and never stored.  The last dimension of the
+    contiguous x holds the mask's columns.  ``counter``: one int64 element on the
+    device, added to the offset when the call runs; gradients read it again, so
+    it has to stay until they have run."""
+    if not x.is_contiguous() or not (residual is None or residual.is_contiguous()):
+        raise ValueError("x and residual must be contiguous")
+    # the backward draws by the description as it is now, whatever becomes of d
+    return _Dropout.apply(x, residual, counter, Dropout.from_buffer_copy(d))
+
+
+class _LinearBwd(torch.autograd.Function):
+    """(x, W, bias, dy) -> (dx, dW, db); its own backward is fbob_linear_bob."""
+
+    @staticmethod
+    def forward(ctx, x, W, bias, dy, z, counter, how, want):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, W, dy, z, counter)
+        ctx.how = how
+        return _model.fbob_linear_bwd(_head(x), _head(W), z, _head(dy), *how, counter, want=want)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, ux, uW, ub):
+        x, W, dy, z, counter = ctx.saved_tensors
+        want = ctx.needs_input_grad[:4]
+        if (ux is None and uW is None and ub is None) or not any(want):
+            return None, None, None, None, None, None, None, None
+        if ux is None and uW is None:
+            ux = torch.zeros_like(x)
+        ux, uW, ub = (None if u is None else _head(u.contiguous()) for u in (ux, uW, ub))
+        gx, gW, gb, gdy = _model.fbob_linear_bob(_head(x), _head(W), z, _head(dy), ux, uW, ub, *ctx.how, counter,
+                                                 want=want)
+        return gx, gW, gb, gdy, None, None, None, None
+
+
+class _Linear(torch.autograd.Function):
+    """(x, W, bias, residual) -> y; its backward is the differentiable _LinearBwd."""
+
+    @staticmethod
+    def forward(ctx, x, W, bias, residual, counter, how, keep):
+        y, z = _model.fbob_linear_fwd(_head(x), _head(W), bias, residual, *how, counter, keep=keep)
+        ctx.save_for_backward(x, W, bias, z, counter)
+        ctx.how = how
+        return y
+
+    @staticmethod
+    def backward(ctx, gy):
+        x, W, bias, z, counter = ctx.saved_tensors
+        want = ctx.needs_input_grad[:3]
+        dx = dW = db = None
+        if any(want):
+            dx, dW, db = _LinearBwd.apply(x, W, bias, gy.contiguous(), z, counter, ctx.how, want)
+        return dx, dW, db, (gy if ctx.needs_input_grad[3] else None), None, None, None
+
+
+def linear(x, weight, bias=None, residual=None, activation="none", dropout=None, counter=None):
+    """residual + m a(x weight^T + bias) of a contiguous x [..., K] and weight
+    [N, K], twice differentiable; bias [N], residual [..., N], the activation
+    ("relu", "gelu", "gelu_tanh", "silu") and the ``Dropout`` m (with its
+    ``counter``, as for ``dropout``) are optional.  All tensors have x's dtype."""
+    if not all(t is None or t.is_contiguous() for t in (x, weight, bias, residual)):
+        raise ValueError("x, weight, bias and residual must be contiguous")
+    keep = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))
+    how = activation, None if dropout is None else Dropout.from_buffer_copy(dropout)
+    return _Linear.apply(x, weight, bias, residual, counter, how, keep)

@@ -380,6 +380,91 @@ fbob_status fbob_linear_ce_bob(const fbob_linear_ce* p, const void* H, const voi
                                const void* UH, const void* UW, void* gH, void* gW, float* gg,
                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Dropout: round(65536 p) of 65,536 elements are dropped (set to 0, whatever
+ * they were), the others multiplied by m = 65536 / (65536 - that).  The element at
+ * (row, column) is dropped by sixteen bits of a counter-based generator, so no
+ * mask is stored and gradients draw the same one again: half column % 2 (low
+ * first) of word column / 2 % 4 of Philox4x32 in ten rounds (Salmon, Moraes,
+ * Dror, Shaw: Parallel Random Numbers: As Easy as 1, 2, 3, 2011) with key = seed
+ * and counter words (column / 8, row, low and high half of the offset), being
+ * below round(65536 p).  Calls with different offsets have independent masks. */
+typedef struct {
+  double p;                         /* 0 <= p <= 1                             */
+  unsigned long long seed, offset;
+} fbob_dropout;
+
+/*
+ * y = r + m x for rows of D elements, contiguous; r optional.  The map of x is
+ * linear and its own transpose: the gradient of x is the same call on y's, that
+ * of r is y's itself.
+ *   counter: null, or a 64-bit integer on the device that is added to the
+ *   offset modulo 2^64 when the call runs (a captured graph's steps advance it)
+ *   rows < 2^32, D < 2^31 - 8, rows D <= 2^40
+ */
+fbob_status fbob_dropout_apply(const fbob_dropout* d, const long long* counter,
+                               long long rows, int D, int dtype, const void* x, const void* r,
+                               void* y, cudaStream_t stream);
+
+typedef enum {
+  FBOB_ACT_NONE = 0,
+  FBOB_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0                          */
+  FBOB_ACT_GELU = 2,      /* z F(z), F the normal distribution's integral     */
+  FBOB_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2  */
+  FBOB_ACT_SILU = 4       /* z / (1 + exp(-z))                                */
+} fbob_activation;
+
+/* A linear layer: T tokens of K columns, N outputs. */
+typedef struct {
+  int T, K, N;     /* up to 2^24, 2^20, 2^20; T K, T N and N K up to 2^40     */
+  int dtype;       /* of every tensor                                         */
+  int activation;  /* fbob_activation                                         */
+} fbob_linear;
+
+/* Bytes of workspace of pass 0 (fwd), 1 (bwd) or 2 (bob); 0 if none is needed
+ * or the calls refuse the descriptors.  dropout may be null. */
+size_t fbob_linear_workspace_bytes(const fbob_linear* p, const fbob_dropout* dropout, int pass);
+
+/*
+ * y = r + m a(z), z = x W^T + b, with a the activation and m the dropout (null:
+ * none) of element (token, output); counter as in fbob_dropout_apply.
+ *   in : x [T, K], W [N, K]; b [N], r [T, N] optional
+ *   out: y [T, N]; z [T, N] optional, which the calls below want unless the
+ *        activation is NONE
+ * bf16 matrices whose rows are multiples of 16 bytes have to start on 16 bytes
+ * where they are multiplied (x, W, dy, ux, uW).  Sums are fp32; fp32 inputs are
+ * multiplied as three bf16 terms each and lose nothing to about 2^-22.  x W^T of up
+ * to 16 tokens is summed outside the tensor cores.
+ */
+fbob_status fbob_linear_fwd(const fbob_linear* p, const fbob_dropout* dropout, const long long* counter,
+                            const void* x, const void* W, const void* b, const void* r,
+                            void* y, void* z, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/*
+ * Gradients: with dz = m dy a'(z),
+ *   dx = dz W, dW = dz^T x, db = sum over tokens of dz; each optional (that of
+ *   r is dy).  dz is formed once, in bf16 for bf16 inputs (in two bf16 terms for
+ *   up to 16 tokens); dW and db are zero for no tokens.
+ */
+fbob_status fbob_linear_bwd(const fbob_linear* p, const fbob_dropout* dropout, const long long* counter,
+                            const void* x, const void* W, const void* z, const void* dy,
+                            void* dx, void* dW, void* db, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/*
+ * The vector-Jacobian product of (x, W, b, dy) -> (dx, dW, db) along
+ * (ux, uW, ub): gradients of <ux, dx> + <uW, dW> + <ub, db>.  With
+ * t = ux W^T + x uW^T + ub and q = m t dy a''(z),
+ *   gdy = m t a'(z), gx = q W + dz uW, gW = q^T x + dz^T ux,
+ *   gb = sum over tokens of q; each optional.  One of ux, uW may be null, ub too
+ *   (zeros).  q is held as dz is.
+ */
+fbob_status fbob_linear_bob(const fbob_linear* p, const fbob_dropout* dropout, const long long* counter,
+                            const void* x, const void* W, const void* z, const void* dy,
+                            const void* ux, const void* uW, const void* ub,
+                            void* gx, void* gW, void* gb, void* gdy,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /*
  * Device status: waits for `stream` to finish (this call DOES synchronise),
  * then returns FBOB_ERR_TIMEOUT if any kernel of this library on the current

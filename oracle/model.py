@@ -1,6 +1,6 @@
 """Plain fp64 NumPy oracle of the operators around the attention: rotary
-positions, layer norm and the linear head's cross entropy, each with its first
-backward and that backward's vector-Jacobian product.  Test infrastructure
+positions, layer norm, the linear head's cross entropy, linear layers and
+dropout, each with its first backward and that backward's vector-Jacobian product.  Test infrastructure
 only; shares no code with the CUDA path.
 
 The first backwards follow the chain rule node by node; the second-order
@@ -150,3 +150,72 @@ def linear_ce_bob(H, W, target, g, UH, UW, ignore_index=-100):
     t_p = g_ * t_G
     t_z = p * (t_p - (p * t_p).sum(-1, keepdims=True))
     return _whole(gh + t_z @ W, rows, len(target)), gW + t_z.T @ h, _whole(gg, rows, len(target))
+
+
+# --- linear layers and dropout ----------------------------------------------------------------------
+
+def philox(c, key):
+    """Four words of Philox4x32 in ten rounds as Python integers (Salmon, Moraes, Dror, Shaw: Parallel
+    Random Numbers: As Easy as 1, 2, 3, 2011)."""
+    c, (k0, k1) = list(c), key
+    for _ in range(10):
+        p, q = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
+        c = [(q >> 32) ^ c[1] ^ k0, q % 2 ** 32, (p >> 32) ^ c[3] ^ k1, p % 2 ** 32]
+        k0, k1 = (k0 + 0x9E3779B9) % 2 ** 32, (k1 + 0xBB67AE85) % 2 ** 32
+    return c
+
+
+def dropout_factor(rows, cols, p, seed, offset):
+    """m [rows, cols]: 0 where the element is dropped."""
+    n = round(65536 * p)
+    m = np.zeros((rows, cols))
+    if n == 65536:
+        return m
+    for i in range(rows if n else 0):
+        for g in range((cols + 7) // 8):
+            words = philox([g, i, offset % 2 ** 32, offset // 2 ** 32], [seed % 2 ** 32, seed // 2 ** 32])
+            for j in range(8 * g, min(8 * g + 8, cols)):
+                m[i, j] = (words[j % 8 // 2] >> 16 * (j % 2)) % 65536 >= n
+    return (m if n else m + 1) * (65536 / (65536 - n))
+
+
+def activation(kind, z):
+    """(a, a', a'') of each z."""
+    if kind == "none":
+        return z, np.ones_like(z), np.zeros_like(z)
+    if kind == "relu":
+        return np.maximum(z, 0), (z > 0) * 1.0, np.zeros_like(z)
+    if kind == "gelu":
+        erfc = np.vectorize(math.erfc, otypes=[float])
+        F, f = 0.5 * erfc(-z / math.sqrt(2)), np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        return z * F, F + z * f, 2 * f - z * z * f
+    if kind == "silu":
+        v, v1, v2 = z / 2, 0.5, 0.0
+    else:  # gelu_tanh
+        k = math.sqrt(2 / math.pi)
+        v, v1, v2 = k * (z + 0.044715 * z ** 3), k * (1 + 0.134145 * z * z), k * 0.26829 * z
+    t = np.tanh(v)  # a = z (1 + tanh v) / 2
+    u = 1 - t * t
+    return z * (1 + t) / 2, (1 + t + z * u * v1) / 2, u * v1 + z * (u * v2 - 2 * t * u * v1 * v1) / 2
+
+
+def linear(x, W, b, r, kind, m):
+    return r + m * activation(kind, x @ W.T + b)[0]
+
+
+def linear_bwd(x, W, b, dy, kind, m):
+    """(dx, dW, db)."""
+    dz = m * dy * activation(kind, x @ W.T + b)[1]
+    return dz @ W, dz.T @ x, dz.sum(0)
+
+
+def linear_bob(x, W, b, dy, ux, uW, ub, kind, m):
+    """(gx, gW, gb, gdy): reverse mode through z = x W^T + b, s = a'(z), dz = m dy s and the three products."""
+    _, s, s1 = activation(kind, x @ W.T + b)
+    dz = m * dy * s
+    t_dz = ux @ W.T + x @ uW.T + ub
+    gW = dz.T @ ux                      # dx = dz W
+    gx = dz @ uW                        # dW = dz^T x
+    gdy = t_dz * m * s
+    t_z = t_dz * m * dy * s1
+    return gx + t_z @ W, gW + t_z.T @ x, t_z.sum(0), gdy
