@@ -188,7 +188,8 @@ def fbob_linear_fwd(x, W, bias=None, residual=None, activation="none", dropout=N
     (contiguous) and W [N, K]; bias [N] and residual [..., N] are optional.
     ``activation``: "none", "relu", "gelu", "gelu_tanh" or "silu".  ``dropout``
     (a ``Dropout``) and ``counter``: as for fbob_dropout_apply.  z, which the
-    calls below take, is None for "none" or with ``keep`` false.
+    calls below take (fp16 beside bf16 tensors), is None for "none" or with
+    ``keep`` false.
     ``workspace``: uint8."""
     return _call("linear_fwd", stream, x, W, bias, residual, _activation(activation), dropout, counter, keep, y, z,
                  workspace)

@@ -513,6 +513,7 @@ struct Layer {
     out.assign(x.sizes().begin(), x.sizes().end());
     out.back() = p.N;
   }
+  ScalarType kept() const { return type == ScalarType::Float ? type : ScalarType::Half; }  // of z
   at::IntArrayRef bias(const Tensor& W) const { return W.sizes().slice(0, 1); }
 };
 
@@ -530,7 +531,7 @@ PyObject* linear_fwd(PyObject* const* a, Py_ssize_t n) {
   Launch at(l.device);
   const std::optional<Tensor> y = output(a[8], "y", x, l.device, l.out, l.type);
   std::optional<Tensor> z;
-  if (keep) z = output(a[9], "z", x, l.device, l.out, l.type);
+  if (keep) z = output(a[9], "z", x, l.device, l.out, l.kept());
   const auto ws = workspace_of(a[10], x, l.device, fbob_linear_workspace_bytes(&l.p, drop.p, 0), ScalarType::Byte);
   done(fbob_linear_fwd(&l.p, drop.p, counter, ptr(&x), ptr(&W), ptr(b), ptr(r), ptr(y), ptr(z), ptr(ws), bytes_of(ws),
                        at.stream));
@@ -539,7 +540,7 @@ PyObject* linear_fwd(PyObject* const* a, Py_ssize_t n) {
 
 const Tensor* check_layer(const Layer& l, PyObject* z, const Tensor& dy) {
   const Tensor* t = l.p.activation == FBOB_ACT_NONE ? nullptr : tensor(z, "z");
-  check(t, "z", l.device, l.type, l.out);
+  check(t, "z", l.device, l.kept(), l.out);
   check(&dy, "dy", l.device, l.type, l.out);
   return t;
 }

@@ -2,8 +2,9 @@
 // vector-Jacobian product (formulas in fbob.h; products in linear_gemm.cuh).
 //
 // Forward: one product whose epilogue adds the bias, applies activation and
-// dropout and adds the residual; a training forward also keeps z in the tensors'
-// type (bf16: off by 2^-9 of z, so dz by 2^-9 |z a''|, less than dz's own rounding).
+// dropout and adds the residual; a training forward also keeps z,
+// beside bf16 tensors in fp16: in bf16 its rounding alone made gx and gW 1.53 times
+// as far off as a result that is rounded once, where q's and dz's leave 1.41.
 // Gradients: dz = m dy a'(z) once (with its column sums, in fp32), then dx = dz W
 // and dW = dz^T x; without activation and dropout dz is dy itself.  Second order: one
 // product for t whose epilogue turns it into gdy, q and dz, then gx = q W + dz uW and
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(256)
 // 256 columns at a time, a lane eight of them.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
-    dz_kernel(const T* dy, const T* z, DropArgs da, int act, int rows, int N, int Np, int rows_each, uint16_t* planes,
+    dz_kernel(const T* dy, const Kept<T>* z, DropArgs da, int act, int rows, int N, int Np, int rows_each, uint16_t* planes,
               int np, float* sums) {
   allow_next();
   wait_previous();
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(256)
         const int r = ra + 8 * u;
         if (r >= r1) break;
         load8<T, VEC>(dy + (size_t)r * N + c, N - c, g[u]);
-        if (z) load8<T, VEC>(z + (size_t)r * N + c, N - c, s[u]);
+        if (z) load8<Kept<T>, VEC>(z + (size_t)r * N + c, N - c, s[u]);
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(512) columns_kernel(const float* sums, int par
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
     slabs_kernel(const float* slab, int splits, long long rows, int N, int Np, T* out, bool fwd, const T* bias,
-                 const T* r, T* z, int act, DropArgs da) {
+                 const T* r, Kept<T>* z, int act, DropArgs da) {
   allow_next();
   wait_previous();
   const Dropper drop(da);
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += w[j];
     }
-    if (z) store8<T, VEC>(z + to, n, v);
+    if (z) store8<Kept<T>, VEC>(z + to, n, v);
     act_values<sizeof(T) == 4, 8>(act, v);
     if (drop.on) drop.apply8((uint32_t)(c >> 3), (uint32_t)row, v);
     if (r) {
@@ -440,7 +441,7 @@ struct Run {
     const dim3 grid((unsigned)((rows * (Np / 8) + 255) / 256));
     return run("linear_slabs", vec ? slabs_kernel<E, true> : slabs_kernel<E, false>, grid, dim3(256), at<float>(p.slab),
                splits, rows, N, Np, static_cast<E*>(out), fwd, static_cast<const E*>(a.b), static_cast<const E*>(a.r),
-               static_cast<E*>(a.z_out), a.act, a.drop);
+               static_cast<Kept<E>*>(a.z_out), a.act, a.drop);
   }
 
   // dz and its column sums out of dy and z.
@@ -450,7 +451,7 @@ struct Run {
   }
   template <typename E>
   cudaError_t make_dz_as(bool planes, bool sums) const {
-    const E* z = a.act == kActNone ? nullptr : static_cast<const E*>(a.z);
+    const Kept<E>* z = a.act == kActNone ? nullptr : static_cast<const Kept<E>*>(a.z);
     const bool vec = a.N % 8 == 0 && aligned(a.dy, 16) && mapped(z);
     return run("linear_dz", vec ? dz_kernel<E, true> : dz_kernel<E, false>, dim3((p.Np + 255) / 256, p.sum_parts),
                dim3(256), static_cast<const E*>(a.dy), z, a.drop, a.act, a.T, a.N, p.Np, p.sum_rows,

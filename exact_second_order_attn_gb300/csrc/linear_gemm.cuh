@@ -38,6 +38,7 @@
 #include "launch.cuh"
 #include "linear.h"
 #include "prof.h"
+#include "vec8.cuh"
 
 namespace fbob {
 namespace lin {
@@ -95,12 +96,17 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
   return v;
 }
 
-// 32 bf16 values of this lane's row out of a box.
+// 32 bf16 (HALF: fp16) values of this lane's row out of a box.
+template <bool HALF>
 __device__ __forceinline__ void read_box(uint32_t box, float* v) {
   const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
   for (uint32_t c = 0; c < 4; ++c) {
     const uint4 u = ld_shared_v4(box + box_at(lane, c));
+    if constexpr (HALF) {
+      half8(u, v + 8 * c);
+      continue;
+    }
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -178,7 +184,8 @@ struct Ep {
     }
   }
 
-  template <bool FP32>
+  // HALF: in fp16, as z is kept beside bf16 tensors.
+  template <bool FP32, bool HALF = false>
   __device__ __forceinline__ void result(const CUtensorMap* map, void* base, int x, int y, const float* v) {
     if constexpr (FP32) {
       const int row = y + (int)(threadIdx.x & 31);
@@ -186,7 +193,7 @@ struct Ep {
     } else {
       uint32_t w[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+      for (int j = 0; j < 16; ++j) w[j] = HALF ? half_pair(v[2 * j], v[2 * j + 1]) : pack_bf16x2(v[2 * j], v[2 * j + 1]);
       put(map, base, p.ep.out_map, x, y, w);
     }
   }
@@ -283,7 +290,7 @@ __device__ __forceinline__ void finish(Ep& e, float* v, float bias, const float*
     }
   }
   if constexpr (EP == kForward) {
-    if (a.out1) e.result<FP32>(e.p.out + 1, a.out1, x, y0, v);
+    if (a.out1) e.result<FP32, true>(e.p.out + 1, a.out1, x, y0, v);
     act_values<FP32, 32>(a.act, v);
     if (e.drop.on) {
 #pragma unroll
@@ -584,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           } else if (in.n) {
             const int slot = in.wait(wt);
             if (!(ok = slot >= 0)) break;
-            if (p.ep.in0) read_box(in.box(slot, 0), in0);
-            if (C::NIN > 1 && p.ep.in1) read_box(in.box(slot, p.ep.in0 ? 1 : 0), in1);
+            if (p.ep.in0) read_box<EP == kSecond>(in.box(slot, 0), in0);
+            if (C::NIN > 1 && p.ep.in1) read_box<false>(in.box(slot, p.ep.in0 ? 1 : 0), in1);
             in.release();
             fetch(t, c + kSlots);
           }

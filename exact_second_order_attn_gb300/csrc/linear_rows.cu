@@ -63,7 +63,7 @@ __device__ __forceinline__ void lane8(const E* row, int k0, int K, float* v) {
 
 template <typename E, int TT, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32, TT >= 8 ? 2 : 3)
-    rows_kernel(const E* x, const E* W, const E* bias, const E* r, E* y, E* z, int T, int K, int N, int act, DropArgs da,
+    rows_kernel(const E* x, const E* W, const E* bias, const E* r, E* y, Kept<E>* z, int T, int K, int N, int act, DropArgs da,
                 int share) {
   allow_next();
   wait_previous();
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kWarps * 32, TT >= 8 ? 2 : 3)
     for (int w = 0; w < share; ++w) v += part[group * share + w][j];
     const size_t at = (size_t)t * N + n;
     if (bias) v += (float)bias[n];
-    if (z) z[at] = (E)v;
+    if (z) store8<Kept<E>, false>(z + at, 1, &v);
     act_values<sizeof(E) == 4, 1>(act, &v);
     if (drop.on) {
       float m[8];
@@ -143,7 +143,7 @@ cudaError_t launch_as(const LinearArgs& a, cudaStream_t s) {
   const cudaError_t e = chained(
       rows_kernel<E, TT, VEC>, dim3((unsigned)((groups + per - 1) / per)), dim3(kWarps * 32), 0, 1, s,
       static_cast<const E*>(a.x), static_cast<const E*>(a.W), static_cast<const E*>(a.b), static_cast<const E*>(a.r),
-      static_cast<E*>(a.y), static_cast<E*>(a.z_out), a.T, a.K, a.N, a.act, a.drop, share);
+      static_cast<E*>(a.y), static_cast<Kept<E>*>(a.z_out), a.T, a.K, a.N, a.act, a.drop, share);
   prof_end(s);
   return e;
 }

@@ -4,15 +4,40 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace fbob {
+
+// How z of a linear layer is kept: fp32, or fp16 beside bf16 tensors - eleven bits
+// where bf16 has eight, and no activation's slope changes beyond its range (which is
+// kept in by clamping; a NaN stays one).
+template <typename T>
+using Kept = std::conditional_t<sizeof(T) == 2, __half, float>;
+__device__ __forceinline__ float kept_range(float z) { return z > 65504.f ? 65504.f : z < -65504.f ? -65504.f : z; }
+
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+  const __half2 h = __floats2half2_rn(kept_range(a), kept_range(b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void half8(const uint4& u, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+    v[2 * j] = f.x, v[2 * j + 1] = f.y;
+  }
+}
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(const T* p, int n, float* v) {
   if constexpr (!VEC) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = j < n ? (float)p[j] : 0.f;
+  } else if constexpr (std::is_same_v<T, __half>) {
+    half8(*reinterpret_cast<const uint4*>(p), v);
   } else if constexpr (sizeof(T) == 2) {
     const uint4 u = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -43,8 +68,11 @@ __device__ __forceinline__ void store8(T* p, int n, const float* v) {
   if constexpr (!VEC) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (j < n) p[j] = (T)v[j];
+      if (j < n) p[j] = (T)(std::is_same_v<T, __half> ? kept_range(v[j]) : v[j]);
     }
+  } else if constexpr (std::is_same_v<T, __half>) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(half_pair(v[0], v[1]), half_pair(v[2], v[3]), half_pair(v[4], v[5]),
+                                              half_pair(v[6], v[7]));
   } else if constexpr (sizeof(T) == 2) {
     *reinterpret_cast<uint4*>(p) = bf16x8(v);
   } else {

@@ -416,7 +416,7 @@ typedef enum {
 /* A linear layer: T tokens of K columns, N outputs. */
 typedef struct {
   int T, K, N;     /* up to 2^24, 2^20, 2^20; T K, T N and N K up to 2^40     */
-  int dtype;       /* of every tensor                                         */
+  int dtype;       /* of every tensor but z: fp32, or fp16 beside bf16        */
   int activation;  /* fbob_activation                                         */
 } fbob_linear;
 
@@ -429,7 +429,8 @@ size_t fbob_linear_workspace_bytes(const fbob_linear* p, const fbob_dropout* dro
  * none) of element (token, output); counter as in fbob_dropout_apply.
  *   in : x [T, K], W [N, K]; b [N], r [T, N] optional
  *   out: y [T, N]; z [T, N] optional, which the calls below want unless the
- *        activation is NONE
+ *        activation is NONE (fp16 beside bf16 tensors, clamped to its range,
+ *        beyond which no slope changes)
  * bf16 matrices whose rows are multiples of 16 bytes have to start on 16 bytes
  * where they are multiplied (x, W, dy, ux, uW).  Sums are fp32; fp32 inputs are
  * multiplied as three bf16 terms each and lose nothing to about 2^-22.  x W^T of up
