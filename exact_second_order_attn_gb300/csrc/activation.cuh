@@ -56,9 +56,15 @@ __device__ __forceinline__ float normal_cdf(float z, float& bell) {
 
 constexpr float kTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
-// z moved into [-32, 32], beyond which s' and f are 0: squares of what lies further
-// out would overflow into 0 inf.  A NaN stays one.
-__device__ __forceinline__ float act_clamp(float z) { return z > 32.f ? 32.f : z < -32.f ? -32.f : z; }
+// z moved into [-top, top]; a NaN stays one.
+__device__ __forceinline__ float act_clamp(float z, float top) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(z) : "f"(top));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(z) : "f"(-top));
+  return z;
+}
+// Beyond these s' and f are 0, and squares of what lies further out would overflow
+// into 0 inf.
+constexpr float kActTop = 32.f, kSiluTop = 128.f;
 
 template <int ACT, bool EXACT>
 __device__ __forceinline__ float act_value(float z) {
@@ -68,8 +74,8 @@ __device__ __forceinline__ float act_value(float z) {
     return z * normal_cdf<EXACT>(z, bell);
   }
   if (ACT == kActGeluTanh) {
-    const float c = act_clamp(z);
-    return z * logistic<EXACT>(kTanhC * c * fmaf(0.044715f * c, c, 1.f));
+    // (no clamp: where z^3 overflows s is 0 or 1)
+    return z * logistic<EXACT>(z * fmaf(0.044715f * kTanhC * z, z, kTanhC));
   }
   if (ACT == kActSilu) return z * logistic<EXACT>(z);
   return z;
@@ -83,21 +89,21 @@ __device__ __forceinline__ float act_slope(float z, float& curve) {
     return z <= 0.f ? 0.f : 1.f;
   }
   if (ACT == kActGelu) {
-    const float c = act_clamp(z);
+    const float c = act_clamp(z, kActTop);
     float bell;
     const float up = normal_cdf<EXACT>(c, bell), f = 0.39894228040143268f * bell;
     if (SECOND) curve = f * fmaf(-c, c, 2.f);
     return fmaf(c, f, up);
   }
   if (ACT == kActGeluTanh) {
-    const float c = act_clamp(z), c2 = 0.044715f * c * c;
+    const float c = act_clamp(z, kActTop), c2 = 0.044715f * c * c;
     const float s = logistic<EXACT>(kTanhC * fmaf(c2, c, c)), d = s * (1.f - s);
     const float v1 = kTanhC * fmaf(3.f, c2, 1.f), zv = c * v1;
     if (SECOND) curve = d * fmaf(zv, v1 * fmaf(-2.f, s, 1.f), fmaf(2.f, v1, kTanhC * 6.f * c2));
     return fmaf(zv, d, s);
   }
   if (ACT == kActSilu) {
-    const float c = z < -128.f ? -128.f : z > 128.f ? 128.f : z;
+    const float c = act_clamp(z, kSiluTop);
     const float s = logistic<EXACT>(c), d = s * (1.f - s);
     if (SECOND) curve = d * fmaf(c, fmaf(-2.f, s, 1.f), 2.f);
     return fmaf(c, d, s);

@@ -2,9 +2,11 @@
 // definition is in dropout.cuh).  The map is linear and its own transpose, so
 // gradients of any order are the same call.
 //
-// A thread takes eight columns of a row, the span of one generator call, with
-// 16-byte accesses where a row's groups start on 16 bytes.  A block walks over its
-// groups with a stride, kGroups of them in flight per thread.
+// Rows that start on 16 bytes: a thread takes eight columns of a row, the span of one
+// generator call, in 16-byte accesses, kGroups of them on their way at once.
+// Other rows: a warp takes 256 columns of a row, an element per lane and step, so that
+// accesses stay together; a lane draws for eight of the columns and hands out their
+// bits.  (A thread's eight columns one by one: 5003 x 1537 fp32 31 us.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -16,50 +18,94 @@
 namespace fbob {
 namespace {
 
-constexpr int kThreads = 256, kGroups = 2;
+constexpr int kThreads = 256, kGroups = 4;
 
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a) {
   allow_next();
   wait_previous();
   const Dropper drop(a.drop);
-  const unsigned per = (a.D + 7) / 8;
+  const unsigned per = a.D / 8;
   const long long total = a.rows * per, step = (long long)gridDim.x * kThreads;
   const T *x = static_cast<const T*>(a.x), *r = static_cast<const T*>(a.r);
   T* y = static_cast<T*>(a.y);
   for (long long i0 = (long long)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += step * kGroups) {
-    float v[kGroups][8], w[kGroups][8];
-    unsigned row[kGroups], group[kGroups];
+    Raw8<T> v[kGroups], w[kGroups];
 #pragma unroll
     for (int u = 0; u < kGroups; ++u) {
       const long long i = i0 + u * step;
-      if (i >= total) break;
-      const long long q = total <= 0xffffffffll ? (unsigned)i / per : i / per;
-      row[u] = (unsigned)q, group[u] = (unsigned)(i - q * per);
-      const long long at = q * a.D + 8ll * group[u];
-      load8<T, VEC>(x + at, a.D - 8 * (int)group[u], v[u]);
-      if (r) load8<T, VEC>(r + at, a.D - 8 * (int)group[u], w[u]);
+      if (i < total) {
+        v[u].template load<true>(x + 8 * i, 8);
+        if (r) w[u].template load<true>(r + 8 * i, 8);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kGroups; ++u) {
-      if (i0 + u * step >= total) break;
-      if (drop.on) drop.apply8(group[u], row[u], v[u]);
-      if (r) {
+      const long long i = i0 + u * step;
+      if (i < total) {
+        float f[8];
+        v[u].values(f);
+        if (drop.on) {
+          const long long row = total <= 0xffffffffll ? (unsigned)i / per : i / per;
+          drop.apply8((uint32_t)(i - row * per), (uint32_t)row, f);
+        }
+        if (r) {
+          float g[8];
+          w[u].values(g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[u][j] += w[u][j];
+          for (int j = 0; j < 8; ++j) f[j] += g[j];
+        }
+        store8<T, true>(y + 8 * i, 8, f);
       }
-      store8<T, VEC>(y + (long long)row[u] * a.D + 8ll * group[u], a.D - 8 * (int)group[u], v[u]);
     }
   }
 }
 
-template <typename T, bool VEC>
-cudaError_t launch(const DropoutArgs& a, cudaStream_t s) {
-  const long long total = a.rows * ((a.D + 7) / 8), each = (long long)kThreads * kGroups;
-  const long long blocks = (total + each - 1) / each, most = 8ll * sm_count();
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dropout_rows_kernel(const DropoutArgs a) {
+  allow_next();
+  wait_previous();
+  const Dropper drop(a.drop);
+  const int lane = threadIdx.x & 31;
+  const unsigned per = (a.D + 255) / 256;
+  const long long total = a.rows * per, step = (long long)gridDim.x * (kThreads / 32);
+  const T *x = static_cast<const T*>(a.x), *r = static_cast<const T*>(a.r);
+  T* y = static_cast<T*>(a.y);
+  for (long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < total; i += step) {
+    const long long row = total <= 0xffffffffll ? (unsigned)i / per : i / per;
+    const int c0 = (int)(i - row * per) * 256 + lane;
+    const long long at = row * a.D + c0;
+    T v[8], w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (c0 + 32 * j < a.D) {
+        v[j] = x[at + 32 * j];
+        if (r) w[j] = r[at + 32 * j];
+      }
+    }
+    unsigned kept = drop.on ? drop.kept8((uint32_t)(c0 - lane) / 8 + lane, (uint32_t)row) : 0xffu;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // column 32 j + lane of the 256 is column lane % 8 of the group 4 j + lane / 8
+      const unsigned bits = __shfl_sync(0xffffffffu, kept, 4 * j + lane / 8);
+      if (c0 + 32 * j < a.D) {
+        float f = bits >> (lane & 7) & 1u ? (float)v[j] * drop.scale : 0.f;
+        if (r) f += (float)w[j];
+        y[at + 32 * j] = (T)f;
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch(const DropoutArgs& a, bool vec, cudaStream_t s) {
+  const long long most = 8ll * sm_count();
+  const long long units = vec ? a.rows * (a.D / 8) : a.rows * ((a.D + 255) / 256);
+  const long long each = vec ? kThreads * kGroups : kThreads / 32;
+  const long long blocks = (units + each - 1) / each;
   prof_begin(s, "dropout");
-  const cudaError_t e =
-      chained(dropout_kernel<T, VEC>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, 1, s, a);
+  const cudaError_t e = chained(vec ? dropout_kernel<T> : dropout_rows_kernel<T>,
+                                dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, 1, s, a);
   prof_end(s);
   return e;
 }
@@ -69,8 +115,7 @@ cudaError_t launch(const DropoutArgs& a, cudaStream_t s) {
 cudaError_t dropout(const DropoutArgs& a, cudaStream_t s) {
   const uintptr_t all = (uintptr_t)a.x | (uintptr_t)a.r | (uintptr_t)a.y;
   const bool vec = a.D % 8 == 0 && all % 16 == 0;
-  if (a.bf16) return vec ? launch<__nv_bfloat16, true>(a, s) : launch<__nv_bfloat16, false>(a, s);
-  return vec ? launch<float, true>(a, s) : launch<float, false>(a, s);
+  return a.bf16 ? launch<__nv_bfloat16>(a, vec, s) : launch<float>(a, vec, s);
 }
 
 }  // namespace fbob

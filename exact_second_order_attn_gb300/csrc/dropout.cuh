@@ -51,6 +51,14 @@ struct Dropper {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (j & 1 ? w[j / 2] : w[j / 2] << 16) > last ? v[j] * scale : 0.f;
   }
+  // Bit j: column 8 group + j is kept.
+  __device__ __forceinline__ uint32_t kept8(uint32_t group, uint32_t row) const {
+    uint32_t w[4], k = 0;
+    words(group, row, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k |= (j & 1 ? w[j / 2] : w[j / 2] << 16) > last ? 1u << j : 0u;
+    return k;
+  }
   // The same as factors.
   __device__ __forceinline__ void factors8(uint32_t group, uint32_t row, float* m) const {
     uint32_t w[4];

@@ -92,7 +92,7 @@ Plan plan(const LinearArgs& a, LinearPass pass) {
   const int one = a.bf16 ? 1 : 6, back = a.bf16 ? p.zp : 6, two = bob && p.curved ? 2 : 1;
   const bool held = !a.bf16;
   p.fwd = choose(a.T, a.N, steps_of(a.K), one, true, held || a.K > kLongTerms);
-  p.sec = choose(a.T, a.N, steps_of(a.K), 2 * one, false, held || 2ll * a.K > kLongTerms);
+  p.sec = choose(a.T, a.N, steps_of(a.K), 2 * one, false, p.zp > 1 || 2ll * a.K > kLongTerms);
   p.dx = choose(a.T, a.K, steps_of(a.N), back * two, true, false);
   p.dw = choose(a.N, a.K, steps_of(a.T), back * two, true, false);
   // rows of a block of dz_kernel: as many blocks as fill the device six times
@@ -128,6 +128,8 @@ Plan plan(const LinearArgs& a, LinearPass pass) {
 __device__ __forceinline__ void store_planes8(uint16_t* to, size_t stride, int np, float* v) {
   for (int k = 0; k < np; ++k) {
     const uint4 w = bf16x8(v);
+    *reinterpret_cast<uint4*>(to + k * stride) = w;
+    if (k + 1 == np) break;
     const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -136,7 +138,6 @@ __device__ __forceinline__ void store_planes8(uint16_t* to, size_t stride, int n
       v[2 * j] = isinf(lo) ? 0.f : v[2 * j] - lo;
       v[2 * j + 1] = isinf(hi) ? 0.f : v[2 * j + 1] - hi;
     }
-    *reinterpret_cast<uint4*>(to + k * stride) = w;
   }
 }
 
@@ -176,8 +177,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // dz = m dy a'(z) as np bf16 planes [np][T][Np] (0: not wanted), and its column sums
-// per block of `rows_each` rows [parts][Np] (sums may be null).  A warp takes a row of
-// 256 columns at a time, a lane eight of them.
+// per block of `rows_each` rows [parts][Np] (sums may be null).  A warp takes rows of
+// 256 columns, a lane eight of them; kDzRows rows are on their way at once, as they
+// came: with two, unpacked, the kernel waited for memory (180 us at 8192 x 11,008).
+constexpr int kDzRows = 4;
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
     dz_kernel(const T* dy, const Kept<T>* z, DropArgs da, int act, int rows, int N, int Np, int rows_each, uint16_t* planes,
@@ -193,28 +197,35 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.f;
   if (c < Np) {
-    for (int ra = r0 + warp; ra < r1; ra += 16) {
-      float g[2][8], s[2][8];
+    for (int ra = r0 + warp; ra < r1; ra += 8 * kDzRows) {
+      Raw8<T> g[kDzRows];
+      Raw8<Kept<T>> s[kDzRows];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kDzRows; ++u) {
         const int r = ra + 8 * u;
-        if (r >= r1) break;
-        load8<T, VEC>(dy + (size_t)r * N + c, N - c, g[u]);
-        if (z) load8<Kept<T>, VEC>(z + (size_t)r * N + c, N - c, s[u]);
+        if (r < r1) {
+          g[u].template load<VEC>(dy + (size_t)r * N + c, N - c);
+          if (z) s[u].template load<VEC>(z + (size_t)r * N + c, N - c);
+        }
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kDzRows; ++u) {
         const int r = ra + 8 * u;
-        if (r >= r1) break;
-        if (z) {
-          act_slopes<sizeof(T) == 4, false, 8>(act, s[u], nullptr);
+        if (r < r1) {
+          float v[8];
+          g[u].values(v);
+          if (z) {
+            float a1[8];
+            s[u].values(a1);
+            act_slopes<sizeof(T) == 4, false, 8>(act, a1, nullptr);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) g[u][j] *= s[u][j];
+            for (int j = 0; j < 8; ++j) v[j] *= a1[j];
+          }
+          if (drop.on) drop.apply8((uint32_t)(c >> 3), (uint32_t)r, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[j] += v[j];
+          if (np) store_planes8(planes + (size_t)r * Np + c, (size_t)rows * Np, np, v);
         }
-        if (drop.on) drop.apply8((uint32_t)(c >> 3), (uint32_t)r, g[u]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += g[u][j];
-        if (np) store_planes8(planes + (size_t)r * Np + c, (size_t)rows * Np, np, g[u]);
       }
     }
   }

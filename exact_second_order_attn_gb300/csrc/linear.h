@@ -34,7 +34,8 @@ enum Layout {
 // What becomes of an accumulator tile.
 enum Epilogue {
   kForward,  // y = r + m a(v + bias), and z = v + bias
-  kSecond,   // v + bias = t: gdy, q, dz and q's column sums
+  kSecond,   // v + bias = t: gdy, q, dz and q's column sums; one term of q and dz
+  kSecondTerms,  // the same with several (tiles of 128 columns)
   kOut,      // in the output type
   kSlab      // fp32
 };
@@ -59,6 +60,7 @@ struct GemmArgs {
   Seg seg[kMaxSegs];
   int nseg, fp32;
   int M, N, K, splits;
+  int stages, boxes;  // of a block, of an epilogue warp: set at the launch
   int chain;  // steps of K after which a chain of the tensor cores ends (0: never)
   EpArgs ep;
   unsigned int* err;
@@ -69,7 +71,7 @@ struct GemmArgs {
 // C = sum over segments of A_seg B_seg^T, then the epilogue; tiles of kTileM x
 // tile_n (128 or 256).  Splits are at most the steps of K.
 cudaError_t gemm_forward(int tile_n, const GemmArgs& g, cudaStream_t s);  // kNT, kForward
-cudaError_t gemm_second(int tile_n, const GemmArgs& g, cudaStream_t s);   // kNT, kSecond
+cudaError_t gemm_second(int tile_n, const GemmArgs& g, cudaStream_t s);   // kNT, kSecond or kSecondTerms
 cudaError_t gemm_out(Layout layout, int tile_n, const GemmArgs& g, cudaStream_t s);  // kNN, kTN
 cudaError_t gemm_slab(Layout layout, const GemmArgs& g, cudaStream_t s);
 

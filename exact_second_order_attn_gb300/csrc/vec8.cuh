@@ -19,8 +19,9 @@ using Kept = std::conditional_t<sizeof(T) == 2, __half, float>;
 __device__ __forceinline__ float kept_range(float z) { return z > 65504.f ? 65504.f : z < -65504.f ? -65504.f : z; }
 
 __device__ __forceinline__ uint32_t half_pair(float a, float b) {
-  const __half2 h = __floats2half2_rn(kept_range(a), kept_range(b));
-  return *reinterpret_cast<const uint32_t*>(&h);
+  uint32_t h;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
+  return h;
 }
 __device__ __forceinline__ void half8(const uint4& u, float* v) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -51,6 +52,39 @@ __device__ __forceinline__ void load8(const T* p, int n, float* v) {
     v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w, v[4] = g.x, v[5] = g.y, v[6] = g.z, v[7] = g.w;
   }
 }
+
+// Eight elements as they came, so that more of them can be on their way.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) == 2 ? 1 : 2];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(w) / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+      T* e = reinterpret_cast<T*>(w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = j < n ? p[j] : T(0.f);
+    }
+  }
+  __device__ __forceinline__ void values(float* v) const {
+    if constexpr (sizeof(T) == 4) {
+      const float* f = reinterpret_cast<const float*>(w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = f[j];
+    } else if constexpr (std::is_same_v<T, __half>) {
+      half8(w[0], v);
+    } else {
+      const uint32_t h[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(h[j] << 16);
+        v[2 * j + 1] = __uint_as_float(h[j] & 0xffff0000u);
+      }
+    }
+  }
+};
 
 // Eight values as bf16 pairs.
 __device__ __forceinline__ uint4 bf16x8(const float* v) {
