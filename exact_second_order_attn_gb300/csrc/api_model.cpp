@@ -222,7 +222,11 @@ fbob_status check_dropout(const fbob_dropout* d, const long long* counter, fbob:
     return fail(FBOB_ERR_INVALID_ARG, "pointer counter is not aligned to its elements");
   out->dropped = (unsigned)nearbyint(65536.0 * d->p);  // (halves to even)
   out->scale = out->dropped < 65536u ? (float)(65536.0 / (65536u - out->dropped)) : 0.f;
-  out->seed = d->seed, out->offset = d->offset, out->counter = counter;
+  out->offset = d->offset, out->counter = counter;
+  for (int i = 0; i < 10; ++i) {
+    out->keys[2 * i] = (unsigned)d->seed + i * 0x9E3779B9u;
+    out->keys[2 * i + 1] = (unsigned)(d->seed >> 32) + i * 0xBB67AE85u;
+  }
   return FBOB_OK;
 }
 
@@ -518,7 +522,8 @@ fbob_status fbob_linear_fwd(const fbob_linear* p, const fbob_dropout* dropout, c
   const int cols[] = {p->K, p->K};
   if ((st = check_args(ps, 6)) != FBOB_OK || (st = check_operands(p, ps, cols, 2)) != FBOB_OK) return st;
   fbob::LinearArgs a = linear_args(p, drop);
-  a.x = x, a.W = W, a.b = b, a.r = r, a.y = y, a.z_out = z, a.ws = workspace;
+  a.x = x, a.W = W, a.b = b, a.r = r, a.y = y, a.ws = workspace;
+  a.z_out = p->activation == FBOB_ACT_NONE ? nullptr : z;
   return linear_run(a, fbob::LinearPass::kFwd, workspace_bytes, "linear_fwd launch", stream);
 }
 

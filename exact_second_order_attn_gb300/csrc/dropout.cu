@@ -6,7 +6,8 @@
 // generator call, in 16-byte accesses, kGroups of them on their way at once.
 // Other rows: a warp takes 256 columns of a row, an element per lane and step, so that
 // accesses stay together; a lane draws for eight of the columns and hands out their
-// bits.  (A thread's eight columns one by one: 5003 x 1537 fp32 31 us.)
+// bits; of rows of up to 128 columns it takes several.  (A thread's eight columns one by
+// one: 5003 x 1537 fp32 31 us.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -21,7 +22,7 @@ namespace {
 constexpr int kThreads = 256, kGroups = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a) {
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutArgs a) {
   allow_next();
   wait_previous();
   const Dropper drop(a.drop);
@@ -29,26 +30,25 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a) 
   const long long total = a.rows * per, step = (long long)gridDim.x * kThreads;
   const T *x = static_cast<const T*>(a.x), *r = static_cast<const T*>(a.r);
   T* y = static_cast<T*>(a.y);
-  for (long long i0 = (long long)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += step * kGroups) {
+  long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  // the place of group i, and how far a step moves it: one division each
+  uint32_t row = (uint32_t)(i / per), group = (uint32_t)(i - (long long)row * per);
+  const uint32_t rows = (uint32_t)(step / per), groups = (uint32_t)(step - (long long)rows * per);
+  while (i < total) {
     Raw8<T> v[kGroups], w[kGroups];
 #pragma unroll
     for (int u = 0; u < kGroups; ++u) {
-      const long long i = i0 + u * step;
-      if (i < total) {
-        v[u].template load<true>(x + 8 * i, 8);
-        if (r) w[u].template load<true>(r + 8 * i, 8);
+      if (i + u * step < total) {
+        v[u].template load<true>(x + 8 * (i + u * step), 8);
+        if (r) w[u].template load<true>(r + 8 * (i + u * step), 8);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kGroups; ++u) {
-      const long long i = i0 + u * step;
+    for (int u = 0; u < kGroups; ++u, i += step) {
       if (i < total) {
         float f[8];
         v[u].values(f);
-        if (drop.on) {
-          const long long row = total <= 0xffffffffll ? (unsigned)i / per : i / per;
-          drop.apply8((uint32_t)(i - row * per), (uint32_t)row, f);
-        }
+        if (drop.on) drop.apply8(group, row, f);
         if (r) {
           float g[8];
           w[u].values(g);
@@ -57,12 +57,14 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a) 
         }
         store8<T, true>(y + 8 * i, 8, f);
       }
+      row += rows, group += groups;
+      if (group >= per) group -= per, ++row;
     }
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) dropout_rows_kernel(const DropoutArgs a) {
+__global__ void __launch_bounds__(kThreads) dropout_rows_kernel(const __grid_constant__ DropoutArgs a) {
   allow_next();
   wait_previous();
   const Dropper drop(a.drop);
@@ -97,15 +99,57 @@ __global__ void __launch_bounds__(kThreads) dropout_rows_kernel(const DropoutArg
   }
 }
 
+// Rows of up to 128 columns: a warp takes as many as its lanes' groups hold (`each`),
+// which lie one behind the other.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    dropout_short_kernel(const __grid_constant__ DropoutArgs a, int each, unsigned inverse) {
+  allow_next();
+  wait_previous();
+  const Dropper drop(a.drop);
+  const int lane = threadIdx.x & 31, groups = (a.D + 7) / 8;
+  const long long step = (long long)gridDim.x * (kThreads / 32) * each;
+  const T *x = static_cast<const T*>(a.x), *r = static_cast<const T*>(a.r);
+  T* y = static_cast<T*>(a.y);
+  for (long long r0 = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * each; r0 < a.rows; r0 += step) {
+    const int rows = (int)(a.rows - r0 < each ? a.rows - r0 : each), n = rows * a.D;
+    const long long at = r0 * a.D + lane;
+    T v[8], w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (lane + 32 * j < n) {
+        v[j] = x[at + 32 * j];
+        if (r) w[j] = r[at + 32 * j];
+      }
+    }
+    const unsigned kept = drop.on ? drop.kept8((uint32_t)(lane % groups), (uint32_t)r0 + lane / groups) : 0xffu;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = lane + 32 * j, row = (int)((unsigned)e * inverse >> 16), c = e - row * a.D;
+      const unsigned bits = __shfl_sync(0xffffffffu, kept, (row * groups + c / 8) & 31);
+      if (e < n) {
+        float f = bits >> (c & 7) & 1u ? (float)v[j] * drop.scale : 0.f;
+        if (r) f += (float)w[j];
+        y[at + 32 * j] = (T)f;
+      }
+    }
+  }
+}
+
 template <typename T>
 cudaError_t launch(const DropoutArgs& a, bool vec, cudaStream_t s) {
-  const long long most = 8ll * sm_count();
-  const long long units = vec ? a.rows * (a.D / 8) : a.rows * ((a.D + 255) / 256);
-  const long long each = vec ? kThreads * kGroups : kThreads / 32;
-  const long long blocks = (units + each - 1) / each;
+  const int each = a.D <= 128 ? 32 / ((a.D + 7) / 8) : 1;
+  const long long units = vec ? a.rows * (a.D / 8) : a.D <= 128 ? (a.rows + each - 1) / each : a.rows * ((a.D + 255) / 256);
+  const long long block = vec ? kThreads * kGroups : kThreads / 32;
+  const long long blocks = (units + block - 1) / block, most = 8ll * sm_count();
+  const dim3 grid((unsigned)(blocks < most ? blocks : most)), threads(kThreads);
   prof_begin(s, "dropout");
-  const cudaError_t e = chained(vec ? dropout_kernel<T> : dropout_rows_kernel<T>,
-                                dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, 1, s, a);
+  // (the inverse is exact for elements below 256: 65,536 / D rounded up is off by less than 1, 256 times that
+  // by less than 65,536 / D)
+  const cudaError_t e =
+      vec          ? chained(dropout_kernel<T>, grid, threads, 0, 1, s, a)
+      : a.D <= 128 ? chained(dropout_short_kernel<T>, grid, threads, 0, 1, s, a, each, 65536u / a.D + 1)
+                   : chained(dropout_rows_kernel<T>, grid, threads, 0, 1, s, a);
   prof_end(s);
   return e;
 }

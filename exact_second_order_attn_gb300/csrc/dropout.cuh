@@ -16,7 +16,8 @@
 namespace fbob {
 
 struct Dropper {
-  uint32_t k0, k1, c2, c3;
+  const uint32_t* keys;  // of the rounds, among the kernel's arguments: constants to the instructions
+  uint32_t c2, c3;
   uint32_t last;  // 65536 dropped - 1: a half (in the upper bits) up to this is dropped
   float scale;
   bool on;
@@ -24,7 +25,7 @@ struct Dropper {
   // Reads the counter: after the kernel's dependencies.
   __device__ __forceinline__ explicit Dropper(const DropArgs& a) {
     on = a.dropped != 0;
-    k0 = (uint32_t)a.seed, k1 = (uint32_t)(a.seed >> 32);
+    keys = a.keys;
     const unsigned long long at = a.offset + (on && a.counter ? (unsigned long long)*a.counter : 0ull);
     c2 = (uint32_t)at, c3 = (uint32_t)(at >> 32);
     last = (uint32_t)(a.dropped * 65536ull - 1ull);
@@ -32,13 +33,12 @@ struct Dropper {
   }
 
   __device__ __forceinline__ void words(uint32_t group, uint32_t row, uint32_t (&w)[4]) const {
-    uint32_t a = group, b = row, c = c2, d = c3, x = k0, y = k1;
+    uint32_t a = group, b = row, c = c2, d = c3;
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
       const uint64_t p = (uint64_t)a * 0xD2511F53u, q = (uint64_t)c * 0xCD9E8D57u;
-      a = (uint32_t)(q >> 32) ^ b ^ x, b = (uint32_t)q;
-      c = (uint32_t)(p >> 32) ^ d ^ y, d = (uint32_t)p;
-      x += 0x9E3779B9u, y += 0xBB67AE85u;
+      a = (uint32_t)(q >> 32) ^ b ^ keys[2 * i], b = (uint32_t)q;
+      c = (uint32_t)(p >> 32) ^ d ^ keys[2 * i + 1], d = (uint32_t)p;
     }
     w[0] = a, w[1] = b, w[2] = c, w[3] = d;
   }

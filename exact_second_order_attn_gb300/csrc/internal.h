@@ -90,7 +90,8 @@ enum class CePass { kFwd, kBwd, kBob };
 
 // Dropout: `dropped` of 65,536 elements; 0 is none.
 struct DropArgs {
-  unsigned long long seed, offset;
+  unsigned int keys[20];  // of the generator's ten rounds, two each
+  unsigned long long offset;
   const long long* counter;  // null, or added to the offset, on the device
   unsigned int dropped;
   float scale;

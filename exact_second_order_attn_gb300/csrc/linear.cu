@@ -184,7 +184,7 @@ constexpr int kDzRows = 4;
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
-    dz_kernel(const T* dy, const Kept<T>* z, DropArgs da, int act, int rows, int N, int Np, int rows_each, uint16_t* planes,
+    dz_kernel(const T* dy, const Kept<T>* z, const __grid_constant__ DropArgs da, int act, int rows, int N, int Np, int rows_each, uint16_t* planes,
               int np, float* sums) {
   allow_next();
   wait_previous();
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(512) columns_kernel(const float* sums, int par
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
     slabs_kernel(const float* slab, int splits, long long rows, int N, int Np, T* out, bool fwd, const T* bias,
-                 const T* r, Kept<T>* z, int act, DropArgs da) {
+                 const T* r, Kept<T>* z, int act, const __grid_constant__ DropArgs da) {
   allow_next();
   wait_previous();
   const Dropper drop(da);

@@ -69,13 +69,15 @@ struct Cfg {
   static constexpr int B_BYTES = BN / 2 * kBK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int NIN = EP == kForward ? 1 : kIsSecond<EP> ? 2 : 0;
-  static constexpr int WARPS = !HELD && (EP == kForward || EP == kSecond) ? 16 : 8;  // of the epilogue
+  static constexpr int WARPS = EP == kForward || EP == kSecond ? 16 : 8;  // of the epilogue
   static constexpr int THREADS = 32 * (WARPS + 3);
   static constexpr int H = BN / (WARPS / 4);  // columns of an epilogue thread
   static_assert(kRoom + 2048 <= 232448, "shared memory budget");
-  // Boxes of a warp: kForward y, z; kSecond z, dy, gdy; else two outgoing ones, then the inputs'.
+  // Boxes of a warp: of y and its residual, and z; of z and q, dy and dz, gdy, then the
+  // further terms of q and dz in turn; of two results.
   static int boxes(const GemmArgs& g) {
-    return EP == kForward ? 1 + (g.ep.out1 != nullptr) : EP == kSecond ? 3 : EP == kSlab ? 0 : 2 + NIN;
+    if (EP == kForward) return g.fp32 ? 0 : 1 + (g.ep.out1 != nullptr);
+    return EP == kSecond ? 3 : EP == kSecondTerms ? (g.fp32 ? 7 : 5) : EP == kOut ? 2 : 0;
   }
   static int stages(const GemmArgs& g) {
     const int n = (kRoom - WARPS * boxes(g) * kBoxBytes) / STAGE;
@@ -110,60 +112,29 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
   return v;
 }
 
-// 32 bf16 (HALF: fp16) values of this lane's row out of a box.
-template <bool HALF>
-__device__ __forceinline__ void read_box(uint32_t box, float* v) {
-  const uint32_t lane = threadIdx.x & 31;
-#pragma unroll
-  for (uint32_t c = 0; c < 4; ++c) {
-    const uint4 u = ld_shared_v4(box + box_at(lane, c));
-    if constexpr (HALF) {
-      half8(u, v + 8 * c);
-      continue;
-    }
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * c + 2 * j] = __uint_as_float(w[j] << 16);
-      v[8 * c + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-  }
+// Eight columns from x of row y of an fp32 matrix [rows][N]; `live`: the row exists.
+__device__ __forceinline__ bool whole8(const void* p, long long ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 31) == 0 && ld % 8 == 0;
 }
-
-// A warp's 32 rows x 32 columns of an fp32 matrix at (y, x), a row per lane;
-// `whole`: rows start on 32 bytes.
-__device__ __forceinline__ void read_rows(const float* p, long long ld, bool live, int y, int x, int N, float* v) {
+__device__ __forceinline__ void read8(const float* p, long long ld, bool live, int y, int x, int N, float* v) {
   const float* o = p + (size_t)(live ? y : 0) * ld + x;
-  const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 4 == 0;
-#pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    if (vec && live && x + j + 4 <= N) {
-      const float4 f = *reinterpret_cast<const float4*>(o + j);
-      v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[j + q] = live && x + j + q < N ? o[j + q] : 0.f;
-    }
+  if (live && whole8(p, ld) && x + 8 <= N) {
+    load8<float, true>(o, 8, v);
+  } else {
+    load8<float, false>(o, live ? N - x : 0, v);
   }
 }
-__device__ __forceinline__ void write_rows(float* p, long long ld, bool live, int y, int x, int N, const float* v) {
+__device__ __forceinline__ void write8(float* p, long long ld, bool live, int y, int x, int N, const float* v) {
   if (!live) return;
   float* o = p + (size_t)y * ld + x;
-  const bool whole = (reinterpret_cast<uintptr_t>(p) & 31) == 0 && ld % 8 == 0;
-#pragma unroll
-  for (int j = 0; j < 32; j += 8) {
-    if (whole && x + j + 8 <= N) {
-      st_global_v8(o + j, reinterpret_cast<const uint32_t*>(v + j));
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (x + j + q < N) o[j + q] = v[j + q];
-      }
-    }
+  if (whole8(p, ld) && x + 8 <= N) {
+    st_global_v8(o, reinterpret_cast<const uint32_t*>(v));
+  } else {
+    store8<float, false>(o, N - x, v);
   }
 }
 
-// 32 values of a vector at x, the same in all lanes (0 beyond N, or without one).
+// Lane j has column x + j of a vector (0 beyond N, or without one).
 template <bool FP32>
 __device__ __forceinline__ float column(const void* p, int x, int N) {
   const int n = x + (int)(threadIdx.x & 31);
@@ -194,7 +165,6 @@ struct Ep {
       return;
     }
     const uint32_t lane = threadIdx.x & 31, box = out.smem;
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // planes may be leaving from here
     __syncwarp();
 #pragma unroll
     for (uint32_t c = 0; c < 4; ++c) st_shared_v4(box + box_at(lane, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
@@ -211,7 +181,7 @@ struct Ep {
       if (in && y + r < rows) o[(size_t)r * p.ep.in_ld] = ld_shared_u16(box + box_element(r, lane));
     }
   }
-  // The boxes of a chunk leave: `to` is their place by bulk store (null map: by rows).
+  // A box that has been written (and synchronised) leaves as a bulk tensor store.
   __device__ __forceinline__ void leave(uint32_t box, const CUtensorMap* map, int x, int y) {
     if ((threadIdx.x & 31) == 0 && y < rows && x < N)
       asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
@@ -220,36 +190,18 @@ struct Ep {
                    : "memory");
   }
 
-  // HALF: in fp16, as z is kept beside bf16 tensors.
-  template <bool FP32, bool HALF = false>
+  template <bool FP32>
   __device__ __forceinline__ void result(const CUtensorMap* map, void* base, int x, int y, const float* v) {
     if constexpr (FP32) {
       const int row = y + (int)(threadIdx.x & 31);
-      write_rows(static_cast<float*>(base), p.ep.in_ld, row < rows, row, x, N, v);
+#pragma unroll
+      for (int j = 0; j < 32; j += 8)
+        write8(static_cast<float*>(base), p.ep.in_ld, row < rows, row, x + j, N, v + j);
     } else {
       uint32_t w[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = HALF ? half_pair(v[2 * j], v[2 * j + 1]) : pack_bf16x2(v[2 * j], v[2 * j + 1]);
-      put(map, base, p.ep.out_map, x, y, w);
-    }
-  }
-
-  // As bf16 planes: plane k holds the rounding of what planes 0..k-1 left.
-  __device__ __forceinline__ void planes(const CUtensorMap* maps, int n, int x, int y, float* v) {
-    for (int k = 0; k < n; ++k) {
-      uint32_t w[16];
-#pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-      if (k + 1 < n) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          // an infinite value has no remainder (inf - inf would make one)
-          const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xffff0000u);
-          v[2 * j] = isinf(lo) ? 0.f : v[2 * j] - lo;
-          v[2 * j + 1] = isinf(hi) ? 0.f : v[2 * j + 1] - hi;
-        }
-      }
-      if (y < rows && x < N) out.put(maps + k, x, y, w);
+      put(map, base, p.ep.out_map, x, y, w);
     }
   }
 };
@@ -263,10 +215,7 @@ struct Inbox {
   bool mapped;
   int issued, taken;  // chunks asked for and used so far
 
-  __device__ __forceinline__ const CUtensorMap* map(int i) const { return &p->in[p->ep.in0 ? i : i + 1]; }
-  __device__ __forceinline__ const uint16_t* base(int i) const {
-    return static_cast<const uint16_t*>(p->ep.in0 && i == 0 ? p->ep.in0 : p->ep.in1);
-  }
+  __device__ __forceinline__ const void* base(int i) const { return i == 0 ? p->ep.in0 : p->ep.in1; }
   __device__ __forceinline__ uint32_t box(int i) const { return smem + i * kBoxBytes; }
 
   // Start the loads of the warp's next chunk, at column x and row y.  The boxes are
@@ -276,14 +225,17 @@ struct Inbox {
     if (mapped) {
       if ((threadIdx.x & 31) == 0) {
         mbar_arrive_expect_tx(bar, n * kBoxBytes);
-        for (int i = 0; i < n; ++i) tma_load_2d(box(i), map(i), smem_u32(bar), x, y);
+        for (int i = 0; i < 2; ++i) {
+          if (base(i)) tma_load_2d(box(i), p->in + i, smem_u32(bar), x, y);
+        }
       }
       return;
     }
     const int lane = threadIdx.x & 31;
     const bool in = x + lane < p->N;
-    for (int i = 0; i < n; ++i) {
-      const uint16_t* q = base(i) + (size_t)y * p->ep.in_ld + x + lane;
+    for (int i = 0; i < 2; ++i) {
+      if (!base(i)) continue;
+      const uint16_t* q = static_cast<const uint16_t*>(base(i)) + (size_t)y * p->ep.in_ld + x + lane;
 #pragma unroll
       for (int r0 = 0; r0 < 32; r0 += 16) {
         uint16_t v[16];
@@ -359,62 +311,77 @@ __device__ __forceinline__ float sum_columns8(float* v) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// Lane c of the warp returns the sum over the lanes of their v[c]: halves of the
-// columns change sides, 16 values, 8, ...
-__device__ __forceinline__ float sum_columns(float* v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int h = 16; h > 0; h >>= 1) {
-    const bool up = lane & h;
-#pragma unroll
-    for (int j = 0; j < h; ++j) {
-      const float give = up ? v[j] : v[j + h], keep = up ? v[j + h] : v[j];
-      v[j] = keep + __shfl_xor_sync(0xffffffffu, give, h);
-    }
-  }
-  return v[0];
-}
-
 // t[j] += bias of the columns 8 g + j, out of the warp's 32 in shared memory.
 __device__ __forceinline__ void add_bias(const float* bias, int g, float* t) {
   const float4 a = *reinterpret_cast<const float4*>(bias + 8 * g), b = *reinterpret_cast<const float4*>(bias + 8 * g + 4);
   t[0] += a.x, t[1] += a.y, t[2] += a.z, t[3] += a.w, t[4] += b.x, t[5] += b.y, t[6] += b.z, t[7] += b.w;
 }
 
-// bf16 tensors, 32 columns (from x) of the forward for the row y0 + lane: y into the
-// box `out`, where its residual is, z into the one behind.
-template <int ACT>
-__device__ __forceinline__ void forward_values(Ep& e, float* v, const float* bias, uint32_t out, int x, int y0) {
+// Where the elementwise epilogues find 32 columns of the product, eight at a time
+// (more live values would not fit 104 registers, more code not the instruction cache):
+// in the accumulator, which is handed back behind the last of them, or (HELD) where
+// the sum of its chains has been put.
+template <bool HELD>
+struct Columns {
+  uint32_t tmem, freed;
+  bool last;
+  __device__ __forceinline__ void load(int g, float* t) const {
+    __syncwarp();  // the load is warp-collective
+    tmem_ld8(tmem + 8 * g, t);
+    if (!HELD && last && g == 3) Acc<false>{0, nullptr, freed}.done();
+  }
+};
+
+// 32 columns (from x) of the forward for the row y0 + lane.  bf16: y into the box
+// `out`, where its residual is, z into the one behind.
+template <int ACT, bool FP32, bool HELD>
+__device__ __forceinline__ void forward_values(Ep& e, const Columns<HELD>& in, const float* bias, uint32_t out, int x,
+                                               int y0) {
   const EpArgs& a = e.p.ep;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
+  const int lane = threadIdx.x & 31, row = y0 + lane;
+  const bool live = row < e.rows;
+#pragma unroll 1
   for (int g = 0; g < 4; ++g) {
-    float* w = v + 8 * g;
-    if (a.bias) add_bias(bias, g, w);
-    if (ACT != kActNone && a.out1)
-      st_shared_v4(out + kBoxBytes + box_at(lane, g), half_pair(w[0], w[1]), half_pair(w[2], w[3]),
-                   half_pair(w[4], w[5]), half_pair(w[6], w[7]));
+    float v[8];
+    in.load(g, v);
+    if (a.bias) add_bias(bias, g, v);
+    if (ACT != kActNone && a.out1) {
+      if (FP32)
+        write8(static_cast<float*>(a.out1), a.in_ld, live, row, x + 8 * g, e.N, v);
+      else
+        st_shared_v4(out + kBoxBytes + box_at(lane, g), half_pair(v[0], v[1]), half_pair(v[2], v[3]),
+                     half_pair(v[4], v[5]), half_pair(v[6], v[7]));
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = act_value<ACT, false>(w[j]);
-    if (e.drop.on) e.drop.apply8((uint32_t)(x >> 3) + g, (uint32_t)(y0 + lane), w);
+    for (int j = 0; j < 8; ++j) v[j] = act_value<ACT, FP32>(v[j]);
+    if (e.drop.on) e.drop.apply8((uint32_t)(x >> 3) + g, (uint32_t)row, v);
     if (a.in0) {
       float r[8];
-      box_values(out, g, r);
+      if (FP32)
+        read8(static_cast<const float*>(a.in0), a.in_ld, live, row, x + 8 * g, e.N, r);
+      else
+        box_values(out, g, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] += r[j];
+      for (int j = 0; j < 8; ++j) v[j] += r[j];
     }
-    box_store(out, g, w);
+    if (FP32)
+      write8(static_cast<float*>(a.out0), a.in_ld, live, row, x + 8 * g, e.N, v);
+    else
+      box_store(out, g, v);
   }
 }
-__device__ __forceinline__ void forward_bf16(Ep& e, float* v, const float* bias, uint32_t out, int x, int y0) {
+template <bool FP32, bool HELD>
+__device__ __forceinline__ void forward_chunk(Ep& e, const Columns<HELD>& in, const float* bias, uint32_t out, int x,
+                                              int y0) {
   const EpArgs& a = e.p.ep;
   switch (a.act) {
-    case kActRelu: forward_values<kActRelu>(e, v, bias, out, x, y0); break;
-    case kActGelu: forward_values<kActGelu>(e, v, bias, out, x, y0); break;
-    case kActGeluTanh: forward_values<kActGeluTanh>(e, v, bias, out, x, y0); break;
-    case kActSilu: forward_values<kActSilu>(e, v, bias, out, x, y0); break;
-    default: forward_values<kActNone>(e, v, bias, out, x, y0);
+    case kActRelu: forward_values<kActRelu, FP32>(e, in, bias, out, x, y0); break;
+    case kActGelu: forward_values<kActGelu, FP32>(e, in, bias, out, x, y0); break;
+    case kActGeluTanh: forward_values<kActGeluTanh, FP32>(e, in, bias, out, x, y0); break;
+    case kActSilu: forward_values<kActSilu, FP32>(e, in, bias, out, x, y0); break;
+    default: forward_values<kActNone, FP32>(e, in, bias, out, x, y0);
   }
+  if (FP32) return;
   if (a.out_map) fence_proxy_async_smem();
   __syncwarp();
   if (a.out_map) {
@@ -427,34 +394,57 @@ __device__ __forceinline__ void forward_bf16(Ep& e, float* v, const float* bias,
   }
 }
 
-// bf16 tensors with one term of dz and q, the second order: v = t; the boxes of z and
-// dy (those that are there), over which q and dz are written, and gdy's.  Eight
-// columns at a time come out of the accumulator: 104 registers a thread hold no more.
-template <int ACT, bool HELD>
-__device__ __forceinline__ void second_values(Ep& e, const Acc<HELD>& acc, int c, bool last, const float* bias,
-                                              uint32_t zbox, uint32_t dybox, uint32_t out, int x, int y0) {
-  const EpArgs& a = e.p.ep;
-  const int lane = threadIdx.x & 31;
-  const bool live = y0 + lane < e.rows;
-#pragma unroll(HELD ? 4 : 1)
-  for (int g = 0; g < 4; ++g) {
-    float t[8];
-    if constexpr (HELD) {
+// The box of term k of q (which = 0) or dz (1).
+__device__ __forceinline__ uint32_t term_box(uint32_t boxes, int which, int k) {
+  return boxes + (k == 0 ? which : 1 + 2 * k + which) * kBoxBytes;
+}
+// v as n bf16 terms (one without TERMS): each holds the rounding of what the ones
+// before it left.
+template <bool TERMS>
+__device__ __forceinline__ void store_terms(uint32_t boxes, int which, int n, int g, float* v) {
+  box_store(term_box(boxes, which, 0), g, v);
+  if constexpr (TERMS) {
+    for (int k = 1; k < n; ++k) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = acc.sum[c + 8 * g + j];
-    } else {
-      __syncwarp();
-      tmem_ld8(acc.tmem + c + 8 * g, t);
-      if (last && g == 3) acc.done();
+      for (int j = 0; j < 8; ++j) {
+        // an infinite value has no remainder (inf - inf would make one)
+        const float h = __bfloat162float(__float2bfloat16_rn(v[j]));
+        v[j] = isinf(h) ? 0.f : v[j] - h;
+      }
+      box_store(term_box(boxes, which, k), g, v);
     }
+  }
+}
+
+// 32 columns (from x) of the second order for the row y0 + lane: the product is t.
+// bf16: z and dy are in the first two boxes, over which q and dz are written.
+template <int ACT, bool FP32, bool TERMS, bool HELD>
+__device__ __forceinline__ void second_values(Ep& e, const Columns<HELD>& in, const float* bias, uint32_t boxes, int x,
+                                              int y0) {
+  const EpArgs& a = e.p.ep;
+  const int lane = threadIdx.x & 31, row = y0 + lane;
+  const bool live = row < e.rows;
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    float t[8], a1[8], a2[8], dy[8], m[8];
+    in.load(g, t);
     if (a.bias) add_bias(bias, g, t);
-    float a1[8], a2[8], dy[8], m[8];
-    if (ACT != kActNone) half8(ld_shared_v4(zbox + box_at(lane, g)), a1);
+    if (ACT != kActNone) {
+      if (FP32)
+        read8(static_cast<const float*>(a.in0), a.in_ld, live, row, x + 8 * g, e.N, a1);
+      else
+        half8(ld_shared_v4(boxes + box_at(lane, g)), a1);
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a1[j] = act_slope<ACT, false, true>(a1[j], a2[j]);
-    if (a.in1) box_values(dybox, g, dy);
+    for (int j = 0; j < 8; ++j) a1[j] = act_slope<ACT, FP32, true>(a1[j], a2[j]);
+    if (a.in1) {
+      if (FP32)
+        read8(static_cast<const float*>(a.in1), a.in_ld, live, row, x + 8 * g, e.N, dy);
+      else
+        box_values(boxes + kBoxBytes, g, dy);
+    }
     if (e.drop.on) {
-      e.drop.factors8((uint32_t)(x >> 3) + g, (uint32_t)(y0 + lane), m);
+      e.drop.factors8((uint32_t)(x >> 3) + g, (uint32_t)row, m);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {  // what is dropped is 0 whatever stands there
         const bool kept = m[j] != 0.f;
@@ -467,17 +457,20 @@ __device__ __forceinline__ void second_values(Ep& e, const Acc<HELD>& acc, int c
     if (a.out0) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) m[j] = t[j] * a1[j];
-      box_store(out, g, m);
+      if (FP32)
+        write8(static_cast<float*>(a.out0), a.in_ld, live, row, x + 8 * g, e.N, m);
+      else
+        box_store(boxes + 2 * kBoxBytes, g, m);
     }
     if (a.dz_planes) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) a1[j] *= dy[j];
-      box_store(dybox, g, a1);
+      store_terms<TERMS>(boxes, 1, a.dz_planes, g, a1);
     }
     if (a.q_planes || a.sums) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = live ? t[j] * dy[j] * a2[j] : 0.f;
-      if (a.q_planes) box_store(zbox, g, t);
+      for (int j = 0; j < 8; ++j) t[j] = m[j] = live ? t[j] * dy[j] * a2[j] : 0.f;
+      if (a.q_planes) store_terms<TERMS>(boxes, 0, a.q_planes, g, m);
       if (a.sums) {
         const float s = sum_columns8(t);
         const int n = x + 8 * g + lane / 4;
@@ -486,101 +479,34 @@ __device__ __forceinline__ void second_values(Ep& e, const Acc<HELD>& acc, int c
     }
   }
 }
-template <bool HELD>
-__device__ __forceinline__ void second_bf16(Ep& e, const Acc<HELD>& v, int c, bool last, const float* bias,
-                                            uint32_t zbox, uint32_t dybox, uint32_t out, int x, int y0) {
+template <bool FP32, bool TERMS, bool HELD>
+__device__ __forceinline__ void second_chunk(Ep& e, const Columns<HELD>& in, const float* bias, uint32_t boxes, int x,
+                                             int y0) {
   const EpArgs& a = e.p.ep;
   switch (a.act) {
-    case kActRelu: second_values<kActRelu>(e, v, c, last, bias, zbox, dybox, out, x, y0); break;
-    case kActGelu: second_values<kActGelu>(e, v, c, last, bias, zbox, dybox, out, x, y0); break;
-    case kActGeluTanh: second_values<kActGeluTanh>(e, v, c, last, bias, zbox, dybox, out, x, y0); break;
-    case kActSilu: second_values<kActSilu>(e, v, c, last, bias, zbox, dybox, out, x, y0); break;
-    default: second_values<kActNone>(e, v, c, last, bias, zbox, dybox, out, x, y0);
+    case kActRelu: second_values<kActRelu, FP32, TERMS>(e, in, bias, boxes, x, y0); break;
+    case kActGelu: second_values<kActGelu, FP32, TERMS>(e, in, bias, boxes, x, y0); break;
+    case kActGeluTanh: second_values<kActGeluTanh, FP32, TERMS>(e, in, bias, boxes, x, y0); break;
+    case kActSilu: second_values<kActSilu, FP32, TERMS>(e, in, bias, boxes, x, y0); break;
+    default: second_values<kActNone, FP32, TERMS>(e, in, bias, boxes, x, y0);
   }
   fence_proxy_async_smem();
   __syncwarp();
-  if (a.out0 && a.out_map) e.leave(out, e.p.out, x, y0);
-  if (a.dz_planes) e.leave(dybox, e.p.out + 2 + kPlanes, x, y0);
-  if (a.q_planes) e.leave(zbox, e.p.out + 2, x, y0);
+  if (!FP32 && a.out0 && a.out_map) e.leave(boxes + 2 * kBoxBytes, e.p.out, x, y0);
+  for (int k = 0; k < (TERMS ? a.dz_planes : a.dz_planes != 0); ++k)
+    e.leave(term_box(boxes, 1, k), e.p.out + 2 + kPlanes + k, x, y0);
+  for (int k = 0; k < (TERMS ? a.q_planes : a.q_planes != 0); ++k)
+    e.leave(term_box(boxes, 0, k), e.p.out + 2 + k, x, y0);
   commit_stores();
-  if (a.out0 && !a.out_map) e.copy_rows(out, a.out0, x, y0);
+  if (!FP32 && a.out0 && !a.out_map) e.copy_rows(boxes + 2 * kBoxBytes, a.out0, x, y0);
 }
 
-// 32 columns (from x) of a tile for this thread's row y0 + lane, fp32 tensors, two
-// terms of dz and q, or no more than a result; in0, in1: the values of the inputs.
+// 32 columns (from x) of a gradient, for the row y0 + lane.
 template <int EP, bool FP32>
-__device__ __forceinline__ void finish(Ep& e, float* v, float bias, const float* in0, float* in1, int x, int y0,
-                                       int split) {
+__device__ __forceinline__ void finish(Ep& e, const float* v, int x, int y0, int split) {
   const EpArgs& a = e.p.ep;
-  const int lane = threadIdx.x & 31, row = y0 + lane;
-  if constexpr (EP == kForward || kIsSecond<EP>) {
-    if (a.bias) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bias, j);
-    }
-  }
-  if constexpr (EP == kForward) {
-    if (a.out1) e.result<FP32, true>(e.p.out + 1, a.out1, x, y0, v);
-    act_values<FP32, 32>(a.act, v);
-    if (e.drop.on) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) e.drop.apply8((uint32_t)(x >> 3) + g, (uint32_t)row, v + 8 * g);
-    }
-    if (a.in0) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] += in0[j];
-    }
-    e.result<FP32>(e.p.out, a.out0, x, y0, v);
-  } else if constexpr (EP == kSecondTerms) {
-    // v = t; in0 = z, in1 = dy
-    const bool live = row < e.rows;
-    float a1[32], a2[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) a1[j] = in0[j];
-    act_slopes<FP32, true, 32>(a.act, a1, a2);
-    if (e.drop.on) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float m[8];
-        e.drop.factors8((uint32_t)(x >> 3) + g, (uint32_t)row, m);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {  // what is dropped is 0 whatever stands there
-          const int c = 8 * g + j;
-          const bool kept = m[j] != 0.f;
-          v[c] = kept ? v[c] : 0.f;
-          in1[c] = kept ? in1[c] * m[j] : 0.f;
-          a1[c] = kept ? a1[c] : 0.f;
-          a2[c] = kept ? a2[c] : 0.f;
-        }
-      }
-    }
-    const float scale = e.drop.on ? e.drop.scale : 1.f;
-    if (a.out0) {
-      float g[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) g[j] = scale * v[j] * a1[j];
-      e.result<FP32>(e.p.out, a.out0, x, y0, g);
-    }
-    if (a.dz_planes) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) a1[j] *= in1[j];
-      e.planes(e.p.out + 2 + kPlanes, a.dz_planes, x, y0, a1);
-    }
-    if (a.q_planes || a.sums) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = live ? v[j] * in1[j] * a2[j] : 0.f;
-      if (a.q_planes) {
-        float q[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) q[j] = v[j];
-        e.planes(e.p.out + 2, a.q_planes, x, y0, q);
-      }
-      if (a.sums) {
-        const float total = sum_columns(v);
-        if (y0 < e.rows && x + lane < e.N) a.sums[(size_t)(y0 / 32) * a.ld + x + lane] = total;
-      }
-    }
-  } else if constexpr (EP == kSlab) {
+  if constexpr (EP == kSlab) {
+    const int row = y0 + (int)(threadIdx.x & 31);
     float* o = a.slab + ((size_t)split * e.rows + row) * a.ld + x;
 #pragma unroll
     for (int j = 0; j < 32; j += 8) {  // ld is a multiple of 8
@@ -596,6 +522,8 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
     linear_kernel(const __grid_constant__ GemmArgs p) {
   using C = Cfg<LAYOUT, EP, HELD, BN>;
   constexpr int H = C::H, CHUNKS = H / 32, EW = C::WARPS;
+  constexpr bool ELEMENTWISE = EP == kForward || kIsSecond<EP>;
+  static_assert(!(HELD && ELEMENTWISE) || BN == 128, "chains' sums lie behind the accumulators of 128 columns");
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Ctrl ctrl;
   __shared__ uint64_t in_bar[EW];
@@ -744,7 +672,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
     const uint32_t boxes = sm0 + nst * C::STAGE + warp * p.boxes * kBoxBytes;
     const Dropper drop(p.ep.drop);
     Ep e{p, Outbox{boxes, 0}, drop, p.M, p.N};
-    Inbox in{EP == kSecondTerms ? boxes + 2 * kBoxBytes : boxes, &in_bar[warp], &p, 0, p.ep.in_map != 0, 0, 0};
+    Inbox in{boxes, &in_bar[warp], &p, 0, p.ep.in_map != 0, 0, 0};
     if (C::NIN > 0 && !FP32) in.n = (p.ep.in0 != nullptr) + (C::NIN > 1 && p.ep.in1 != nullptr);
     // chunk c of the warp's tiles, counted from tile t
     auto fetch = [&](int t, int c) {
@@ -792,58 +720,39 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
         ++chain;
       }
       if (!ok) break;
-      const Acc<HELD> acc{tb + lane + buf * kBufCols + part * H, sum, freed + buf * 8};
-#pragma unroll(HELD ? CHUNKS : 1)
-      for (int c = 0; c < CHUNKS; ++c) {
-        float v[32];
-        const int x = x0 + 32 * c;
-        const float bias = EP == kForward || kIsSecond<EP> ? column<FP32>(p.ep.bias, x, p.N) : 0.f;
-        if constexpr (C::NIN > 0 && !FP32) {
-          if (!(ok = in.wait(wt))) break;
+      if constexpr (ELEMENTWISE) {
+        uint32_t from = tb + lane + buf * kBufCols + part * H;
+        if constexpr (HELD) {  // (columns 128.. of the first buffer)
+          from = tb + lane + 128 + part * H;
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < H; j += 16) tmem_st16_nowait(from + j, reinterpret_cast<const uint32_t*>(sum) + j);
+          tmem_st_wait();
         }
-        if constexpr (EP != kSecond) {
-          acc.load(32 * c, 32 * c, v);
-          if (c + 1 == CHUNKS) acc.done();
-        }
-        if constexpr (!FP32 && (EP == kForward || EP == kSecond)) {
+        for (int c = 0; c < CHUNKS; ++c) {
+          const int x = x0 + 32 * c;
           if (p.ep.bias) {
-            bias_row[warp][tid & 31] = bias;
+            bias_row[warp][tid & 31] = column<FP32>(p.ep.bias, x, p.N);
             __syncwarp();
           }
-          if (EP == kForward)
-            forward_bf16(e, v, bias_row[warp], boxes, x, y0);
+          if (!FP32 && !(ok = in.wait(wt))) break;
+          const Columns<HELD> cols{from + 32 * c, freed + buf * 8, c + 1 == CHUNKS};
+          if constexpr (EP == kForward)
+            forward_chunk<FP32>(e, cols, bias_row[warp], boxes, x, y0);
           else
-            second_bf16(e, acc, 32 * c, c + 1 == CHUNKS, bias_row[warp], in.box(0), in.box(p.ep.in0 ? 1 : 0), boxes + 2 * kBoxBytes, x, y0);
+            second_chunk<FP32, EP == kSecondTerms>(e, cols, bias_row[warp], boxes, x, y0);
           boxes_free();
-          fetch(t, c + 1);
-        } else if constexpr (EP == kSecondTerms && !FP32) {
-          float in0[32], in1[32];
-          if (p.ep.in0) read_box<true>(in.box(0), in0);
-          if (p.ep.in1) read_box<false>(in.box(p.ep.in0 ? 1 : 0), in1);
+          if (!FP32) fetch(t, c + 1);
+        }
+      } else {
+        const Acc<HELD> acc{tb + lane + buf * kBufCols + part * H, sum, freed + buf * 8};
+#pragma unroll(HELD ? CHUNKS : 1)
+        for (int c = 0; c < CHUNKS; ++c) {
+          float v[32];
+          acc.load(32 * c, 32 * c, v);
+          if (c + 1 == CHUNKS) acc.done();
           __syncwarp();
-          fetch(t, c + 1);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (!p.ep.in0) in0[j] = 0.f;
-            if (!p.ep.in1) in1[j] = 0.f;
-          }
-          finish<EP, FP32>(e, v, bias, in0, in1, x, y0, split);
-        } else {
-          float in0[32], in1[32];
-          const int row = y0 + (tid & 31);
-          if (C::NIN > 0 && p.ep.in0)
-            read_rows(static_cast<const float*>(p.ep.in0), p.ep.in_ld, row < p.M, row, x, p.N, in0);
-          if (C::NIN > 1 && p.ep.in1)
-            read_rows(static_cast<const float*>(p.ep.in1), p.ep.in_ld, row < p.M, row, x, p.N, in1);
-          if (C::NIN > 0) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (!p.ep.in0) in0[j] = 0.f;
-              if (C::NIN > 1 && !p.ep.in1) in1[j] = 0.f;
-            }
-          }
-          __syncwarp();
-          finish<EP, FP32>(e, v, bias, in0, in1, x, y0, split);
+          finish<EP, FP32>(e, v, x0 + 32 * c, y0, split);
         }
       }
     }

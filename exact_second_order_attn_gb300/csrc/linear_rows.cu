@@ -63,7 +63,7 @@ __device__ __forceinline__ void lane8(const E* row, int k0, int K, float* v) {
 
 template <typename E, int TT, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32, TT >= 8 ? 2 : 3)
-    rows_kernel(const E* x, const E* W, const E* bias, const E* r, E* y, Kept<E>* z, int T, int K, int N, int act, DropArgs da,
+    rows_kernel(const E* x, const E* W, const E* bias, const E* r, E* y, Kept<E>* z, int T, int K, int N, int act, const __grid_constant__ DropArgs da,
                 int share) {
   allow_next();
   wait_previous();
