@@ -11,13 +11,15 @@
 // EXACT (fp32 tensors) takes expf and erfcf.  For bf16 tensors, whose results are
 // rounded to 2^-9, 2^x and 1/x of the special function unit (2^-22), and
 // Abramowitz and Stegun 7.1.26 for erfc (1.5e-7; relative to F 2e-4 at z = -4,
-// 2e-3 at z = -5): the epilogues that call them are bound by issue.
+// 2e-3 at z = -5), two values in a packed instruction: the epilogues that call them
+// are bound by issue.
 #pragma once
 
 #include <math.h>
 #include <stdint.h>
 
 #include "internal.h"
+#include "rowvec.cuh"
 
 namespace fbob {
 
@@ -112,46 +114,163 @@ __device__ __forceinline__ float act_slope(float z, float& curve) {
   return 1.f;
 }
 
-// a(z) of n values.
-template <bool EXACT, int N>
-__device__ __forceinline__ void act_values(int act, float* z) {
-#define FBOB_ACT_CASE(A)                                                 \
-  case A:                                                                \
-    _Pragma("unroll") for (int j = 0; j < N; ++j) z[j] = act_value<A, EXACT>(z[j]); \
-    break;
-  switch (act) {
-    FBOB_ACT_CASE(kActRelu)
-    FBOB_ACT_CASE(kActGelu)
-    FBOB_ACT_CASE(kActGeluTanh)
-    FBOB_ACT_CASE(kActSilu)
-    default: break;
-  }
-#undef FBOB_ACT_CASE
+// --- eight values at a time, in packed pairs where they are not EXACT -------------
+
+using row::F2;
+
+__device__ __forceinline__ F2 both(float f) { return row::pair(f, f); }
+__device__ __forceinline__ F2 exp2_pair(F2 x) {
+  const float2 f = row::parts(x);
+  float a, b;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(f.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(f.y));
+  return row::pair(a, b);
+}
+__device__ __forceinline__ F2 rcp_pair(F2 x) {
+  const float2 f = row::parts(x);
+  return row::pair(act_rcp(f.x), act_rcp(f.y));
+}
+// The logistic function of v, from -v log2(e).
+__device__ __forceinline__ F2 logistic_pair(F2 x) { return rcp_pair(exp2_pair(x) + both(1.f)); }
+constexpr float kActLog2e = 1.4426950408889634f;
+
+// As normal_cdf.
+__device__ __forceinline__ F2 cdf_pair(F2 z, F2& bell) {
+  const F2 z2 = z * z;
+  bell = exp2_pair(z2 * both(-0.5f * kActLog2e));
+  const float2 f = row::parts(z);
+  const F2 t = row::pair(act_rcp(fmaf(fabsf(f.x), 0.3275911f * 0.70710678118654752f, 1.f)),
+                         act_rcp(fmaf(fabsf(f.y), 0.3275911f * 0.70710678118654752f, 1.f)));
+  F2 p = mad(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+  p = mad(p, t, both(0.5f * 1.421413741f));
+  p = mad(p, t, both(0.5f * -0.284496736f));
+  p = mad(p, t, both(0.5f * 0.254829592f));
+  const F2 h = p * t * bell;
+  const float2 lo = row::parts(h), hi = row::parts(mad(h, both(-1.f), both(1.f)));
+  return row::pair(f.x > 0.f ? hi.x : lo.x, f.y > 0.f ? hi.y : lo.y);
 }
 
-// z[j] becomes a'(z[j]) of n values, a2[j] a''(z[j]).
-template <bool EXACT, bool SECOND, int N>
-__device__ __forceinline__ void act_slopes(int act, float* z, float* a2) {
-  float none;
-#define FBOB_ACT_CASE(A)                                                              \
-  case A:                                                                             \
-    _Pragma("unroll") for (int j = 0; j < N; ++j) z[j] =                              \
-        act_slope<A, EXACT, SECOND>(z[j], SECOND ? a2[j] : none);                     \
-    break;
+template <int ACT>
+__device__ __forceinline__ F2 value_pair(F2 z) {
+  if (ACT == kActGelu) {
+    F2 bell;
+    return z * cdf_pair(z, bell);
+  }
+  if (ACT == kActGeluTanh)
+    return z * logistic_pair(z * mad(z * z, both(-0.044715f * kTanhC * kActLog2e), both(-kTanhC * kActLog2e)));
+  return z * logistic_pair(z * both(-kActLog2e));  // kActSilu
+}
+
+// (z was kept in fp16: no power of it overflows)
+template <int ACT, bool SECOND>
+__device__ __forceinline__ F2 slope_pair(F2 c, F2& curve) {
+  if (ACT == kActGelu) {
+    F2 bell;
+    const F2 up = cdf_pair(c, bell), f = bell * both(0.39894228040143268f);
+    if (SECOND) curve = f * mad(c * c, both(-1.f), both(2.f));
+    return mad(c, f, up);
+  }
+  if (ACT == kActGeluTanh) {
+    const F2 c2 = c * c;
+    const F2 s = logistic_pair(c * mad(c2, both(-0.044715f * kTanhC * kActLog2e), both(-kTanhC * kActLog2e)));
+    const F2 d = s * mad(s, both(-1.f), both(1.f));
+    const F2 v1 = mad(c2, both(3.f * 0.044715f * kTanhC), both(kTanhC)), zv = c * v1;
+    if (SECOND)  // 2 v' + z v'' = 4 v' - 4 sqrt(2 / pi)
+      curve = d * mad(zv, v1 * mad(s, both(-2.f), both(1.f)), mad(v1, both(4.f), both(-2.f * kTanhC)));
+    return mad(zv, d, s);
+  }
+  // kActSilu
+  const F2 s = logistic_pair(c * both(-kActLog2e)), d = s * mad(s, both(-1.f), both(1.f));
+  if (SECOND) curve = d * mad(c, mad(s, both(-2.f), both(1.f)), both(2.f));
+  return mad(c, d, s);
+}
+
+// a[j] *= b[j], a[j] += b[j].
+__device__ __forceinline__ void mul8(float* a, const float* b) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 f = row::parts(row::pair(a[j], a[j + 1]) * row::pair(b[j], b[j + 1]));
+    a[j] = f.x, a[j + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void add8(float* a, const float* b) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 f = row::parts(row::pair(a[j], a[j + 1]) + row::pair(b[j], b[j + 1]));
+    a[j] = f.x, a[j + 1] = f.y;
+  }
+}
+
+template <int ACT>
+constexpr bool kSmooth = ACT == kActGelu || ACT == kActGeluTanh || ACT == kActSilu;
+
+// z[j] becomes a(z[j]).
+template <int ACT, bool EXACT>
+__device__ __forceinline__ void act_values8(float* z) {
+  if constexpr (!EXACT && kSmooth<ACT>) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 f = row::parts(value_pair<ACT>(row::pair(z[j], z[j + 1])));
+      z[j] = f.x, z[j + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = act_value<ACT, EXACT>(z[j]);
+  }
+}
+// z[j] becomes a'(z[j]), and (SECOND) a2[j] a''.
+template <int ACT, bool EXACT, bool SECOND>
+__device__ __forceinline__ void act_slopes8(float* z, float* a2) {
+  if constexpr (!EXACT && kSmooth<ACT>) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      F2 c;
+      const float2 f = row::parts(slope_pair<ACT, SECOND>(row::pair(z[j], z[j + 1]), c));
+      z[j] = f.x, z[j + 1] = f.y;
+      if (SECOND) {
+        const float2 g = row::parts(c);
+        a2[j] = g.x, a2[j + 1] = g.y;
+      }
+    }
+  } else {
+    float none;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = act_slope<ACT, EXACT, SECOND>(z[j], SECOND ? a2[j] : none);
+  }
+}
+
+// The same with the activation as a value.
+template <bool EXACT>
+__device__ __forceinline__ void act_values8(int act, float* z) {
   switch (act) {
-    FBOB_ACT_CASE(kActRelu)
-    FBOB_ACT_CASE(kActGelu)
-    FBOB_ACT_CASE(kActGeluTanh)
-    FBOB_ACT_CASE(kActSilu)
+    case kActRelu: return act_values8<kActRelu, EXACT>(z);
+    case kActGelu: return act_values8<kActGelu, EXACT>(z);
+    case kActGeluTanh: return act_values8<kActGeluTanh, EXACT>(z);
+    case kActSilu: return act_values8<kActSilu, EXACT>(z);
+    default: return;
+  }
+}
+template <bool EXACT>
+__device__ __forceinline__ float act_value(int act, float z) {
+  switch (act) {
+    case kActRelu: return act_value<kActRelu, EXACT>(z);
+    case kActGelu: return act_value<kActGelu, EXACT>(z);
+    case kActGeluTanh: return act_value<kActGeluTanh, EXACT>(z);
+    case kActSilu: return act_value<kActSilu, EXACT>(z);
+    default: return z;
+  }
+}
+template <bool EXACT>
+__device__ __forceinline__ void act_slopes8(int act, float* z) {
+  switch (act) {
+    case kActRelu: return act_slopes8<kActRelu, EXACT, false>(z, nullptr);
+    case kActGelu: return act_slopes8<kActGelu, EXACT, false>(z, nullptr);
+    case kActGeluTanh: return act_slopes8<kActGeluTanh, EXACT, false>(z, nullptr);
+    case kActSilu: return act_slopes8<kActSilu, EXACT, false>(z, nullptr);
     default:
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        z[j] = 1.f;
-        if (SECOND) a2[j] = 0.f;
-      }
-      break;
+      for (int j = 0; j < 8; ++j) z[j] = 1.f;
   }
-#undef FBOB_ACT_CASE
 }
 
 }  // namespace fbob

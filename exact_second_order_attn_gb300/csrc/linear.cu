@@ -39,29 +39,64 @@ constexpr int kPairs = 76;                     // block pairs of a GB300, for th
 constexpr size_t kSlabBytes = 512ull << 20;    // slabs of a product
 constexpr long long kLongTerms = 16384;        // bf16 sums above end their chains there
 
+// Times in cycles, estimated, decide between tile widths and numbers of slabs: a step
+// of a tile takes 575 (256 columns) or 400 (128: as much of A is loaded for half the
+// products), the hand-over of a tile 1,000; slabs cost a launch and a read of fp32.
+double tile_cost(long long steps, int nseg, int tile_n) { return (double)steps * nseg * (tile_n == 256 ? 575. : 400.) + 1000.; }
+double slab_cost(long long M, long long N, int s) { return s > 1 ? 3500. + 4. * (double)M * (double)N * s / 2500. : 0.; }
+long long tiles_of(long long M, long long N, int tile_n) { return ((M + kTileM - 1) / kTileM) * ((N + tile_n - 1) / tile_n); }
+bool slabs_fit(long long M, long long N, int s) { return (size_t)M * up(N, 8) * 4 * s <= kSlabBytes; }
+
 // Tile width and slabs of a product of M x N outputs over `steps` steps of the
 // contraction in each of nseg segments.
 struct Shape {
   int tile_n, splits;
 };
-
-// The estimated time in cycles decides.  Per step of a tile 575 cycles (256 columns)
-// or 400 (128: as much of A is loaded for half the products), per wave of tiles 1,000
-// for the hand-over; slabs cost a write and a read of fp32 at 3,500 bytes a cycle and
-// a launch.
 Shape choose(long long M, long long N, int steps, int nseg, bool slabs, bool narrow_only) {
   auto cost = [&](int tile, int s) {
-    const long long tiles = ((M + kTileM - 1) / kTileM) * ((N + tile - 1) / tile) * s;
-    const double waves = (double)((tiles + kPairs - 1) / kPairs);
-    const double each = (double)((steps + s - 1) / s) * nseg * (tile == 256 ? 575. : 400.) + 1000.;
-    return waves * each + (s > 1 ? 4000. + 8. * (double)M * (double)N * s / 3500. : 0.);
+    const long long tiles = tiles_of(M, N, tile) * s;
+    return (double)((tiles + kPairs - 1) / kPairs) * tile_cost((steps + s - 1) / s, nseg, tile) + slab_cost(M, N, s);
   };
   Shape best{narrow_only ? 128 : 256, 1};
   double least = cost(best.tile_n, 1);
   if (cost(128, 1) < least) best = Shape{128, 1}, least = cost(128, 1);
-  const size_t slab = (size_t)M * up(N, 8) * 4;
-  for (int s = 2; slabs && s <= 64 && s <= steps && slab * s <= kSlabBytes; ++s) {
+  for (int s = 2; slabs && s <= 64 && s <= steps && slabs_fit(M, N, s); ++s) {
     if (cost(256, s) < least) best = Shape{256, s}, least = cost(256, s);
+  }
+  return best;
+}
+
+// Slabs of two products in one launch (either may be absent: M = 0).  The pairs take
+// the tiles of the first, which last longer, then those of the second, in turn.
+struct Size {
+  long long M, N;
+  int steps, nseg;
+};
+struct Splits {
+  int s[2];
+};
+Splits share(const Size (&z)[2]) {
+  Splits best{{1, 1}};
+  double least = -1.;
+  static constexpr int kTry[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32};  // (the host pays for each pair)
+  for (int a : kTry) {
+    if (a > 1 && (z[0].M == 0 || a > z[0].steps || !slabs_fit(z[0].M, z[0].N, a))) break;
+    for (int b : kTry) {
+      if (b > 1 && (z[1].M == 0 || b > z[1].steps || !slabs_fit(z[1].M, z[1].N, b))) break;
+      const int s[2] = {a, b};
+      long long n[2];
+      double each[2], cost = 0.;
+      for (int i = 0; i < 2; ++i) {
+        n[i] = z[i].M ? tiles_of(z[i].M, z[i].N, 256) * s[i] : 0;
+        each[i] = tile_cost((z[i].steps + s[i] - 1) / s[i], z[i].nseg, 256);
+        cost += (double)(n[i] / kPairs) * each[i] + (z[i].M ? slab_cost(z[i].M, z[i].N, s[i]) : 0.);
+      }
+      // what the busiest pair has beyond that: a tile of either, or of both
+      const long long r[2] = {n[0] % kPairs, n[1] % kPairs};
+      const double most = each[0] > each[1] ? each[0] : each[1];
+      cost += r[0] + r[1] > kPairs ? each[0] + each[1] : r[0] && r[1] ? most : r[0] ? each[0] : r[1] ? each[1] : 0.;
+      if (least < 0. || cost < least) best = Splits{{a, b}}, least = cost;
+    }
   }
   return best;
 }
@@ -73,7 +108,8 @@ struct Plan {
   bool copy_k, copy_n;  // [.][K] and [.][N] operands are not read in place
   bool own_dz;          // dz is not dy itself
   bool curved;          // a'' is not zero
-  Shape fwd, sec, dx, dw;
+  Shape fwd, sec;
+  Splits both, dx, dw;  // slabs of dx and dW together, and of each alone
   int sum_rows, sum_parts;
   size_t x, W, ux, uW, dz, q, sums, slab, bytes;
 };
@@ -93,8 +129,8 @@ Plan plan(const LinearArgs& a, LinearPass pass) {
   const bool held = !a.bf16;
   p.fwd = choose(a.T, a.N, steps_of(a.K), one, true, held || a.K > kLongTerms);
   p.sec = choose(a.T, a.N, steps_of(a.K), 2 * one, false, p.zp > 1 || 2ll * a.K > kLongTerms);
-  p.dx = choose(a.T, a.K, steps_of(a.N), back * two, true, false);
-  p.dw = choose(a.N, a.K, steps_of(a.T), back * two, true, false);
+  const Size dx{a.T, a.K, steps_of(a.N), back * two}, dw{a.N, a.K, steps_of(a.T), back * two}, none{0, 0, 1, 1};
+  if (bwd || bob) p.both = share({dx, dw}), p.dx = share({dx, none}), p.dw = share({none, dw});
   // rows of a block of dz_kernel: as many blocks as fill the device six times
   const long long across = (p.Np + 255) / 256;
   p.sum_rows = (int)up((size_t)((long long)a.T * across / (152 * 6) + 1), 8);
@@ -115,9 +151,16 @@ Plan plan(const LinearArgs& a, LinearPass pass) {
   p.q = take(bob && p.curved, T * N * 2 * p.zp);
   p.sums = take(bwd || (bob && p.curved), parts * N * 4);
   const size_t f = p.fwd.splits > 1 ? p.fwd.splits * T * N * 4 : 0;
-  const size_t d = p.dx.splits > 1 ? p.dx.splits * T * K * 4 : 0;
-  const size_t w = p.dw.splits > 1 ? p.dw.splits * (size_t)a.N * K * 4 : 0;
-  p.slab = take(true, pass == LinearPass::kFwd ? f : d > w ? d : w);
+  auto grads = [&](const Splits& n, bool x, bool w) {
+    return (x && n.s[0] > 1 ? up(n.s[0] * T * K * 4, ce::kWorkspaceAlign) : 0) +
+           (w && n.s[1] > 1 ? up(n.s[1] * (size_t)a.N * K * 4, ce::kWorkspaceAlign) : 0);
+  };
+  size_t g = 0;
+  if (bwd || bob) {
+    const size_t each[3] = {grads(p.both, true, true), grads(p.dx, true, false), grads(p.dw, false, true)};
+    for (size_t n : each) g = n > g ? n : g;
+  }
+  p.slab = take(true, pass == LinearPass::kFwd ? f : g);
   p.bytes = at;
   return p;
 }
@@ -217,13 +260,11 @@ __global__ void __launch_bounds__(256)
           if (z) {
             float a1[8];
             s[u].values(a1);
-            act_slopes<sizeof(T) == 4, false, 8>(act, a1, nullptr);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= a1[j];
+            act_slopes8<sizeof(T) == 4>(act, a1);
+            mul8(v, a1);
           }
           if (drop.on) drop.apply8((uint32_t)(c >> 3), (uint32_t)r, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sum[j] += v[j];
+          add8(sum, v);
           if (np) store_planes8(planes + (size_t)r * Np + c, (size_t)rows * Np, np, v);
         }
       }
@@ -268,51 +309,77 @@ __global__ void __launch_bounds__(512) columns_kernel(const float* sums, int par
   out[n] = (T)s;
 }
 
-// out [rows][N] = the sum of the slabs [splits][rows][Np]; with `fwd` the forward's
-// epilogue on it.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256)
-    slabs_kernel(const float* slab, int splits, long long rows, int N, int Np, T* out, bool fwd, const T* bias,
-                 const T* r, Kept<T>* z, int act, const __grid_constant__ DropArgs da) {
+// out [rows][N] = the sum of the slabs [splits][rows][Np], of one or two outputs; the
+// forward's epilogue on the first with FWD.  One thread per 8 columns.
+struct SlabSum {
+  const float* slab;
+  void* out;
+  long long rows;
+  int splits, N, Np, vec;
+  unsigned first;  // block
+};
+struct SlabSums {
+  SlabSum o[2];
+  int n;
+  const void *bias, *r;
+  void* z;
+  int act;
+  DropArgs drop;
+};
+
+template <typename T, bool FWD>
+__global__ void __launch_bounds__(256) slabs_kernel(const __grid_constant__ SlabSums all) {
   allow_next();
   wait_previous();
-  const Dropper drop(da);
-  const int per = Np / 8;
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, row = i / per;
-  const int c = (int)(i - row * per) * 8, n = N - c;
-  if (row >= rows) return;
-  const size_t stride = (size_t)rows * Np, at = (size_t)row * Np + c, to = (size_t)row * N + c;
+  const SlabSum& o = all.o[all.n > 1 && blockIdx.x >= all.o[1].first];
+  const int per = o.Np / 8;
+  const long long i = (long long)(blockIdx.x - o.first) * blockDim.x + threadIdx.x, row = i / per;
+  const int c = (int)(i - row * per) * 8, n = o.N - c;
+  if (row >= o.rows) return;
+  const size_t stride = (size_t)o.rows * o.Np, at = (size_t)row * o.Np + c, to = (size_t)row * o.N + c;
   float v[8], w[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  for (int s0 = 0; s0 < splits; s0 += 4) {
+  for (int s0 = 0; s0 < o.splits; s0 += 4) {
     float f[4][8];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      if (s0 + u < splits) load8<float, true>(slab + (s0 + u) * stride + at, 8, f[u]);
+      if (s0 + u < o.splits) load8<float, true>(o.slab + (s0 + u) * stride + at, 8, f[u]);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += s0 + u < splits ? f[u][j] : 0.f;
+      if (s0 + u < o.splits) add8(v, f[u]);
     }
   }
-  if (fwd) {
+  T* const out = static_cast<T*>(o.out);
+  if constexpr (FWD) {
+    const T *bias = static_cast<const T*>(all.bias), *r = static_cast<const T*>(all.r);
+    Kept<T>* z = static_cast<Kept<T>*>(all.z);
     if (bias) {
       load8<T, false>(bias + c, n, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += w[j];
+      add8(v, w);
     }
-    if (z) store8<Kept<T>, VEC>(z + to, n, v);
-    act_values<sizeof(T) == 4, 8>(act, v);
+    if (z) {
+      if (o.vec)
+        store8<Kept<T>, true>(z + to, n, v);
+      else
+        store8<Kept<T>, false>(z + to, n, v);
+    }
+    act_values8<sizeof(T) == 4>(all.act, v);
+    const Dropper drop(all.drop);
     if (drop.on) drop.apply8((uint32_t)(c >> 3), (uint32_t)row, v);
     if (r) {
-      load8<T, VEC>(r + to, n, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += w[j];
+      if (o.vec)
+        load8<T, true>(r + to, n, w);
+      else
+        load8<T, false>(r + to, n, w);
+      add8(v, w);
     }
   }
-  store8<T, VEC>(out + to, n, v);
+  if (o.vec)
+    store8<T, true>(out + to, n, v);
+  else
+    store8<T, false>(out + to, n, v);
 }
 
 // --- the passes --------------------------------------------------------------------------------------
@@ -360,22 +427,18 @@ struct Run {
                   : run("linear_operands", operands_kernel<float>, grid, dim3(256), o, a.K, p.Kp, p.np);
   }
 
-  GemmArgs base(long long M, long long N, long long K) const {
-    GemmArgs g;
+  void base(GemmArgs& g) const {
     memset(&g, 0, sizeof(g));
-    g.M = (int)M, g.N = (int)N, g.K = (int)K, g.splits = 1, g.fp32 = !a.bf16;
-    g.err = c.err, g.wait_ns = c.wait_ns, g.stall = c.stall;
-    return g;
+    g.fp32 = !a.bf16, g.err = c.err, g.wait_ns = c.wait_ns, g.stall = c.stall;
+  }
+  static void sizes(Problem& q, long long M, long long N, long long K, int splits) {
+    q.M = (int)M, q.N = (int)N, q.K = (int)K, q.splits = splits;
   }
   // Chains of fp32 operands are 128 columns of each plane product; long sums of bf16
   // ones end theirs every 16,384 terms.
-  void chains(GemmArgs& g) const {
-    if (!a.bf16) {
-      g.chain = 2;
-      return;
-    }
-    const long long terms = ((long long)g.K + g.splits - 1) / g.splits * g.nseg;
-    g.chain = terms > kLongTerms ? (int)(kLongTerms / kBK / g.nseg) : 0;
+  void chains(Problem& q) const {
+    const long long terms = ((long long)q.K + q.splits - 1) / q.splits * q.nseg;
+    q.chain = !a.bf16 ? 2 : terms > kLongTerms ? (int)(kLongTerms / kBK / q.nseg) : 0;
   }
 
   // Maps of the planes of a [rows][K] operand, boxes of `box` rows x 64 columns.
@@ -403,7 +466,7 @@ struct Run {
 
   // The products of na terms of A operand x and the terms of B operand y (0 or 1
   // each): of fp32 those that reach 2^-16 of the first; smallest first.
-  void products(GemmArgs& g, int x, int y, int na) const {
+  void products(Problem& g, int x, int y, int na) const {
     auto add = [&](int i, int j) { g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + i), (uint8_t)(kPlanes * y + j)}; };
     if (a.bf16) {
       for (int i = na - 1; i >= 0; --i) add(i, 0);
@@ -420,16 +483,24 @@ struct Run {
   cudaError_t forward() const {
     if (a.T <= kRowsTokens) return rows(a, s);
     LIN_TRY(operands(a.x, a.W, nullptr, nullptr));
-    GemmArgs g = base(a.T, a.N, a.K);
+    GemmArgs g;
+    base(g);
+    Problem& q = g.prob[0];
     const Shape sh = p.fwd;
-    g.splits = sh.splits;
-    products(g, 0, 0, 1);
-    chains(g);
-    if (!maps(g.a, a.x, p.x, a.T, 128) || !maps(g.b, a.W, p.W, a.N, sh.tile_n / 2)) return cudaErrorInvalidValue;
+    g.problems = 1;
+    sizes(q, a.T, a.N, a.K, sh.splits);
+    products(q, 0, 0, 1);
+    chains(q);
+    if (!maps(q.a, a.x, p.x, a.T, 128) || !maps(q.b, a.W, p.W, a.N, sh.tile_n / 2)) return cudaErrorInvalidValue;
     if (sh.splits > 1) {
-      g.ep.slab = at<float>(p.slab), g.ep.ld = p.Np;
-      LIN_TRY(gemm_slab(kNT, g, s));
-      return slabs(sh.splits, a.T, a.N, a.y, true);
+      q.slab = at<float>(p.slab), q.slab_ld = p.Np;
+      LIN_TRY(gemm_slabs(g, s));
+      SlabSums all;
+      memset(&all, 0, sizeof(all));
+      add_slabs(all, q, a.N, a.y);
+      all.bias = a.b, all.r = a.r, all.z = a.z_out, all.act = a.act, all.drop = a.drop;
+      all.o[0].vec = all.o[0].vec && mapped(a.r) && mapped(a.z_out);
+      return finish_slabs(all, true);
     }
     EpArgs& e = g.ep;
     e.bias = a.b, e.in0 = a.r, e.out0 = a.y, e.out1 = a.z_out, e.in_ld = a.N, e.act = a.act, e.drop = a.drop;
@@ -442,17 +513,20 @@ struct Run {
     return gemm_forward(sh.tile_n, g, s);
   }
 
-  cudaError_t slabs(int splits, long long rows, int N, void* out, bool fwd) const {
-    return a.bf16 ? slabs_as<__nv_bfloat16>(splits, rows, N, out, fwd) : slabs_as<float>(splits, rows, N, out, fwd);
-  }
-  template <typename E>
-  cudaError_t slabs_as(int splits, long long rows, int N, void* out, bool fwd) const {
+  // The output of a problem whose sums lie in slabs.
+  void add_slabs(SlabSums& all, const Problem& q, int N, void* out) const {
     const int Np = (int)up(N, 8);
-    const bool vec = N % 8 == 0 && aligned(out, 16) && (!fwd || (mapped(a.r) && mapped(a.z_out)));
-    const dim3 grid((unsigned)((rows * (Np / 8) + 255) / 256));
-    return run("linear_slabs", vec ? slabs_kernel<E, true> : slabs_kernel<E, false>, grid, dim3(256), at<float>(p.slab),
-               splits, rows, N, Np, static_cast<E*>(out), fwd, static_cast<const E*>(a.b), static_cast<const E*>(a.r),
-               static_cast<Kept<E>*>(a.z_out), a.act, a.drop);
+    unsigned first = 0;
+    if (all.n) first = all.o[0].first + (unsigned)((all.o[0].rows * (all.o[0].Np / 8) + 255) / 256);
+    all.o[all.n++] = SlabSum{q.slab, out, q.M, q.splits, N, Np, N % 8 == 0 && aligned(out, 16), first};
+  }
+  cudaError_t finish_slabs(const SlabSums& all, bool fwd) const {
+    if (all.n == 0) return cudaSuccess;
+    const SlabSum& last = all.o[all.n - 1];
+    const dim3 grid(last.first + (unsigned)((last.rows * (last.Np / 8) + 255) / 256)), block(256);
+    if (a.bf16)
+      return run("linear_slabs", fwd ? slabs_kernel<__nv_bfloat16, true> : slabs_kernel<__nv_bfloat16, false>, grid, block, all);
+    return run("linear_slabs", fwd ? slabs_kernel<float, true> : slabs_kernel<float, false>, grid, block, all);
   }
 
   // dz and its column sums out of dy and z.
@@ -476,42 +550,66 @@ struct Run {
                         static_cast<float*>(out));
   }
 
-  // dx [T, K] = q W + dz uW, or dW [N, K] = q^T x + dz^T ux; either term may be absent
-  // (the backward's has dz with the first operand).
-  cudaError_t gradient(Layout layout, Shape sh, void* out, const void* u, size_t u_off, const void* v, size_t v_off) const {
-    const bool dw = layout == kTN;
-    const long long rows_a = dw ? a.N : a.T, over = dw ? a.T : a.N, rows_b = dw ? a.T : a.N;
-    GemmArgs g = base(rows_a, a.K, over);
+  // dx [T, K] = q W + dz uW, or (dw) dW [N, K] = q^T x + dz^T ux; either term may be
+  // absent (the backward's has dz with the first operand).
+  bool gradient(Problem& g, bool dw, int splits, void* out, const void* u, size_t u_off, const void* v,
+                size_t v_off) const {
+    const long long rows_b = dw ? a.T : a.N;
+    sizes(g, dw ? a.N : a.T, a.K, dw ? a.T : a.N, splits);
+    g.a_mn = dw;
     const int box_a = dw ? kBK : 128;
     if (u) {  // with q
-      if (!z_maps(g.a, true, box_a) || !maps(g.b, u, u_off, rows_b, kBK)) return cudaErrorInvalidValue;
+      if (!z_maps(g.a, true, box_a) || !maps(g.b, u, u_off, rows_b, kBK)) return false;
       products(g, 0, 0, p.zp);
     }
     if (v) {  // with dz
-      if (!z_maps(g.a + kPlanes, false, box_a) || !maps(g.b + kPlanes, v, v_off, rows_b, kBK)) return cudaErrorInvalidValue;
+      if (!z_maps(g.a + kPlanes, false, box_a) || !maps(g.b + kPlanes, v, v_off, rows_b, kBK)) return false;
       products(g, 1, 1, p.zp);
     }
-    if (g.nseg == 0) return cudaMemsetAsync(out, 0, (size_t)rows_a * a.K * element(), s);
-    g.splits = sh.splits;
+    if (g.nseg == 0) return true;
     chains(g);
-    if (sh.splits > 1) {
-      g.ep.slab = at<float>(p.slab), g.ep.ld = p.Kp;
-      LIN_TRY(gemm_slab(layout, g, s));
-      return slabs(sh.splits, rows_a, a.K, out, false);
+    g.out0 = out;
+    g.out_map = a.bf16 && a.K % 8 == 0 && aligned(out, 16);
+    return !g.out_map || store_map(&g.out, out, g.M, a.K, a.K);
+  }
+  // Both gradients in one launch: u_x, v_x are multiplied by q and dz for dx, u_w, v_w
+  // for dW.
+  cudaError_t gradients(const void* u_x, const void* v_x, size_t v_x_off, const void* u_w, const void* v_w,
+                        size_t v_w_off) const {
+    GemmArgs g;
+    base(g);
+    const bool want[2] = {a.dx && (u_x || v_x), a.dW && (u_w || v_w)};
+    if (a.dx && !want[0]) LIN_TRY(cudaMemsetAsync(a.dx, 0, (size_t)a.T * a.K * element(), s));
+    if (a.dW && !want[1]) LIN_TRY(cudaMemsetAsync(a.dW, 0, (size_t)a.N * a.K * element(), s));
+    if (!want[0] && !want[1]) return cudaSuccess;
+    const Splits& n = want[0] && want[1] ? p.both : want[0] ? p.dx : p.dw;
+    SlabSums all;
+    memset(&all, 0, sizeof(all));
+    size_t slab = p.slab;
+    // (the order of the slabs in the workspace; the longer tiles' problem is the first of the launch)
+    const bool dw_first = want[1] && (!want[0] || steps_of(a.T) / n.s[1] >= steps_of(a.N) / n.s[0]);
+    for (int i = 0; i < 2; ++i) {
+      if (!want[i]) continue;
+      Problem& q = g.prob[want[0] && want[1] ? i != (int)dw_first : 0];
+      ++g.problems;
+      const bool ok = i ? gradient(q, true, n.s[1], a.dW, u_w, p.x, v_w, v_w_off)
+                        : gradient(q, false, n.s[0], a.dx, u_x, p.W, v_x, v_x_off);
+      if (!ok) return cudaErrorInvalidValue;
+      if (q.splits > 1) {
+        q.slab = at<float>(slab), q.slab_ld = p.Kp;
+        slab += up((size_t)q.splits * q.M * p.Kp * 4, ce::kWorkspaceAlign);
+        add_slabs(all, q, a.K, i ? a.dW : a.dx);
+      }
     }
-    g.ep.out0 = out, g.ep.in_ld = a.K;
-    g.ep.out_map = a.bf16 && a.K % 8 == 0 && aligned(out, 16);
-    if (g.ep.out_map && !store_map(g.out, out, rows_a, a.K, a.K)) return cudaErrorInvalidValue;
-    return gemm_out(layout, sh.tile_n, g, s);
+    LIN_TRY(gemm_gradients(g, s));
+    return finish_slabs(all, false);
   }
 
   cudaError_t backward() const {
     LIN_TRY(operands(a.dW ? a.x : nullptr, a.dx ? a.W : nullptr, nullptr, nullptr));
     LIN_TRY(make_dz(p.own_dz && (a.dx || a.dW), a.db != nullptr));
     if (a.db) LIN_TRY(columns(p.sum_parts, a.db));
-    if (a.dx) LIN_TRY(gradient(kNN, p.dx, a.dx, nullptr, 0, a.W, p.W));
-    if (a.dW) LIN_TRY(gradient(kTN, p.dw, a.dW, nullptr, 0, a.x, p.x));
-    return cudaSuccess;
+    return gradients(nullptr, a.dx ? a.W : nullptr, p.W, nullptr, a.dW ? a.x : nullptr, p.x);
   }
 
   // dx, dW, db here are gx, gW, gb.
@@ -522,18 +620,22 @@ struct Run {
     LIN_TRY(operands((product && a.uW) || (want_q && a.dW) ? a.x : nullptr,
                      (product && a.ux) || (want_q && a.dx) ? a.W : nullptr, a.ux, a.uW));
     if (product) {
-      GemmArgs g = base(a.T, a.N, a.K);
+      GemmArgs g;
+      base(g);
+      Problem& t = g.prob[0];
+      g.problems = 1;
+      sizes(t, a.T, a.N, a.K, 1);
       const int box = p.sec.tile_n / 2;
       if (a.ux) {
-        if (!maps(g.a, a.ux, p.ux, a.T, 128) || !maps(g.b, a.W, p.W, a.N, box)) return cudaErrorInvalidValue;
-        products(g, 0, 0, 1);
+        if (!maps(t.a, a.ux, p.ux, a.T, 128) || !maps(t.b, a.W, p.W, a.N, box)) return cudaErrorInvalidValue;
+        products(t, 0, 0, 1);
       }
       if (a.uW) {
-        if (!maps(g.a + kPlanes, a.x, p.x, a.T, 128) || !maps(g.b + kPlanes, a.uW, p.uW, a.N, box))
+        if (!maps(t.a + kPlanes, a.x, p.x, a.T, 128) || !maps(t.b + kPlanes, a.uW, p.uW, a.N, box))
           return cudaErrorInvalidValue;
-        products(g, 1, 1, 1);
+        products(t, 1, 1, 1);
       }
-      chains(g);
+      chains(t);
       EpArgs& e = g.ep;
       e.bias = a.ub, e.act = a.act, e.drop = a.drop, e.in_ld = a.N, e.ld = p.Np;
       e.q_planes = want_q && (a.dx || a.dW) ? p.zp : 0;
@@ -557,9 +659,7 @@ struct Run {
     }
     if (a.db && !p.curved) LIN_TRY(cudaMemsetAsync(a.db, 0, a.N * element(), s));
     const bool q = p.curved;
-    if (a.dx) LIN_TRY(gradient(kNN, p.dx, a.dx, q ? a.W : nullptr, p.W, a.uW, p.uW));
-    if (a.dW) LIN_TRY(gradient(kTN, p.dw, a.dW, q ? a.x : nullptr, p.x, a.ux, p.ux));
-    return cudaSuccess;
+    return gradients(q ? a.W : nullptr, a.uW, p.uW, q ? a.x : nullptr, a.ux, p.ux);
   }
 };
 

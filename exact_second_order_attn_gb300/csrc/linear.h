@@ -27,41 +27,49 @@ struct Seg {
 
 // How A [M, K] and B [N, K] are stored.
 enum Layout {
-  kNT,  // A [M][K], B [N][K]
-  kNN,  // A [M][K], B [K][N]
-  kTN   // A [K][M], B [K][N]
+  kNT,         // A [M][K], B [N][K]
+  kGradients,  // A [M][K] (dz for dx) or [K][M] (dz for dW), B [K][N]
 };
 // What becomes of an accumulator tile.
 enum Epilogue {
-  kForward,  // y = r + m a(v + bias), and z = v + bias
-  kSecond,   // v + bias = t: gdy, q, dz and q's column sums; one term of q and dz
+  kForward,      // y = r + m a(v + bias), and z = v + bias
+  kSecond,       // v + bias = t: gdy, q, dz and q's column sums; one term of q and dz
   kSecondTerms,  // the same with several (tiles of 128 columns)
-  kOut,      // in the output type
-  kSlab      // fp32
+  kGradient,     // in the output type, or a slab
+  kSlab          // fp32
 };
 
 struct EpArgs {
   const void *bias;         // [N], or null
   const void *in0, *in1;    // kForward: r, -; kSecond: z, dy (null: absent)
-  void *out0, *out1;        // kForward: y, z; kSecond: gdy; kOut: the output (null: not wanted)
-  float* slab;              // kSlab: [splits][M][ld]
+  void *out0, *out1;        // kForward: y, z; kSecond: gdy (null: not wanted)
   float* sums;              // kSecond: column sums of q [rows / 32][ld], or null
-  long long ld, in_ld;      // of the slabs and sums; of the inputs and outputs (elements)
+  long long ld, in_ld;      // of the sums; of the inputs and outputs (elements)
   int in_map, out_map;      // inputs and outputs move through the maps (bf16)
   int q_planes, dz_planes;  // bf16 terms of q and dz (0: not wanted), stored through out[2], out[5]
   int act;
   DropArgs drop;
 };
 
-struct GemmArgs {
+struct Problem {
   CUtensorMap a[2 * kPlanes], b[2 * kPlanes];
-  CUtensorMap in[2];                // store_map()s of in0, in1
-  CUtensorMap out[2 + 2 * kPlanes];  // of out0, out1, q's planes, dz's planes
+  CUtensorMap out;  // store_map() of out0
   Seg seg[kMaxSegs];
-  int nseg, fp32;
+  int nseg, a_mn;
   int M, N, K, splits;
+  int chain;          // steps of K after which a chain of the tensor cores ends (0: never)
+  int out_map;        // results leave through the map (bf16)
+  void* out0;         // kGradient: [M][N]
+  float* slab;        // or [splits][M][slab_ld]
+  long long slab_ld;
+};
+
+struct GemmArgs {
+  Problem prob[2];
+  CUtensorMap in[2];                 // store_map()s of in0, in1
+  CUtensorMap out[2 + 2 * kPlanes];  // of out0, out1, q's planes, dz's planes
+  int problems, fp32;
   int stages, boxes;  // of a block, of an epilogue warp: set at the launch
-  int chain;  // steps of K after which a chain of the tensor cores ends (0: never)
   EpArgs ep;
   unsigned int* err;
   unsigned long long wait_ns;
@@ -72,8 +80,8 @@ struct GemmArgs {
 // tile_n (128 or 256).  Splits are at most the steps of K.
 cudaError_t gemm_forward(int tile_n, const GemmArgs& g, cudaStream_t s);  // kNT, kForward
 cudaError_t gemm_second(int tile_n, const GemmArgs& g, cudaStream_t s);   // kNT, kSecond or kSecondTerms
-cudaError_t gemm_out(Layout layout, int tile_n, const GemmArgs& g, cudaStream_t s);  // kNN, kTN
-cudaError_t gemm_slab(Layout layout, const GemmArgs& g, cudaStream_t s);
+cudaError_t gemm_slabs(const GemmArgs& g, cudaStream_t s);                // kNT, kSlab
+cudaError_t gemm_gradients(const GemmArgs& g, cudaStream_t s);            // kGradients, kGradient
 
 // y (and z) of up to kRowsTokens tokens without tensor cores (linear_rows.cu).
 constexpr int kRowsTokens = 16;

@@ -1,6 +1,7 @@
 // The matrix products of linear layers on the fifth generation tensor cores, with
 // the layer's elementwise work in the epilogue.
 //
+// One or two problems in a launch (dx and dW read the same dz and share their waves),
 // C[256 x BN] = sum over segments of A_seg B_seg^T per pair of thread blocks
 // (cta_group::2): each block holds its 128 rows of A and its half of B's rows of
 // every 64-column stage; the accumulator's 128 rows x BN columns lie in the block's
@@ -63,8 +64,7 @@ constexpr bool kIsSecond = EP == kSecond || EP == kSecondTerms;
 template <int LAYOUT, int EP, bool HELD, int BN_>
 struct Cfg {
   static constexpr int BN = BN_;
-  static constexpr bool A_MN = LAYOUT == kTN;
-  static constexpr bool B_MN = LAYOUT != kNT;
+  static constexpr bool B_MN = LAYOUT == kGradients;
   static constexpr int A_BYTES = 128 * kBK * 2;
   static constexpr int B_BYTES = BN / 2 * kBK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
@@ -77,7 +77,7 @@ struct Cfg {
   // further terms of q and dz in turn; of two results.
   static int boxes(const GemmArgs& g) {
     if (EP == kForward) return g.fp32 ? 0 : 1 + (g.ep.out1 != nullptr);
-    return EP == kSecond ? 3 : EP == kSecondTerms ? (g.fp32 ? 7 : 5) : EP == kOut ? 2 : 0;
+    return EP == kSecond ? 3 : EP == kSecondTerms ? (g.fp32 ? 7 : 5) : EP == kGradient ? 2 : 0;
   }
   static int stages(const GemmArgs& g) {
     const int n = (kRoom - WARPS * boxes(g) * kBoxBytes) / STAGE;
@@ -155,7 +155,8 @@ struct Ep {
   const GemmArgs& p;
   Outbox out;
   const Dropper& drop;
-  int rows, N;
+  int rows, N;      // of the tile's problem,
+  long long ld;     // and its outputs' rows
 
   // bf16 results leave through the map, or from the box row by row.
   __device__ __forceinline__ void put(const CUtensorMap* map, void* base, bool mapped, int x, int y,
@@ -174,11 +175,11 @@ struct Ep {
   // A box that has been written (and synchronised) goes out row by row.
   __device__ __forceinline__ void copy_rows(uint32_t box, void* base, int x, int y) {
     const uint32_t lane = threadIdx.x & 31;
-    uint16_t* o = static_cast<uint16_t*>(base) + (size_t)y * p.ep.in_ld + x + lane;
+    uint16_t* o = static_cast<uint16_t*>(base) + (size_t)y * ld + x + lane;
     const bool in = x + (int)lane < N;
 #pragma unroll 8
     for (int r = 0; r < 32; ++r) {
-      if (in && y + r < rows) o[(size_t)r * p.ep.in_ld] = ld_shared_u16(box + box_element(r, lane));
+      if (in && y + r < rows) o[(size_t)r * ld] = ld_shared_u16(box + box_element(r, lane));
     }
   }
   // A box that has been written (and synchronised) leaves as a bulk tensor store.
@@ -191,17 +192,17 @@ struct Ep {
   }
 
   template <bool FP32>
-  __device__ __forceinline__ void result(const CUtensorMap* map, void* base, int x, int y, const float* v) {
+  __device__ __forceinline__ void result(const Problem& q, int x, int y, const float* v) {
     if constexpr (FP32) {
       const int row = y + (int)(threadIdx.x & 31);
 #pragma unroll
       for (int j = 0; j < 32; j += 8)
-        write8(static_cast<float*>(base), p.ep.in_ld, row < rows, row, x + j, N, v + j);
+        write8(static_cast<float*>(q.out0), ld, row < rows, row, x + j, N, v + j);
     } else {
       uint32_t w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-      put(map, base, p.ep.out_map, x, y, w);
+      put(&q.out, q.out0, q.out_map, x, y, w);
     }
   }
 };
@@ -232,7 +233,7 @@ struct Inbox {
       return;
     }
     const int lane = threadIdx.x & 31;
-    const bool in = x + lane < p->N;
+    const bool in = x + lane < p->prob[0].N;
     for (int i = 0; i < 2; ++i) {
       if (!base(i)) continue;
       const uint16_t* q = static_cast<const uint16_t*>(base(i)) + (size_t)y * p->ep.in_ld + x + lane;
@@ -240,7 +241,7 @@ struct Inbox {
       for (int r0 = 0; r0 < 32; r0 += 16) {
         uint16_t v[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = in && y + r0 + r < p->M ? q[(size_t)(r0 + r) * p->ep.in_ld] : (uint16_t)0;
+        for (int r = 0; r < 16; ++r) v[r] = in && y + r0 + r < p->prob[0].M ? q[(size_t)(r0 + r) * p->ep.in_ld] : (uint16_t)0;
 #pragma unroll
         for (int r = 0; r < 16; ++r) st_shared_u16(box(i) + box_element(r0 + r, lane), v[r]);
       }
@@ -314,7 +315,8 @@ __device__ __forceinline__ float sum_columns8(float* v) {
 // t[j] += bias of the columns 8 g + j, out of the warp's 32 in shared memory.
 __device__ __forceinline__ void add_bias(const float* bias, int g, float* t) {
   const float4 a = *reinterpret_cast<const float4*>(bias + 8 * g), b = *reinterpret_cast<const float4*>(bias + 8 * g + 4);
-  t[0] += a.x, t[1] += a.y, t[2] += a.z, t[3] += a.w, t[4] += b.x, t[5] += b.y, t[6] += b.z, t[7] += b.w;
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  add8(t, v);
 }
 
 // Where the elementwise epilogues find 32 columns of the product, eight at a time
@@ -352,8 +354,7 @@ __device__ __forceinline__ void forward_values(Ep& e, const Columns<HELD>& in, c
         st_shared_v4(out + kBoxBytes + box_at(lane, g), half_pair(v[0], v[1]), half_pair(v[2], v[3]),
                      half_pair(v[4], v[5]), half_pair(v[6], v[7]));
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = act_value<ACT, FP32>(v[j]);
+    act_values8<ACT, FP32>(v);
     if (e.drop.on) e.drop.apply8((uint32_t)(x >> 3) + g, (uint32_t)row, v);
     if (a.in0) {
       float r[8];
@@ -361,8 +362,7 @@ __device__ __forceinline__ void forward_values(Ep& e, const Columns<HELD>& in, c
         read8(static_cast<const float*>(a.in0), a.in_ld, live, row, x + 8 * g, e.N, r);
       else
         box_values(out, g, r);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += r[j];
+      add8(v, r);
     }
     if (FP32)
       write8(static_cast<float*>(a.out0), a.in_ld, live, row, x + 8 * g, e.N, v);
@@ -428,15 +428,14 @@ __device__ __forceinline__ void second_values(Ep& e, const Columns<HELD>& in, co
   for (int g = 0; g < 4; ++g) {
     float t[8], a1[8], a2[8], dy[8], m[8];
     in.load(g, t);
-    if (a.bias) add_bias(bias, g, t);
+    if (a.bias && live) add_bias(bias, g, t);  // (rows past the last are 0)
     if (ACT != kActNone) {
       if (FP32)
         read8(static_cast<const float*>(a.in0), a.in_ld, live, row, x + 8 * g, e.N, a1);
       else
         half8(ld_shared_v4(boxes + box_at(lane, g)), a1);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a1[j] = act_slope<ACT, FP32, true>(a1[j], a2[j]);
+    act_slopes8<ACT, FP32, true>(a1, a2);
     if (a.in1) {
       if (FP32)
         read8(static_cast<const float*>(a.in1), a.in_ld, live, row, x + 8 * g, e.N, dy);
@@ -456,20 +455,22 @@ __device__ __forceinline__ void second_values(Ep& e, const Columns<HELD>& in, co
     }
     if (a.out0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m[j] = t[j] * a1[j];
+      for (int j = 0; j < 8; ++j) m[j] = t[j];
+      mul8(m, a1);
       if (FP32)
         write8(static_cast<float*>(a.out0), a.in_ld, live, row, x + 8 * g, e.N, m);
       else
         box_store(boxes + 2 * kBoxBytes, g, m);
     }
     if (a.dz_planes) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a1[j] *= dy[j];
+      mul8(a1, dy);
       store_terms<TERMS>(boxes, 1, a.dz_planes, g, a1);
     }
     if (a.q_planes || a.sums) {
+      mul8(t, dy);
+      mul8(t, a2);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = m[j] = live ? t[j] * dy[j] * a2[j] : 0.f;
+      for (int j = 0; j < 8; ++j) m[j] = t[j];
       if (a.q_planes) store_terms<TERMS>(boxes, 0, a.q_planes, g, m);
       if (a.sums) {
         const float s = sum_columns8(t);
@@ -501,21 +502,50 @@ __device__ __forceinline__ void second_chunk(Ep& e, const Columns<HELD>& in, con
   if (!FP32 && a.out0 && !a.out_map) e.copy_rows(boxes + 2 * kBoxBytes, a.out0, x, y0);
 }
 
-// 32 columns (from x) of a gradient, for the row y0 + lane.
+// 32 columns (from x) of a gradient or a slab, for the row y0 + lane.
 template <int EP, bool FP32>
-__device__ __forceinline__ void finish(Ep& e, const float* v, int x, int y0, int split) {
-  const EpArgs& a = e.p.ep;
-  if constexpr (EP == kSlab) {
+__device__ __forceinline__ void finish(Ep& e, const Problem& q, const float* v, int x, int y0, int split) {
+  if (EP == kSlab || q.slab) {
     const int row = y0 + (int)(threadIdx.x & 31);
-    float* o = a.slab + ((size_t)split * e.rows + row) * a.ld + x;
+    float* o = q.slab + ((size_t)split * e.rows + row) * q.slab_ld + x;
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {  // ld is a multiple of 8
-      if (row < e.rows && x + j < a.ld) st_global_v8(o + j, reinterpret_cast<const uint32_t*>(v + j));
+    for (int j = 0; j < 32; j += 8) {  // slab_ld is a multiple of 8
+      if (row < e.rows && x + j < q.slab_ld) st_global_v8(o + j, reinterpret_cast<const uint32_t*>(v + j));
     }
   } else {
-    e.result<FP32>(e.p.out, a.out0, x, y0, v);
+    e.result<FP32>(q, x, y0, v);
   }
 }
+
+// The tiles of a launch: those of the first problem, then those of the second.
+struct Plan {
+  Tiles first, second;
+  int n0, total;
+  __device__ __forceinline__ Plan(const GemmArgs& p, int bn)
+      : first(tiles(p.prob[0], bn)), second(tiles(p.prob[1], bn)), n0(first.count()),
+        total(n0 + (p.problems > 1 ? second.count() : 0)) {}
+  static __device__ __forceinline__ Tiles tiles(const Problem& q, int bn) {
+    return Tiles{(q.M + kTileM - 1) / kTileM, (q.N + bn - 1) / bn, q.splits, (q.K + kBK - 1) / kBK};
+  }
+};
+// Where a tile lies and the steps of its contraction.
+struct Place {
+  int which, m, n, split, k0, k1, chain;
+  __device__ __forceinline__ Place(const GemmArgs& p, const Plan& plan, int t) {
+    which = t >= plan.n0;
+    const Tiles& ts = which ? plan.second : plan.first;
+    if (which) t -= plan.n0;
+    ts.at(t, m, n);
+    split = ts.split(t);
+    k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
+    chain = p.prob[which].chain;
+  }
+  // the step at which a chain of the tensor cores that starts at kc ends
+  template <bool HELD>
+  __device__ __forceinline__ int end(int kc) const {
+    return HELD && chain ? min(kc + chain, k1) : k1;
+  }
+};
 
 template <int LAYOUT, int EP, bool FP32, bool HELD, int BN>
 __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
@@ -563,11 +593,8 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
   const bool live = ctrl.abort_flag == 0;
   const uint32_t sm0 = smem_u32(smem);
   wait_previous();
-  const Tiles ts{(p.M + kTileM - 1) / kTileM, (p.N + BN - 1) / BN, p.splits, (p.K + kBK - 1) / kBK};
-  const int total = ts.count(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int chain_steps = p.chain;
-  auto chain_end = [chain_steps](int kc, int k1) { return HELD ? min(kc + chain_steps, k1) : k1; };
-
+  const Plan plan(p, BN);
+  const int total = plan.total, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int nst = p.stages;
   if (warp == EW || warp == EW + 2) {
     // ------------------------------------------- TMA: one warp loads A, the other B
@@ -578,16 +605,15 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
       long long issued = 0;
       bool ok = true;
       for (int t = pair; ok && t < total; t += pairs) {
-        int m, n;
-        ts.at(t, m, n);
-        const int split = ts.split(t);
-        const int row = m * kTileM + (int)rank * 128, col = n * BN + (int)rank * (BN / 2);
-        const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
-        for (int kc = k0; ok && kc < k1; kc = chain_end(kc, k1)) {
-          const int ke = chain_end(kc, k1);
-          for (int s = 0; ok && s < p.nseg; ++s) {
-            const CUtensorMap* ma = &p.a[p.seg[s].a];
-            const CUtensorMap* mb = &p.b[p.seg[s].b];
+        const Place at_tile(p, plan, t);
+        const Problem& q = p.prob[at_tile.which];
+        const int row = at_tile.m * kTileM + (int)rank * 128, col = at_tile.n * BN + (int)rank * (BN / 2);
+        const bool a_mn = LAYOUT == kGradients && q.a_mn;
+        for (int kc = at_tile.k0; ok && kc < at_tile.k1; kc = at_tile.template end<HELD>(kc)) {
+          const int ke = at_tile.template end<HELD>(kc);
+          for (int s = 0; ok && s < q.nseg; ++s) {
+            const CUtensorMap* ma = &q.a[q.seg[s].a];
+            const CUtensorMap* mb = &q.b[q.seg[s].b];
             for (int k = kc; k < ke; ++k, ++issued, at.next()) {
               const int st = at.s;
               if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.empty[st], at.pass ^ 1, wt)))) break;
@@ -596,7 +622,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
               const uint32_t da = sm0 + st * C::STAGE, db = da + C::A_BYTES;
               if (is_a) {
                 if (rank == 0) mbar_expect_tx_w(&ctrl.full[st], 2 * C::STAGE);
-                if (C::A_MN) {
+                if (a_mn) {
                   tma_load_2d_pair(da, ma, bar, row, k * kBK);
                   tma_load_2d_pair(da + 8192, ma, bar, row + 64, k * kBK);
                 } else {
@@ -629,21 +655,22 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
   } else if (warp == EW + 1) {
     // ------------------------------------------------------------------ MMA
     if (live && rank == 0) {
-      constexpr uint32_t id = idesc_bf16(kTileM, BN, C::A_MN, C::B_MN);
-      constexpr uint32_t lbo_a = C::A_MN ? 8192 : 16, lbo_b = C::B_MN ? 8192 : 16;
-      constexpr uint32_t step_a = C::A_MN ? 2048 >> 4 : 32 >> 4, step_b = C::B_MN ? 2048 >> 4 : 32 >> 4;
+      constexpr uint32_t lbo_b = C::B_MN ? 8192 : 16, step_b = C::B_MN ? 2048 >> 4 : 32 >> 4;
       Ring at{nst};
       int chain = 0;  // accumulator buffers handed to the epilogue so far
       bool ok = true;
       for (int t = pair; ok && t < total; t += pairs) {
-        const int split = ts.split(t);
-        const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
-        for (int kc = k0; ok && kc < k1; kc = chain_end(kc, k1), ++chain) {
-          const int ke = chain_end(kc, k1), buf = chain & 1;
+        const Place tile(p, plan, t);
+        const Problem& q = p.prob[tile.which];
+        const bool a_mn = LAYOUT == kGradients && q.a_mn;
+        const uint32_t id = a_mn ? idesc_bf16(kTileM, BN, true, C::B_MN) : idesc_bf16(kTileM, BN, false, C::B_MN);
+        const uint32_t lbo_a = a_mn ? 8192 : 16, step_a = a_mn ? 2048 >> 4 : 32 >> 4;
+        for (int kc = tile.k0; ok && kc < tile.k1; kc = tile.template end<HELD>(kc), ++chain) {
+          const int ke = tile.template end<HELD>(kc), buf = chain & 1;
           ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_empty[buf], ((chain >> 1) & 1) ^ 1, wt));
           tc_fence_after();
           const uint32_t d = tb + buf * kBufCols;
-          for (int s = 0; ok && s < p.nseg; ++s) {
+          for (int s = 0; ok && s < q.nseg; ++s) {
             for (int k = kc; k < ke; ++k, at.next()) {
               const int st = at.s;
               ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.full[st], at.pass, wt));
@@ -671,7 +698,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
     const uint32_t freed = map_rank(smem_u32(&ctrl.tile_empty[0]), 0);
     const uint32_t boxes = sm0 + nst * C::STAGE + warp * p.boxes * kBoxBytes;
     const Dropper drop(p.ep.drop);
-    Ep e{p, Outbox{boxes, 0}, drop, p.M, p.N};
+    Ep e{p, Outbox{boxes, 0}, drop, p.prob[0].M, p.prob[0].N, p.ep.in_ld};
     Inbox in{boxes, &in_bar[warp], &p, 0, p.ep.in_map != 0, 0, 0};
     if (C::NIN > 0 && !FP32) in.n = (p.ep.in0 != nullptr) + (C::NIN > 1 && p.ep.in1 != nullptr);
     // chunk c of the warp's tiles, counted from tile t
@@ -679,34 +706,37 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
       if (C::NIN == 0 || in.n == 0) return;
       if (c >= CHUNKS) c -= CHUNKS, t += pairs;
       if (t >= total) return;
-      int m, n;
-      ts.at(t, m, n);
-      in.fetch(n * BN + part * H + 32 * c, m * kTileM + (int)rank * 128 + quarter);
+      const Place tile(p, plan, t);
+      in.fetch(tile.n * BN + part * H + 32 * c, tile.m * kTileM + (int)rank * 128 + quarter);
     };
     int chain = 0;
     bool ok = live;
-    if (ok) fetch(pair, 0);
+    if (ok && C::NIN > 0 && in.n) {
+      // The first boxes are wanted when a whole tile's products are done: behind them the
+      // first stages would come late (second order: products began 5 us late).
+      __nanosleep(1000);
+      fetch(pair, 0);
+    }
     for (int t = pair; ok && t < total; t += pairs) {
-      int m, n;
-      ts.at(t, m, n);
-      const int split = ts.split(t);
-      const int y0 = m * kTileM + (int)rank * 128 + quarter, x0 = n * BN + part * H;
+      const Place tile(p, plan, t);
+      const Problem& q = p.prob[tile.which];
+      const int y0 = tile.m * kTileM + (int)rank * 128 + quarter, x0 = tile.n * BN + part * H;
+      if (LAYOUT == kGradients) e.rows = q.M, e.N = q.N, e.ld = q.N;
       float sum[HELD ? H : 1];
       int buf = 0;
       if constexpr (HELD) {
 #pragma unroll
         for (int j = 0; j < H; ++j) sum[j] = 0.f;
-        const int k0 = ts.k_first(split), k1 = ts.k_first(split + 1);
-        for (int kc = k0; kc < k1; kc = chain_end(kc, k1), ++chain) {
+        for (int kc = tile.k0; kc < tile.k1; kc = tile.template end<HELD>(kc), ++chain) {
           buf = chain & 1;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
           tc_fence_after();
 #pragma unroll
-          for (int q = 0; q < CHUNKS; ++q) {
+          for (int c = 0; c < CHUNKS; ++c) {
             float v[32];
-            tmem_ld32(tb + lane + buf * kBufCols + part * H + q * 32, v);
+            tmem_ld32(tb + lane + buf * kBufCols + part * H + c * 32, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sum[q * 32 + j] += v[j];
+            for (int j = 0; j < 32; ++j) sum[c * 32 + j] += v[j];
           }
           tc_fence_before();
           __syncwarp();
@@ -729,11 +759,13 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
           for (int j = 0; j < H; j += 16) tmem_st16_nowait(from + j, reinterpret_cast<const uint32_t*>(sum) + j);
           tmem_st_wait();
         }
+        float bias = column<FP32>(p.ep.bias, x0, e.N);
         for (int c = 0; c < CHUNKS; ++c) {
           const int x = x0 + 32 * c;
           if (p.ep.bias) {
-            bias_row[warp][tid & 31] = column<FP32>(p.ep.bias, x, p.N);
+            bias_row[warp][tid & 31] = bias;
             __syncwarp();
+            if (c + 1 < CHUNKS) bias = column<FP32>(p.ep.bias, x + 32, e.N);
           }
           if (!FP32 && !(ok = in.wait(wt))) break;
           const Columns<HELD> cols{from + 32 * c, freed + buf * 8, c + 1 == CHUNKS};
@@ -752,7 +784,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
           acc.load(32 * c, 32 * c, v);
           if (c + 1 == CHUNKS) acc.done();
           __syncwarp();
-          finish<EP, FP32>(e, v, x0 + 32 * c, y0, split);
+          finish<EP, FP32>(e, q, v, x0 + 32 * c, y0, tile.split);
         }
       }
     }
@@ -775,7 +807,11 @@ cudaError_t launch_as(GemmArgs g, const char* name, cudaStream_t s) {
   auto kernel = linear_kernel<LAYOUT, EP, FP32, HELD, BN>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)((g.M + kTileM - 1) / kTileM) * ((g.N + BN - 1) / BN) * g.splits;
+  long long tiles = 0;
+  for (int i = 0; i < g.problems; ++i) {
+    const Problem& q = g.prob[i];
+    tiles += (long long)((q.M + kTileM - 1) / kTileM) * ((q.N + BN - 1) / BN) * q.splits;
+  }
   if (tiles == 0) return cudaSuccess;
   const long long pairs = sm_count() / 2;
   g.boxes = C::boxes(g), g.stages = C::stages(g);
@@ -785,14 +821,18 @@ cudaError_t launch_as(GemmArgs g, const char* name, cudaStream_t s) {
   return e;
 }
 
-// Sums over slabs have tiles of 256 columns only (their number fills the device);
-// forward and second order of 128 where their epilogues need the registers.
+// Gradients and slabs have tiles of 256 columns only (their number fills the device);
+// forward and second order of 128 where chains are held, whose sums lie behind them.
 template <int LAYOUT, int EP, bool FP32, bool HELD>
 cudaError_t launch_tile(int tile_n, const GemmArgs& g, const char* name, cudaStream_t s) {
-  if constexpr (!(EP == kSecondTerms || ((EP == kSecond || EP == kForward) && HELD))) {
-    if (tile_n == 256 || EP == kSlab) return launch_as<LAYOUT, EP, FP32, HELD, 256>(g, name, s);
+  constexpr bool GRADIENT = EP == kSlab || EP == kGradient;
+  if constexpr (GRADIENT || !(EP == kSecondTerms || HELD)) {
+    if (tile_n == 256) return launch_as<LAYOUT, EP, FP32, HELD, 256>(g, name, s);
   }
-  if constexpr (EP != kSlab) return launch_as<LAYOUT, EP, FP32, HELD, 128>(g, name, s);
+  if constexpr (!GRADIENT) {
+    if (tile_n == 128) return launch_as<LAYOUT, EP, FP32, HELD, 128>(g, name, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <int LAYOUT, int EP>
@@ -800,7 +840,7 @@ cudaError_t launch(int tile_n, const GemmArgs& g, const char* name, cudaStream_t
   if constexpr (EP != kSecond) {
     if (g.fp32) return launch_tile<LAYOUT, EP, true, true>(tile_n, g, name, s);
   }
-  if (g.chain) return launch_tile<LAYOUT, EP, false, true>(tile_n, g, name, s);
+  if (g.prob[0].chain || (g.problems > 1 && g.prob[1].chain)) return launch_tile<LAYOUT, EP, false, true>(tile_n, g, name, s);
   return launch_tile<LAYOUT, EP, false, false>(tile_n, g, name, s);
 }
 

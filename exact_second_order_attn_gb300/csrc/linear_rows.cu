@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kWarps * 32, TT >= 8 ? 2 : 3)
     const size_t at = (size_t)t * N + n;
     if (bias) v += (float)bias[n];
     if (z) store8<Kept<E>, false>(z + at, 1, &v);
-    act_values<sizeof(E) == 4, 1>(act, &v);
+    v = act_value<sizeof(E) == 4>(act, v);
     if (drop.on) {
       float m[8];
       drop.factors8((uint32_t)(n >> 3), (uint32_t)t, m);
