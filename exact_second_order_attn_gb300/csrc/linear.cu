@@ -40,9 +40,11 @@ constexpr size_t kSlabBytes = 512ull << 20;    // slabs of a product
 constexpr long long kLongTerms = 16384;        // bf16 sums above end their chains there
 
 // Times in cycles, estimated, decide between tile widths and numbers of slabs: a step
-// of a tile takes 575 (256 columns) or 400 (128: as much of A is loaded for half the
-// products), the hand-over of a tile 1,000; slabs cost a launch and a read of fp32.
-double tile_cost(long long steps, int nseg, int tile_n) { return (double)steps * nseg * (tile_n == 256 ? 575. : 400.) + 1000.; }
+// of a tile takes 575 (256 columns), 475 or 400 (192, 128: as much of A is loaded for
+// fewer products), the hand-over of a tile 1,000; slabs cost a launch and a read of fp32.
+double tile_cost(long long steps, int nseg, int tile_n) {
+  return (double)steps * nseg * (tile_n == 256 ? 575. : tile_n == 192 ? 475. : 400.) + 1000.;
+}
 double slab_cost(long long M, long long N, int s) { return s > 1 ? 3500. + 4. * (double)M * (double)N * s / 2500. : 0.; }
 long long tiles_of(long long M, long long N, int tile_n) { return ((M + kTileM - 1) / kTileM) * ((N + tile_n - 1) / tile_n); }
 bool slabs_fit(long long M, long long N, int s) { return (size_t)M * up(N, 8) * 4 * s <= kSlabBytes; }
@@ -59,7 +61,9 @@ Shape choose(long long M, long long N, int steps, int nseg, bool slabs, bool nar
   };
   Shape best{narrow_only ? 128 : 256, 1};
   double least = cost(best.tile_n, 1);
-  if (cost(128, 1) < least) best = Shape{128, 1}, least = cost(128, 1);
+  for (int tile : {192, 128}) {
+    if (!narrow_only && cost(tile, 1) < least) best = Shape{tile, 1}, least = cost(tile, 1);
+  }
   for (int s = 2; slabs && s <= 64 && s <= steps && slabs_fit(M, N, s); ++s) {
     if (cost(256, s) < least) best = Shape{256, s}, least = cost(256, s);
   }
@@ -222,11 +226,13 @@ __global__ void __launch_bounds__(256)
 // dz = m dy a'(z) as np bf16 planes [np][T][Np] (0: not wanted), and its column sums
 // per block of `rows_each` rows [parts][Np] (sums may be null).  A warp takes rows of
 // 256 columns, a lane eight of them; kDzRows rows are on their way at once, as they
-// came: with two, unpacked, the kernel waited for memory (180 us at 8192 x 11,008).
-constexpr int kDzRows = 4;
+// came: with two, unpacked, the kernel waited for memory (180 us at 8192 x 11,008,
+// 100 now).
+template <bool SLOPES>
+constexpr int kDzRows = SLOPES ? 4 : 8;
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256)
+template <typename T, bool VEC, bool SLOPES>
+__global__ void __launch_bounds__(256, SLOPES ? 2 : 3)
     dz_kernel(const T* dy, const Kept<T>* z, const __grid_constant__ DropArgs da, int act, int rows, int N, int Np, int rows_each, uint16_t* planes,
               int np, float* sums) {
   allow_next();
@@ -240,24 +246,24 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.f;
   if (c < Np) {
-    for (int ra = r0 + warp; ra < r1; ra += 8 * kDzRows) {
-      Raw8<T> g[kDzRows];
-      Raw8<Kept<T>> s[kDzRows];
+    for (int ra = r0 + warp; ra < r1; ra += 8 * kDzRows<SLOPES>) {
+      Raw8<T> g[kDzRows<SLOPES>];
+      Raw8<Kept<T>> s[SLOPES ? kDzRows<SLOPES> : 1];
 #pragma unroll
-      for (int u = 0; u < kDzRows; ++u) {
+      for (int u = 0; u < kDzRows<SLOPES>; ++u) {
         const int r = ra + 8 * u;
         if (r < r1) {
           g[u].template load<VEC>(dy + (size_t)r * N + c, N - c);
-          if (z) s[u].template load<VEC>(z + (size_t)r * N + c, N - c);
+          if constexpr (SLOPES) s[u].template load<VEC>(z + (size_t)r * N + c, N - c);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kDzRows; ++u) {
+      for (int u = 0; u < kDzRows<SLOPES>; ++u) {
         const int r = ra + 8 * u;
         if (r < r1) {
           float v[8];
           g[u].values(v);
-          if (z) {
+          if constexpr (SLOPES) {
             float a1[8];
             s[u].values(a1);
             act_slopes8<sizeof(T) == 4>(act, a1);
@@ -283,34 +289,10 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// out [N] = sum over the parts [parts][Np], in their order per way: 32 columns and 16
-// ways per block.
-template <typename T>
-__global__ void __launch_bounds__(512) columns_kernel(const float* sums, int parts, int N, int Np, T* out) {
-  allow_next();
-  wait_previous();
-  __shared__ float sh[16][32];
-  const int n = blockIdx.x * 32 + threadIdx.x;
-  float s = 0.f;
-  if (n < N) {
-    for (int i0 = threadIdx.y; i0 < parts; i0 += 16 * 8) {
-      float q[8];  // loads first: their latency would be paid one by one
-#pragma unroll
-      for (int u = 0; u < 8; ++u) q[u] = i0 + 16 * u < parts ? sums[(size_t)(i0 + 16 * u) * Np + n] : 0.f;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) s += q[u];
-    }
-  }
-  sh[threadIdx.y][threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.y != 0 || n >= N) return;
-  s = 0.f;
-  for (int w = 0; w < 16; ++w) s += sh[w][threadIdx.x];
-  out[n] = (T)s;
-}
-
-// out [rows][N] = the sum of the slabs [splits][rows][Np], of one or two outputs; the
-// forward's epilogue on the first with FWD.  One thread per 8 columns.
+// What is left when the products are done, in one launch: out [rows][N] = the sum of
+// the slabs [splits][rows][Np] of up to two outputs, one thread per 8 columns, with the
+// forward's epilogue (FWD); and column sums: col_out [N] = the sum over the parts
+// [parts][Np], 32 columns and 8 ways per block, each way and then the ways in order.
 struct SlabSum {
   const float* slab;
   void* out;
@@ -318,19 +300,46 @@ struct SlabSum {
   int splits, N, Np, vec;
   unsigned first;  // block
 };
-struct SlabSums {
+struct Finish {
   SlabSum o[2];
   int n;
+  unsigned col_first;  // the first block of column sums
+  const float* sums;
+  void* col_out;
+  int parts, col_N, col_Np;
   const void *bias, *r;
   void* z;
   int act;
   DropArgs drop;
 };
 
+template <typename T>
+__device__ __forceinline__ void sum_parts(const Finish& all) {
+  __shared__ float sh[8][32];
+  const int x = threadIdx.x & 31, way = threadIdx.x >> 5, n = (int)(blockIdx.x - all.col_first) * 32 + x;
+  float s = 0.f;
+  if (n < all.col_N) {
+    for (int i0 = way; i0 < all.parts; i0 += 8 * 16) {
+      float q[16];  // loads first: their latency would be paid one by one
+#pragma unroll
+      for (int u = 0; u < 16; ++u) q[u] = i0 + 8 * u < all.parts ? all.sums[(size_t)(i0 + 8 * u) * all.col_Np + n] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) s += q[u];
+    }
+  }
+  sh[way][x] = s;
+  __syncthreads();
+  if (way != 0 || n >= all.col_N) return;
+  s = 0.f;
+  for (int w = 0; w < 8; ++w) s += sh[w][x];
+  static_cast<T*>(all.col_out)[n] = (T)s;
+}
+
 template <typename T, bool FWD>
-__global__ void __launch_bounds__(256) slabs_kernel(const __grid_constant__ SlabSums all) {
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Finish all) {
   allow_next();
   wait_previous();
+  if (!FWD && blockIdx.x >= all.col_first) return sum_parts<T>(all);
   const SlabSum& o = all.o[all.n > 1 && blockIdx.x >= all.o[1].first];
   const int per = o.Np / 8;
   const long long i = (long long)(blockIdx.x - o.first) * blockDim.x + threadIdx.x, row = i / per;
@@ -495,12 +504,12 @@ struct Run {
     if (sh.splits > 1) {
       q.slab = at<float>(p.slab), q.slab_ld = p.Np;
       LIN_TRY(gemm_slabs(g, s));
-      SlabSums all;
+      Finish all;
       memset(&all, 0, sizeof(all));
       add_slabs(all, q, a.N, a.y);
       all.bias = a.b, all.r = a.r, all.z = a.z_out, all.act = a.act, all.drop = a.drop;
       all.o[0].vec = all.o[0].vec && mapped(a.r) && mapped(a.z_out);
-      return finish_slabs(all, true);
+      return finish(all, true);
     }
     EpArgs& e = g.ep;
     e.bias = a.b, e.in0 = a.r, e.out0 = a.y, e.out1 = a.z_out, e.in_ld = a.N, e.act = a.act, e.drop = a.drop;
@@ -514,19 +523,26 @@ struct Run {
   }
 
   // The output of a problem whose sums lie in slabs.
-  void add_slabs(SlabSums& all, const Problem& q, int N, void* out) const {
+  void add_slabs(Finish& all, const Problem& q, int N, void* out) const {
     const int Np = (int)up(N, 8);
     unsigned first = 0;
     if (all.n) first = all.o[0].first + (unsigned)((all.o[0].rows * (all.o[0].Np / 8) + 255) / 256);
     all.o[all.n++] = SlabSum{q.slab, out, q.M, q.splits, N, Np, N % 8 == 0 && aligned(out, 16), first};
   }
-  cudaError_t finish_slabs(const SlabSums& all, bool fwd) const {
-    if (all.n == 0) return cudaSuccess;
-    const SlabSum& last = all.o[all.n - 1];
-    const dim3 grid(last.first + (unsigned)((last.rows * (last.Np / 8) + 255) / 256)), block(256);
+  void add_columns(Finish& all, int parts, void* out) const {
+    all.sums = at<float>(p.sums), all.col_out = out, all.parts = parts, all.col_N = a.N, all.col_Np = p.Np;
+  }
+  cudaError_t finish(Finish& all, bool fwd) const {
+    unsigned blocks = 0;
+    for (int i = 0; i < all.n; ++i) blocks = all.o[i].first + (unsigned)((all.o[i].rows * (all.o[i].Np / 8) + 255) / 256);
+    all.col_first = blocks;
+    if (all.col_out) blocks += (unsigned)((all.col_N + 31) / 32);
+    if (blocks == 0) return cudaSuccess;
+    const dim3 grid(blocks), block(256);
     if (a.bf16)
-      return run("linear_slabs", fwd ? slabs_kernel<__nv_bfloat16, true> : slabs_kernel<__nv_bfloat16, false>, grid, block, all);
-    return run("linear_slabs", fwd ? slabs_kernel<float, true> : slabs_kernel<float, false>, grid, block, all);
+      return run("linear_finish", fwd ? finish_kernel<__nv_bfloat16, true> : finish_kernel<__nv_bfloat16, false>, grid,
+                 block, all);
+    return run("linear_finish", fwd ? finish_kernel<float, true> : finish_kernel<float, false>, grid, block, all);
   }
 
   // dz and its column sums out of dy and z.
@@ -538,18 +554,12 @@ struct Run {
   cudaError_t make_dz_as(bool planes, bool sums) const {
     const Kept<E>* z = a.act == kActNone ? nullptr : static_cast<const Kept<E>*>(a.z);
     const bool vec = a.N % 8 == 0 && aligned(a.dy, 16) && mapped(z);
-    return run("linear_dz", vec ? dz_kernel<E, true> : dz_kernel<E, false>, dim3((p.Np + 255) / 256, p.sum_parts),
+    auto kernel = z ? (vec ? dz_kernel<E, true, true> : dz_kernel<E, false, true>)
+                    : (vec ? dz_kernel<E, true, false> : dz_kernel<E, false, false>);
+    return run("linear_dz", kernel, dim3((p.Np + 255) / 256, p.sum_parts),
                dim3(256), static_cast<const E*>(a.dy), z, a.drop, a.act, a.T, a.N, p.Np, p.sum_rows,
                at<uint16_t>(p.dz), planes ? p.zp : 0, sums ? at<float>(p.sums) : nullptr);
   }
-  cudaError_t columns(int parts, void* out) const {
-    const dim3 grid((a.N + 31) / 32), block(32, 16);
-    return a.bf16 ? run("linear_columns", columns_kernel<__nv_bfloat16>, grid, block, at<float>(p.sums), parts, a.N,
-                        p.Np, static_cast<__nv_bfloat16*>(out))
-                  : run("linear_columns", columns_kernel<float>, grid, block, at<float>(p.sums), parts, a.N, p.Np,
-                        static_cast<float*>(out));
-  }
-
   // dx [T, K] = q W + dz uW, or (dw) dW [N, K] = q^T x + dz^T ux; either term may be
   // absent (the backward's has dz with the first operand).
   bool gradient(Problem& g, bool dw, int splits, void* out, const void* u, size_t u_off, const void* v,
@@ -573,18 +583,16 @@ struct Run {
     return !g.out_map || store_map(&g.out, out, g.M, a.K, a.K);
   }
   // Both gradients in one launch: u_x, v_x are multiplied by q and dz for dx, u_w, v_w
-  // for dW.
-  cudaError_t gradients(const void* u_x, const void* v_x, size_t v_x_off, const void* u_w, const void* v_w,
+  // for dW; then what is left, the column sums of `all` among it.
+  cudaError_t gradients(Finish& all, const void* u_x, const void* v_x, size_t v_x_off, const void* u_w, const void* v_w,
                         size_t v_w_off) const {
     GemmArgs g;
     base(g);
     const bool want[2] = {a.dx && (u_x || v_x), a.dW && (u_w || v_w)};
     if (a.dx && !want[0]) LIN_TRY(cudaMemsetAsync(a.dx, 0, (size_t)a.T * a.K * element(), s));
     if (a.dW && !want[1]) LIN_TRY(cudaMemsetAsync(a.dW, 0, (size_t)a.N * a.K * element(), s));
-    if (!want[0] && !want[1]) return cudaSuccess;
+    if (!want[0] && !want[1]) return finish(all, false);
     const Splits& n = want[0] && want[1] ? p.both : want[0] ? p.dx : p.dw;
-    SlabSums all;
-    memset(&all, 0, sizeof(all));
     size_t slab = p.slab;
     // (the order of the slabs in the workspace; the longer tiles' problem is the first of the launch)
     const bool dw_first = want[1] && (!want[0] || steps_of(a.T) / n.s[1] >= steps_of(a.N) / n.s[0]);
@@ -602,14 +610,16 @@ struct Run {
       }
     }
     LIN_TRY(gemm_gradients(g, s));
-    return finish_slabs(all, false);
+    return finish(all, false);
   }
 
   cudaError_t backward() const {
     LIN_TRY(operands(a.dW ? a.x : nullptr, a.dx ? a.W : nullptr, nullptr, nullptr));
     LIN_TRY(make_dz(p.own_dz && (a.dx || a.dW), a.db != nullptr));
-    if (a.db) LIN_TRY(columns(p.sum_parts, a.db));
-    return gradients(nullptr, a.dx ? a.W : nullptr, p.W, nullptr, a.dW ? a.x : nullptr, p.x);
+    Finish all;
+    memset(&all, 0, sizeof(all));
+    if (a.db) add_columns(all, p.sum_parts, a.db);
+    return gradients(all, nullptr, a.dx ? a.W : nullptr, p.W, nullptr, a.dW ? a.x : nullptr, p.x);
   }
 
   // dx, dW, db here are gx, gW, gb.
@@ -617,6 +627,8 @@ struct Run {
     const bool want_q = p.curved && (a.dx || a.dW || a.db);
     const bool want_dz = (a.dx && a.uW) || (a.dW && a.ux);
     const bool product = a.gdy || want_q;
+    Finish all;
+    memset(&all, 0, sizeof(all));
     LIN_TRY(operands((product && a.uW) || (want_q && a.dW) ? a.x : nullptr,
                      (product && a.ux) || (want_q && a.dx) ? a.W : nullptr, a.ux, a.uW));
     if (product) {
@@ -653,13 +665,13 @@ struct Run {
       if ((e.q_planes && !z_stores(g.out + 2, true)) || (e.dz_planes && !z_stores(g.out + 2 + kPlanes, false)))
         return cudaErrorInvalidValue;
       LIN_TRY(gemm_second(p.sec.tile_n, g, s));
-      if (e.sums) LIN_TRY(columns((a.T + 31) / 32, a.db));
+      if (e.sums) add_columns(all, (a.T + 31) / 32, a.db);
     } else if (want_dz && p.own_dz) {
       LIN_TRY(make_dz(true, false));
     }
     if (a.db && !p.curved) LIN_TRY(cudaMemsetAsync(a.db, 0, a.N * element(), s));
     const bool q = p.curved;
-    return gradients(q ? a.W : nullptr, a.uW, p.uW, q ? a.x : nullptr, a.ux, p.ux);
+    return gradients(all, q ? a.W : nullptr, a.uW, p.uW, q ? a.x : nullptr, a.ux, p.ux);
   }
 };
 

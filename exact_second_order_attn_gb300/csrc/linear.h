@@ -77,7 +77,7 @@ struct GemmArgs {
 };
 
 // C = sum over segments of A_seg B_seg^T, then the epilogue; tiles of kTileM x
-// tile_n (128 or 256).  Splits are at most the steps of K.
+// tile_n (128, 192 or 256).  Splits are at most the steps of K.
 cudaError_t gemm_forward(int tile_n, const GemmArgs& g, cudaStream_t s);  // kNT, kForward
 cudaError_t gemm_second(int tile_n, const GemmArgs& g, cudaStream_t s);   // kNT, kSecond or kSecondTerms
 cudaError_t gemm_slabs(const GemmArgs& g, cudaStream_t s);                // kNT, kSlab

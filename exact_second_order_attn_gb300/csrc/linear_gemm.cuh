@@ -14,7 +14,7 @@
 // columns and the epilogue threads add the chains up in registers (HELD); so do sums
 // of bf16 operands over more than 16,384 terms, every 16,384 (3e-5 of the result).
 //
-// Roles of a block's warps: the first eight or sixteen epilogue (thread = accumulator
+// Roles of a block's warps: the first eight, twelve or sixteen epilogue (thread = accumulator
 // row, the warpgroups take equal parts of the columns), then the TMA producer of A, MMA
 // issue (the leader block's) with TMEM allocation, and the producer of B.  Sixteen where
 // the epilogue computes (forward, second order): with eight, two per scheduler, it
@@ -69,7 +69,8 @@ struct Cfg {
   static constexpr int B_BYTES = BN / 2 * kBK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int NIN = EP == kForward ? 1 : kIsSecond<EP> ? 2 : 0;
-  static constexpr int WARPS = EP == kForward || EP == kSecond ? 16 : 8;  // of the epilogue
+  // of the epilogue; 64 columns a thread of tiles of 256 and 192
+  static constexpr int WARPS = EP == kForward || EP == kSecond ? (BN == 192 ? 12 : 16) : 8;
   static constexpr int THREADS = 32 * (WARPS + 3);
   static constexpr int H = BN / (WARPS / 4);  // columns of an epilogue thread
   static_assert(kRoom + 2048 <= 232448, "shared memory budget");
@@ -828,6 +829,9 @@ cudaError_t launch_tile(int tile_n, const GemmArgs& g, const char* name, cudaStr
   constexpr bool GRADIENT = EP == kSlab || EP == kGradient;
   if constexpr (GRADIENT || !(EP == kSecondTerms || HELD)) {
     if (tile_n == 256) return launch_as<LAYOUT, EP, FP32, HELD, 256>(g, name, s);
+  }
+  if constexpr (!GRADIENT && !(EP == kSecondTerms || HELD)) {
+    if (tile_n == 192) return launch_as<LAYOUT, EP, FP32, HELD, 192>(g, name, s);
   }
   if constexpr (!GRADIENT) {
     if (tile_n == 128) return launch_as<LAYOUT, EP, FP32, HELD, 128>(g, name, s);
