@@ -474,13 +474,15 @@ struct Run {
   }
 
   // The products of na terms of A operand x and the terms of B operand y (0 or 1
-  // each): of fp32 those that reach 2^-16 of the first; smallest first.
-  void products(Problem& g, int x, int y, int na) const {
+  // each), smallest first: of fp32 those that reach 2^-16 of the first, which share
+  // a stage unless `apart`.
+  void products(Problem& g, int x, int y, int na, bool apart = false) const {
     auto add = [&](int i, int j) { g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + i), (uint8_t)(kPlanes * y + j)}; };
     if (a.bf16) {
       for (int i = na - 1; i >= 0; --i) add(i, 0);
       return;
     }
+    if (!apart) return add(0, 0);
     for (int order = kPlanes - 1; order >= 0; --order) {
       for (int i = order; i >= 0; --i) add(i, order - i);
     }
@@ -640,12 +642,12 @@ struct Run {
       const int box = p.sec.tile_n / 2;
       if (a.ux) {
         if (!maps(t.a, a.ux, p.ux, a.T, 128) || !maps(t.b, a.W, p.W, a.N, box)) return cudaErrorInvalidValue;
-        products(t, 0, 0, 1);
+        products(t, 0, 0, 1, true);
       }
       if (a.uW) {
         if (!maps(t.a + kPlanes, a.x, p.x, a.T, 128) || !maps(t.b + kPlanes, a.uW, p.uW, a.N, box))
           return cudaErrorInvalidValue;
-        products(t, 1, 1, 1);
+        products(t, 1, 1, 1, true);
       }
       chains(t);
       EpArgs& e = g.ep;

@@ -9,7 +9,8 @@
 // of the next.
 //
 // fp32 operands are three bf16 terms each, and the six products of terms that reach
-// 2^-16 of the first are summed, smallest first.  The tensor cores drop the bits of
+// 2^-16 of the first are summed, smallest first, out of one stage that holds all terms
+// (a stage for each product would load twice the bytes, at 12 TB/s what bound it).  The tensor cores drop the bits of
 // a step's sum below the accumulator's last one, so there a chain ends after 128
 // columns and the epilogue threads add the chains up in registers (HELD); so do sums
 // of bf16 operands over more than 16,384 terms, every 16,384 (3e-5 of the result).
@@ -61,13 +62,17 @@ constexpr int kRoom = 229376;   // bytes of stages and boxes
 template <int EP>
 constexpr bool kIsSecond = EP == kSecond || EP == kSecondTerms;
 
-template <int LAYOUT, int EP, bool HELD, int BN_>
+template <int LAYOUT, int EP, bool FP32, bool HELD, int BN_>
 struct Cfg {
   static constexpr int BN = BN_;
   static constexpr bool B_MN = LAYOUT == kGradients;
   static constexpr int A_BYTES = 128 * kBK * 2;
   static constexpr int B_BYTES = BN / 2 * kBK * 2;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
+  // fp32: a stage holds all terms of both operands for the six products; the second
+  // order's boxes leave no room for two of those.
+  static constexpr bool TERMS = FP32 && EP != kSecondTerms;
+  static constexpr int STAGE = (A_BYTES + B_BYTES) * (TERMS ? kPlanes : 1);  // [A.. | B..]
+  static constexpr int B_OFF = A_BYTES * (TERMS ? kPlanes : 1);
   static constexpr int NIN = EP == kForward ? 1 : kIsSecond<EP> ? 2 : 0;
   // of the epilogue; 64 columns a thread of tiles of 256 and 192
   static constexpr int WARPS = EP == kForward || EP == kSecond ? (BN == 192 ? 12 : 16) : 8;
@@ -77,8 +82,8 @@ struct Cfg {
   // Boxes of a warp: of y and its residual, and z; of z and q, dy and dz, gdy, then the
   // further terms of q and dz in turn; of two results.
   static int boxes(const GemmArgs& g) {
-    if (EP == kForward) return g.fp32 ? 0 : 1 + (g.ep.out1 != nullptr);
-    return EP == kSecond ? 3 : EP == kSecondTerms ? (g.fp32 ? 7 : 5) : EP == kGradient ? 2 : 0;
+    if (EP == kForward) return FP32 ? 0 : 1 + (g.ep.out1 != nullptr);
+    return EP == kSecond ? 3 : EP == kSecondTerms ? (FP32 ? 7 : 5) : EP == kGradient && !FP32 ? 2 : 0;
   }
   static int stages(const GemmArgs& g) {
     const int n = (kRoom - WARPS * boxes(g) * kBoxBytes) / STAGE;
@@ -549,9 +554,9 @@ struct Place {
 };
 
 template <int LAYOUT, int EP, bool FP32, bool HELD, int BN>
-__global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<LAYOUT, EP, FP32, HELD, BN>::THREADS, 1)
     linear_kernel(const __grid_constant__ GemmArgs p) {
-  using C = Cfg<LAYOUT, EP, HELD, BN>;
+  using C = Cfg<LAYOUT, EP, FP32, HELD, BN>;
   constexpr int H = C::H, CHUNKS = H / 32, EW = C::WARPS;
   constexpr bool ELEMENTWISE = EP == kForward || kIsSecond<EP>;
   static_assert(!(HELD && ELEMENTWISE) || BN == 128, "chains' sums lie behind the accumulators of 128 columns");
@@ -620,20 +625,24 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
               if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.empty[st], at.pass ^ 1, wt)))) break;
               if (p.stall && issued == 0) continue;  // test hook: nothing fills the first stage
               const uint32_t bar = full0 + 8 * st;
-              const uint32_t da = sm0 + st * C::STAGE, db = da + C::A_BYTES;
-              if (is_a) {
-                if (rank == 0) mbar_expect_tx_w(&ctrl.full[st], 2 * C::STAGE);
-                if (a_mn) {
-                  tma_load_2d_pair(da, ma, bar, row, k * kBK);
-                  tma_load_2d_pair(da + 8192, ma, bar, row + 64, k * kBK);
+              if (is_a && rank == 0) mbar_expect_tx_w(&ctrl.full[st], 2 * C::STAGE);
+#pragma unroll
+              for (int i = 0; i < (C::TERMS ? kPlanes : 1); ++i) {
+                const uint32_t da = sm0 + st * C::STAGE + i * C::A_BYTES;
+                const uint32_t db = sm0 + st * C::STAGE + C::B_OFF + i * C::B_BYTES;
+                if (is_a) {
+                  if (a_mn) {
+                    tma_load_2d_pair(da, ma + i, bar, row, k * kBK);
+                    tma_load_2d_pair(da + 8192, ma + i, bar, row + 64, k * kBK);
+                  } else {
+                    tma_load_2d_pair(da, ma + i, bar, k * kBK, row);
+                  }
+                } else if (C::B_MN) {
+                  tma_load_2d_pair(db, mb + i, bar, col, k * kBK);
+                  if (BN == 256) tma_load_2d_pair(db + 8192, mb + i, bar, col + 64, k * kBK);
                 } else {
-                  tma_load_2d_pair(da, ma, bar, k * kBK, row);
+                  tma_load_2d_pair(db, mb + i, bar, k * kBK, col);
                 }
-              } else if (C::B_MN) {
-                tma_load_2d_pair(db, mb, bar, col, k * kBK);
-                if (BN == 256) tma_load_2d_pair(db + 8192, mb, bar, col + 64, k * kBK);
-              } else {
-                tma_load_2d_pair(db, mb, bar, k * kBK, col);
               }
             }
           }
@@ -679,10 +688,25 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
               tc_fence_after();
               const uint32_t more = s > 0 || k > kc;  // the accumulator holds a product already
               const uint32_t a = desc_lo(sm0 + st * C::STAGE, lbo_a);
-              const uint32_t b = desc_lo(sm0 + st * C::STAGE + C::A_BYTES, lbo_b);
+              const uint32_t b = desc_lo(sm0 + st * C::STAGE + C::B_OFF, lbo_b);
+              if constexpr (C::TERMS) {
+                // the products of terms that reach 2^-16 of the first, smallest first
 #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk)
-                mma_ss_pair(d, a + kk * step_a, b + kk * step_b, id, kk > 0 ? 1u : more);
+                for (int order = kPlanes - 1; order >= 0; --order) {
+#pragma unroll
+                  for (int i = order; i >= 0; --i) {
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                      mma_ss_pair(d, a + i * (C::A_BYTES >> 4) + kk * step_a,
+                                  b + (order - i) * (C::B_BYTES >> 4) + kk * step_b, id,
+                                  kk > 0 || i < kPlanes - 1 ? 1u : more);
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk)
+                  mma_ss_pair(d, a + kk * step_a, b + kk * step_b, id, kk > 0 ? 1u : more);
+              }
               mma_commit_pair(&ctrl.empty[st]);
             }
           }
@@ -804,7 +828,7 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, HELD, BN>::THREADS, 1)
 
 template <int LAYOUT, int EP, bool FP32, bool HELD, int BN>
 cudaError_t launch_as(GemmArgs g, const char* name, cudaStream_t s) {
-  using C = Cfg<LAYOUT, EP, HELD, BN>;
+  using C = Cfg<LAYOUT, EP, FP32, HELD, BN>;
   auto kernel = linear_kernel<LAYOUT, EP, FP32, HELD, BN>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
   if (e != cudaSuccess) return e;
