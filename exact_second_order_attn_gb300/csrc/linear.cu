@@ -443,11 +443,26 @@ struct Run {
   static void sizes(Problem& q, long long M, long long N, long long K, int splits) {
     q.M = (int)M, q.N = (int)N, q.K = (int)K, q.splits = splits;
   }
-  // Chains of fp32 operands are 128 columns of each plane product; long sums of bf16
-  // ones end theirs every 16,384 terms.
+  // fp32's products of each segment in stages of their own (the second order's boxes
+  // leave no room for all terms): those that reach 2^-16 of the first, smallest first
+  // among all segments.
+  static void apart(Problem& q) {
+    const Seg from[2] = {q.seg[0], q.seg[1]};
+    const int n = q.nseg;
+    q.nseg = 0;
+    for (int order = kPlanes - 1; order >= 0; --order) {
+      for (int k = 0; k < n; ++k) {
+        for (int i = order; i >= 0; --i)
+          q.seg[q.nseg++] = Seg{(uint8_t)(from[k].a + i), (uint8_t)(from[k].b + order - i)};
+      }
+    }
+  }
+  // Chains of fp32 operands are a stage, so that its small products come before the
+  // large ones (chains of two stages: errors of 7e-7 in place of 1.5e-7), or 128 columns
+  // of products that are apart; long sums of bf16 ones end theirs every 16,384 terms.
   void chains(Problem& q) const {
     const long long terms = ((long long)q.K + q.splits - 1) / q.splits * q.nseg;
-    q.chain = !a.bf16 ? 2 : terms > kLongTerms ? (int)(kLongTerms / kBK / q.nseg) : 0;
+    q.chain = !a.bf16 ? (q.nseg > 2 ? 2 : 1) : terms > kLongTerms ? (int)(kLongTerms / kBK / q.nseg) : 0;
   }
 
   // Maps of the planes of a [rows][K] operand, boxes of `box` rows x 64 columns.
@@ -474,18 +489,14 @@ struct Run {
   }
 
   // The products of na terms of A operand x and the terms of B operand y (0 or 1
-  // each), smallest first: of fp32 those that reach 2^-16 of the first, which share
-  // a stage unless `apart`.
-  void products(Problem& g, int x, int y, int na, bool apart = false) const {
+  // each), smallest first; fp32's six share a stage.
+  void products(Problem& g, int x, int y, int na) const {
     auto add = [&](int i, int j) { g.seg[g.nseg++] = Seg{(uint8_t)(kPlanes * x + i), (uint8_t)(kPlanes * y + j)}; };
     if (a.bf16) {
       for (int i = na - 1; i >= 0; --i) add(i, 0);
       return;
     }
-    if (!apart) return add(0, 0);
-    for (int order = kPlanes - 1; order >= 0; --order) {
-      for (int i = order; i >= 0; --i) add(i, order - i);
-    }
+    add(0, 0);
   }
 
   bool mapped(const void* t) const { return !t || aligned(t, 16); }
@@ -642,13 +653,14 @@ struct Run {
       const int box = p.sec.tile_n / 2;
       if (a.ux) {
         if (!maps(t.a, a.ux, p.ux, a.T, 128) || !maps(t.b, a.W, p.W, a.N, box)) return cudaErrorInvalidValue;
-        products(t, 0, 0, 1, true);
+        products(t, 0, 0, 1);
       }
       if (a.uW) {
         if (!maps(t.a + kPlanes, a.x, p.x, a.T, 128) || !maps(t.b + kPlanes, a.uW, p.uW, a.N, box))
           return cudaErrorInvalidValue;
-        products(t, 1, 1, 1, true);
+        products(t, 1, 1, 1);
       }
+      if (!a.bf16) apart(t);
       chains(t);
       EpArgs& e = g.ep;
       e.bias = a.ub, e.act = a.act, e.drop = a.drop, e.in_ld = a.N, e.ld = p.Np;

@@ -11,7 +11,7 @@
 // fp32 operands are three bf16 terms each, and the six products of terms that reach
 // 2^-16 of the first are summed, smallest first, out of one stage that holds all terms
 // (a stage for each product would load twice the bytes, at 12 TB/s what bound it).  The tensor cores drop the bits of
-// a step's sum below the accumulator's last one, so there a chain ends after 128
+// a step's sum below the accumulator's last one, so there a chain ends after 64 or 128
 // columns and the epilogue threads add the chains up in registers (HELD); so do sums
 // of bf16 operands over more than 16,384 terms, every 16,384 (3e-5 of the result).
 //
@@ -675,18 +675,23 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, FP32, HELD, BN>::THREADS, 1)
         const bool a_mn = LAYOUT == kGradients && q.a_mn;
         const uint32_t id = a_mn ? idesc_bf16(kTileM, BN, true, C::B_MN) : idesc_bf16(kTileM, BN, false, C::B_MN);
         const uint32_t lbo_a = a_mn ? 8192 : 16, step_a = a_mn ? 2048 >> 4 : 32 >> 4;
-        for (int kc = tile.k0; ok && kc < tile.k1; kc = tile.template end<HELD>(kc), ++chain) {
-          const int ke = tile.template end<HELD>(kc), buf = chain & 1;
-          ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_empty[buf], ((chain >> 1) & 1) ^ 1, wt));
-          tc_fence_after();
-          const uint32_t d = tb + buf * kBufCols;
+        for (int kc = tile.k0; ok && kc < tile.k1; kc = tile.template end<HELD>(kc)) {
+          const int ke = tile.template end<HELD>(kc);
+          uint32_t d = 0;
+          auto open = [&]() {  // the chain's accumulator is free
+            ok = __all_sync(0xffffffffu, wait_cluster(&ctrl.tile_empty[chain & 1], ((chain >> 1) & 1) ^ 1, wt));
+            tc_fence_after();
+            d = tb + (chain & 1) * kBufCols;
+          };
+          if (!C::TERMS) open();
           for (int s = 0; ok && s < q.nseg; ++s) {
-            for (int k = kc; k < ke; ++k, at.next()) {
+            if (C::TERMS) open();  // (a chain is one step of one segment)
+            for (int k = kc; ok && k < ke; ++k, at.next()) {
               const int st = at.s;
               ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.full[st], at.pass, wt));
               if (!ok) break;
               tc_fence_after();
-              const uint32_t more = s > 0 || k > kc;  // the accumulator holds a product already
+              const uint32_t more = (!C::TERMS && s > 0) || k > kc;  // the accumulator holds a product already
               const uint32_t a = desc_lo(sm0 + st * C::STAGE, lbo_a);
               const uint32_t b = desc_lo(sm0 + st * C::STAGE + C::B_OFF, lbo_b);
               if constexpr (C::TERMS) {
@@ -709,8 +714,9 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, FP32, HELD, BN>::THREADS, 1)
               }
               mma_commit_pair(&ctrl.empty[st]);
             }
+            if (C::TERMS) mma_commit_pair(&ctrl.tile_full[chain & 1]), ++chain;
           }
-          mma_commit_pair(&ctrl.tile_full[buf]);
+          if (!C::TERMS) mma_commit_pair(&ctrl.tile_full[chain & 1]), ++chain;
         }
       }
       mma_commit_pair(&ctrl.drain);  // the last MMA has read its operands
@@ -752,7 +758,9 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, FP32, HELD, BN>::THREADS, 1)
       if constexpr (HELD) {
 #pragma unroll
         for (int j = 0; j < H; ++j) sum[j] = 0.f;
-        for (int kc = tile.k0; kc < tile.k1; kc = tile.template end<HELD>(kc), ++chain) {
+        int chains = 0;
+        for (int kc = tile.k0; kc < tile.k1; kc = tile.template end<HELD>(kc)) chains += C::TERMS ? q.nseg : 1;
+        for (int i = 0; i < chains; ++i, ++chain) {
           buf = chain & 1;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl.tile_full[buf], (chain >> 1) & 1, wt)))) break;
           tc_fence_after();
