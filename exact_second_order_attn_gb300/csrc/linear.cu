@@ -233,8 +233,8 @@ constexpr int kDzRows = SLOPES ? 4 : 8;
 
 template <typename T, bool VEC, bool SLOPES>
 __global__ void __launch_bounds__(256, SLOPES ? 2 : 3)
-    dz_kernel(const T* dy, const Kept<T>* z, const __grid_constant__ DropArgs da, int act, int rows, int N, int Np, int rows_each, uint16_t* planes,
-              int np, float* sums) {
+    dz_kernel(const T* dy, const Kept<T>* z, const __grid_constant__ DropArgs da, int act, int rows, int N, int Np,
+              int rows_each, uint16_t* planes, int np, float* sums) {
   allow_next();
   wait_previous();
   __shared__ float part[8][256];
@@ -323,8 +323,10 @@ __device__ __forceinline__ void sum_parts(const Finish& all) {
       float q[16];  // loads first: their latency would be paid one by one
 #pragma unroll
       for (int u = 0; u < 16; ++u) q[u] = i0 + 8 * u < all.parts ? all.sums[(size_t)(i0 + 8 * u) * all.col_Np + n] : 0.f;
+      float t = 0.f;
 #pragma unroll
-      for (int u = 0; u < 16; ++u) s += q[u];
+      for (int u = 0; u < 16; ++u) t += q[u];
+      s += t;
     }
   }
   sh[way][x] = s;

@@ -211,6 +211,20 @@ def test_nothing_is_written_past_the_outputs(T, K, N, dtype):
             assert (flat[k][-64:] == 9.0).all() and (flat[k][:shift] == 9.0).all(), k
 
 
+@pytest.mark.parametrize("odd", ["dx", "dW"])
+def test_one_gradient_off_its_bound(odd):
+    """Results of one launch that leave by bulk stores and row by row."""
+    T, K, N = 4000, 264, 520
+    t = make(T, K, N, "bf16", seed=18)
+    ref = chain(t, "gelu")
+    flat = torch.empty(max(T, N) * K + 1, dtype=torch.bfloat16, device="cuda")
+    out = {"dx": None, "dW": None, odd: flat[1:(T if odd == "dx" else N) * K + 1].view(-1, K)}
+    for _ in range(5):
+        flat.fill_(9.0)
+        dx, dW, _ = fb.fbob_linear_bwd(t["x"], t["W"], ref["z"], t["dy"], "gelu", dx=out["dx"], dW=out["dW"])
+        assert torch.equal(dx, ref["dx"]) and torch.equal(dW, ref["dW"])
+
+
 def test_leading_dimensions_and_no_tokens():
     t = make(24, 40, 56, "bf16", seed=12)
     y, z = fb.fbob_linear_fwd(t["x"], t["W"], t["b"], t["r"], "gelu")
