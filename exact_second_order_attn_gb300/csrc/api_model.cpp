@@ -267,8 +267,8 @@ fbob_status linear_run(const fbob::LinearArgs& a, fbob::LinearPass pass, size_t 
                        cudaStream_t stream) {
   fbob_status st = check_workspace(a.ws, have, fbob::linear_workspace(a, pass));
   if (st != FBOB_OK) return st;
-  fbob::DevCtx c;
-  if ((st = fbob::make_ctx(&c)) != FBOB_OK) return st;
+  fbob::DevCtx c = {};
+  if (!fbob::linear_is_plain(a, pass) && (st = fbob::make_ctx(&c)) != FBOB_OK) return st;
   const cudaError_t e = fbob::linear(a, pass, c, stream);
   if (e != cudaSuccess) return cuda_fail(e, where);
   return FBOB_OK;

@@ -152,6 +152,7 @@ cudaError_t linear_ce(const CeArgs& a, CePass pass, const DevCtx& c, cudaStream_
 // dropout.cu, linear.cu
 cudaError_t dropout(const DropoutArgs& a, cudaStream_t s);
 size_t linear_workspace(const LinearArgs& a, LinearPass pass);
+bool linear_is_plain(const LinearArgs& a, LinearPass pass);  // no kernel that waits: the context is not used
 cudaError_t linear(const LinearArgs& a, LinearPass pass, const DevCtx& c, cudaStream_t s);
 
 // bob_static.cu: the fixed (alpha, E) workspace of fbob_attn_bob_noalloc.

@@ -505,7 +505,6 @@ struct Run {
 
   // y and z from x and W.
   cudaError_t forward() const {
-    if (a.T <= kRowsTokens) return rows(a, s);
     LIN_TRY(operands(a.x, a.W, nullptr, nullptr));
     GemmArgs g;
     base(g);
@@ -694,13 +693,18 @@ struct Run {
 }  // namespace
 }  // namespace lin
 
+bool linear_is_plain(const LinearArgs& a, LinearPass pass) {
+  return pass == LinearPass::kFwd && a.T <= lin::kRowsTokens;
+}
+
 size_t linear_workspace(const LinearArgs& a, LinearPass pass) {
-  if (pass == LinearPass::kFwd && a.T <= lin::kRowsTokens) return 0;
+  if (linear_is_plain(a, pass)) return 0;
   const size_t n = lin::plan(a, pass).bytes;
   return n ? n + ce::kWorkspaceSlack : 0;
 }
 
 cudaError_t linear(const LinearArgs& a, LinearPass pass, const DevCtx& c, cudaStream_t s) {
+  if (linear_is_plain(a, pass)) return lin::rows(a, s);
   const lin::Run r{a, c, s, lin::plan(a, pass), static_cast<char*>(ce::workspace_base(a.ws))};
   switch (pass) {
     case LinearPass::kFwd: return r.forward();

@@ -1,40 +1,48 @@
 // The matrix products of linear layers on the fifth generation tensor cores, with
 // the layer's elementwise work in the epilogue.
 //
-// One or two problems in a launch (dx and dW read the same dz and share their waves),
-// C[256 x BN] = sum over segments of A_seg B_seg^T per pair of thread blocks
-// (cta_group::2): each block holds its 128 rows of A and its half of B's rows of
-// every 64-column stage; the accumulator's 128 rows x BN columns lie in the block's
-// tensor memory, two of them, so the epilogue of one tile runs under the products
-// of the next.
+// One or two problems in a launch (dx and dW read the same dz and share their waves:
+// 768 -> 2304, 8192 tokens, 52 us in two launches, 39 in one).  C[256 x BN] = sum over
+// segments of A_seg B_seg^T per pair of thread blocks (cta_group::2): each block holds
+// its 128 rows of A and its half of B's rows of every 64-column stage; the
+// accumulator's 128 rows x BN columns lie in the block's tensor memory, two of them, so
+// the epilogue of one tile runs under the products of the next.
 //
 // fp32 operands are three bf16 terms each, and the six products of terms that reach
 // 2^-16 of the first are summed, smallest first, out of one stage that holds all terms
-// (a stage for each product would load twice the bytes, at 12 TB/s what bound it).  The tensor cores drop the bits of
-// a step's sum below the accumulator's last one, so there a chain ends after 64 or 128
-// columns and the epilogue threads add the chains up in registers (HELD); so do sums
-// of bf16 operands over more than 16,384 terms, every 16,384 (3e-5 of the result).
+// (a stage for each product would load twice the bytes, at 12 TB/s what bound it).  The
+// tensor cores drop the bits of a step's sum below the accumulator's last one, so there
+// a chain ends after 64 or 128 columns and the epilogue threads add the chains up in
+// registers (HELD); so do sums of bf16 operands over more than 16,384 terms, every
+// 16,384 (3e-5 of the result).
 //
-// Roles of a block's warps: the first eight, twelve or sixteen epilogue (thread = accumulator
-// row, the warpgroups take equal parts of the columns), then the TMA producer of A, MMA
-// issue (the leader block's) with TMEM allocation, and the producer of B.  Sixteen where
-// the epilogue computes (forward, second order): with eight, two per scheduler, it
-// waited for its own results (30 % issue; gelu_tanh, 8192 x 2048 from 768 columns 44 us,
-// its second order 90 us).  Barriers: full[s] of the
+// Roles of a block's warps: the first eight, twelve or sixteen epilogue (thread =
+// accumulator row, the warpgroups take equal parts of the columns), then the TMA
+// producer of A, MMA issue (the leader block's) with TMEM allocation, and the producer
+// of B.  Sixteen (twelve for 192 columns) where the epilogue computes: with eight, two
+// per scheduler, it waited for its own results (30 % issue; gelu_tanh, 8192 x 2048 from
+// 768 columns 44 us, its second order 90 us; 26 and 70 now).  Barriers: full[s] of the
 // leader counts both blocks' bytes; empty[s] and tile_full[b] are signalled in both
 // blocks by the MMAs' commit; tile_empty[b] of the leader counts the epilogue warps of
-// the pair.  Every wait is bounded.  Blocks are persistent: pair i takes
-// tiles i, i + pairs, ...
+// the pair.  Every wait is bounded.  Blocks are persistent: pair i takes tiles i, i +
+// pairs, ...
 //
-// What the epilogue reads beside the accumulator (the residual; z and dy of the
-// second order) comes in boxes of a warp's 32 rows x 32 columns: bulk tensor loads
-// ahead of their use, which run under the products of the tile that the warp waits
-// for; results leave in such boxes too (y from its residual's, q and dz from z's and
-// dy's).  A row per lane, straight from registers,
-// would cost the load-store unit 32 lines per instruction.  bf16 matrices whose rows
-// are no multiples of 16 bytes move through the same boxes, a row per step of the
-// warp.  The elementwise work goes by eight columns, 16 bytes of each box and one
-// call of dropout's generator, so that little of it is live at a time.
+// What the epilogue reads beside the accumulator (the residual; z and dy of the second
+// order) comes in boxes of a warp's 32 rows x 32 columns: bulk tensor loads ahead of
+// their use, which run under the products of the tile that the warp waits for; results
+// leave in such boxes too (y from its residual's, q and dz from z's and dy's).  A row
+// per lane, straight from registers, would cost the load-store unit 32 lines per
+// instruction.  bf16 matrices whose rows are no multiples of 16 bytes move through the
+// same boxes, a row per step of the warp.  The elementwise work goes by eight columns,
+// 16 bytes of each box and one call of dropout's generator, in a loop that is not
+// unrolled: with all 32 columns in line the code did not fit the instruction cache
+// (fp32 gelu forward, 1021 x 2048 from 512 columns, 49 us; 33 in the loop).
+//
+// Measured on 8192 tokens, bf16, alone: 768 -> 2304 forward 22.5 us (1,290 TFLOP/s), dx
+// and dW 37 (1,570); 4096 -> 11,008 under the power cap 440 (1,680) and 795 (1,860).
+// Bound by the loads of the stages (a tile of K = 768 takes 4.1 us where its MMAs need
+// 3.2) and, in short launches, by their ends: 1.2 us until the first stage, 2.9 for the
+// last tile's epilogue, 2 until the next kernel's start.
 #pragma once
 
 #include <cuda_bf16.h>
