@@ -492,7 +492,7 @@ fbob_status fbob_dropout_apply(const fbob_dropout* d, const long long* counter, 
   if (!d) return fail(FBOB_ERR_INVALID_ARG, "dropout descriptor is null");
   if ((st = check_dropout(d, counter, &a.drop)) != FBOB_OK) return st;
   if (rows < 0 || D <= 0) return fail(FBOB_ERR_INVALID_ARG, "bad sizes rows=%lld D=%d", rows, D);
-  if (rows >= (1ll << 32) || D >= 0x7fffffff - 8 || (double)rows * D > (double)(1ll << 40))
+  if (rows >= (1ll << 32) || D > (1 << 30) || (double)rows * D > (double)(1ll << 40))
     return fail(FBOB_ERR_UNSUPPORTED, "%lld rows of %d are too large", rows, D);
   if (rows == 0) return FBOB_OK;
   const Arg ps[] = {{x, "x", dtype, true}, {r, "r", dtype, false}, {y, "y", dtype, true}};

@@ -107,6 +107,10 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Byte offset of 16-byte chunk c of row r in a box (64-byte swizzle).
 __device__ __forceinline__ uint32_t box_at(uint32_t r, uint32_t c) { return r * 64 + ((c ^ ((r >> 1) & 3u)) << 4); }
 // ... of element e of row r.
@@ -578,19 +582,34 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, FP32, HELD, BN>::THREADS, 1)
   const uint32_t rank = cluster_rank();
   allow_next();
 
+  if (tid < 32) {  // a barrier or two per lane
+    static_assert(kMaxStages == 8 && EW <= 32, "lanes below");
+    if (tid < p.stages) mbar_init(&ctrl.full[tid], 1);
+    if (tid >= 8 && tid - 8 < p.stages) mbar_init(&ctrl.empty[tid - 8], 1);
+    if (tid == 16 || tid == 17) mbar_init(&ctrl.tile_full[tid - 16], 1);
+    if (tid == 18 || tid == 19) mbar_init(&ctrl.tile_empty[tid - 18], 2 * EW);
+    if (tid == 20) mbar_init(&ctrl.drain, 1);
+    if (tid < EW) mbar_init(&in_bar[tid], 1);
+    fence_mbar_init();
+  }
+  // The maps' descriptors are on their way while the kernel before this one ends.
+  if (warp == EW || warp == EW + 2) {
+    const int lane = tid & 31, seg = C::TERMS ? lane / kPlanes : lane, term = C::TERMS ? lane % kPlanes : 0;
+    for (int i = 0; i < p.problems; ++i) {
+      const Problem& q = p.prob[i];
+      if (seg < q.nseg) prefetch_map(warp == EW ? &q.a[q.seg[seg].a + term] : &q.b[q.seg[seg].b + term]);
+      if (EP == kGradient && warp == EW && lane == 31 && q.out_map && !q.slab) prefetch_map(&q.out);
+    }
+  } else if (ELEMENTWISE && warp == 1) {
+    const EpArgs& e = p.ep;
+    const int lane = tid & 31, k = lane % 4;
+    if (lane < 2 && e.in_map && (lane ? e.in1 : e.in0)) prefetch_map(&p.in[lane]);
+    if (lane >= 2 && lane < 4 && e.out_map && (k == 2 ? e.out0 : e.out1)) prefetch_map(&p.out[k - 2]);
+    if (lane >= 4 && lane < 8 && k < e.q_planes) prefetch_map(&p.out[2 + k]);
+    if (lane >= 8 && lane < 12 && k < e.dz_planes) prefetch_map(&p.out[2 + kPlanes + k]);
+  }
   if (tid == 0) {
     ctrl.abort_flag = 0;
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&ctrl.full[s], 1);
-      mbar_init(&ctrl.empty[s], 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&ctrl.tile_full[b], 1);
-      mbar_init(&ctrl.tile_empty[b], 2 * EW);
-    }
-    for (int w = 0; w < EW; ++w) mbar_init(&in_bar[w], 1);
-    mbar_init(&ctrl.drain, 1);
-    fence_mbar_init();
     if ((smem_u32(smem) & 1023u) != 0u) {
       ctrl.abort_flag = 1;
       atomicOr(p.err, kErrTimeout);
@@ -763,6 +782,8 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, FP32, HELD, BN>::THREADS, 1)
       const Problem& q = p.prob[tile.which];
       const int y0 = tile.m * kTileM + (int)rank * 128 + quarter, x0 = tile.n * BN + part * H;
       if (LAYOUT == kGradients) e.rows = q.M, e.N = q.N, e.ld = q.N;
+      // (on its way while the tile's products are)
+      float bias = ELEMENTWISE ? column<FP32>(p.ep.bias, x0, e.N) : 0.f;
       float sum[HELD ? H : 1];
       int buf = 0;
       if constexpr (HELD) {
@@ -802,7 +823,6 @@ __global__ void __launch_bounds__(Cfg<LAYOUT, EP, FP32, HELD, BN>::THREADS, 1)
           for (int j = 0; j < H; j += 16) tmem_st16_nowait(from + j, reinterpret_cast<const uint32_t*>(sum) + j);
           tmem_st_wait();
         }
-        float bias = column<FP32>(p.ep.bias, x0, e.N);
         for (int c = 0; c < CHUNKS; ++c) {
           const int x = x0 + 32 * c;
           if (p.ep.bias) {

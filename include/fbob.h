@@ -399,7 +399,7 @@ typedef struct {
  * of r is y's itself.
  *   counter: null, or a 64-bit integer on the device that is added to the
  *   offset modulo 2^64 when the call runs (a captured graph's steps advance it)
- *   rows < 2^32, D < 2^31 - 8, rows D <= 2^40
+ *   rows < 2^32, D <= 2^30, rows D <= 2^40
  */
 fbob_status fbob_dropout_apply(const fbob_dropout* d, const long long* counter,
                                long long rows, int D, int dtype, const void* x, const void* r,

@@ -247,6 +247,9 @@ def test_infinite_and_nan_inputs_reach_their_rows_only():
         y, z = fb.fbob_linear_fwd(t["x"], t["W"], t["b"], t["r"], "gelu")
         rows = [i for i in range(T) if i not in (1, 2)]
         assert torch.equal(y[rows], clean["y"][rows]) and torch.equal(z[rows], clean["z"][rows])
+        assert torch.isnan(z[2]).all()
+        dx, dW, db = fb.fbob_linear_bwd(t["x"], t["W"], z, t["dy"], "gelu")
+        assert torch.isnan(dx[2]).all() and torch.equal(dx[rows], clean["dx"][rows]) and torch.isnan(db).all()
         # (among the terms of fp32 operands an infinite value meets zeros and both signs)
         assert torch.isnan(y[2]).all() and not torch.isfinite(y[1]).all()
         assert dtype == "fp32" or torch.isinf(y[1]).any()

@@ -26,7 +26,7 @@ def drop_call(lib, d, counter=None, rows=4, D=8, dtype=0, x=0x1000, r=None, y=0x
 @pytest.mark.parametrize("kw,status", [
     (dict(rows=-1), INVALID), (dict(D=0), INVALID), (dict(D=-8), INVALID), (dict(dtype=2), INVALID),
     (dict(rows=1 << 32), UNSUPPORTED), (dict(rows=1 << 30, D=1 << 11), UNSUPPORTED),
-    (dict(D=0x7ffffffb), UNSUPPORTED), (dict(x=0), INVALID), (dict(y=0), INVALID), (dict(x=0x1001), INVALID),
+    (dict(D=(1 << 30) + 1), UNSUPPORTED), (dict(x=0), INVALID), (dict(y=0), INVALID), (dict(x=0x1001), INVALID),
     (dict(r=0x1001), INVALID), (dict(y=0x2002, dtype=1), INVALID), (dict(counter=0x1004), INVALID),
 ])
 def test_dropout_refusals(lib, kw, status):
