@@ -35,8 +35,8 @@ __device__ __forceinline__ float act_rcp(float x) {
 }
 
 template <bool EXACT>
-__device__ __forceinline__ float logistic(float v) {
-  return EXACT ? 1.f / (1.f + expf(-v)) : act_rcp(1.f + act_exp(-v));
+__device__ __forceinline__ float logistic(float v) {  // (the reciprocal is off by 2^-23 at most)
+  return act_rcp(1.f + (EXACT ? expf(-v) : act_exp(-v)));
 }
 
 // F(z), and f(z) sqrt(2 pi) = exp(-z^2 / 2).
@@ -83,38 +83,7 @@ __device__ __forceinline__ float act_value(float z) {
   return z;
 }
 
-// a' (and, SECOND, a'').
-template <int ACT, bool EXACT, bool SECOND>
-__device__ __forceinline__ float act_slope(float z, float& curve) {
-  if (ACT == kActRelu) {
-    curve = 0.f;
-    return z <= 0.f ? 0.f : 1.f;
-  }
-  if (ACT == kActGelu) {
-    const float c = act_clamp(z, kActTop);
-    float bell;
-    const float up = normal_cdf<EXACT>(c, bell), f = 0.39894228040143268f * bell;
-    if (SECOND) curve = f * fmaf(-c, c, 2.f);
-    return fmaf(c, f, up);
-  }
-  if (ACT == kActGeluTanh) {
-    const float c = act_clamp(z, kActTop), c2 = 0.044715f * c * c;
-    const float s = logistic<EXACT>(kTanhC * fmaf(c2, c, c)), d = s * (1.f - s);
-    const float v1 = kTanhC * fmaf(3.f, c2, 1.f), zv = c * v1;
-    if (SECOND) curve = d * fmaf(zv, v1 * fmaf(-2.f, s, 1.f), fmaf(2.f, v1, kTanhC * 6.f * c2));
-    return fmaf(zv, d, s);
-  }
-  if (ACT == kActSilu) {
-    const float c = act_clamp(z, kSiluTop);
-    const float s = logistic<EXACT>(c), d = s * (1.f - s);
-    if (SECOND) curve = d * fmaf(c, fmaf(-2.f, s, 1.f), 2.f);
-    return fmaf(c, d, s);
-  }
-  curve = 0.f;
-  return 1.f;
-}
-
-// --- eight values at a time, in packed pairs where they are not EXACT -------------
+// --- eight values at a time, in packed pairs ----------------------------------------
 
 using row::F2;
 
@@ -134,8 +103,21 @@ __device__ __forceinline__ F2 rcp_pair(F2 x) {
 __device__ __forceinline__ F2 logistic_pair(F2 x) { return rcp_pair(exp2_pair(x) + both(1.f)); }
 constexpr float kActLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ F2 clamp_pair(F2 z, float top) {
+  const float2 f = row::parts(z);
+  return row::pair(act_clamp(f.x, top), act_clamp(f.y, top));
+}
+
 // As normal_cdf.
+template <bool EXACT>
 __device__ __forceinline__ F2 cdf_pair(F2 z, F2& bell) {
+  if (EXACT) {
+    const float2 f = row::parts(z);
+    float a, b;
+    const float x = normal_cdf<true>(f.x, a), y = normal_cdf<true>(f.y, b);
+    bell = row::pair(a, b);
+    return row::pair(x, y);
+  }
   const F2 z2 = z * z;
   bell = exp2_pair(z2 * both(-0.5f * kActLog2e));
   const float2 f = row::parts(z);
@@ -154,25 +136,35 @@ template <int ACT>
 __device__ __forceinline__ F2 value_pair(F2 z) {
   if (ACT == kActGelu) {
     F2 bell;
-    return z * cdf_pair(z, bell);
+    return z * cdf_pair<false>(z, bell);
   }
   if (ACT == kActGeluTanh)
     return z * logistic_pair(z * mad(z * z, both(-0.044715f * kTanhC * kActLog2e), both(-kTanhC * kActLog2e)));
   return z * logistic_pair(z * both(-kActLog2e));  // kActSilu
 }
 
-// (z was kept in fp16: no power of it overflows)
-template <int ACT, bool SECOND>
-__device__ __forceinline__ F2 slope_pair(F2 c, F2& curve) {
+// The logistic function of v; EXACT with expf.
+template <bool EXACT>
+__device__ __forceinline__ F2 logistic_of(F2 v) {
+  if (!EXACT) return logistic_pair(v * both(-kActLog2e));
+  const float2 f = row::parts(v);
+  return rcp_pair(row::pair(expf(-f.x), expf(-f.y)) + both(1.f));
+}
+
+// a' (and, SECOND, a'').  (Not EXACT: z was kept in fp16, no power of it overflows.)
+template <int ACT, bool EXACT, bool SECOND>
+__device__ __forceinline__ F2 slope_pair(F2 z, F2& curve) {
+  const F2 c = EXACT ? clamp_pair(z, ACT == kActSilu ? kSiluTop : kActTop) : z;
   if (ACT == kActGelu) {
     F2 bell;
-    const F2 up = cdf_pair(c, bell), f = bell * both(0.39894228040143268f);
+    const F2 up = cdf_pair<EXACT>(c, bell), f = bell * both(0.39894228040143268f);
     if (SECOND) curve = f * mad(c * c, both(-1.f), both(2.f));
     return mad(c, f, up);
   }
   if (ACT == kActGeluTanh) {
     const F2 c2 = c * c;
-    const F2 s = logistic_pair(c * mad(c2, both(-0.044715f * kTanhC * kActLog2e), both(-kTanhC * kActLog2e)));
+    const F2 s = EXACT ? logistic_of<true>(c * mad(c2, both(0.044715f * kTanhC), both(kTanhC)))
+                       : logistic_pair(c * mad(c2, both(-0.044715f * kTanhC * kActLog2e), both(-kTanhC * kActLog2e)));
     const F2 d = s * mad(s, both(-1.f), both(1.f));
     const F2 v1 = mad(c2, both(3.f * 0.044715f * kTanhC), both(kTanhC)), zv = c * v1;
     if (SECOND)  // 2 v' + z v'' = 4 v' - 4 sqrt(2 / pi)
@@ -180,7 +172,7 @@ __device__ __forceinline__ F2 slope_pair(F2 c, F2& curve) {
     return mad(zv, d, s);
   }
   // kActSilu
-  const F2 s = logistic_pair(c * both(-kActLog2e)), d = s * mad(s, both(-1.f), both(1.f));
+  const F2 s = logistic_of<EXACT>(c), d = s * mad(s, both(-1.f), both(1.f));
   if (SECOND) curve = d * mad(c, mad(s, both(-2.f), both(1.f)), both(2.f));
   return mad(c, d, s);
 }
@@ -221,11 +213,11 @@ __device__ __forceinline__ void act_values8(float* z) {
 // z[j] becomes a'(z[j]), and (SECOND) a2[j] a''.
 template <int ACT, bool EXACT, bool SECOND>
 __device__ __forceinline__ void act_slopes8(float* z, float* a2) {
-  if constexpr (!EXACT && kSmooth<ACT>) {
+  if constexpr (kSmooth<ACT>) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       F2 c;
-      const float2 f = row::parts(slope_pair<ACT, SECOND>(row::pair(z[j], z[j + 1]), c));
+      const float2 f = row::parts(slope_pair<ACT, EXACT, SECOND>(row::pair(z[j], z[j + 1]), c));
       z[j] = f.x, z[j + 1] = f.y;
       if (SECOND) {
         const float2 g = row::parts(c);
@@ -233,9 +225,11 @@ __device__ __forceinline__ void act_slopes8(float* z, float* a2) {
       }
     }
   } else {
-    float none;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = act_slope<ACT, EXACT, SECOND>(z[j], SECOND ? a2[j] : none);
+    for (int j = 0; j < 8; ++j) {
+      z[j] = ACT == kActRelu && z[j] <= 0.f ? 0.f : 1.f;
+      if (SECOND) a2[j] = 0.f;
+    }
   }
 }
 

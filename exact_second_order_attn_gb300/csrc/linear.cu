@@ -445,26 +445,12 @@ struct Run {
   static void sizes(Problem& q, long long M, long long N, long long K, int splits) {
     q.M = (int)M, q.N = (int)N, q.K = (int)K, q.splits = splits;
   }
-  // fp32's products of each segment in stages of their own (the second order's boxes
-  // leave no room for all terms): those that reach 2^-16 of the first, smallest first
-  // among all segments.
-  static void apart(Problem& q) {
-    const Seg from[2] = {q.seg[0], q.seg[1]};
-    const int n = q.nseg;
-    q.nseg = 0;
-    for (int order = kPlanes - 1; order >= 0; --order) {
-      for (int k = 0; k < n; ++k) {
-        for (int i = order; i >= 0; --i)
-          q.seg[q.nseg++] = Seg{(uint8_t)(from[k].a + i), (uint8_t)(from[k].b + order - i)};
-      }
-    }
-  }
   // Chains of fp32 operands are a stage, so that its small products come before the
-  // large ones (chains of two stages: errors of 7e-7 in place of 1.5e-7), or 128 columns
-  // of products that are apart; long sums of bf16 ones end theirs every 16,384 terms.
+  // large ones (chains of two stages: errors of 7e-7 in place of 1.5e-7); long sums of
+  // bf16 ones end theirs every 16,384 terms.
   void chains(Problem& q) const {
     const long long terms = ((long long)q.K + q.splits - 1) / q.splits * q.nseg;
-    q.chain = !a.bf16 ? (q.nseg > 2 ? 2 : 1) : terms > kLongTerms ? (int)(kLongTerms / kBK / q.nseg) : 0;
+    q.chain = !a.bf16 ? 1 : terms > kLongTerms ? (int)(kLongTerms / kBK / q.nseg) : 0;
   }
 
   // Maps of the planes of a [rows][K] operand, boxes of `box` rows x 64 columns.
@@ -661,7 +647,6 @@ struct Run {
           return cudaErrorInvalidValue;
         products(t, 1, 1, 1);
       }
-      if (!a.bf16) apart(t);
       chains(t);
       EpArgs& e = g.ep;
       e.bias = a.ub, e.act = a.act, e.drop = a.drop, e.in_ld = a.N, e.ld = p.Np;

@@ -16,11 +16,12 @@ namespace lin {
 constexpr int kTileM = 256;  // rows of a pair's tile (128 per block)
 constexpr int kBK = 64;      // contraction per stage (128 bytes of bf16)
 constexpr int kPlanes = 3;   // bf16 terms that stand for one fp32 operand
-constexpr int kMaxSegs = 12;
+constexpr int kMaxSegs = 4;
 // bf16 operands: up to this many tokens dz and q keep two bf16 terms.
 constexpr int kExactTokens = 16;
 
-// A segment multiplies plane a by plane b; the sum over the segments is the product.
+// A segment multiplies plane a by plane b (fp32: the planes from a and b on, the six
+// products that count); the sum over the segments is the product.
 struct Seg {
   uint8_t a, b;
 };

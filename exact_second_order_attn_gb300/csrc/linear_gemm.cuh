@@ -12,7 +12,7 @@
 // 2^-16 of the first are summed, smallest first, out of one stage that holds all terms
 // (a stage for each product would load twice the bytes, at 12 TB/s what bound it).  The
 // tensor cores drop the bits of a step's sum below the accumulator's last one, so there
-// a chain ends after 64 or 128 columns and the epilogue threads add the chains up in
+// a chain ends after 64 columns and the epilogue threads add the chains up in
 // registers (HELD); so do sums of bf16 operands over more than 16,384 terms, every
 // 16,384 (3e-5 of the result).
 //
@@ -76,9 +76,8 @@ struct Cfg {
   static constexpr bool B_MN = LAYOUT == kGradients;
   static constexpr int A_BYTES = 128 * kBK * 2;
   static constexpr int B_BYTES = BN / 2 * kBK * 2;
-  // fp32: a stage holds all terms of both operands for the six products; the second
-  // order's boxes leave no room for two of those.
-  static constexpr bool TERMS = FP32 && EP != kSecondTerms;
+  // fp32: a stage holds all terms of both operands for the six products
+  static constexpr bool TERMS = FP32;
   static constexpr int STAGE = (A_BYTES + B_BYTES) * (TERMS ? kPlanes : 1);  // [A.. | B..]
   static constexpr int B_OFF = A_BYTES * (TERMS ? kPlanes : 1);
   static constexpr int NIN = EP == kForward ? 1 : kIsSecond<EP> ? 2 : 0;
@@ -88,10 +87,10 @@ struct Cfg {
   static constexpr int H = BN / (WARPS / 4);  // columns of an epilogue thread
   static_assert(kRoom + 2048 <= 232448, "shared memory budget");
   // Boxes of a warp: of y and its residual, and z; of z and q, dy and dz, gdy, then the
-  // further terms of q and dz in turn; of two results.
+  // further terms of q and dz in turn (fp32: of one's terms); of two results.
   static int boxes(const GemmArgs& g) {
     if (EP == kForward) return FP32 ? 0 : 1 + (g.ep.out1 != nullptr);
-    return EP == kSecond ? 3 : EP == kSecondTerms ? (FP32 ? 7 : 5) : EP == kGradient && !FP32 ? 2 : 0;
+    return EP == kSecond ? 3 : EP == kSecondTerms ? (FP32 ? 3 : 5) : EP == kGradient && !FP32 ? 2 : 0;
   }
   static int stages(const GemmArgs& g) {
     const int n = (kRoom - WARPS * boxes(g) * kBoxBytes) / STAGE;
@@ -414,15 +413,16 @@ __device__ __forceinline__ void forward_chunk(Ep& e, const Columns<HELD>& in, co
   }
 }
 
-// The box of term k of q (which = 0) or dz (1).
+// The box of term k of q (which = 0) or dz (1); fp32's terms of both take turns in three.
+template <bool FP32>
 __device__ __forceinline__ uint32_t term_box(uint32_t boxes, int which, int k) {
-  return boxes + (k == 0 ? which : 1 + 2 * k + which) * kBoxBytes;
+  return boxes + (FP32 ? k : k == 0 ? which : 1 + 2 * k + which) * kBoxBytes;
 }
 // v as n bf16 terms (one without TERMS): each holds the rounding of what the ones
 // before it left.
-template <bool TERMS>
+template <bool FP32, bool TERMS>
 __device__ __forceinline__ void store_terms(uint32_t boxes, int which, int n, int g, float* v) {
-  box_store(term_box(boxes, which, 0), g, v);
+  box_store(term_box<FP32>(boxes, which, 0), g, v);
   if constexpr (TERMS) {
     for (int k = 1; k < n; ++k) {
 #pragma unroll
@@ -431,49 +431,58 @@ __device__ __forceinline__ void store_terms(uint32_t boxes, int which, int n, in
         const float h = __bfloat162float(__float2bfloat16_rn(v[j]));
         v[j] = isinf(h) ? 0.f : v[j] - h;
       }
-      box_store(term_box(boxes, which, k), g, v);
+      box_store(term_box<FP32>(boxes, which, k), g, v);
     }
   }
 }
 
 // 32 columns (from x) of the second order for the row y0 + lane: the product is t.
-// bf16: z and dy are in the first two boxes, over which q and dz are written.
-template <int ACT, bool FP32, bool TERMS, bool HELD>
+// bf16: z and dy are in the first two boxes, over which q and dz are written (PART is
+// kAll).  fp32: z and dy come from memory, eight columns ahead; first what t makes, then
+// (kDz) dz, in the boxes that q has left.
+enum Part { kAll, kFromT, kDz };
+template <int ACT, bool FP32, bool TERMS, bool HELD, int PART>
 __device__ __forceinline__ void second_values(Ep& e, const Columns<HELD>& in, const float* bias, uint32_t boxes, int x,
                                               int y0) {
   const EpArgs& a = e.p.ep;
   const int lane = threadIdx.x & 31, row = y0 + lane;
   const bool live = row < e.rows;
+  float z_next[8], dy_next[8];
+  auto ahead = [&](int g) {
+    if (ACT != kActNone) read8(static_cast<const float*>(a.in0), a.in_ld, live, row, x + 8 * g, e.N, z_next);
+    if (a.in1) read8(static_cast<const float*>(a.in1), a.in_ld, live, row, x + 8 * g, e.N, dy_next);
+  };
+  if (FP32) ahead(0);
 #pragma unroll 1
   for (int g = 0; g < 4; ++g) {
     float t[8], a1[8], a2[8], dy[8], m[8];
-    in.load(g, t);
-    if (a.bias && live) add_bias(bias, g, t);  // (rows past the last are 0)
-    if (ACT != kActNone) {
-      if (FP32)
-        read8(static_cast<const float*>(a.in0), a.in_ld, live, row, x + 8 * g, e.N, a1);
-      else
-        half8(ld_shared_v4(boxes + box_at(lane, g)), a1);
+    if (FP32) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a1[j] = z_next[j], dy[j] = dy_next[j];
+      if (g < 3) ahead(g + 1);
+    } else {
+      if (ACT != kActNone) half8(ld_shared_v4(boxes + box_at(lane, g)), a1);
+      if (a.in1) box_values(boxes + kBoxBytes, g, dy);
     }
-    act_slopes8<ACT, FP32, true>(a1, a2);
-    if (a.in1) {
-      if (FP32)
-        read8(static_cast<const float*>(a.in1), a.in_ld, live, row, x + 8 * g, e.N, dy);
-      else
-        box_values(boxes + kBoxBytes, g, dy);
+    if (PART != kDz) {
+      in.load(g, t);
+      if (a.bias && live) add_bias(bias, g, t);  // (rows past the last are 0)
     }
+    act_slopes8<ACT, FP32, PART != kDz>(a1, a2);
     if (e.drop.on) {
       e.drop.factors8((uint32_t)(x >> 3) + g, (uint32_t)row, m);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {  // what is dropped is 0 whatever stands there
         const bool kept = m[j] != 0.f;
-        t[j] = kept ? t[j] : 0.f;
         a1[j] = kept ? a1[j] * e.drop.scale : 0.f;
-        a2[j] = kept ? a2[j] * e.drop.scale : 0.f;
         if (a.in1) dy[j] = kept ? dy[j] : 0.f;
+        if (PART != kDz) {
+          t[j] = kept ? t[j] : 0.f;
+          a2[j] = kept ? a2[j] * e.drop.scale : 0.f;
+        }
       }
     }
-    if (a.out0) {
+    if (PART != kDz && a.out0) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) m[j] = t[j];
       mul8(m, a1);
@@ -482,16 +491,16 @@ __device__ __forceinline__ void second_values(Ep& e, const Columns<HELD>& in, co
       else
         box_store(boxes + 2 * kBoxBytes, g, m);
     }
-    if (a.dz_planes) {
+    if (PART != kFromT && a.dz_planes) {
       mul8(a1, dy);
-      store_terms<TERMS>(boxes, 1, a.dz_planes, g, a1);
+      store_terms<FP32, TERMS>(boxes, 1, a.dz_planes, g, a1);
     }
-    if (a.q_planes || a.sums) {
+    if (PART != kDz && (a.q_planes || a.sums)) {
       mul8(t, dy);
       mul8(t, a2);
 #pragma unroll
       for (int j = 0; j < 8; ++j) m[j] = t[j];
-      if (a.q_planes) store_terms<TERMS>(boxes, 0, a.q_planes, g, m);
+      if (a.q_planes) store_terms<FP32, TERMS>(boxes, 0, a.q_planes, g, m);
       if (a.sums) {
         const float s = sum_columns8(t);
         const int n = x + 8 * g + lane / 4;
@@ -500,24 +509,34 @@ __device__ __forceinline__ void second_values(Ep& e, const Columns<HELD>& in, co
     }
   }
 }
+template <bool FP32, bool TERMS, int PART, bool HELD>
+__device__ __forceinline__ void second_part(Ep& e, const Columns<HELD>& in, const float* bias, uint32_t boxes, int x,
+                                            int y0) {
+  switch (e.p.ep.act) {
+    case kActRelu: second_values<kActRelu, FP32, TERMS, HELD, PART>(e, in, bias, boxes, x, y0); break;
+    case kActGelu: second_values<kActGelu, FP32, TERMS, HELD, PART>(e, in, bias, boxes, x, y0); break;
+    case kActGeluTanh: second_values<kActGeluTanh, FP32, TERMS, HELD, PART>(e, in, bias, boxes, x, y0); break;
+    case kActSilu: second_values<kActSilu, FP32, TERMS, HELD, PART>(e, in, bias, boxes, x, y0); break;
+    default: second_values<kActNone, FP32, TERMS, HELD, PART>(e, in, bias, boxes, x, y0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
 template <bool FP32, bool TERMS, bool HELD>
 __device__ __forceinline__ void second_chunk(Ep& e, const Columns<HELD>& in, const float* bias, uint32_t boxes, int x,
                                              int y0) {
   const EpArgs& a = e.p.ep;
-  switch (a.act) {
-    case kActRelu: second_values<kActRelu, FP32, TERMS>(e, in, bias, boxes, x, y0); break;
-    case kActGelu: second_values<kActGelu, FP32, TERMS>(e, in, bias, boxes, x, y0); break;
-    case kActGeluTanh: second_values<kActGeluTanh, FP32, TERMS>(e, in, bias, boxes, x, y0); break;
-    case kActSilu: second_values<kActSilu, FP32, TERMS>(e, in, bias, boxes, x, y0); break;
-    default: second_values<kActNone, FP32, TERMS>(e, in, bias, boxes, x, y0);
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
+  second_part<FP32, TERMS, FP32 ? kFromT : kAll>(e, in, bias, boxes, x, y0);
   if (!FP32 && a.out0 && a.out_map) e.leave(boxes + 2 * kBoxBytes, e.p.out, x, y0);
-  for (int k = 0; k < (TERMS ? a.dz_planes : a.dz_planes != 0); ++k)
-    e.leave(term_box(boxes, 1, k), e.p.out + 2 + kPlanes + k, x, y0);
   for (int k = 0; k < (TERMS ? a.q_planes : a.q_planes != 0); ++k)
-    e.leave(term_box(boxes, 0, k), e.p.out + 2 + k, x, y0);
+    e.leave(term_box<FP32>(boxes, 0, k), e.p.out + 2 + k, x, y0);
+  if (FP32 && a.dz_planes) {
+    commit_stores();
+    boxes_free();
+    second_part<FP32, TERMS, kDz>(e, in, bias, boxes, x, y0);
+  }
+  for (int k = 0; k < (TERMS ? a.dz_planes : a.dz_planes != 0); ++k)
+    e.leave(term_box<FP32>(boxes, 1, k), e.p.out + 2 + kPlanes + k, x, y0);
   commit_stores();
   if (!FP32 && a.out0 && !a.out_map) e.copy_rows(boxes + 2 * kBoxBytes, a.out0, x, y0);
 }
