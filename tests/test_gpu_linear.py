@@ -328,3 +328,58 @@ def test_withheld_stages_time_out(dtype):
     got = chain(t, "gelu")
     for k in ref:
         assert torch.equal(ref[k], got[k])
+
+
+def test_calls_from_several_host_threads():
+    """Through the C ABI at the same time, each thread on its own stream and
+    workspace: every call succeeds and computes what it computes alone."""
+    import ctypes
+    import threading
+    lib = _lib.load()
+    drop = fb.Dropout(0.25, 7, 8)
+
+    def calls(dtype, T, K, N, act, seed):
+        t = make(T, K, N, dtype, seed)
+        ref = chain(t, act, drop)
+        code = _lib.BF16 if dtype == "bf16" else _lib.FP32
+        l = _lib.Linear(T, K, N, code, _lib.ACTIVATIONS[act])
+        d, q = ctypes.byref(l), ctypes.byref(drop)
+        ws = [torch.empty(lib.fbob_linear_workspace_bytes(d, q, i) + 16, dtype=torch.uint8, device="cuda") for i in range(3)]
+        out = {k: torch.empty_like(v) for k, v in ref.items()}
+        p = {k: ctypes.c_void_p(v.data_ptr()) for k, v in {**{k: v for k, v in t.items() if v is not None}, **out}.items()}
+        p = {**{k: None for k in t}, **p}
+        stream = torch.cuda.Stream()
+        s = ctypes.c_void_p(stream.cuda_stream)
+
+        def run():
+            w = [(ctypes.c_void_p(v.data_ptr()), v.numel(), s) for v in ws]
+            st = (lib.fbob_linear_fwd(d, q, None, *(p[k] for k in ("x", "W", "b", "r", "y", "z")), *w[0]),
+                  lib.fbob_linear_bwd(d, q, None, *(p[k] for k in ("x", "W", "z", "dy", "dx", "dW", "db")), *w[1]),
+                  lib.fbob_linear_bob(d, q, None, *(p[k] for k in ("x", "W", "z", "dy", "ux", "uW", "ub", "gx", "gW", "gb",
+                                                                   "gdy")), *w[2]))
+            assert st == (0, 0, 0)
+        return run, stream, out, ref, (t, ws)
+
+    jobs = [calls("bf16", 300, 264, 520, "gelu", 1), calls("fp32", 70, 72, 136, "silu", 2),
+            calls("bf16", 8, 96, 64, "relu", 3), calls("bf16", 41, 33, 77, "gelu_tanh", 4)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(run):
+        try:
+            for _ in range(300):
+                run()
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(j[0],)) for j in jobs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    fb.device_status()
+    assert not failed
+    for _, _, out, ref, _ in jobs:
+        for k in ref:
+            assert torch.equal(out[k], ref[k]), k
