@@ -3,7 +3,9 @@
 // gradients of any order are the same call.
 //
 // Rows that start on 16 bytes: a thread takes eight columns of a row, the span of one
-// generator call, in 16-byte accesses, kGroups of them on their way at once.
+// generator call, in 16-byte accesses; kGroups of them at once, one of bf16 (32,768 x 4096
+// 82 us; four, which leave room for fewer threads, 88), two of fp32 (16,384 x 4096 81 us;
+// one 91).
 // Other rows: a warp takes 256 columns of a row, an element per lane and step, so that
 // accesses stay together; a lane draws for eight of the columns and hands out their
 // bits; of rows of up to 128 columns it takes several.  (A thread's eight columns one by
@@ -19,7 +21,9 @@
 namespace fbob {
 namespace {
 
-constexpr int kThreads = 256, kGroups = 4;
+constexpr int kThreads = 256;
+template <typename T>
+constexpr int kGroups = sizeof(T) == 2 ? 1 : 2;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutArgs a) {
@@ -35,16 +39,16 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
   uint32_t row = (uint32_t)(i / per), group = (uint32_t)(i - (long long)row * per);
   const uint32_t rows = (uint32_t)(step / per), groups = (uint32_t)(step - (long long)rows * per);
   while (i < total) {
-    Raw8<T> v[kGroups], w[kGroups];
+    Raw8<T> v[kGroups<T>], w[kGroups<T>];
 #pragma unroll
-    for (int u = 0; u < kGroups; ++u) {
+    for (int u = 0; u < kGroups<T>; ++u) {
       if (i + u * step < total) {
         v[u].template load<true>(x + 8 * (i + u * step), 8);
         if (r) w[u].template load<true>(r + 8 * (i + u * step), 8);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kGroups; ++u, i += step) {
+    for (int u = 0; u < kGroups<T>; ++u, i += step) {
       if (i < total) {
         float f[8];
         v[u].values(f);
@@ -140,8 +144,8 @@ template <typename T>
 cudaError_t launch(const DropoutArgs& a, bool vec, cudaStream_t s) {
   const int each = a.D <= 128 ? 32 / ((a.D + 7) / 8) : 1;
   const long long units = vec ? a.rows * (a.D / 8) : a.D <= 128 ? (a.rows + each - 1) / each : a.rows * ((a.D + 255) / 256);
-  const long long block = vec ? kThreads * kGroups : kThreads / 32;
-  const long long blocks = (units + block - 1) / block, most = 8ll * sm_count();
+  const long long block = vec ? kThreads * kGroups<T> : kThreads / 32;
+  const long long blocks = (units + block - 1) / block, most = 16ll * sm_count();
   const dim3 grid((unsigned)(blocks < most ? blocks : most)), threads(kThreads);
   prof_begin(s, "dropout");
   // (the inverse is exact for elements below 256: 65,536 / D rounded up is off by less than 1, 256 times that
