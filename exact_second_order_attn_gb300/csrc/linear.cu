@@ -461,11 +461,12 @@ struct Run {
     }
     return true;
   }
-  // ... of dz (or q): [T][N].
+  // ... of dz (or q): [T][N].  The maps end with the outputs, as those that the epilogue
+  // stores through do: what stands in the padding to Np columns is not read (loads fill in zeros).
   bool z_maps(CUtensorMap* m, bool q, int box) const {
     for (int k = 0; k < p.zp; ++k) {
       const void* b = !q && !p.own_dz ? a.dy : at<uint16_t>(q ? p.q : p.dz) + (size_t)k * a.T * p.Np;
-      if (!matrix_map(m + k, b, a.T, p.Np, p.Np, box)) return false;
+      if (!matrix_map(m + k, b, a.T, a.N, p.Np, box)) return false;
     }
     return true;
   }
