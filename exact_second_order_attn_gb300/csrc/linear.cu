@@ -371,10 +371,12 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
       add8(v, w);
     }
     if (z) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = sizeof(T) == 2 && all.act == kActRelu ? kept_sign(v[j]) : v[j];
       if (o.vec)
-        store8<Kept<T>, true>(z + to, n, v);
+        store8<Kept<T>, true>(z + to, n, w);
       else
-        store8<Kept<T>, false>(z + to, n, v);
+        store8<Kept<T>, false>(z + to, n, w);
     }
     act_values8<sizeof(T) == 4>(all.act, v);
     const Dropper drop(all.drop);

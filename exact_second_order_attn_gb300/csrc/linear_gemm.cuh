@@ -369,9 +369,13 @@ __device__ __forceinline__ void forward_values(Ep& e, const Columns<HELD>& in, c
     if (ACT != kActNone && a.out1) {
       if (FP32)
         write8(static_cast<float*>(a.out1), a.in_ld, live, row, x + 8 * g, e.N, v);
-      else
-        st_shared_v4(out + kBoxBytes + box_at(lane, g), half_pair(v[0], v[1]), half_pair(v[2], v[3]),
-                     half_pair(v[4], v[5]), half_pair(v[6], v[7]));
+      else {
+        float z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = ACT == kActRelu ? kept_sign(v[j]) : v[j];
+        st_shared_v4(out + kBoxBytes + box_at(lane, g), half_pair(z[0], z[1]), half_pair(z[2], z[3]),
+                     half_pair(z[4], z[5]), half_pair(z[6], z[7]));
+      }
     }
     act_values8<ACT, FP32>(v);
     if (e.drop.on) e.drop.apply8((uint32_t)(x >> 3) + g, (uint32_t)row, v);

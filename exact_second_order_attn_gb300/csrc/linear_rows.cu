@@ -116,7 +116,10 @@ __global__ void __launch_bounds__(kWarps * 32, TT >= 8 ? 2 : 3)
     for (int w = 0; w < share; ++w) v += part[group * share + w][j];
     const size_t at = (size_t)t * N + n;
     if (bias) v += (float)bias[n];
-    if (z) store8<Kept<E>, false>(z + at, 1, &v);
+    if (z) {
+      const float kept = sizeof(E) == 2 && act == kActRelu ? kept_sign(v) : v;
+      store8<Kept<E>, false>(z + at, 1, &kept);
+    }
     v = act_value<sizeof(E) == 4>(act, v);
     if (drop.on) {
       float m[8];

@@ -12,11 +12,14 @@
 namespace fbob {
 
 // How z of a linear layer is kept: fp32, or fp16 beside bf16 tensors - eleven bits
-// where bf16 has eight, and no activation's slope changes beyond its range (which is
-// kept in by clamping; a NaN stays one).
+// where bf16 has eight, and no activation's slope changes above its range (which is
+// kept in by clamping; a NaN stays one).  Below 2^-25 it rounds to 0, where the smooth slopes
+// are what they are at 0, but relu's is not that of a positive z: those are kept as
+// 2^-24 at least.
 template <typename T>
 using Kept = std::conditional_t<sizeof(T) == 2, __half, float>;
 __device__ __forceinline__ float kept_range(float z) { return z > 65504.f ? 65504.f : z < -65504.f ? -65504.f : z; }
+__device__ __forceinline__ float kept_sign(float z) { return z > 0.f ? fmaxf(z, 0x1p-24f) : z; }
 
 __device__ __forceinline__ uint32_t half_pair(float a, float b) {
   uint32_t h;

@@ -429,8 +429,9 @@ size_t fbob_linear_workspace_bytes(const fbob_linear* p, const fbob_dropout* dro
  * none) of element (token, output); counter as in fbob_dropout_apply.
  *   in : x [T, K], W [N, K]; b [N], r [T, N] optional
  *   out: y [T, N]; z [T, N] optional, which the calls below want unless the
- *        activation is NONE, where it is left as it was (fp16 beside bf16 tensors, clamped to its range,
- *        beyond which no slope changes)
+ *        activation is NONE, where it is left as it was (fp16 beside bf16 tensors: clamped to
+ *        its range, above which no slope changes; for RELU a positive value is kept as 2^-24 at
+ *        least, so that its slope stays 1)
  * bf16 matrices whose rows are multiples of 16 bytes have to start on 16 bytes
  * where they are multiplied (x, W, dy, ux, uW).  Sums are fp32; fp32 inputs are
  * multiplied as three bf16 terms each and lose nothing to about 2^-22.  x W^T of up
