@@ -405,7 +405,8 @@ __device__ __forceinline__ void forward_chunk(Ep& e, const Columns<HELD>& in, co
     default: forward_values<kActNone, FP32>(e, in, bias, out, x, y0);
   }
   if (FP32) return;
-  if (a.out_map) fence_proxy_async_smem();
+  // before the box's bulk store, or its next bulk load, where y itself goes out row by row
+  if (a.in_map || a.out_map) fence_proxy_async_smem();
   __syncwarp();
   if (a.out_map) {
     e.leave(out, e.p.out, x, y0);
