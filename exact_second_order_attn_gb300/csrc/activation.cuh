@@ -5,8 +5,9 @@
 //   gelu_tanh  z s(v), s the logistic function, v = 2 sqrt(2 / pi) (z + 0.044715 z^3),
 //              which is z (1 + tanh(v / 2)) / 2 without its cancellation at z < 0
 //   silu       z s(z)
-// With s' = s (1 - s): (z s(v))' = s + z s' v', and
-// (z s(v))'' = s' (2 v' + z v'' + z v'^2 (1 - 2 s)).
+// (z s(v))' = s + z s' v', and (z s(v))'' = s' (2 v' + z v'' + z v'^2 (1 - 2 s)).
+// s' = s(v) s(-v) is made of the exponential: s (1 - s) would lose it in the steps of s
+// below 1 (gelu_tanh'' from z = 3 on, all of it at 5).
 //
 // EXACT (fp32 tensors) takes expf and erfcf.  For bf16 tensors, whose results are
 // rounded to 2^-9, 2^x and 1/x of the special function unit (2^-22), and
@@ -58,9 +59,14 @@ __device__ __forceinline__ float normal_cdf(float z, float& bell) {
 
 constexpr float kTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
+// The lesser of two values; a NaN stays one.
+__device__ __forceinline__ float act_least(float z, float top) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(z) : "f"(top));
+  return z;
+}
 // z moved into [-top, top]; a NaN stays one.
 __device__ __forceinline__ float act_clamp(float z, float top) {
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(z) : "f"(top));
+  z = act_least(z, top);
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(z) : "f"(-top));
   return z;
 }
@@ -101,6 +107,14 @@ __device__ __forceinline__ F2 rcp_pair(F2 x) {
 }
 // The logistic function of v, from -v log2(e).
 __device__ __forceinline__ F2 logistic_pair(F2 x) { return rcp_pair(exp2_pair(x) + both(1.f)); }
+// ... and its slope, u s^2 with u = 2^x, which stays finite (the slope is 0 long before).
+__device__ __forceinline__ F2 logistic_pair(F2 x, F2& slope) {
+  const float2 f = row::parts(x);
+  const F2 u = exp2_pair(row::pair(act_least(f.x, 126.f), act_least(f.y, 126.f)));
+  const F2 s = rcp_pair(u + both(1.f));
+  slope = u * s * s;
+  return s;
+}
 constexpr float kActLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ F2 clamp_pair(F2 z, float top) {
@@ -143,12 +157,16 @@ __device__ __forceinline__ F2 value_pair(F2 z) {
   return z * logistic_pair(z * both(-kActLog2e));  // kActSilu
 }
 
-// The logistic function of v; EXACT with expf.
+// The logistic function of v and its slope; EXACT with expf.
 template <bool EXACT>
-__device__ __forceinline__ F2 logistic_of(F2 v) {
-  if (!EXACT) return logistic_pair(v * both(-kActLog2e));
+__device__ __forceinline__ F2 logistic_of(F2 v, F2& slope) {
+  if (!EXACT) return logistic_pair(v * both(-kActLog2e), slope);
   const float2 f = row::parts(v);
-  return rcp_pair(row::pair(expf(-f.x), expf(-f.y)) + both(1.f));
+  const F2 e = row::pair(expf(-fabsf(f.x)), expf(-fabsf(f.y)));  // s(|v|) = 1 / (1 + e), s(-|v|) = e / (1 + e)
+  const F2 hi = rcp_pair(e + both(1.f)), lo = e * hi;
+  slope = lo * hi;
+  const float2 a = row::parts(hi), b = row::parts(lo);
+  return row::pair(f.x < 0.f ? b.x : a.x, f.y < 0.f ? b.y : a.y);
 }
 
 // a' (and, SECOND, a'').  (Not EXACT: z was kept in fp16, no power of it overflows.)
@@ -163,16 +181,17 @@ __device__ __forceinline__ F2 slope_pair(F2 z, F2& curve) {
   }
   if (ACT == kActGeluTanh) {
     const F2 c2 = c * c;
-    const F2 s = EXACT ? logistic_of<true>(c * mad(c2, both(0.044715f * kTanhC), both(kTanhC)))
-                       : logistic_pair(c * mad(c2, both(-0.044715f * kTanhC * kActLog2e), both(-kTanhC * kActLog2e)));
-    const F2 d = s * mad(s, both(-1.f), both(1.f));
+    F2 d;
+    const F2 s = EXACT ? logistic_of<true>(c * mad(c2, both(0.044715f * kTanhC), both(kTanhC)), d)
+                       : logistic_pair(c * mad(c2, both(-0.044715f * kTanhC * kActLog2e), both(-kTanhC * kActLog2e)), d);
     const F2 v1 = mad(c2, both(3.f * 0.044715f * kTanhC), both(kTanhC)), zv = c * v1;
     if (SECOND)  // 2 v' + z v'' = 4 v' - 4 sqrt(2 / pi)
       curve = d * mad(zv, v1 * mad(s, both(-2.f), both(1.f)), mad(v1, both(4.f), both(-2.f * kTanhC)));
     return mad(zv, d, s);
   }
   // kActSilu
-  const F2 s = logistic_of<EXACT>(c), d = s * mad(s, both(-1.f), both(1.f));
+  F2 d;
+  const F2 s = logistic_of<EXACT>(c, d);
   if (SECOND) curve = d * mad(c, mad(s, both(-2.f), both(1.f)), both(2.f));
   return mad(c, d, s);
 }
