@@ -54,7 +54,7 @@ def reference(act, z):
     return z * s, s + z * d * v1, d * (2 * v1 + z * v2 + z * v1 * v1 * w), np.abs(v)
 
 
-@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("few", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_activations_and_slopes_by_element(dtype, few, act):
