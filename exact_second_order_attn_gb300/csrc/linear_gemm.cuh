@@ -507,6 +507,10 @@ __device__ __forceinline__ void second_values(Ep& e, const Columns<HELD>& in, co
       for (int j = 0; j < 8; ++j) m[j] = t[j];
       if (a.q_planes) store_terms<FP32, TERMS>(boxes, 0, a.q_planes, g, m);
       if (a.sums) {
+        if (y0 + 32 > e.rows) {  // rows past the last: their t is 0 times uW, which need not be finite
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t[j] = live ? t[j] : 0.f;
+        }
         const float s = sum_columns8(t);
         const int n = x + 8 * g + lane / 4;
         if (lane % 4 == 0 && y0 < e.rows && n < e.N) a.sums[(size_t)(y0 / 32) * a.ld + n] = s;
