@@ -194,7 +194,7 @@ def dropout(d, x, residual=None, counter=None):
     if not x.is_contiguous() or not (residual is None or residual.is_contiguous()):
         raise ValueError("x and residual must be contiguous")
     # the backward draws by the description as it is now, whatever becomes of d
-    return _Dropout.apply(x, residual, counter, Dropout.from_buffer_copy(d))
+    return _Dropout.apply(x, residual, counter, Dropout.from_buffer_copy(_model._mask(d)))
 
 
 class _LinearBwd(torch.autograd.Function):
@@ -250,5 +250,5 @@ def linear(x, weight, bias=None, residual=None, activation="none", dropout=None,
     if not all(t is None or t.is_contiguous() for t in (x, weight, bias, residual)):
         raise ValueError("x, weight, bias and residual must be contiguous")
     keep = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))
-    how = activation, None if dropout is None else Dropout.from_buffer_copy(dropout)
+    how = activation, None if dropout is None else Dropout.from_buffer_copy(_model._mask(dropout))
     return _Linear.apply(x, weight, bias, residual, counter, how, keep)
