@@ -33,6 +33,7 @@ def _bind():
             raise RuntimeError("the binding of the model operators is missing: build it with "
                                "exact_second_order_attn_gb300.build.build()") from e
         ext.set_check(_check)
+        ext.set_dropout(Dropout)
         _ext = ext
     return _ext
 
@@ -158,13 +159,6 @@ def _activation(name):
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}") from None
 
 
-def _mask(dropout, optional=False):
-    """A ``Dropout`` (the binding tells descriptions apart by their size alone)."""
-    if not (isinstance(dropout, Dropout) or dropout is None and optional):
-        raise TypeError("dropout: a Dropout description is needed")
-    return dropout
-
-
 def linear_for(x: torch.Tensor, W: torch.Tensor, activation: str = "none") -> Linear:
     if x.dim() < 1 or W.dim() != 2 or x.shape[-1] != W.shape[1]:
         raise ValueError(f"x [..., K] and W [N, K] are needed, got {tuple(x.shape)} and {tuple(W.shape)}")
@@ -186,7 +180,7 @@ def fbob_dropout_apply(dropout, x, residual=None, counter=None, y=None, stream=N
     describes; rows are the last dimension of x (contiguous, any leading
     shape).  ``counter``: one int64 element on the device, added to the offset
     when the call runs.  The gradient of x is the same call on y's."""
-    return _call("dropout_apply", stream, _mask(dropout), x, residual, counter, y)
+    return _call("dropout_apply", stream, dropout, x, residual, counter, y)
 
 
 def fbob_linear_fwd(x, W, bias=None, residual=None, activation="none", dropout=None, counter=None, keep=True, y=None,
@@ -198,16 +192,16 @@ def fbob_linear_fwd(x, W, bias=None, residual=None, activation="none", dropout=N
     calls below take (fp16 beside bf16 tensors), is None for "none" or with
     ``keep`` false.
     ``workspace``: uint8."""
-    return _call("linear_fwd", stream, x, W, bias, residual, _activation(activation), _mask(dropout, True), counter,
-                 keep, y, z, workspace)
+    return _call("linear_fwd", stream, x, W, bias, residual, _activation(activation), dropout, counter, keep, y, z,
+                 workspace)
 
 
 def fbob_linear_bwd(x, W, z, dy, activation="none", dropout=None, counter=None, dx=None, dW=None, db=None,
                     want=(True, True, True), workspace=None, stream=None):
     """(dx, dW, db) of a linear layer; ``want`` says which to compute (the
     others are None).  The residual's gradient is dy."""
-    return _call("linear_bwd", stream, x, W, z, dy, _activation(activation), _mask(dropout, True), counter, dx, dW, db,
-                 *want, workspace)
+    return _call("linear_bwd", stream, x, W, z, dy, _activation(activation), dropout, counter, dx, dW, db, *want,
+                 workspace)
 
 
 def fbob_linear_bob(x, W, z, dy, ux, uW, ub=None, activation="none", dropout=None, counter=None, gx=None, gW=None,
@@ -215,5 +209,5 @@ def fbob_linear_bob(x, W, z, dy, ux, uW, ub=None, activation="none", dropout=Non
     """(gx, gW, gb, gdy) = the vector-Jacobian product of
     (x, W, bias, dy) -> (dx, dW, db) along (ux, uW, ub), where ub and one of
     ux and uW may be None; ``want`` says which to compute."""
-    return _call("linear_bob", stream, x, W, z, dy, ux, uW, ub, _activation(activation), _mask(dropout, True), counter,
-                 gx, gW, gb, gdy, *want, workspace)
+    return _call("linear_bob", stream, x, W, z, dy, ux, uW, ub, _activation(activation), dropout, counter, gx, gW, gb,
+                 gdy, *want, workspace)

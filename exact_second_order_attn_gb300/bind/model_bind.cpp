@@ -25,7 +25,8 @@ namespace {
 using at::ScalarType;
 using at::Tensor;
 
-PyObject* g_check = nullptr;  // raises the package's error for a status
+PyObject* g_check = nullptr;    // raises the package's error for a status
+PyObject* g_dropout = nullptr;  // the package's Dropout: other descriptions have its size too
 
 // A Python error has been set.
 struct Raised {};
@@ -448,7 +449,8 @@ struct Drop {
   const fbob_dropout* p = nullptr;
   explicit Drop(PyObject* o) {
     if (o == Py_None) return;
-    if (!PyObject_CheckBuffer(o)) raise(PyExc_TypeError, "dropout", "a Dropout description is needed");
+    if (!g_dropout || !PyObject_TypeCheck(o, (PyTypeObject*)g_dropout))
+      raise(PyExc_TypeError, "dropout", "a Dropout description is needed");
     if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) throw Raised{};
     if (b.len != (Py_ssize_t)sizeof(fbob_dropout)) {
       PyBuffer_Release(&b);
@@ -522,8 +524,8 @@ PyObject* linear_fwd(PyObject* const* a, Py_ssize_t n) {
   count(n, 11);
   const Tensor &x = *tensor(a[0], "x"), &W = *tensor(a[1], "W");
   const Tensor *b = tensor(a[2], "bias", true), *r = tensor(a[3], "residual", true);
-  const Layer l(x, W, a[4]);
   const Drop drop(a[5]);
+  const Layer l(x, W, a[4]);
   check(b, "bias", l.device, l.type, l.bias(W));
   check(r, "residual", l.device, l.type, l.out);
   const long long* counter = counter_of(a[6], l.device);
@@ -549,9 +551,9 @@ const Tensor* check_layer(const Layer& l, PyObject* z, const Tensor& dy) {
 PyObject* linear_bwd(PyObject* const* a, Py_ssize_t n) {
   count(n, 14);
   const Tensor &x = *tensor(a[0], "x"), &W = *tensor(a[1], "W"), &dy = *tensor(a[3], "dy");
+  const Drop drop(a[5]);
   const Layer l(x, W, a[4]);
   const Tensor* z = check_layer(l, a[2], dy);
-  const Drop drop(a[5]);
   const long long* counter = counter_of(a[6], l.device);
   const bool want_dx = flag(a[10]), want_dW = flag(a[11]), want_db = flag(a[12]);
   Launch at(l.device);
@@ -571,12 +573,12 @@ PyObject* linear_bob(PyObject* const* a, Py_ssize_t n) {
   count(n, 19);
   const Tensor &x = *tensor(a[0], "x"), &W = *tensor(a[1], "W"), &dy = *tensor(a[3], "dy");
   const Tensor *ux = tensor(a[4], "ux", true), *uW = tensor(a[5], "uW", true), *ub = tensor(a[6], "ub", true);
+  const Drop drop(a[8]);
   const Layer l(x, W, a[7]);
   const Tensor* z = check_layer(l, a[2], dy);
   check(ux, "ux", l.device, l.type, x.sizes());
   check(uW, "uW", l.device, l.type, W.sizes());
   check(ub, "ub", l.device, l.type, l.bias(W));
-  const Drop drop(a[8]);
   const long long* counter = counter_of(a[9], l.device);
   const bool want_gx = flag(a[14]), want_gW = flag(a[15]), want_gb = flag(a[16]), want_gdy = flag(a[17]);
   Launch at(l.device);
@@ -609,11 +611,22 @@ PyObject* set_check(PyObject*, PyObject* f) {
   Py_RETURN_NONE;
 }
 
+PyObject* set_dropout(PyObject*, PyObject* t) {
+  if (!PyType_Check(t)) {
+    PyErr_SetString(PyExc_TypeError, "a class is needed");
+    return nullptr;
+  }
+  Py_INCREF(t);
+  Py_XSETREF(g_dropout, t);
+  Py_RETURN_NONE;
+}
+
 #define ENTRY(f) {#f, (PyCFunction)(void (*)(void))entry<f>, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {
     ENTRY(rotary_apply),   ENTRY(layer_norm_fwd), ENTRY(layer_norm_bwd), ENTRY(layer_norm_bob),
     ENTRY(linear_ce_fwd),  ENTRY(linear_ce_bwd),  ENTRY(linear_ce_bob),  ENTRY(dropout_apply),
     ENTRY(linear_fwd),     ENTRY(linear_bwd),     ENTRY(linear_bob),     {"set_check", set_check, METH_O, nullptr},
+    {"set_dropout", set_dropout, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fbob_model", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

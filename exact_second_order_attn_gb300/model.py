@@ -169,6 +169,13 @@ def linear_cross_entropy(H, W, target, ignore_index=-100):
     return _Ce.apply(H, W, target, int(ignore_index))
 
 
+def _description(d):
+    """A copy of a ``Dropout``, which a later change of ``d`` does not reach."""
+    if not isinstance(d, Dropout):
+        raise TypeError("dropout: a Dropout description is needed")
+    return Dropout.from_buffer_copy(d)
+
+
 class _Dropout(torch.autograd.Function):
     """(x, residual) -> residual + m x; the backward is the same map of x."""
 
@@ -194,7 +201,7 @@ def dropout(d, x, residual=None, counter=None):
     if not x.is_contiguous() or not (residual is None or residual.is_contiguous()):
         raise ValueError("x and residual must be contiguous")
     # the backward draws by the description as it is now, whatever becomes of d
-    return _Dropout.apply(x, residual, counter, Dropout.from_buffer_copy(_model._mask(d)))
+    return _Dropout.apply(x, residual, counter, _description(d))
 
 
 class _LinearBwd(torch.autograd.Function):
@@ -250,5 +257,5 @@ def linear(x, weight, bias=None, residual=None, activation="none", dropout=None,
     if not all(t is None or t.is_contiguous() for t in (x, weight, bias, residual)):
         raise ValueError("x, weight, bias and residual must be contiguous")
     keep = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))
-    how = activation, None if dropout is None else Dropout.from_buffer_copy(_model._mask(dropout))
+    how = activation, None if dropout is None else _description(dropout)
     return _Linear.apply(x, weight, bias, residual, counter, how, keep)
