@@ -682,7 +682,7 @@ struct Run {
 }  // namespace lin
 
 bool linear_is_plain(const LinearArgs& a, LinearPass pass) {
-  return pass == LinearPass::kFwd && a.T <= lin::kRowsTokens;
+  return pass == LinearPass::kFwd && lin::takes_rows(a);
 }
 
 size_t linear_workspace(const LinearArgs& a, LinearPass pass) {

@@ -1,5 +1,5 @@
 // Internal interface of linear layers: the tensor-core product kernel
-// (linear_gemm.cu), the product of a few tokens (linear_rows.cu) and the passes
+// (linear_gemm.cuh), the product of a few tokens (linear_rows.cu) and the passes
 // that call them (linear.cu).
 #pragma once
 
@@ -84,8 +84,16 @@ cudaError_t gemm_second(int tile_n, const GemmArgs& g, cudaStream_t s);   // kNT
 cudaError_t gemm_slabs(const GemmArgs& g, cudaStream_t s);                // kNT, kSlab
 cudaError_t gemm_gradients(const GemmArgs& g, cudaStream_t s);            // kGradients, kGradient
 
-// y (and z) of up to kRowsTokens tokens without tensor cores (linear_rows.cu).
+// y (and z) of up to kRowsTokens tokens without tensor cores (linear_rows.cu, which has
+// the times of both ways).  For bf16 the tiles are as fast from 2^25 products on, from three
+// times as many where they need a copy of W (rows that are no multiples of 16 bytes); one
+// token never is.  fp32 tiles read W in three terms: they are as fast from some 2^29
+// products, 12 tokens of the widest layers, which is left to the rows.
 constexpr int kRowsTokens = 16;
+inline bool takes_rows(const LinearArgs& a) {
+  if (a.T <= 1) return true;
+  return a.T <= kRowsTokens && (!a.bf16 || (long long)a.T * a.K * a.N <= (a.K % 8 ? 3ll : 1ll) << 25);
+}
 cudaError_t rows(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace lin

@@ -1,5 +1,16 @@
-// A linear layer of up to 16 tokens: reading W bounds it, and a tensor-core tile of
-// 256 rows would leave most of the device idle.
+// A linear layer of few tokens: one token is bound by reading W (4096 -> 16,384, bf16,
+// 23.6 us: 5.7 TB/s), more by the issue of their products, some 7 per picosecond, where a
+// tensor-core tile of 256 rows takes the same time for 16 as for one.  takes_rows() is where
+// the two meet.  us of a call, here / in tiles:
+//                            1 token      2           4           8           16
+//   bf16   768 ->  2304     2.6 /  7.0   3.0 /  6.9  3.5 /  6.9  4.3 /  7.4   6.4 /  7.4
+//         2048 ->  2048     3.5 /  8.1   5.5 /  8.1  6.1 /  8.2  8.3 /  8.1  12.1 /  8.3
+//         4096 ->  4096     7.5 / 14.0  13.2 / 13.7 16.2 / 13.2 23.3 / 13.8  37.8 / 12.0
+//         4096 -> 16,384   23.6 / 35.9  45.7 / 34.1 61.8 / 38.0 92.3 / 33.2 163   / 28.5
+//         4097 ->  4096    13.3 / 26.9  16.7 / 26.8 22.0 / 27.0 29.1 / 26.4  46.2 / 23.3
+//   fp32   768 ->  2304     3.3 / 16.8   3.5 / 16.8  3.9 / 16.2  4.7 / 16.1   6.7 / 16.0
+//         4096 ->  4096    14.2 / 63.0  15.9 / 64.1 19.8 / 65.7 25.6 / 65.9  40.2 / 66.2
+//         4096 -> 16,384   47.8 / 218   54.9 / 218  86.3 / 218  143  / 219   263  / 220
 //
 // A warp takes four rows of W (outputs) and all tokens; a lane eight columns per step,
 // so every 16 bytes of W serve all tokens and x comes from the L1 cache.  Sums are

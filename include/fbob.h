@@ -434,8 +434,8 @@ size_t fbob_linear_workspace_bytes(const fbob_linear* p, const fbob_dropout* dro
  *        least, so that its slope stays 1)
  * bf16 matrices whose rows are multiples of 16 bytes have to start on 16 bytes
  * where they are multiplied (x, W, dy, ux, uW).  Sums are fp32; fp32 inputs are
- * multiplied as three bf16 terms each and lose nothing to about 2^-22.  x W^T of up
- * to 16 tokens is summed outside the tensor cores.
+ * multiplied as three bf16 terms each and lose nothing to about 2^-22.  x W^T of few
+ * tokens (one; up to 16 of fp32 or narrow layers) is summed outside the tensor cores.
  */
 fbob_status fbob_linear_fwd(const fbob_linear* p, const fbob_dropout* dropout, const long long* counter,
                             const void* x, const void* W, const void* b, const void* r,
