@@ -85,14 +85,15 @@ cudaError_t gemm_slabs(const GemmArgs& g, cudaStream_t s);                // kNT
 cudaError_t gemm_gradients(const GemmArgs& g, cudaStream_t s);            // kGradients, kGradient
 
 // y (and z) of up to kRowsTokens tokens without tensor cores (linear_rows.cu, which has
-// the times of both ways).  For bf16 the tiles are as fast from 2^25 products on, from three
-// times as many where they need a copy of W (rows that are no multiples of 16 bytes); one
-// token never is.  fp32 tiles read W in three terms: they are as fast from some 2^29
-// products, 12 tokens of the widest layers, which is left to the rows.
+// the times of both ways).  For bf16 the tiles are as fast on the GPU from 2^25 products on,
+// from 2^26.5 where they need a copy of W (rows that are no multiples of 16 bytes), but a call
+// costs the host 8.9 us against 3.8: the bounds are 2^26 and 2^27 (1024 -> 4096, 16 tokens,
+// 12.2 us here and 7.9 in tiles).  One token never is.  fp32 tiles read W in three terms: they
+// are as fast from some 2^29 products, 12 tokens of the widest layers, which is left to the rows.
 constexpr int kRowsTokens = 16;
 inline bool takes_rows(const LinearArgs& a) {
   if (a.T <= 1) return true;
-  return a.T <= kRowsTokens && (!a.bf16 || (long long)a.T * a.K * a.N <= (a.K % 8 ? 3ll : 1ll) << 25);
+  return a.T <= kRowsTokens && (!a.bf16 || (long long)a.T * a.K * a.N <= 1ll << (a.K % 8 ? 27 : 26));
 }
 cudaError_t rows(const LinearArgs& a, cudaStream_t s);
 
